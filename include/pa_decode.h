@@ -12,6 +12,18 @@
  *   pa_kv_write, pa_kv_write_fp8, pa_kv_write_nvfp4, pa_mla_cache_write
  *                           the paged writes
  *
+ * and the step of speculative decoding with drafted trees around them:
+ *
+ *   pa_plan_step            pages, block tables, slots, positions and tree masks of a
+ *                           step's new tokens, from the requests' lengths
+ *   pa_qk_norm_rope_write (_fp8, _nvfp4)
+ *                           per-head norms of queries and keys, the position rotation
+ *                           and the paged write in one pass
+ *   pa_tree_gqa (_fp8, _nvfp4)
+ *                           attention of each row's drafted tree over its paged context
+ *                           and its own ancestors
+ *   pa_kv_compact           moves an accepted path's keys and values together
+ *
  * The operations are the ones the following pages describe:
  *   - paged cache: K/V pools [pages, block_size, Hkv, D], per-request
  *     seq_lens, and a block table (vllm.cpp kernel-matrix, rows
@@ -117,6 +129,9 @@ typedef enum { PA_KIND_GQA = 0, PA_KIND_MLA_ABSORBED = 1 } pa_kind;
 #define PA_DEV_BAD_LEN 0x2u  /* a context length was < 0 or > max_context_len */
 #define PA_DEV_TIMEOUT 0x4u  /* a bounded wait inside a kernel gave up (never expected at the default limit) */
 #define PA_DEV_BAD_SLOT 0x8u /* a cache write named a slot at or past num_pages * page_size */
+#define PA_DEV_NO_PAGES 0x10u /* a plan ran out of free pages: some rows were refused */
+#define PA_DEV_BAD_POS 0x20u  /* a token's position was outside the angle table */
+#define PA_DEV_BAD_TREE 0x40u /* a parent or an accepted path was not one of a tree in order */
 
 /*
  * Bytes of device workspace a call with these arguments needs.  For
@@ -355,6 +370,208 @@ int pa_kv_write_nvfp4(const void *k, const void *v, const int64_t *slot_mapping,
 int pa_mla_cache_write(const void *c_lat, const void *k_rope, const int64_t *slot_mapping, void *cache,
                        int num_tokens, int page_size, int num_pages, uint32_t *status,
                        cudaStream_t stream);
+
+/*
+ * Plan of one step: gives every row the pages that its new tokens need and
+ * builds what the rest of the step reads -- the block table's new entries, the
+ * packed tokens' row starts, their cache slots and positions and, for drafted
+ * trees, each token's ancestor mask.  Everything is read and written on the
+ * device; nothing is copied to the host.
+ *   context_lens [batch] int32: tokens that row b holds in the cache, >= 0
+ *   new_lens     [batch] int32: new tokens of row b in this step (0: none); negative:
+ *                the row has ended and its pages go back to the free list
+ *   held_pages   [batch] int32: pages that row b holds (entries 0 .. held - 1 of its
+ *                block-table row), which may be more than its tokens fill
+ *   free_list    [num_pages] int32: a stack of free pages, of which free_count[0] are
+ *                valid; ended rows' pages are pushed, in row order, before any page is
+ *                taken
+ *   free_count   [1] int32
+ *   parents      [max_tokens] int32 or NULL: for the packed token i of a row its parent's
+ *                index in the row, smaller than i, or -1 for a token that follows
+ *                the context directly
+ *   block_table  [batch, max_pages_per_seq] int32: the new pages' entries are written
+ *                behind the held ones; nothing else in it is
+ *   context_lens_out, held_pages_out [batch] int32, free_count_out [1] int32: the
+ *                state after the step.  Each may be its input itself (updated in
+ *                place); any other overlap is refused
+ *   query_start  [batch + 1] int32: row b's tokens are [query_start[b], query_start[b + 1])
+ *   slot_mapping [max_tokens] int64: page * page_size + offset of each token, -1 for
+ *                tokens of refused rows and behind the last row
+ *   positions    [max_tokens] int32: context_lens[b] + i, or context_lens[b] + depth under
+ *                parents (a token's depth is its number of ancestors); 0 behind the last row
+ *   tree_mask    [max_tokens] uint64, given if and only if parents is: bit j of a
+ *                token's mask is set if token j of its row is itself or one of its
+ *                ancestors; 0 behind the last row.  A row of more than 64 new tokens
+ *                is a chain: its parents are not read and its masks are 0
+ * Row b needs max(0, ceil((context + new) / page_size) - held) pages.  The rows take
+ * them in row order from the top of the stack; a row that needs any and whose
+ * running sum of needs passes the pages there are gets none, and neither do the
+ * rows behind it that need some.  Such a row is refused: PA_DEV_NO_PAGES is set in
+ * *status, its tokens keep their places with slot -1, and its state is unchanged.
+ * A row is refused with PA_DEV_BAD_LEN where its lengths are negative, it would
+ * pass max_pages_per_seq pages, or its tokens would pass max_tokens; an ended row
+ * with held_pages out of range gives nothing back and sets PA_DEV_BAD_LEN.  A
+ * parent out of order sets PA_DEV_BAD_TREE and counts as -1; a page outside
+ * [0, num_pages) sets PA_DEV_BAD_PAGE and gives slot -1.
+ * batch in [0, 8192] and max_pages_per_seq * page_size below 2^31 (more:
+ * PA_ERR_UNSUPPORTED); page_size >= 1; status: a device word or NULL, whose bits
+ * are only ever set.  batch == 0 writes query_start[0],
+ * the padding and free_count_out.
+ */
+int pa_plan_step(const int32_t *context_lens, const int32_t *new_lens, const int32_t *held_pages,
+                 int32_t *free_list, const int32_t *free_count, const int32_t *parents,
+                 int32_t *block_table, int32_t *context_lens_out, int32_t *held_pages_out,
+                 int32_t *free_count_out, int32_t *query_start, int64_t *slot_mapping,
+                 int32_t *positions, uint64_t *tree_mask, int batch, int page_size, int num_pages,
+                 int max_pages_per_seq, int max_tokens, uint32_t *status, cudaStream_t stream);
+
+/*
+ * Norms of queries and keys, position rotation and paged write in one pass.
+ * For each head row x of q (and of k) of a token at position p, in fp32:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight      (weight NULL: y = x, no norm)
+ *   the first rot_dim values of y are rotated in pairs (u, v) by the angles
+ *   i = 0 .. rot_dim / 2 - 1 of cos_sin's row p: u cos - v sin, v cos + u sin.
+ *   A pair is (y[i], y[i + rot_dim / 2]), or (y[2 i], y[2 i + 1]) if interleaved;
+ *   the values from rot_dim on stay as they are
+ * and rounded once, q to bf16 into q_out, k to the pool's type into its slot; v is
+ * stored as pa_kv_write does.
+ *   q            [num_tokens, num_q_heads, head_dim] bf16, tokens q_stride values apart
+ *   k, v         [num_tokens, num_kv_heads, head_dim] bf16, tokens k_stride / v_stride
+ *                values apart: views of one projection's output are read in place.
+ *                Strides are multiples of 8 and at least a token's values
+ *   q_weight, k_weight [head_dim] bf16 or NULL
+ *   cos_sin      [max_position, rot_dim] fp32: row p holds the cosines of its rot_dim / 2
+ *                angles, then their sines
+ *   positions    [num_tokens] int32, slot_mapping [num_tokens] int64 (pa_plan_step's)
+ *   q_out        [num_tokens, num_q_heads, head_dim] bf16, dense.  May be q itself where
+ *                that is dense; any other overlap with an input is refused
+ *   k_pool, v_pool as for pa_kv_write
+ * A token with a negative slot is padding: nothing of it is written.  A slot past
+ * the pool sets PA_DEV_BAD_SLOT, a position outside [0, max_position) PA_DEV_BAD_POS
+ * in *status (or status NULL), and nothing of that token is written.  The slots of
+ * one call must be distinct.  head_dim in {64, 128, 256}; rot_dim a multiple of 16 in
+ * [16, head_dim]; eps finite and >= 0.  num_tokens == 0 is a no-op.
+ */
+int pa_qk_norm_rope_write(const void *q, const void *k, const void *v, const void *q_weight,
+                          const void *k_weight, const float *cos_sin, const int32_t *positions,
+                          const int64_t *slot_mapping, void *q_out, void *k_pool, void *v_pool,
+                          int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                          long long q_stride, long long k_stride, long long v_stride, int rot_dim,
+                          int interleaved, int max_position, float eps, int page_size, int num_pages,
+                          uint32_t *status, cudaStream_t stream);
+
+/*
+ * The same into FP8 E4M3 pools: the codes are those nearest to the fp32 quotients
+ * y / k_scale and v / v_scale (the layout and rounding of pa_kv_write_fp8; keys are
+ * not rounded to bf16 on the way).
+ */
+int pa_qk_norm_rope_write_fp8(const void *q, const void *k, const void *v, const void *q_weight,
+                              const void *k_weight, const float *cos_sin, const int32_t *positions,
+                              const int64_t *slot_mapping, void *q_out, void *k_pool, void *v_pool,
+                              int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                              long long q_stride, long long k_stride, long long v_stride, int rot_dim,
+                              int interleaved, int max_position, float eps, float k_scale, float v_scale,
+                              int page_size, int num_pages, uint32_t *status, cudaStream_t stream);
+
+/*
+ * The same into NVFP4 pools (the row layout and quantization of pa_kv_write_nvfp4,
+ * from the fp32 keys).
+ */
+int pa_qk_norm_rope_write_nvfp4(const void *q, const void *k, const void *v, const void *q_weight,
+                                const void *k_weight, const float *cos_sin, const int32_t *positions,
+                                const int64_t *slot_mapping, void *q_out, void *k_pool, void *v_pool,
+                                int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                long long q_stride, long long k_stride, long long v_stride, int rot_dim,
+                                int interleaved, int max_position, float eps, float k_scale,
+                                float v_scale, int page_size, int num_pages, uint32_t *status,
+                                cudaStream_t stream);
+
+/*
+ * Attention of drafted trees over the paged cache: the newest n_b tokens of row b,
+ * already written to the cache, are the nodes of a tree and the row's queries.
+ *   q            [num_tokens, num_q_heads, head_dim] bf16: the rows' nodes one row after
+ *                the other
+ *   query_start  [batch + 1] int32: row b's nodes are tokens [query_start[b],
+ *                query_start[b + 1]), n_b of them, 0 <= n_b <= max_query (0: the row
+ *                has no query in this step)
+ *   tree_mask    [num_tokens] uint64: bit j of a node's mask is set if the node attends
+ *                to its row's node j (itself among them; bits from n_b on are not read)
+ *   context_lens [batch] int32: L, the row's tokens including its n_b nodes
+ *   out          [num_tokens, num_q_heads, head_dim] bf16 (written for the rows' nodes;
+ *                tokens behind the last row are left as they were)
+ *   lse          [num_tokens, num_q_heads] fp32 (written likewise), or NULL
+ * Node i of a row attends to the row's tokens before the tree, [0, L - n_b), and to
+ * the nodes of its mask.  Under a window only to those fewer than `window` positions
+ * back, its position being L - n_b + depth, where a node's depth is the number of
+ * other nodes in its mask.  A node with nothing to attend to: out = 0, lse = -inf.
+ * A node's result does not depend on keys and values that it does not attend to,
+ * infinities and NaN among them.  A chain (mask 2^(i + 1) - 1) gives pa_verify_gqa's
+ * results within rounding, a single node (mask 1) pa_decode_gqa's.
+ *   max_query    in [1, 64]
+ * Rows whose query_start is not ascending within [0, num_tokens], has more than
+ * max_query nodes, or whose L is below n_b or out of range set PA_DEV_BAD_LEN and
+ * have unspecified results.  The other arguments and the error codes are those of
+ * pa_verify_gqa; the workspace is pa_tree_workspace_size bytes, and its status
+ * word is read by pa_read_device_status.  For a fixed num_splits results are
+ * bitwise reproducible and independent of the physical page order.  batch == 0
+ * is a no-op.
+ */
+int pa_tree_gqa(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+                const int32_t *context_lens, const int32_t *query_start, const uint64_t *tree_mask,
+                void *out, float *lse, int batch, int num_tokens, int max_query, int num_q_heads,
+                int num_kv_heads, int head_dim, int page_size, int num_pages, int max_pages_per_seq,
+                int max_context_len, float scale, int window, int num_splits, void *workspace,
+                size_t workspace_bytes, cudaStream_t stream);
+
+/* The same over FP8 E4M3 pools (the layout of pa_decode_gqa_fp8); head_dim in {64, 128, 256}. */
+int pa_tree_gqa_fp8(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+                    const int32_t *context_lens, const int32_t *query_start, const uint64_t *tree_mask,
+                    void *out, float *lse, int batch, int num_tokens, int max_query, int num_q_heads,
+                    int num_kv_heads, int head_dim, int page_size, int num_pages, int max_pages_per_seq,
+                    int max_context_len, float scale, float k_scale, float v_scale, int window,
+                    int num_splits, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* The same over NVFP4 pools (the layout of pa_decode_gqa_nvfp4). */
+int pa_tree_gqa_nvfp4(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+                      const int32_t *context_lens, const int32_t *query_start, const uint64_t *tree_mask,
+                      void *out, float *lse, int batch, int num_tokens, int max_query, int num_q_heads,
+                      int num_kv_heads, int head_dim, int page_size, int num_pages,
+                      int max_pages_per_seq, int max_context_len, float scale, float k_scale,
+                      float v_scale, int window, int num_splits, void *workspace,
+                      size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Bytes of device workspace a pa_tree_gqa call (of any cache format) with these
+ * arguments needs; 0 for arguments that the call would reject.
+ */
+size_t pa_tree_workspace_size(int batch, int max_query, int num_q_heads, int num_kv_heads, int head_dim,
+                              int max_context_len, int page_size, int num_splits);
+
+/*
+ * Accepted path: after a tree was verified, moves the keys and values of the
+ * accepted nodes together, so that they are the row's newest tokens in order and
+ * the row is an ordinary one again.
+ *   k_pool, v_pool [num_layers, num_pages, page_size, token_bytes]: pools of any format,
+ *                token_bytes the bytes of one token (all its heads), a multiple of 16
+ *   block_table, context_lens, query_start as for pa_tree_gqa (L includes the n_b nodes)
+ *   accepted     [batch, max_accepted] int32: the accepted nodes of row b, ascending;
+ *                entries from num_accepted[b] on are not read
+ *   num_accepted [batch] int32, in [0, max_accepted]
+ *   context_lens_out [batch] int32: L - n_b + num_accepted (written); must not overlap
+ *                context_lens
+ * Token L - n_b + i of every layer gets the rows of node accepted[b][i].  The pages
+ * that the rejected nodes filled stay the row's (pa_plan_step takes them up).  A
+ * path that is not ascending within [0, n_b) is cut before its first bad entry and
+ * sets PA_DEV_BAD_TREE; lengths out of range set PA_DEV_BAD_LEN and move nothing; a
+ * page outside [0, num_pages) sets PA_DEV_BAD_PAGE and that row is not moved.
+ * max_accepted in [1, 64]; batch up to 65535; max_pages_per_seq * page_size below
+ * 2^31; status a device word or NULL.
+ */
+int pa_kv_compact(void *k_pool, void *v_pool, const int32_t *block_table, const int32_t *context_lens,
+                  const int32_t *query_start, const int32_t *accepted, const int32_t *num_accepted,
+                  int32_t *context_lens_out, int num_layers, int batch, int max_accepted,
+                  int token_bytes, int page_size, int num_pages, int max_pages_per_seq,
+                  uint32_t *status, cudaStream_t stream);
 
 /* Static text for a pa_status value (never NULL). */
 const char *pa_status_string(int status);

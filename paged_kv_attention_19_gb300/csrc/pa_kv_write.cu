@@ -16,13 +16,11 @@
 // SM holds at once (one wave), with a grid-stride loop.
 #include <cmath>
 #include <cstdint>
-#include <cstring>
-
-#include <cuda_fp4.h>
 
 #include "pa_common.cuh"
 #include "pa_decode.h"
 #include "pa_launch.h"
+#include "pa_quant.cuh"
 
 namespace pa {
 
@@ -114,42 +112,6 @@ __global__ void __launch_bounds__(256) mla_cache_write_kernel(const uint4 *__res
 // codes each, so that a warp's loads and its stores are both contiguous: the fp32 quotient
 // x / scale (correctly rounded division), then the nearest code (ties to even), magnitudes
 // beyond 448 saturated.
-//
-// The correctly rounded quotient a / b is taken in one of three ways (the host picks per scale):
-//   * b a normal power of two with a normal reciprocal: the product a * (1 / b), exact;
-//   * b in [2^-100, 2^100]: Markstein's correction (P. Markstein, "Computation of elementary
-//     functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990): with
-//     y = RN(1 / b), q = RN(a y) is within one ulp of a / b, the remainder r = a - b q is exact
-//     (one fma), and RN(q + r y) is RN(a / b) whenever a and the quotient are normal numbers.  A
-//     quotient that overflows (q infinite) stays infinite.  Where a or the quotient is subnormal
-//     the result may be an ulp off, which changes no code derived from it: the quotient is then
-//     below 2^-26 and rounds to the zero code of E4M3 and of E2M1 (its sign is a's), and a block
-//     scale derived from it is the zero code;
-//   * otherwise the correctly rounded division.
-struct Fp8Scale {
-  float sc;    // the pool's scale b
-  float rcp;   // 1 / b when exact (a power of two), else 0
-  float rcpn;  // RN(1 / b) when b and 1 / b are normal and b is not a power of two, else 0
-};
-
-__device__ __forceinline__ float markstein_quot(float a, float b, float y) {
-  const float q = a * y;
-  const float r = fmaf(-q, b, a);
-  return fabsf(q) == INFINITY ? q : fmaf(r, y, q);
-}
-
-// The same for a quotient known to be finite (no infinite q to keep).
-__device__ __forceinline__ float markstein_quot_finite(float a, float b, float y) {
-  const float q = a * y;
-  return fmaf(fmaf(-q, b, a), y, q);
-}
-
-__device__ __forceinline__ float quot(float x, Fp8Scale s) {
-  if (s.rcp != 0.f) return x * s.rcp;
-  if (s.rcpn != 0.f) return markstein_quot(x, s.sc, s.rcpn);
-  return __fdiv_rn(x, s.sc);
-}
-
 __device__ __forceinline__ uint32_t quant4(uint32_t x0, uint32_t x1, Fp8Scale s) {
   const float2 a = make_float2(quot(__uint_as_float(x0 << 16), s), quot(__uint_as_float(x0 & 0xffff0000u), s));
   const float2 b = make_float2(quot(__uint_as_float(x1 << 16), s), quot(__uint_as_float(x1 & 0xffff0000u), s));
@@ -178,36 +140,6 @@ __global__ void __launch_bounds__(256) kv_write_fp8_kernel(const uint4 *__restri
 // bf16 vectors) of k and of v into 8 bytes of E2M1 code pairs and one E4M3 scale code, in fp32
 // with every step correctly rounded: the scale code of (amax / s) / 6, then each value's code of
 // (x / s) / E4M3(scale code).  The thread of a row's block 0 also writes the row's padding.
-struct Nvfp4Row {
-  int log2_nb;   // blocks per row, head_dim / 16, as a power of two
-  int code_off;  // byte offset of the block scales in a row: head_dim / 2
-  int row;       // bytes per row (a multiple of 16)
-};
-
-// Nearest E2M1 codes of two values (never NaN here): the conversion instruction rounds to nearest
-// with ties to the even mantissa bit, saturates at 6 and keeps the sign (a negative value that
-// rounds to zero gives the negative-zero code); lo goes to the low nibble.
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
-  return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest) & 0xffu;
-}
-
-// Value of a non-negative, non-NaN E4M3 code (exact in fp32).
-__device__ __forceinline__ float e4m3_value(uint32_t c) {
-  const uint32_t e = c >> 3, m = c & 7u;
-  return e == 0 ? (float)m * 0.001953125f : __uint_as_float(((e + 120u) << 23) | (m << 20));
-}
-
-struct Nvfp4Block {
-  uint2 codes;
-  uint32_t scale;
-};
-
-// The value of each non-negative E4M3 scale code and its correctly rounded reciprocal (0 for the
-// zero code), tabulated once per thread block.
-struct E4m3Table {
-  float val[128], rcp[128];
-};
-
 __device__ __forceinline__ Nvfp4Block quant_nvfp4(uint4 x0, uint4 x1, Fp8Scale s, const E4m3Table &tab) {
   const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
   // the largest magnitude as bf16 bits: the bits of |x| order like the values, NaN above infinity
@@ -314,20 +246,6 @@ int grid_for(Kernel kernel, long long n_vec) {
   const long long want = (n_vec + 255) / 256;
   const long long cap = (long long)sms * per_sm;
   return (int)(want < cap ? want : cap);
-}
-
-// How x / sc is divided (see Fp8Scale): the exact reciprocal of a normal power of two whose
-// reciprocal is normal, else RN(1 / sc) for Markstein's correction when sc and 1 / sc are normal,
-// else neither (the correctly rounded division).
-Fp8Scale fp8_scale(float sc) {
-  uint32_t b;
-  std::memcpy(&b, &sc, 4);
-  const uint32_t e = (b >> 23) & 0xffu;
-  const bool pow2 = (b & 0x807fffffu) == 0 && e >= 1 && e <= 253;  // sc = 2^(e - 127), 1 / sc = 2^(127 - e)
-  if (pow2) return {sc, 1.0f / sc, 0.f};
-  const float y = 1.0f / sc;  // host IEEE division: correctly rounded
-  const bool in_range = sc >= 0x1p-100f && sc <= 0x1p100f;
-  return {sc, 0.f, in_range ? y : 0.f};
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

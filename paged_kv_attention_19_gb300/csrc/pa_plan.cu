@@ -1,0 +1,480 @@
+// pa_plan.cu -- the plan of a step (pages, block tables, slots, positions and tree masks of its new
+// tokens) and the compaction of an accepted path in the paged cache.
+#include <climits>
+#include <cstdint>
+
+#include "pa_common.cuh"
+#include "pa_decode.h"
+#include "pa_launch.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanMaxBatch = 8192;
+constexpr int kPlanMaxCluster = 8;  // the portable cluster size
+constexpr int kTreeNodes = 64;      // nodes of a tree: bits of a mask
+
+struct PlanArgs {
+  const int32_t *context_lens, *new_lens, *held_pages;
+  int32_t *free_list;
+  const int32_t *free_count;
+  const int32_t *parents;  // or null: chains
+  int32_t *block_table, *context_lens_out, *held_pages_out, *free_count_out, *query_start;
+  int64_t *slot_mapping;
+  int32_t *positions;
+  uint64_t *tree_mask;
+  uint32_t *status;  // or null
+  int batch, page_size, num_pages, max_pages_per_seq, max_tokens;
+};
+
+// What a CTA keeps of a row, in shared memory.  need: pages to take; PLAN_REFUSED: a row with bad
+// lengths; PLAN_ENDED: its pages are given back (first: where they start among the given ones).
+struct PlanRow {
+  int32_t ctx, held, start, need, first;
+};
+constexpr int32_t PLAN_REFUSED = -1, PLAN_ENDED = -2;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// All threads of the cluster's CTAs; global writes before it are visible to all of them behind it.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Exclusive scan over the CTA's threads of two 64-bit values; the totals in *ta, *tb.
+__device__ __forceinline__ void block_scan2(long long &a, long long &b, long long *ta, long long *tb,
+                                            long long (*part)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  long long x = a, y = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(FULL, x, o), v = __shfl_up_sync(FULL, y, o);
+    if (lane >= o) {
+      x += u;
+      y += v;
+    }
+  }
+  if (lane == 31) {
+    part[warp][0] = x;
+    part[warp][1] = y;
+  }
+  __syncthreads();
+  long long pa = 0, pb = 0;
+  *ta = *tb = 0;
+  for (int w = 0; w < nw; ++w) {
+    if (w == warp) {
+      pa = *ta;
+      pb = *tb;
+    }
+    *ta += part[w][0];
+    *tb += part[w][1];
+  }
+  __syncthreads();
+  a = pa + x - a;
+  b = pb + y - b;
+}
+
+// One cluster of CTAs plans the step: a few thousand integers in and out, bound by the launch and by
+// the few dependent trips to memory.  Every CTA scans all rows (the lengths are read by each, which
+// costs no more than handing the sums over), keeps them in shared memory, and after one barrier of
+// the cluster writes its share of the rows and tokens.  Nothing that may be updated in place is
+// written before that barrier, and every CTA has read all of its inputs by then.  The page of a
+// token comes from the free list where it is a new one, so tokens need not wait for the table's
+// new entries.
+__global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs a) {
+  extern __shared__ PlanRow rows[];  // [batch + 1]: the last one holds the total of the tokens
+  __shared__ long long part[kPlanThreads / 32][2];
+  __shared__ int8_t up[kTreeNodes - 1 + kPlanThreads];  // parents of the chunk's tokens and 63 before it
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int rank = (int)cluster_rank(), nranks = (int)gridDim.x;  // one cluster is the grid
+  const int P = a.page_size;
+  uint32_t bad = 0;
+
+  long long tokens = 0, given = 0, needed = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int ctx = 0, n = 0, held = 0;
+    if (b < a.batch) {
+      ctx = a.context_lens[b];
+      n = a.new_lens[b];
+      held = a.held_pages[b];
+    }
+    const bool ended = n < 0;
+    const bool held_ok = held >= 0 && held <= a.max_pages_per_seq;
+    if (ended && !held_ok) bad |= PA_DEV_BAD_LEN;
+    long long t = ended ? 0 : n, g = ended && held_ok ? held : 0, tt, tg;
+    block_scan2(t, g, &tt, &tg, part);
+    t += tokens;
+    g += given;
+    tokens += tt;
+    given += tg;
+    // pages the row holds behind this step
+    const long long pages = ((long long)ctx + max(n, 0) + P - 1) / P;
+    const bool ok = ctx >= 0 && held_ok && pages <= a.max_pages_per_seq && t + max(n, 0) <= a.max_tokens;
+    if (!ended && !ok) bad |= PA_DEV_BAD_LEN;
+    const long long need = ok && !ended && n > 0 ? max(pages - held, 0ll) : 0;
+    long long f = need, z = 0, tf, tz;
+    block_scan2(f, z, &tf, &tz, part);
+    f += needed;
+    needed += tf;
+    if (b < a.batch) {
+      PlanRow r;
+      r.ctx = ctx;
+      r.held = held_ok ? held : 0;
+      r.start = (int)min(t, (long long)INT_MAX);
+      r.need = ended ? PLAN_ENDED : ok ? (int)need : PLAN_REFUSED;
+      r.first = (int)min(ended ? g : f, (long long)INT_MAX);
+      rows[b] = r;
+    }
+  }
+  const int count = min(max(*a.free_count, 0), a.num_pages);
+  if (*a.free_count != count) bad |= PA_DEV_BAD_LEN;
+  long long top_ = count + given;
+  if (top_ > a.num_pages) {  // more pages than there are: the ones past the list are lost
+    bad |= PA_DEV_BAD_LEN;
+    top_ = a.num_pages;
+  }
+  const int top = (int)top_;
+  const int total = (int)min(tokens, (long long)INT_MAX);
+  if (tid == 0) rows[a.batch].start = total;
+  __syncthreads();
+
+  // the ended rows' pages, one warp a row
+  const int nwarps = nranks * (kPlanThreads / 32), warp = rank * (kPlanThreads / 32) + (tid >> 5);
+  for (int b = warp; b < a.batch; b += nwarps) {
+    const PlanRow r = rows[b];
+    if (r.need != PLAN_ENDED) continue;
+    const int32_t *bt = a.block_table + (size_t)b * a.max_pages_per_seq;
+    for (int j = lane; j < r.held; j += 32) {
+      const long long to = (long long)count + r.first + j;
+      if (to < top) a.free_list[to] = bt[j];
+    }
+  }
+  cluster_barrier();
+
+  // rows: new table entries and state.  Page j of the step is entry top - 1 - j of the list.
+  auto granted = [&](const PlanRow &r) { return r.need == 0 || (r.need > 0 && (long long)r.first + r.need <= top); };
+  for (int b = warp; b < a.batch; b += nwarps) {
+    const PlanRow r = rows[b];
+    const bool ok = granted(r);
+    if (r.need > 0 && !ok) bad |= PA_DEV_NO_PAGES;
+    if (ok) {
+      int32_t *bt = a.block_table + (size_t)b * a.max_pages_per_seq + r.held;
+      for (int j = lane; j < r.need; j += 32) {
+        const int page = a.free_list[top - 1 - r.first - j];
+        if (page < 0 || page >= a.num_pages) bad |= PA_DEV_BAD_PAGE;
+        bt[j] = page;
+      }
+    }
+    if (lane == 0) {
+      const bool ended = r.need == PLAN_ENDED;
+      a.context_lens_out[b] = ended ? 0 : ok ? r.ctx + (rows[b + 1].start - r.start) : r.ctx;
+      a.held_pages_out[b] = ended ? 0 : ok ? r.held + r.need : r.held;
+      a.query_start[b] = r.start;
+    }
+  }
+  if (rank == 0) {
+    // pages taken: the needs are granted up to the first that passes the list, in row order
+    long long taken = 0;
+    for (int b = tid; b < a.batch; b += kPlanThreads) {
+      const PlanRow r = rows[b];
+      if (r.need > 0 && granted(r)) taken = max(taken, (long long)r.first + r.need);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) taken = max(taken, __shfl_xor_sync(FULL, taken, o));
+    if (lane == 0) part[tid >> 5][0] = taken;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 1; w < kPlanThreads / 32; ++w) taken = max(taken, part[w][0]);
+      *a.free_count_out = top - (int)taken;
+      a.query_start[a.batch] = total;
+    }
+  }
+
+  // tokens, a chunk of kPlanThreads at a time
+  for (int t0 = rank * kPlanThreads; t0 < a.max_tokens; t0 += nranks * kPlanThreads) {
+    const int t = t0 + tid;
+    if (a.parents) {
+      __syncthreads();
+      for (int e = tid; e < kTreeNodes - 1 + kPlanThreads; e += kPlanThreads) {
+        const int s = t0 - (kTreeNodes - 1) + e;
+        const int p = s >= 0 && s < total && s < a.max_tokens ? a.parents[s] : -1;
+        up[e] = (int8_t)(p < -1 || p >= kTreeNodes ? -2 : p);
+      }
+      __syncthreads();
+    }
+    if (t >= a.max_tokens) continue;
+    int64_t slot = -1;
+    int pos = 0;
+    uint64_t mask = 0;
+    if (t < total) {
+      int lo = 0, hi = a.batch - 1;  // the last row that starts at or before t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (rows[mid].start <= t) lo = mid;
+        else hi = mid - 1;
+      }
+      const PlanRow r = rows[lo];
+      const int i = t - r.start, n = rows[lo + 1].start - r.start;
+      int depth = i;
+      if (a.parents && n <= kTreeNodes) {
+        for (int j = i;;) {  // up the ancestors: each step goes to a smaller index
+          mask |= 1ull << j;
+          const int p = up[kTreeNodes - 1 + tid - i + j];
+          if (p < 0 || p >= j) {
+            if (p != -1) bad |= PA_DEV_BAD_TREE;
+            break;
+          }
+          j = p;
+        }
+        depth = __popcll(mask) - 1;
+      }
+      const long long at = (long long)r.ctx + i;
+      pos = (int)min((long long)r.ctx + depth, (long long)INT_MAX);
+      if (granted(r)) {  // then at < max_pages_per_seq * P, which the host keeps below 2^31
+        const unsigned k = (unsigned)at / (unsigned)P;
+        const int page = (int)k < r.held ? a.block_table[(size_t)lo * a.max_pages_per_seq + k]
+                                         : a.free_list[top - 1 - r.first - ((int)k - r.held)];
+        if (page < 0 || page >= a.num_pages) bad |= PA_DEV_BAD_PAGE;
+        else slot = (int64_t)page * P + ((unsigned)at - k * (unsigned)P);
+      }
+    }
+    a.slot_mapping[t] = slot;
+    a.positions[t] = pos;
+    if (a.tree_mask) a.tree_mask[t] = mask;
+  }
+  if (bad && a.status) atomicOr(a.status, bad);
+}
+
+// Accepted paths.  Block (x, y) moves 256 16-byte columns of row y: a column is one 16-byte piece of
+// a token in one pool of one layer, and each thread moves its column's accepted nodes in ascending
+// order, eight loads in flight.  A node's target lies at or before its source and behind every
+// earlier source, so no source is overwritten before it is read.
+constexpr int kCompactThreads = 256;
+
+struct CompactArgs {
+  uint4 *k_pool, *v_pool;
+  const int32_t *block_table, *context_lens, *query_start, *accepted, *num_accepted;
+  int32_t *context_lens_out;
+  uint32_t *status;
+  long long columns;      // 2 * layers * vectors per token
+  long long layer_vecs;   // vectors of a layer's pool
+  int vecs;               // 16-byte vectors per token
+  int max_accepted, page_size, num_pages, max_pages_per_seq;
+};
+
+__global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const CompactArgs a) {
+  __shared__ long long src[kTreeNodes], dst[kTreeNodes];  // slots; -1: not moved
+  __shared__ int moves;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  if (tid < 32) {
+    uint32_t bad = 0;
+    const int L = a.context_lens[b], n = a.query_start[b + 1] - a.query_start[b];
+    int m = a.num_accepted[b];
+    const long long room = (long long)a.max_pages_per_seq * a.page_size;
+    const bool ok = n >= 0 && L >= n && L <= room && m >= 0 && m <= a.max_accepted;
+    if (!ok) {
+      bad |= PA_DEV_BAD_LEN;
+      m = 0;
+    }
+    const int prefix = L - n;
+    int good = 0;  // entries before the first bad one
+    bool stop = false;
+    for (int i0 = 0; i0 < m && !stop; i0 += 32) {
+      const int i = i0 + lane;
+      int p = 0, before = -1;
+      if (i < m) {
+        p = a.accepted[(size_t)b * a.max_accepted + i];
+        before = i > 0 ? a.accepted[(size_t)b * a.max_accepted + i - 1] : -1;
+      }
+      const uint32_t wrong = __ballot_sync(FULL, i < m && (p <= before || p < 0 || p >= n));
+      stop = wrong != 0;
+      good = stop ? i0 + __ffs((int)wrong) - 1 : min(m, i0 + 32);
+      if (i < good) {
+        const int32_t *bt = a.block_table + (size_t)b * a.max_pages_per_seq;
+        const int s = prefix + p, d = prefix + i;
+        const int ps = bt[s / a.page_size], pd = bt[d / a.page_size];
+        const bool in = ps >= 0 && ps < a.num_pages && pd >= 0 && pd < a.num_pages;
+        if (!in) bad |= PA_DEV_BAD_PAGE;
+        src[i] = in && s != d ? (long long)ps * a.page_size + s % a.page_size : -1;
+        dst[i] = (long long)pd * a.page_size + d % a.page_size;
+      }
+    }
+    if (stop) bad |= PA_DEV_BAD_TREE;
+    if (lane == 0) {
+      moves = good;
+      if (blockIdx.x == 0) a.context_lens_out[b] = ok ? prefix + good : max(L, 0);
+    }
+    if (bad && a.status && blockIdx.x == 0) atomicOr(a.status, bad);
+  }
+  __syncthreads();
+  const long long col = (long long)blockIdx.x * kCompactThreads + tid;
+  if (col >= a.columns) return;
+  const int e = (int)(col % a.vecs);
+  const long long lp = col / a.vecs;  // layer * 2 + pool
+  uint4 *pool = ((lp & 1) ? a.v_pool : a.k_pool) + (lp >> 1) * a.layer_vecs + e;
+  const int m = moves;
+  constexpr int U = 8;
+  for (int i0 = 0; i0 < m; i0 += U) {
+    uint4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u < m && src[i0 + u] >= 0) x[u] = pool[src[i0 + u] * a.vecs];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u < m && src[i0 + u] >= 0) pool[dst[i0 + u] * a.vecs] = x[u];
+  }
+}
+
+bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+// Do [p, p + np) and [q, q + nq) share a byte?
+bool overlap(const void *p, size_t np, const void *q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + nq && b < a + np;
+}
+
+template <typename Args>
+cudaError_t launch(void (*kernel)(Args), dim3 grid, int threads, size_t smem, int cluster, const Args &a,
+                   cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+}  // namespace pa
+
+extern "C" int pa_plan_step(const int32_t *context_lens, const int32_t *new_lens, const int32_t *held_pages,
+                            int32_t *free_list, const int32_t *free_count, const int32_t *parents,
+                            int32_t *block_table, int32_t *context_lens_out, int32_t *held_pages_out,
+                            int32_t *free_count_out, int32_t *query_start, int64_t *slot_mapping,
+                            int32_t *positions, uint64_t *tree_mask, int batch, int page_size, int num_pages,
+                            int max_pages_per_seq, int max_tokens, uint32_t *status, cudaStream_t stream) {
+  using namespace pa;
+  note_launches(0);
+  if (batch < 0 || page_size <= 0 || num_pages <= 0 || max_pages_per_seq <= 0 || max_tokens < 0)
+    return PA_ERR_INVALID_ARGUMENT;
+  if (batch > kPlanMaxBatch || (long long)max_pages_per_seq * page_size > INT_MAX) return PA_ERR_UNSUPPORTED;
+  if (!free_list || !free_count || !free_count_out || !query_start) return PA_ERR_INVALID_ARGUMENT;
+  if (batch > 0 && (!context_lens || !new_lens || !held_pages || !block_table || !context_lens_out || !held_pages_out))
+    return PA_ERR_INVALID_ARGUMENT;
+  if (max_tokens > 0 && (!slot_mapping || !positions)) return PA_ERR_INVALID_ARGUMENT;
+  if ((parents != nullptr) != (tree_mask != nullptr)) return PA_ERR_INVALID_ARGUMENT;
+  const void *words[] = {context_lens, new_lens, held_pages, free_list, free_count, parents, block_table,
+                         context_lens_out, held_pages_out, free_count_out, query_start, positions, status};
+  for (const void *p : words)
+    if (!aligned_to(p, 4)) return PA_ERR_MISALIGNED;
+  if (!aligned_to(slot_mapping, 8) || !aligned_to(tree_mask, 8)) return PA_ERR_MISALIGNED;
+  // every output against every input and every other output; in place means the same array
+  const size_t nb = (size_t)batch * 4, nt = (size_t)max_tokens;
+  struct Range {
+    const void *p;
+    size_t n;
+  };
+  const Range in[] = {{context_lens, nb}, {held_pages, nb}, {free_count, 4}, {new_lens, nb}, {parents, parents ? nt * 4 : 0}};
+  const Range out[] = {{context_lens_out, nb}, {held_pages_out, nb}, {free_count_out, 4}, {query_start, nb + 4},
+                       {slot_mapping, nt * 8}, {positions, nt * 4}, {tree_mask, tree_mask ? nt * 8 : 0},
+                       {block_table, (size_t)max_pages_per_seq * nb}, {free_list, (size_t)num_pages * 4},
+                       {status, status ? 4u : 0u}};
+  constexpr int n_in = sizeof(in) / sizeof(in[0]), n_out = sizeof(out) / sizeof(out[0]);
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j) {
+      const bool same = i == j && i < 3 && out[i].p == in[j].p;
+      if (!same && overlap(out[i].p, out[i].n, in[j].p, in[j].n)) return PA_ERR_INVALID_ARGUMENT;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return PA_ERR_INVALID_ARGUMENT;
+  }
+  PlanArgs a = {context_lens, new_lens, held_pages, free_list, free_count, parents, block_table, context_lens_out,
+                held_pages_out, free_count_out, query_start, slot_mapping, positions, tree_mask, status, batch,
+                page_size, num_pages, max_pages_per_seq, max_tokens};
+  const size_t smem = (size_t)(batch + 1) * sizeof(PlanRow);
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(plan_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (kPlanMaxBatch + 1) * (int)sizeof(PlanRow));
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  const int chunks = (max_tokens + kPlanThreads - 1) / kPlanThreads;
+  const int cluster = chunks <= 1 && batch <= 64 ? 1 : kPlanMaxCluster;
+  if (const cudaError_t e = launch(plan_step_kernel, dim3((unsigned)cluster), kPlanThreads, smem, cluster, a, stream);
+      e != cudaSuccess)
+    return cuda_fail(e);
+  note_launches(1);
+  return PA_OK;
+}
+
+extern "C" int pa_kv_compact(void *k_pool, void *v_pool, const int32_t *block_table, const int32_t *context_lens,
+                             const int32_t *query_start, const int32_t *accepted, const int32_t *num_accepted,
+                             int32_t *context_lens_out, int num_layers, int batch, int max_accepted, int token_bytes,
+                             int page_size, int num_pages, int max_pages_per_seq, uint32_t *status,
+                             cudaStream_t stream) {
+  using namespace pa;
+  note_launches(0);
+  if (num_layers <= 0 || batch < 0 || token_bytes <= 0 || page_size <= 0 || num_pages <= 0 || max_pages_per_seq <= 0 ||
+      max_accepted <= 0)
+    return PA_ERR_INVALID_ARGUMENT;
+  if (token_bytes % 16 != 0 || max_accepted > kTreeNodes || batch > 65535 ||
+      (long long)max_pages_per_seq * page_size > INT_MAX)
+    return PA_ERR_UNSUPPORTED;
+  if (batch == 0) return PA_OK;
+  if (!k_pool || !v_pool || !block_table || !context_lens || !query_start || !accepted || !num_accepted ||
+      !context_lens_out)
+    return PA_ERR_INVALID_ARGUMENT;
+  if (!aligned_to(k_pool, 16) || !aligned_to(v_pool, 16)) return PA_ERR_MISALIGNED;
+  const void *words[] = {block_table, context_lens, query_start, accepted, num_accepted, context_lens_out, status};
+  for (const void *p : words)
+    if (!aligned_to(p, 4)) return PA_ERR_MISALIGNED;
+  const size_t nb = (size_t)batch * 4;
+  const size_t pool = (size_t)num_layers * num_pages * page_size * token_bytes;
+  if (overlap(context_lens_out, nb, context_lens, nb) || overlap(context_lens_out, nb, query_start, nb + 4) ||
+      overlap(context_lens_out, nb, num_accepted, nb) || overlap(context_lens_out, nb, accepted, nb * max_accepted) ||
+      overlap(context_lens_out, nb, block_table, nb * max_pages_per_seq) || overlap(k_pool, pool, v_pool, pool))
+    return PA_ERR_INVALID_ARGUMENT;
+  CompactArgs a;
+  a.k_pool = static_cast<uint4 *>(k_pool);
+  a.v_pool = static_cast<uint4 *>(v_pool);
+  a.block_table = block_table;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.accepted = accepted;
+  a.num_accepted = num_accepted;
+  a.context_lens_out = context_lens_out;
+  a.status = status;
+  a.vecs = token_bytes / 16;
+  a.columns = 2ll * num_layers * a.vecs;
+  a.layer_vecs = (long long)num_pages * page_size * a.vecs;
+  a.max_accepted = max_accepted;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  a.max_pages_per_seq = max_pages_per_seq;
+  const long long gx = (a.columns + kCompactThreads - 1) / kCompactThreads;
+  if (gx > INT_MAX) return PA_ERR_UNSUPPORTED;
+  if (const cudaError_t e = launch(kv_compact_kernel, dim3((unsigned)gx, (unsigned)batch), kCompactThreads, 0, 0, a, stream);
+      e != cudaSuccess)
+    return cuda_fail(e);
+  note_launches(1);
+  return PA_OK;
+}

@@ -1,0 +1,794 @@
+"""The tree-drafting operators on the GPU against plain references in 64 bits: step plan, norm + rotation +
+paged write, tree attention, path compaction, and a run of them together."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import tree_refs as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pa():
+    import paged_kv_attention_19_gb300 as pkg
+    return pkg
+
+
+def dev(a, dtype=None):
+    return torch.as_tensor(np.asarray(a)).to("cuda", dtype)
+
+
+def i32(a):
+    return dev(np.asarray(a, np.int64), torch.int32)
+
+
+def masks_i64(masks):
+    return dev(np.array([m & (2 ** 64 - 1) for m in masks], np.uint64).view(np.int64))
+
+
+def raw(t):
+    return (t.view(torch.int16) if t.dtype == torch.bfloat16 else t).cpu().numpy().view(
+        np.uint16 if t.dtype == torch.bfloat16 else np.uint8)
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+# ------------------------------------------------------------------------------------------ tree attention
+
+NAN_BYTES = {"bf16": 0x7FFF, "fp8": 0x7F, "nvfp4": 0x7F}
+
+
+class Tree:
+    """Rows of (L, n) over a shuffled pool; slots that no row fills hold NaN."""
+
+    def __init__(self, seed, rows, hq, hkv, D, page, fmt="bf16", chain=False, masks=None, extra=3, shuffle=True,
+                 big_q=1.0):
+        self.rng = rng = np.random.default_rng(seed)
+        self.rows, self.hq, self.hkv, self.D, self.page, self.fmt = rows, hq, hkv, D, page, fmt
+        g = torch.Generator().manual_seed(seed)
+        pages = [-(-L // page) for L, _ in rows]
+        total = sum(pages) + 2
+        order = rng.permutation(total)  # drawn either way: the same masks and values with and without
+        order = order if shuffle else np.arange(total)
+        W = max(pages + [1]) + 1
+        self.table = np.full((len(rows), W), -7, np.int64)  # entries behind a row's last page are not read
+        at = 0
+        for b, n in enumerate(pages):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        self.scales = {"bf16": (1.0, 1.0), "fp8": (0.013, 0.021), "nvfp4": (0.25, 0.0625)}[fmt]
+        width = D if fmt == "bf16" else R.row_bytes(fmt, D)
+        pools = []
+        for _ in range(2):
+            if fmt == "bf16":
+                p = torch.full((total, page, hkv, D), math.nan).to(torch.bfloat16)
+            else:
+                p = torch.full((total, page, hkv, width), 0x7F, dtype=torch.uint8)
+            pools.append(p)
+        lens = [L for L, _ in rows]
+        for b, L in enumerate(lens):
+            if L == 0:
+                continue
+            t = np.arange(L)
+            pg, off = self.table[b, t // page], t % page
+            for p in pools:
+                x = torch.randn(L, hkv, D, generator=g)
+                if fmt == "bf16":
+                    v = x.to(torch.bfloat16)
+                elif fmt == "fp8":
+                    v = (x / 0.015).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+                else:
+                    v = torch.zeros(L, hkv, width, dtype=torch.uint8)
+                    v[..., :D // 2] = torch.randint(0, 256, (L, hkv, D // 2), generator=g).to(torch.uint8)
+                    blk = (torch.rand(L, hkv, D // 16, generator=g) * 2 + 0.25).to(torch.float8_e4m3fn)
+                    v[..., D // 2:D // 2 + D // 16] = blk.view(torch.uint8)
+                p[pg, off] = v
+        self.k, self.v = (p.cuda() for p in pools)
+        self.start = np.concatenate(([0], np.cumsum([n for _, n in rows]))).astype(int)
+        self.T = int(self.start[-1])
+        self.extra = extra  # padded tokens behind the last row
+        self.q = (torch.randn(self.T + extra, hq, D, generator=g) * big_q).to(torch.bfloat16).cuda()
+        self.masks = masks if masks is not None else [m for _, n in rows for m in R.random_tree(rng, n, chain)[1]]
+        self.scale = 1.0 / math.sqrt(D)
+
+    def args(self):
+        m = list(self.masks) + [2 ** 64 - 1] * self.extra
+        return (self.q, self.k, self.v, i32(self.table), i32([L for L, _ in self.rows]), i32(self.start), masks_i64(m))
+
+    def call(self, pa, max_query=None, window=0, num_splits=0, args=None, out=None, lse=None, ws=None, stream=None):
+        args = args or self.args()
+        if out is None:
+            out = torch.full(self.q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+            lse = torch.full(self.q.shape[:2], 7.0, device="cuda")
+        mq = max_query or max([n for _, n in self.rows] + [1])
+        if ws is None:
+            ws = pa.workspace_for_tree(self.q, self.k, args[3], mq, num_splits)
+        fn = {"bf16": pa.pa_tree_gqa, "fp8": pa.pa_tree_gqa_fp8, "nvfp4": pa.pa_tree_gqa_nvfp4}[self.fmt]
+        more = {} if self.fmt == "bf16" else {"k_scale": self.scales[0], "v_scale": self.scales[1]}
+        fn(*args, out, lse, max_query=mq, scale=self.scale, window=window, num_splits=num_splits, workspace=ws,
+           stream=stream, **more)
+        return out, lse, ws
+
+    def reference(self, window=0):
+        kk = R.pool_values(raw(self.k), self.fmt, self.D, self.scales[0])
+        vv = R.pool_values(raw(self.v), self.fmt, self.D, self.scales[1])
+        q = f64(self.q)
+        parts = []
+        for b, (L, n) in enumerate(self.rows):
+            if n == 0:
+                continue
+            t = np.arange(L)
+            pg, off = self.table[b, t // self.page], t % self.page
+            s = slice(self.start[b], self.start[b + 1])
+            parts.append(R.tree_attention(q[s], kk[pg, off], vv[pg, off], self.masks[s], L, self.scale, window))
+        return [np.concatenate(x) for x in zip(*parts)]
+
+    def check(self, pa, window=0, num_splits=0, max_query=None):
+        out, lse, ws = self.call(pa, window=window, num_splits=num_splits, max_query=max_query)
+        torch.cuda.synchronize()
+        assert pa.pa_read_device_status(ws) == 0
+        assert bool((out[self.T:] == 7.0).all()) and bool((lse[self.T:] == 7.0).all()), "tokens behind the last row"
+        R.check_tree(f64(out[:self.T]), f64(lse[:self.T]), *self.reference(window), self.D)
+        return out, lse
+
+
+LADDER = [(1, 1), (2, 2), (3, 1), (31, 7), (32, 5), (33, 33), (64, 16), (100, 0), (129, 12), (685, 20), (1000, 3)]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("hq,hkv,D,page", [(8, 2, 128, 16), (5, 5, 64, 32), (16, 2, 256, 32), (36, 3, 128, 8),
+                                           (14, 2, 64, 128), (40, 2, 128, 64)])
+def test_tree_ladder(pa, fmt, hq, hkv, D, page):
+    Tree(10 + hq + D, LADDER, hq, hkv, D, page, fmt).check(pa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
+def test_tree_of_64_nodes_and_many_heads(pa, fmt):
+    Tree(40, [(64, 64), (777, 64), (1500, 64), (70, 63)], 24, 2, 128, 16, fmt).check(pa)
+
+
+def test_tree_more_heads_than_a_tile(pa):
+    """One key head for 130 and 200 query heads."""
+    Tree(41, [(90, 5), (300, 9)], 130, 1, 64, 16).check(pa)
+    Tree(42, [(90, 5), (300, 2)], 200, 1, 128, 16).check(pa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("window", [1, 2, 7, 64, 100, 640, 100000])
+def test_tree_window(pa, fmt, window):
+    Tree(50 + window, LADDER, 8, 2, 128, 16, fmt).check(pa, window=window)
+    Tree(51 + window, [(300, 64), (64, 64)], 4, 1, 64, 32, fmt if fmt == "bf16" else "nvfp4", chain=True).check(pa, window=window)
+
+
+@pytest.mark.parametrize("splits", [1, 3, 64, 1000])
+def test_tree_splits(pa, splits):
+    Tree(60, [(5000, 12), (3, 2), (900, 40), (1, 1), (77, 0)], 16, 2, 128, 16).check(pa, num_splits=splits)
+
+
+def test_tree_long_context(pa):
+    Tree(61, [(20011, 6), (9000, 17)], 4, 1, 128, 64).check(pa)
+    Tree(62, [(20011, 6), (9000, 17)], 4, 1, 128, 64, "nvfp4").check(pa)
+
+
+def test_tree_many_rows(pa):
+    """More rows than threads of a block, most of them of one node."""
+    Tree(63, [(1 + (i * 7) % 50, 1 if i % 9 else (i * 7) % 50 % 5) for i in range(700)], 4, 2, 64, 8).check(pa)
+
+
+def test_tree_masks_that_are_no_trees(pa):
+    """Any mask: nodes behind, nothing at all, bits past the row's nodes."""
+    rng = np.random.default_rng(7)
+    rows = [(5, 5), (40, 9), (64, 64), (500, 33), (3, 3)]
+    masks = []
+    for b, (_, n) in enumerate(rows):
+        m = [int(rng.integers(0, 2 ** 63)) * 2 + int(rng.integers(0, 2)) for _ in range(n)]
+        m[0] = 0
+        masks += [0] * n if b == 4 else m
+    t = Tree(70, rows, 8, 2, 128, 16, masks=masks)
+    out, lse = t.check(pa)
+    assert bool((out[t.T - 3:t.T] == 0).all()) and bool(torch.isneginf(lse[t.T - 3:t.T]).all())
+    t.check(pa, window=3)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("what", ["nan", "inf"])
+def test_tree_nodes_do_not_see_others(pa, fmt, what):
+    """NaN (and infinite) keys and values of nodes that a node does not attend to change nothing of it; of
+    nodes that it does, they reach it."""
+    if what == "inf" and fmt != "bf16":
+        pytest.skip("the 8- and 4-bit formats have no infinities")
+    rows = [(150, 11), (30, 30), (64, 20)]
+    t = Tree(80, rows, 8, 2, 128, 16, fmt)
+    want, want_l, _ = t.call(pa)
+    bad = []  # nodes made bad: the last two of every row, and one in the middle
+    for b, (L, n) in enumerate(rows):
+        for i in (n - 1, n - 2, n // 2):
+            bad.append((b, i))
+            tok = L - n + i
+            pg, off = int(t.table[b, tok // 16]), tok % 16
+            for p in (t.k, t.v):
+                if fmt == "bf16":
+                    p[pg, off, :, ::3] = math.nan if what == "nan" else math.inf
+                    if what == "inf":
+                        p[pg, off, :, 1::3] = -math.inf
+                else:
+                    p[pg, off, :, -(t.k.shape[-1] // 4):] = 0x7F
+                    p[pg, off, :, t.D // 2:t.D // 2 + 4] = 0x7F
+    out, lse, ws = t.call(pa)
+    torch.cuda.synchronize()
+    seen = torch.zeros(t.T, dtype=torch.bool)
+    for b, (L, n) in enumerate(rows):
+        for i in range(n):
+            m = t.masks[t.start[b] + i]
+            seen[t.start[b] + i] = any(m >> j & 1 for bb, j in bad if bb == b)
+    assert seen.any() and not seen.all()
+    clean = (~seen).nonzero()[:, 0].cuda()
+    assert torch.equal(out[clean], want[clean]) and torch.equal(lse[clean], want_l[clean])
+    hit = out[seen.nonzero()[:, 0].cuda()].float()
+    assert bool((~torch.isfinite(hit)).any(-1).all()), "a node that attends to such a node has no finite output"
+
+
+def test_tree_infinite_values_only(pa):
+    """An infinite value with ordinary keys: the attending nodes get that infinity there, and finite results
+    elsewhere; the others are as before."""
+    rows = [(40, 6)]
+    t = Tree(81, rows, 4, 1, 64, 8, chain=True)
+    want, want_l, _ = t.call(pa)
+    tok = 40 - 6 + 3
+    t.v[int(t.table[0, tok // 8]), tok % 8, 0, 5] = math.inf
+    t.v[int(t.table[0, tok // 8]), tok % 8, 0, 9] = -math.inf
+    out, lse, _ = t.call(pa)
+    assert torch.equal(out[:3], want[:3]) and torch.equal(lse[:6], want_l[:6])
+    assert bool((out[3:6, :, 5] == math.inf).all()) and bool((out[3:6, :, 9] == -math.inf).all())
+    rest = [d for d in range(64) if d not in (5, 9)]
+    assert torch.equal(out[3:6][:, :, rest], want[3:6][:, :, rest])
+
+
+def test_tree_lowest_and_huge_scores(pa):
+    """Scores of thousands, of either sign: the running maximum keeps the weights in range."""
+    t = Tree(82, [(200, 9), (65, 17), (3, 3)], 8, 2, 128, 16, big_q=300.0)
+    out, lse, _ = t.call(pa)
+    o, l, spread, size = t.reference()
+    R.check_tree(f64(out[:t.T]), f64(lse[:t.T]), o, l, spread, size, t.D)
+
+
+def test_tree_chain_is_verify_and_one_node_is_decode(pa):
+    """Within both sides' rounding: half a bf16 step of each output and of each weight."""
+    rows = [(100, 5), (685, 5), (33, 5)]
+    t = Tree(90, rows, 16, 4, 128, 32, chain=True, extra=0)
+    out, lse, _ = t.call(pa)
+    q = t.q.view(3, 5, 16, 128)
+    vo, vl = torch.empty_like(q), torch.empty(3, 5, 16, device="cuda")
+    bt, lens = i32(t.table), i32([L for L, _ in rows])
+    pa.pa_verify_gqa(q, t.k, t.v, bt, lens, vo, vl, scale=t.scale, workspace=pa.workspace_for_gqa(q, t.k, bt))
+    ref = t.reference()
+    tol = 2 * (2.0 ** -8 * np.abs(ref[0]) + (2.0 ** -8 + 1e-4) * 1.01 * ref[2])
+    assert np.all(np.abs(f64(out) - f64(vo.view_as(out))) <= tol)
+    assert np.all(np.abs(f64(lse) - f64(vl.view_as(lse))) <= 1e-4)
+
+
+def test_tree_bitwise_repeatable_and_independent_of_page_order(pa):
+    rows = [(1000, 12), (64, 64), (7, 2), (3000, 30)]
+    a, b = Tree(91, rows, 16, 2, 128, 16), Tree(91, rows, 16, 2, 128, 16, shuffle=False)
+    oa, la, _ = a.call(pa)
+    ob, lb, _ = b.call(pa)
+    oc, lc, _ = a.call(pa)
+    assert torch.equal(oa, ob) and torch.equal(la, lb) and torch.equal(oa, oc) and torch.equal(la, lc)
+
+
+def test_tree_captured_and_replayed_with_other_lengths(pa):
+    """A graph of the call replays with new lengths, masks and tables in the same arrays."""
+    first, second = Tree(92, [(300, 8), (90, 3)], 8, 2, 128, 16), Tree(93, [(90, 3), (250, 8)], 8, 2, 128, 16)
+    args = [x.clone() for x in first.args()]
+    args[3] = torch.zeros(2, 24, dtype=torch.int32, device="cuda")
+    args[1], args[2] = (torch.zeros(40, 16, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def load(t):
+        a = t.args()
+        for i in (0, 4, 5, 6):
+            args[i].copy_(a[i])
+        args[3][:, :a[3].shape[1]].copy_(a[3])
+        for i in (1, 2):
+            args[i][:a[i].shape[0]].copy_(a[i])
+
+    load(first)
+    out, lse = torch.zeros_like(first.q), torch.zeros(first.q.shape[:2], device="cuda")
+    ws = pa.workspace_for_tree(first.q, args[1], args[3], 8)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        first.call(pa, 8, args=args, out=out, lse=lse, ws=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first.call(pa, 8, args=args, out=out, lse=lse, ws=ws)
+    for t in (second, first):
+        load(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        R.check_tree(f64(out[:t.T]), f64(lse[:t.T]), *t.reference(), t.D)
+
+
+def test_tree_two_streams(pa):
+    """Two calls at once, each with its own workspace."""
+    a, b = Tree(94, [(4000, 30)], 16, 2, 128, 16), Tree(95, [(3000, 7), (50, 9)], 16, 2, 128, 16, "fp8")
+    xa, xb = a.args(), b.args()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(3):
+        got = [t.call(pa, args=x, stream=s) for t, x, s in ((a, xa, s1), (b, xb, s2))]
+    torch.cuda.synchronize()
+    for t, (o, l, _) in zip((a, b), got):
+        R.check_tree(f64(o[:t.T]), f64(l[:t.T]), *t.reference(), t.D)
+
+
+def test_tree_bad_rows_are_reported(pa):
+    """Bad lengths and pages are clamped or skipped and reported; the other rows are as they should be."""
+    rows = [(100, 4), (64, 3), (200, 6)]
+    t = Tree(96, rows, 8, 2, 128, 16)
+    good = t.reference()
+
+    def call(change, bit):
+        args = list(t.args())
+        change(args)
+        out, lse, ws = t.call(pa, max_query=6, args=args)
+        torch.cuda.synchronize()
+        assert pa.pa_read_device_status(ws) & bit
+        s = slice(int(t.start[0]), int(t.start[1]))  # row 0 is a good one in every case
+        R.check_tree(f64(out[s]), f64(lse[s]), *(x[s] for x in good), t.D)
+
+    call(lambda a: a[4].__setitem__(1, 2), pa.PA_DEV_BAD_LEN)        # fewer tokens than nodes
+    call(lambda a: a[4].__setitem__(1, -3), pa.PA_DEV_BAD_LEN)
+    call(lambda a: a[4].__setitem__(2, 1 << 20), pa.PA_DEV_BAD_LEN)  # past the table
+    call(lambda a: a[5].__setitem__(3, 1 << 20), pa.PA_DEV_BAD_LEN)  # nodes past the tokens
+    call(lambda a: a[5].__setitem__(2, 1), pa.PA_DEV_BAD_LEN)        # descending
+    call(lambda a: a[3][1].__setitem__(2, 1 << 20), pa.PA_DEV_BAD_PAGE)
+    call(lambda a: a[3][2].__setitem__(0, -1), pa.PA_DEV_BAD_PAGE)
+
+
+# ------------------------------------------------------------------------------------------ plan
+
+def run_plan(pa, c, in_place=False, parents=None, max_tokens=None, num_pages=None):
+    T = max_tokens
+    B, W = c["table"].shape
+    a = {k: i32(c[k]) for k in ("lens", "news", "held", "table", "free_list")}
+    a["count"] = i32([c["count"]])
+    o = {k: a[k] if in_place else torch.full_like(a[k], -99) for k in ("lens", "held", "count")}
+    start = torch.full((B + 1,), -99, dtype=torch.int32, device="cuda")
+    slots = torch.full((T,), -99, dtype=torch.int64, device="cuda")
+    pos = torch.full((T,), -99, dtype=torch.int32, device="cuda")
+    mask = torch.full((T,), -99, dtype=torch.int64, device="cuda") if parents is not None else None
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_plan_step(a["lens"], a["news"], a["held"], a["free_list"], a["count"], a["table"], start, slots, pos,
+                    page_size=c["P"], context_lens_out=None if in_place else o["lens"],
+                    held_pages_out=None if in_place else o["held"], free_count_out=None if in_place else o["count"],
+                    parents=None if parents is None else i32(parents), tree_mask=mask, status=st)
+    torch.cuda.synchronize()
+    got = dict(table=a["table"], free_list=a["free_list"], lens=o["lens"], held=o["held"], count=o["count"][0],
+               start=start, slots=slots, positions=pos)
+    got = {k: v.cpu().numpy() for k, v in got.items()}
+    if mask is not None:
+        got["mask"] = mask.cpu().numpy().view(np.uint64)
+    return got, int(st[0])
+
+
+def check_plan(pa, c, parents=None, max_tokens=None, bits=None):
+    T = max_tokens if max_tokens is not None else sum(max(0, n) for n in c["news"]) + 5
+    if parents is not None:
+        parents = list(parents)[:T] + [-1] * (T - len(parents))
+    want = R.plan(c["lens"], c["news"], c["held"], c["free_list"], c["count"], c["table"], c["P"], T,
+                  len(c["free_list"]), parents)
+    for in_place in (False, True):
+        got, st = run_plan(pa, c, in_place, parents, T)
+        for k, v in got.items():
+            w = np.array(want[k], dtype=np.uint64) if k == "mask" else np.array(want[k])
+            assert np.array_equal(v, w), f"{k}: {v} is not {w}"
+        assert st == want["bits"], (st, want["bits"])
+    if bits is not None:
+        assert want["bits"] == bits
+    return want
+
+
+def plan_case(seed, B, P, most, new_most, ended=0, scarce=False, width=None):
+    rng = np.random.default_rng(seed)
+    lens = [int(x) for x in rng.integers(0, most + 1, B)]
+    news = [int(x) for x in rng.integers(0, new_most + 1, B)]
+    for b in rng.permutation(B)[:ended]:
+        news[b] = -1
+    held = [-(-n // P) + int(rng.integers(0, 3)) for n in lens]
+    need = sum(max(0, -(-(n + k) // P) - h) for n, k, h in zip(lens, news, held) if k >= 0)
+    free = need // 2 if scarce else need + 3
+    total = sum(held) + free
+    W = width or -(-(most + new_most) // P) + 3
+    perm = rng.permutation(max(total, 1))
+    table = np.full((B, W), -1, np.int64)
+    at = 0
+    for b, h in enumerate(held):
+        table[b, :h] = perm[at:at + h]
+        at += h
+    fl = np.full(max(total, 1), -5, np.int64)
+    fl[:free] = perm[at:at + free]
+    return dict(lens=lens, news=news, held=held, count=free, free_list=fl, table=table, P=P)
+
+
+@pytest.mark.parametrize("B,P,most,new_most,ended,scarce", [
+    (1, 16, 0, 1, 0, False), (1, 16, 100, 1, 1, False), (3, 8, 40, 9, 1, False), (65, 32, 500, 1, 7, False),
+    (65, 16, 500, 3, 20, True), (513, 16, 300, 40, 60, False), (513, 16, 300, 40, 5, True), (1025, 256, 2000, 70, 0, True),
+    (7, 24, 333, 2000, 2, False), (2, 1, 9, 5, 0, True)])
+def test_plan(pa, B, P, most, new_most, ended, scarce):
+    check_plan(pa, plan_case(B + P, B, P, most, new_most, ended, scarce))
+
+
+@pytest.mark.parametrize("B,chain", [(1, True), (5, False), (70, False), (300, True)])
+def test_plan_trees(pa, B, chain):
+    """Rows of up to 64 nodes get masks and depths; a longer one is a chain."""
+    c = plan_case(B + 7, B, 16, 200, 64, ended=B // 4)
+    rng = np.random.default_rng(B)
+    if B > 4:
+        c["news"][2], c["news"][3] = 64, 65
+        c["lens"][3], c["held"][3] = 0, 5
+    parents = []
+    for n in c["news"]:
+        if n > 64:
+            parents += [99] * n  # not read
+        elif n > 0:
+            parents += R.random_tree(rng, n, chain)[0]
+    check_plan(pa, c, parents)
+
+
+def test_plan_refusals_and_bad_input(pa):
+    P = 16
+    c = plan_case(3, 6, P, 60, 4)
+    c["lens"][1] = -4                                # a negative length
+    check_plan(pa, c, bits=pa.PA_DEV_BAD_LEN)
+    c = plan_case(4, 6, P, 60, 4)
+    c["news"][2] = 100000                            # past the table, and past the tokens
+    check_plan(pa, c, max_tokens=40, bits=pa.PA_DEV_BAD_LEN)
+    c = plan_case(5, 6, P, 60, 4)
+    c["news"][2], c["held"][2] = -1, 1000            # an ended row with more pages than its table has
+    check_plan(pa, c, bits=pa.PA_DEV_BAD_LEN)
+    c = plan_case(6, 6, P, 60, 4)
+    c["lens"][0], c["news"][0], c["held"][0] = 5, 3, 1
+    c["table"][0, 0] = 10 ** 6                       # a page that is none
+    check_plan(pa, c, bits=pa.PA_DEV_BAD_PAGE)
+    c = plan_case(7, 6, P, 60, 8)
+    c["news"] = [5, 3, 8, 0, 2, 1]
+    check_plan(pa, c, parents=[-1, 0, 5, -2, 2, -1, 1, 0, -1, 99] + [-1] * 9, bits=pa.PA_DEV_BAD_TREE)
+
+
+def test_plan_empty(pa):
+    check_plan(pa, dict(lens=[], news=[], held=[], count=3, free_list=np.arange(5), table=np.zeros((0, 4), np.int64), P=16),
+               max_tokens=9)
+
+
+# ------------------------------------------------------------------------------------------ norm, rotation, write
+
+def rope_case(seed, T, hq, hkv, D, rot, page=16, far=500, fused=True, fmt="bf16", pad=0):
+    g = torch.Generator().manual_seed(seed)
+    pages = -(-T // page) + 2
+    x = (torch.randn(T, hq + 2 * hkv, D, generator=g) * 3).to(torch.bfloat16).cuda()
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    if not fused:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    slots = torch.randperm(pages * page, generator=g)[:T]
+    if pad:
+        slots[torch.randperm(T, generator=g)[:pad]] = -1
+    angle = torch.rand(far, rot // 2, generator=g, dtype=torch.float64) * 6.28
+    c = dict(q=q, k=k, v=v, slots=slots.cuda(), positions=torch.randint(0, far, (T,), generator=g).int().cuda(),
+             cos_sin=torch.cat((angle.cos(), angle.sin()), -1).float().cuda(), D=D, rot=rot, fmt=fmt, far=far,
+             wq=(torch.randn(D, generator=g)).to(torch.bfloat16).cuda(),
+             wk=(torch.randn(D, generator=g)).to(torch.bfloat16).cuda(),
+             scales={"bf16": (), "fp8": (0.013, 0.021), "nvfp4": (0.3, 0.0625)}[fmt])
+    width = D if fmt == "bf16" else R.row_bytes(fmt, D)
+    fill = torch.full((pages, page, hkv, width), 0x55, dtype=torch.uint8) if fmt != "bf16" else torch.full(
+        (pages, page, hkv, D), 9.0).to(torch.bfloat16)
+    c["kp"], c["vp"] = fill.cuda(), fill.clone().cuda()
+    c["q_out"] = torch.full((T, hq, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    return c
+
+
+def rope_call(pa, c, wq="wq", wk="wk", interleaved=False, eps=1e-6, status=None, **over):
+    c = {**c, **over}
+    fn = {"bf16": pa.pa_qk_norm_rope_write, "fp8": pa.pa_qk_norm_rope_write_fp8,
+          "nvfp4": pa.pa_qk_norm_rope_write_nvfp4}[c["fmt"]]
+    more = dict(zip(("k_scale", "v_scale"), c["scales"]))
+    fn(c["q"], c["k"], c["v"], wq and c[wq], wk and c[wk], c["cos_sin"], c["positions"], c["slots"], c["q_out"],
+       c["kp"], c["vp"], eps=eps, interleaved=interleaved, status=status, **more)
+    torch.cuda.synchronize()
+
+
+def stored_ok(pool, exact, fmt, D, scale):
+    """Stored rows against exact values: half a step of the type, plus the fp32 arithmetic before it
+    (2^-19 of the value and of the row's largest)."""
+    slack = 2.0 ** -19 * (np.abs(exact) + np.abs(exact).max(-1, keepdims=True))
+    if fmt == "bf16":
+        return np.abs(R.bf16_values(pool) - exact) <= 2.0 ** -8 * np.abs(exact) + slack
+    if fmt == "fp8":
+        x, slack = exact / scale, slack / scale
+        got = R.e4m3_table()[pool]
+        x = np.clip(x, -448, 448)
+        return np.abs(got - x) <= np.maximum(2.0 ** -4 * np.abs(x), 2.0 ** -10) + slack
+    x, slack = exact / scale, slack / scale
+    blk = R.e4m3_table()[pool[..., D // 2:D // 2 + D // 16]]
+    amax = np.abs(x).reshape(*x.shape[:-1], D // 16, 16).max(-1) / 6
+    ok = np.abs(blk - np.minimum(amax, 448)) <= np.maximum(2.0 ** -4 * amax, 2.0 ** -10) + 2.0 ** -18 * amax
+    got = R.pool_values(pool, "nvfp4", D, 1.0)
+    by = np.repeat(blk, 16, -1)
+    r = np.abs(got) / np.maximum(by, 1e-30)
+    half = np.where(r < 1.75, 0.25, np.where(r < 3.5, 0.5, 1.0))  # half the step above the code (the wider one)
+    return np.repeat(ok, 16, -1) & (np.abs(got - x) <= by * half * (1 + 2.0 ** -10) + slack)
+
+
+def check_rope(pa, c, wq="wq", wk="wk", interleaved=False, eps=1e-6):
+    q, k, v = f64(c["q"]), f64(c["k"]), f64(c["v"])
+    rope_call(pa, c, wq, wk, interleaved, eps)
+    slots, D, rot = c["slots"].cpu().numpy(), c["D"], c["rot"]
+    cs = f64(c["cos_sin"])[c["positions"].cpu().numpy()]
+    weight = lambda w: f64(c[w]) if w else None  # noqa: E731
+    real = slots >= 0
+    eq = R.norm_rope(q, weight(wq), cs, rot, interleaved, eps)
+    ek = R.norm_rope(k, weight(wk), cs, rot, interleaved, eps)
+    got = raw(c["q_out"])
+    assert np.all(stored_ok(got[real], eq[real], "bf16", D, 1.0))
+    assert np.all(got[~real] == 0x4110), "padding tokens are left as they were"
+    s = c["scales"] or (1.0, 1.0)
+    for pool, exact, scale in ((c["kp"], ek, s[0]), (c["vp"], v, s[1])):
+        flat = raw(pool).reshape(-1, *pool.shape[2:])
+        ok = stored_ok(flat[slots[real]], exact[real], c["fmt"], D, scale)
+        assert np.all(ok), f"{(~ok).sum()} of {ok.size} values are off"
+        rest = np.ones(len(flat), bool)
+        rest[slots[real]] = False
+        assert np.all(flat[rest] == (0x4110 if c["fmt"] == "bf16" else 0x55)), "other slots are left as they were"
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("T,hq,hkv,D,rot,interleaved", [
+    (1, 8, 2, 128, 128, False), (5, 5, 1, 64, 64, True), (33, 14, 2, 64, 32, False), (17, 16, 4, 256, 256, False),
+    (9, 12, 3, 128, 16, True), (70, 9, 3, 128, 48, False), (257, 64, 8, 128, 128, True), (3, 3, 3, 256, 80, False),
+    (3000, 7, 1, 64, 64, False)])
+def test_rope_write(pa, fmt, T, hq, hkv, D, rot, interleaved):
+    check_rope(pa, rope_case(T + D, T, hq, hkv, D, rot, fmt=fmt, pad=T // 4), interleaved=interleaved)
+
+
+@pytest.mark.parametrize("wq,wk", [("wq", None), (None, "wk"), (None, None)])
+def test_rope_write_without_norms(pa, wq, wk):
+    check_rope(pa, rope_case(5, 20, 8, 2, 128, 64, fused=False), wq, wk)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+def test_rope_write_without_turn_is_the_plain_write(pa, fmt):
+    """No norms and angles of zero: the pools' bits are pa_kv_write's."""
+    c = rope_case(6, 50, 4, 2, 128, 128, fmt=fmt, pad=5)
+    c["cos_sin"] = torch.cat((torch.ones(c["far"], 64), torch.zeros(c["far"], 64)), -1).cuda()
+    c["k"][3, 0, :40] = 0.0
+    c["v"][4, 1] *= 1e30
+    c["v"][7, 1, 5], c["v"][9, 0, 77] = math.nan, math.inf
+    kp, vp = c["kp"].clone(), c["vp"].clone()
+    fn = {"bf16": pa.pa_kv_write, "fp8": pa.pa_kv_write_fp8, "nvfp4": pa.pa_kv_write_nvfp4}[fmt]
+    fn(c["k"].contiguous(), c["v"].contiguous(), c["slots"], kp, vp, **dict(zip(("k_scale", "v_scale"), c["scales"])))
+    rope_call(pa, c, None, None)
+    for mine, theirs in ((c["kp"], kp), (c["vp"], vp)):
+        a, b = raw(mine), raw(theirs)
+        if fmt == "bf16":
+            same = (a == b) | ((a & 0x7FFF) == 0) & ((b & 0x7FFF) == 0) | np.isnan(R.bf16_values(a)) & np.isnan(R.bf16_values(b))
+        else:  # x cos - y sin of a zero loses the zero's sign
+            same = (a == b) if mine is c["vp"] else (a == b) | (fmt == "fp8") & ((a & 0x7F) == 0) & ((b & 0x7F) == 0) | (fmt == "nvfp4")
+        assert same.all()
+
+
+def test_rope_write_in_place_and_zero_rows(pa):
+    """q_out may be a dense q; rows of zeros stay zero under eps, tiny and huge rows keep their norm."""
+    c = rope_case(8, 40, 8, 2, 128, 128, fused=False)
+    c["q"][0] = 0
+    c["q"][1] *= 1e-18
+    c["q"][2] *= 1e15
+    c["k"][3] = 0
+    other = {**c, "q": c["q"].clone(), "q_out": c["q_out"].clone(), "kp": c["kp"].clone(), "vp": c["vp"].clone()}
+    check_rope(pa, other, eps=1e-6)
+    rope_call(pa, c, q_out=c["q"])
+    assert torch.equal(c["q"], other["q_out"]) and bool((c["q"][0] == 0).all())
+
+
+def test_rope_write_bad_tokens_are_reported(pa):
+    for key, at, value, bit in (("slots", 3, 1 << 40, pa.PA_DEV_BAD_SLOT), ("positions", 4, 500, pa.PA_DEV_BAD_POS),
+                                ("positions", 5, -1, pa.PA_DEV_BAD_POS)):
+        c = rope_case(9, 8, 8, 2, 128, 64)
+        c[key][at] = value
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        rope_call(pa, c, status=st)
+        assert int(st[0]) == bit
+        assert bool((c["q_out"][at] == 9.0).all()) and not bool((c["q_out"][at - 1] == 9.0).all())
+        st.zero_()
+        c["slots"][at] = -1  # a padding token's position is not looked at
+        rope_call(pa, c, status=st)
+        assert int(st[0]) == 0
+
+
+# ------------------------------------------------------------------------------------------ compaction
+
+def compact_case(seed, rows, layers, hkv, R_, page, kind, accepted):
+    """rows of (L, n); accepted: a list of paths."""
+    rng = np.random.default_rng(seed)
+    pages = [-(-L // page) for L, _ in rows]
+    total = sum(pages) + 2
+    perm = rng.permutation(total)
+    table = np.full((len(rows), max(pages)), -3, np.int64)
+    at = 0
+    for b, n in enumerate(pages):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    g = torch.Generator().manual_seed(seed)
+    shape = (layers, total, page, hkv, R_) if layers else (total, page, hkv, R_)
+    k, v = (torch.randint(0, 255, shape, generator=g, dtype=torch.uint8) for _ in range(2))
+    if kind == torch.bfloat16:
+        k, v = (torch.randn(shape, generator=g).to(torch.bfloat16) for _ in range(2))
+    M = max(len(p) for p in accepted) or 1
+    acc = np.full((len(rows), M), 12345, np.int64)  # not read
+    for b, p in enumerate(accepted):
+        acc[b, :len(p)] = p
+    start = np.concatenate(([0], np.cumsum([n for _, n in rows])))
+    return dict(k=k.cuda(), v=v.cuda(), table=table, lens=[L for L, _ in rows], start=start, acc=acc,
+                num=[len(p) for p in accepted], page=page)
+
+
+def run_compact(pa, c, table=None, acc=None, num=None, lens=None, start=None):
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((len(c["lens"]),), -9, dtype=torch.int32, device="cuda")
+    pa.pa_kv_compact(c["k"], c["v"], i32(c["table"] if table is None else table), i32(lens or c["lens"]),
+                     i32(c["start"] if start is None else start), i32(c["acc"] if acc is None else acc),
+                     i32(num or c["num"]), context_lens_out=out, status=st)
+    torch.cuda.synchronize()
+    return out.tolist(), int(st[0])
+
+
+def compacted(c):
+    want = []
+    for p in (c["k"], c["v"]):
+        x = raw(p).copy()
+        y = x.reshape(-1, *x.shape[-4:]).copy()
+        src = y.copy()
+        for b, L in enumerate(c["lens"]):
+            n = c["start"][b + 1] - c["start"][b]
+            for i in range(c["num"][b]):
+                s, d = L - n + c["acc"][b, i], L - n + i
+                pg, P = c["table"][b], c["page"]
+                y[:, pg[d // P], d % P] = src[:, pg[s // P], s % P]
+        want.append(y.reshape(x.shape))
+    return want, [L - int(c["start"][b + 1] - c["start"][b]) + c["num"][b] for b, L in enumerate(c["lens"])]
+
+
+@pytest.mark.parametrize("layers,hkv,R_,kind,page", [(0, 8, 128, torch.bfloat16, 16), (3, 2, 64, torch.bfloat16, 8),
+                                                     (5, 1, 80, torch.uint8, 32), (2, 3, 144, torch.uint8, 24),
+                                                     (1, 1, 16, torch.uint8, 16)])
+def test_compact(pa, layers, hkv, R_, kind, page):
+    rows = [(50, 9), (64, 64), (20, 20), (33, 1), (100, 5), (17, 12), (77, 0)]
+    paths = [[0, 2, 8], list(range(1, 64)), list(range(0, 20)), [0], [], [3, 4, 7, 9, 11], []]
+    c = compact_case(1 + page, rows, layers, hkv, R_, page, kind, paths)
+    want, lens = compacted(c)
+    got, st = run_compact(pa, c)
+    assert st == 0 and got == lens
+    assert np.array_equal(raw(c["k"]), want[0]) and np.array_equal(raw(c["v"]), want[1])
+
+
+def test_compact_bad_input(pa):
+    rows, paths = [(50, 9), (64, 20)], [[0, 2, 8], [1, 5, 9, 13]]
+    make = lambda: compact_case(2, rows, 2, 2, 64, 16, torch.bfloat16, paths)  # noqa: E731
+
+    def case(bit, keep, **change):
+        """Row 1 is cut to `keep` moves (None: no row 1 at all)."""
+        c = make()
+        cut = {**c, "k": c["k"].clone(), "v": c["v"].clone(), "num": [3, keep], "acc": change.get("acc", c["acc"])}
+        want, lens = compacted(cut)
+        got, st = run_compact(pa, c, **change)
+        assert st == bit and got[0] == lens[0]
+        assert np.array_equal(raw(c["k"]), want[0]) and np.array_equal(raw(c["v"]), want[1])
+        return got
+
+    acc = make()["acc"]
+    for bad, keep in (([1, 5, 20, 13], 2), ([1, 5, 5, 13], 2), ([-1, 5, 9, 13], 0), ([4, 3, 9, 13], 1)):
+        a = acc.copy()
+        a[1, :4] = bad
+        got = case(pa.PA_DEV_BAD_TREE, keep, acc=a)
+        assert got[1] == 64 - 20 + keep
+    case(pa.PA_DEV_BAD_LEN, 0, num=[3, 99])
+    case(pa.PA_DEV_BAD_LEN, 0, num=[3, -1])
+    case(pa.PA_DEV_BAD_LEN, 0, lens=[50, 7])
+    case(pa.PA_DEV_BAD_LEN, 0, lens=[50, 10 ** 6])
+    t = make()["table"]
+    t[1, 2] = 10 ** 6  # tokens 32 to 47: the targets' page
+    case(pa.PA_DEV_BAD_PAGE, 0, table=t)
+
+
+# ------------------------------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+def test_steps_of_tree_drafting(pa, fmt):
+    """Steps of drafting as a program makes them: plan, norm + rotation + write, tree attention, compaction,
+    the next plan; requests come, go and wait for pages.  Each step's attention is that of the tokens that
+    each request holds, from the pools' own values at the places that the test itself keeps track of."""
+    rng = np.random.default_rng(11)
+    hq, hkv, D, P, pages, B, T, eps = 8, 2, 128, 16, 40, 5, 70, 1e-6
+    width = D if fmt == "bf16" else R.row_bytes(fmt, D)
+    kind = torch.bfloat16 if fmt == "bf16" else torch.uint8
+    scales = {"bf16": (1.0, 1.0), "fp8": (0.013, 0.021), "nvfp4": (0.25, 0.25)}[fmt]
+    sc = {} if fmt == "bf16" else dict(k_scale=scales[0], v_scale=scales[1])
+    write = {"bf16": pa.pa_qk_norm_rope_write, "fp8": pa.pa_qk_norm_rope_write_fp8, "nvfp4": pa.pa_qk_norm_rope_write_nvfp4}[fmt]
+    attend = {"bf16": pa.pa_tree_gqa, "fp8": pa.pa_tree_gqa_fp8, "nvfp4": pa.pa_tree_gqa_nvfp4}[fmt]
+    kp, vp = (torch.zeros(pages, P, hkv, width, dtype=kind, device="cuda") for _ in range(2))
+    angle = torch.rand(512, D // 2, dtype=torch.float64) * 6.28
+    cs = torch.cat((angle.cos(), angle.sin()), -1).float().cuda()
+    wq, wk = (torch.randn(D).to(torch.bfloat16).cuda() for _ in range(2))
+    lens, held, count = i32([0] * B), i32([0] * B), i32([pages])
+    lens2 = torch.zeros_like(lens)
+    fl, table = i32(rng.permutation(pages)), torch.full((B, 20), -1, dtype=torch.int32, device="cuda")
+    start = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    slots = torch.zeros(T, dtype=torch.int64, device="cuda")
+    pos, mask = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.zeros(T, dtype=torch.int64, device="cuda")
+    q_out = torch.zeros(T, hq, D, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.zeros_like(q_out), torch.zeros(T, hq, device="cuda")
+    ws = pa.workspace_for_tree(q_out, kp, table, 14)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kept = [[] for _ in range(B)]  # per row: what the test knows of its tokens, (key row, value row) in 64 bits
+    for step in range(12):
+        news = [int(rng.integers(0, 15)) for _ in range(B)]
+        if step % 4 == 3:
+            news[int(rng.integers(0, B))] = -1
+        parents, n_total = [], sum(max(0, n) for n in news)
+        for n in news:
+            if n > 0:
+                parents += R.random_tree(rng, n)[0]
+        pa.pa_plan_step(lens, i32(news), held, fl, count, table, start, slots, pos, page_size=P,
+                        parents=i32(parents + [-1] * (T - len(parents))), tree_mask=mask, status=st)
+        x = (torch.randn(T, hq + 2 * hkv, D) * 2).to(torch.bfloat16).cuda()
+        q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+        write(q, k, v, wq, wk, cs, pos, slots, q_out, kp, vp, eps=eps, status=st, **sc)
+        attend(q_out, kp, vp, table, lens, start, mask, out, lse, max_query=14, scale=D ** -0.5, workspace=ws, **sc)
+        torch.cuda.synchronize()
+        assert int(st[0]) & ~pa.PA_DEV_NO_PAGES == 0 and pa.pa_read_device_status(ws) & ~pa.PA_DEV_BAD_LEN == 0
+        # what each request holds now, by the test's own account
+        hs, hl, ht, hp = start.tolist(), lens.tolist(), table.cpu().numpy(), pos.tolist()
+        kv, vv = (R.pool_values(raw(p), fmt, D, s) for p, s in ((kp, scales[0]), (vp, scales[1])))
+        ek = R.norm_rope(f64(k), f64(wk), f64(cs)[pos.cpu().numpy()], D, False, eps)
+        hm = mask.cpu().numpy().view(np.uint64)
+        paths, num = np.zeros((B, 14), np.int64), []
+        for b, n in enumerate(news):
+            if n < 0:
+                kept[b] = []
+                assert hl[b] == 0
+            n = max(n, 0)
+            got = hl[b] == len(kept[b]) + n
+            assert got or hl[b] == len(kept[b]), "a row is granted whole or not at all"
+            path = []
+            if got and n:
+                now = []
+                for i in range(n):
+                    t, at = hs[b] + i, len(kept[b]) + i
+                    row = kv[ht[b, at // P], at % P], vv[ht[b, at // P], at % P]
+                    assert np.abs(row[0] - ek[t]).max() < (0.02 if fmt == "bf16" else 0.4) * np.abs(ek[t]).max()
+                    now.append(row)
+                keys = np.stack([r[0] for r in kept[b] + now])
+                vals = np.stack([r[1] for r in kept[b] + now])
+                s = slice(hs[b], hs[b] + n)
+                R.check_tree(f64(out[s]), f64(lse[s]), *R.tree_attention(
+                    f64(q_out[s]), keys, vals, [int(m) for m in hm[s]], hl[b], D ** -0.5, 0), D)
+                # accept a path down the tree
+                leaf = int(rng.integers(0, n))
+                path = [i for i in range(n) if int(hm[hs[b] + leaf]) >> i & 1]
+                assert [hp[hs[b] + i] for i in path] == list(range(len(kept[b]), len(kept[b]) + len(path)))
+                kept[b] = kept[b] + [now[i] for i in path]
+            paths[b, :len(path)] = path
+            num.append(len(path))
+        # a refused row has no nodes in the cache: it takes no part in the compaction
+        own = [hs[b + 1] - hs[b] if hl[b] == len(kept[b]) - num[b] + hs[b + 1] - hs[b] else 0 for b in range(B)]
+        pa.pa_kv_compact(kp, vp, table, lens, i32(np.concatenate(([0], np.cumsum(own)))), i32(paths), i32(num),
+                         context_lens_out=lens2, status=st)
+        lens, lens2 = lens2, lens
+        torch.cuda.synchronize()
+        assert lens.tolist() == [len(x) for x in kept]
+    assert max(len(x) for x in kept) > 20
