@@ -1,27 +1,21 @@
-// pa_tree.cu -- attention of drafted trees over the paged cache.
-//
-// Mathematics: node i of row b (n nodes, L tokens with them, prefix = L - n) attends to the set A of
-// prefix tokens and of the nodes its mask names (under a window those fewer than `window` positions
-// back, a node's position being prefix + its number of other mask bits):
-//   out = sum_{t in A} exp(s_t - m) v_t / l,  lse = m + ln l,  s_t = scale q . k_t,
-//   m = max s_t,  l = sum exp(s_t - m), in fp32 and rounded once.
+// pa_tree.cu -- the host side of the tree attention (pa_tree.cuh): argument checks, workspace, tensor maps
+// and the launches of a call.
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
-#include "pa_common.cuh"
+#include <cudaTypedefs.h>
+
 #include "pa_decode.h"
 #include "pa_launch.h"
-#include "pa_quant.cuh"
+#include "pa_tree.cuh"
 
 namespace pa {
 
 namespace {
 
-enum TreeFmt { TREE_BF16 = 0, TREE_FP8 = 1, TREE_NVFP4 = 2 };
-constexpr int kTreeNodes = 64;
-
-struct TreeArgs {
+struct PlainArgs {
   const uint16_t *q;
   const uint8_t *k_pool, *v_pool;
   const int32_t *block_table, *context_lens, *query_start;
@@ -33,24 +27,9 @@ struct TreeArgs {
   float qscale, kscale, vscale;  // scale * log2(e); the pools' scales
 };
 
-template <int FMT, int D>
-__device__ __forceinline__ float cache_value(const uint8_t *row, int d) {
-  if constexpr (FMT == TREE_BF16) {
-    return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(row)[d] << 16);
-  } else if constexpr (FMT == TREE_FP8) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(row[d], __NV_E4M3);
-    return __half2float(*reinterpret_cast<const __half *>(&h));
-  } else {
-    const uint32_t c = (row[d >> 1] >> (4 * (d & 1))) & 15u;
-    const float mag = (c & 7u) < 2 ? 0.5f * (float)(c & 7u) : __uint_as_float((((c & 7u) >> 1) + 126u) << 23 | (c & 1u) << 22);
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(row[D / 2 + (d >> 4)], __NV_E4M3);
-    return (c & 8u ? -mag : mag) * __half2float(*reinterpret_cast<const __half *>(&h));
-  }
-}
-
 // One block per (token, query head), a warp per fourth key.
 template <int FMT, int D>
-__global__ void __launch_bounds__(128) tree_plain_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(128) tree_plain_kernel(const PlainArgs a) {
   constexpr int PER = D / 32, W = 4;
   constexpr int ROW = FMT == TREE_BF16 ? 2 * D : FMT == TREE_FP8 ? D : (D / 2 + D / 16 + 15) / 16 * 16;
   __shared__ float so[W][D], sm[W], sl[W];
@@ -106,17 +85,117 @@ __global__ void __launch_bounds__(128) tree_plain_kernel(const TreeArgs a) {
   if (threadIdx.x == 0 && a.lse) a.lse[(size_t)t * a.Hq + h] = Z != 0.f ? (M + log2f(Z)) * LN2 : -INFINITY;
 }
 
+constexpr int kMaxSplits = 4096, kAutoParts = 256;
+// Fixed cost of a piece of work in the partition, as the bytes of cache that an SM streams meanwhile.
+constexpr long long kPieceCostBytes = 160 << 10;
+
 bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
+int ilog2(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-int tree_shape(int batch, int max_query, int Hq, int Hkv, int D, int max_ctx, int P, int num_splits, size_t *total) {
+// How a call's query rows are tiled, and where its workspace's parts lie.
+struct TreePlan {
+  int G, gt, qt, nsub, QT, nseqh, nparts_max;
+  size_t off_desc, off_lse, off_o, off_half, off_seq, total;
+};
+
+int tree_plan(int batch, int max_query, int Hq, int Hkv, int D, int max_ctx, int P, int num_splits, TreePlan *pl) {
   if (batch < 0 || max_query <= 0 || Hq <= 0 || Hkv <= 0 || max_ctx < 0 || num_splits < 0 || Hq % Hkv != 0)
     return PA_ERR_INVALID_ARGUMENT;
-  if (max_query > kTreeNodes || num_splits > 4096 || (D != 64 && D != 128 && D != 256) || !is_pow2(P) || P < 8 ||
+  if (max_query > kTreeNodes || num_splits > kMaxSplits || (D != 64 && D != 128 && D != 256) || !is_pow2(P) || P < 8 ||
       P > 256)
     return PA_ERR_UNSUPPORTED;
-  *total = sizeof(WsHeader);
+  pl->G = Hq / Hkv;
+  pl->gt = pl->G < kTreeRows ? pl->G : kTreeRows;
+  pl->nsub = (pl->G + kTreeRows - 1) / kTreeRows;
+  pl->qt = pl->nsub > 1 ? 1 : kTreeRows / pl->G;
+  const int ntile = pl->nsub > 1 ? max_query * pl->nsub : (max_query + pl->qt - 1) / pl->qt;
+  pl->QT = D <= 128 && ntile > 1 ? 2 : 1;
+  pl->nseqh = (ntile + pl->QT - 1) / pl->QT;
+  pl->nparts_max = num_splits > 0 ? num_splits : kAutoParts;
+  const size_t np = (size_t)pl->nparts_max, rows = np * 2 * pl->QT * kTreeRows;
+  size_t off = sizeof(WsHeader);
+  pl->off_desc = off;
+  off = round_up(off + np * sizeof(uint32_t), 256);
+  pl->off_lse = off;
+  off = round_up(off + rows * sizeof(float), 256);
+  pl->off_o = off;
+  off = round_up(off + rows * D * sizeof(float), 256);
+  pl->off_half = off;
+  off = round_up(off + np * 2 * kTreeRows * sizeof(TreeHalf), 256);
+  pl->off_seq = off;
+  off = round_up(off + 2 * (size_t)(batch > 0 ? batch : 1) * Hkv * pl->nseqh * sizeof(int32_t), 256);
+  pl->total = off;
   return PA_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// A dense map of `rank` dimensions of bf16 values (the first one contiguous), 128-byte swizzle.
+template <int RANK>
+bool encode_map(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[RANK], const cuuint32_t (&box)[RANK]) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t strides[RANK - 1], s = 2;
+  cuuint32_t ones[RANK];
+  for (int i = 0; i < RANK; ++i) {
+    ones[i] = 1u;
+    if (i < RANK - 1) strides[i] = s = s * dims[i];
+  }
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, RANK, const_cast<void *>(base), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return -1;
+  return n;
+}
+
+template <typename K, typename... A>
+cudaError_t launch_pdl(K kernel, dim3 grid, int threads, int smem, cudaStream_t stream, A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D, int FMT, int QT>
+cudaError_t launch_tree(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CUtensorMap &tm_q, const TreeArgs &a,
+                        uint32_t *status, cudaStream_t stream) {
+  using C = TreeCfg<D, FMT, QT>;
+  // (made at every call: the attribute is the device's, and costs less than to remember where it is set)
+  cudaError_t e = cudaFuncSetAttribute(tree_split_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeSmem<C>::BYTES);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(tree_split_kernel<C>, dim3((unsigned)a.nparts), C::THREADS, TreeSmem<C>::BYTES, stream, tm_k, tm_v, tm_q, a);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)(a.batch * a.Hkv * a.nseqh), QT * kTreeRows / kCombineRows);
+  return launch_pdl(tree_combine_kernel<D, QT>, grid, 256, 0, stream, a, status);
 }
 
 int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
@@ -125,13 +204,14 @@ int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32
               int max_ctx, float scale, int fmt, float k_scale, float v_scale, int window, int num_splits, void *workspace,
               size_t workspace_bytes, cudaStream_t stream) {
   note_launches(0);
-  size_t need = 0;
-  const int rc = tree_shape(batch, max_query, Hq, Hkv, D, max_ctx, P, num_splits, &need);
+  TreePlan pl;
+  const int rc = tree_plan(batch, max_query, Hq, Hkv, D, max_ctx, P, num_splits, &pl);
   if (rc != PA_OK) return rc;
   if (tokens < 0 || num_pages <= 0 || max_pages <= 0 || !std::isfinite(scale)) return PA_ERR_INVALID_ARGUMENT;
   if (fmt != TREE_BF16 && !(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
     return PA_ERR_INVALID_ARGUMENT;
   if ((long long)max_pages * P < (long long)max_ctx) return PA_ERR_INVALID_ARGUMENT;
+  if ((long long)batch * Hkv * pl.nseqh > INT_MAX) return PA_ERR_UNSUPPORTED;
   if (batch == 0 || tokens == 0) return PA_OK;
   if (!q || !k_pool || !v_pool || !block_table || !context_lens || !query_start || !tree_mask || !out || !workspace)
     return PA_ERR_INVALID_ARGUMENT;
@@ -142,23 +222,81 @@ int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32
   for (const void *p : words)
     if (!aligned_to(p, 4)) return PA_ERR_MISALIGNED;
   if (!aligned_to(tree_mask, 8)) return PA_ERR_MISALIGNED;
-  if (workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
-  TreeArgs a = {static_cast<const uint16_t *>(q), static_cast<const uint8_t *>(k_pool), static_cast<const uint8_t *>(v_pool),
-                block_table, context_lens, query_start, tree_mask, static_cast<uint16_t *>(out), lse,
-                &static_cast<WsHeader *>(workspace)->status, batch, tokens, max_query, Hq, Hkv, Hq / Hkv, P, num_pages,
-                max_pages, max_ctx, window > 0 ? window : 0, scale * LOG2E, fmt == TREE_BF16 ? 1.f : k_scale,
-                fmt == TREE_BF16 ? 1.f : v_scale};
-  if (const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(WsHeader), stream); e != cudaSuccess) return cuda_fail(e);
-  const dim3 grid((unsigned)tokens, (unsigned)Hq);
-  auto run = [&](auto kernel) { kernel<<<grid, 128, 0, stream>>>(a); };
-  if (fmt == TREE_BF16)
-    D == 64 ? run(tree_plain_kernel<TREE_BF16, 64>) : D == 128 ? run(tree_plain_kernel<TREE_BF16, 128>) : run(tree_plain_kernel<TREE_BF16, 256>);
-  else if (fmt == TREE_FP8)
-    D == 64 ? run(tree_plain_kernel<TREE_FP8, 64>) : D == 128 ? run(tree_plain_kernel<TREE_FP8, 128>) : run(tree_plain_kernel<TREE_FP8, 256>);
-  else
-    D == 64 ? run(tree_plain_kernel<TREE_NVFP4, 64>) : D == 128 ? run(tree_plain_kernel<TREE_NVFP4, 128>) : run(tree_plain_kernel<TREE_NVFP4, 256>);
-  if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return cuda_fail(e);
-  note_launches(1);
+  if (workspace_bytes < pl.total) return PA_ERR_WORKSPACE_TOO_SMALL;
+  if (fmt != TREE_BF16) {
+    PlainArgs p = {static_cast<const uint16_t *>(q), static_cast<const uint8_t *>(k_pool), static_cast<const uint8_t *>(v_pool),
+                   block_table, context_lens, query_start, tree_mask, static_cast<uint16_t *>(out), lse,
+                   &static_cast<WsHeader *>(workspace)->status, batch, tokens, max_query, Hq, Hkv, Hq / Hkv, P, num_pages,
+                   max_pages, max_ctx, window > 0 ? window : 0, scale * LOG2E, k_scale, v_scale};
+    if (const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(WsHeader), stream); e != cudaSuccess) return cuda_fail(e);
+    const dim3 grid((unsigned)tokens, (unsigned)Hq);
+    auto run = [&](auto kernel) { kernel<<<grid, 128, 0, stream>>>(p); };
+    if (fmt == TREE_FP8)
+      D == 64 ? run(tree_plain_kernel<TREE_FP8, 64>) : D == 128 ? run(tree_plain_kernel<TREE_FP8, 128>) : run(tree_plain_kernel<TREE_FP8, 256>);
+    else
+      D == 64 ? run(tree_plain_kernel<TREE_NVFP4, 64>) : D == 128 ? run(tree_plain_kernel<TREE_NVFP4, 128>) : run(tree_plain_kernel<TREE_NVFP4, 256>);
+    if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return cuda_fail(e);
+    note_launches(1);
+    return PA_OK;
+  }
+  const int BN = D <= 128 ? 128 : 64;  // tokens per stage (TreeCfg::BN)
+  const int BH = P < BN ? P : BN;      // tokens per TMA box: a unit
+  const int sms = sm_count();
+  if (sms <= 0) return cuda_fail(cudaSuccess);
+  CUtensorMap tm_k, tm_v, tm_q;
+  const cuuint64_t pool[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)P, (cuuint64_t)num_pages};
+  const cuuint32_t pbox[4] = {64u, 1u, (cuuint32_t)BH, 1u};
+  const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)tokens};
+  const cuuint32_t qbox[3] = {64u, (cuuint32_t)pl.gt, (cuuint32_t)(pl.qt < max_query ? pl.qt : max_query)};
+  if (!encode_map(&tm_k, k_pool, pool, pbox) || !encode_map(&tm_v, v_pool, pool, pbox) || !encode_map(&tm_q, q, qd, qbox))
+    return PA_ERR_UNSUPPORTED;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  TreeArgs a;
+  a.v_pool = static_cast<const uint8_t *>(v_pool);
+  a.block_table = block_table;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.tree_mask = tree_mask;
+  a.out = static_cast<uint16_t *>(out);
+  a.lse = lse;
+  a.desc = reinterpret_cast<uint32_t *>(ws + pl.off_desc);
+  a.part_lse = reinterpret_cast<float *>(ws + pl.off_lse);
+  a.part_o = reinterpret_cast<float *>(ws + pl.off_o);
+  a.halves = reinterpret_cast<TreeHalf *>(ws + pl.off_half);
+  a.seq_first = reinterpret_cast<int32_t *>(ws + pl.off_seq);
+  a.seq_last = a.seq_first + (size_t)batch * Hkv * pl.nseqh;
+  a.batch = batch;
+  a.tokens = tokens;
+  a.max_query = max_query;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = pl.G;
+  a.gt = pl.gt;
+  a.qt = pl.qt;
+  a.nsub = pl.nsub;
+  a.nseqh = pl.nseqh;
+  a.log2_page = ilog2(P);
+  a.log2_bh = ilog2(BH);
+  a.num_pages = num_pages;
+  a.max_pages_per_seq = max_pages;
+  a.max_context_len = max_ctx;
+  a.window = window > 0 ? window : 0;
+  const long long unit_bytes = (long long)BH * D * 4;
+  a.piece_cost = (int)((kPieceCostBytes + unit_bytes - 1) / unit_bytes);
+  a.nparts = num_splits > 0 ? num_splits : sms < kAutoParts ? sms : kAutoParts;
+  const int hs = Hkv * pl.nseqh;
+  a.hg = hs < a.nparts ? hs : a.nparts;
+  a.qscale = scale * LOG2E;
+  a.vscale = 1.f;
+  uint32_t *status = &reinterpret_cast<WsHeader *>(ws)->status;
+  cudaError_t e;
+  if (D == 256) e = launch_tree<256, TREE_BF16, 1>(tm_k, tm_v, tm_q, a, status, stream);
+  else if (D == 128) e = pl.QT == 2 ? launch_tree<128, TREE_BF16, 2>(tm_k, tm_v, tm_q, a, status, stream)
+                                    : launch_tree<128, TREE_BF16, 1>(tm_k, tm_v, tm_q, a, status, stream);
+  else e = pl.QT == 2 ? launch_tree<64, TREE_BF16, 2>(tm_k, tm_v, tm_q, a, status, stream)
+                      : launch_tree<64, TREE_BF16, 1>(tm_k, tm_v, tm_q, a, status, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  note_launches(2);
   return PA_OK;
 }
 
@@ -168,10 +306,10 @@ int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32
 
 extern "C" size_t pa_tree_workspace_size(int batch, int max_query, int num_q_heads, int num_kv_heads, int head_dim,
                                          int max_context_len, int page_size, int num_splits) {
-  size_t n = 0;
-  return pa::tree_shape(batch, max_query, num_q_heads, num_kv_heads, head_dim, max_context_len, page_size, num_splits,
-                        &n) == PA_OK
-             ? n
+  pa::TreePlan pl;
+  return pa::tree_plan(batch, max_query, num_q_heads, num_kv_heads, head_dim, max_context_len, page_size, num_splits,
+                       &pl) == PA_OK
+             ? pl.total
              : 0;
 }
 

@@ -1,0 +1,1124 @@
+// pa_tree.cuh -- attention of drafted trees over the paged cache on the 5th-generation tensor cores
+// (sm_103a).
+//
+// Mathematics.  Node i of row b (n nodes; L tokens with them; prefix = L - n) attends to the set A of
+// the prefix tokens and of the nodes that its mask names (under a window those fewer than `window`
+// positions back, a node's position being prefix + its number of other mask bits):
+//   out = sum_{t in A} exp(s_t - m) v_t / l,  lse = m + ln l,  s_t = scale q . k_t,
+//   m = max s_t,  l = sum exp(s_t - m).
+// One pass over the keys with a running maximum and sum in fp32; the maximum is only raised when it
+// grows by more than 2^8, so the weights stay below 2^8 and are rounded once, as the operand of
+// the second product (bf16, half a step 2^-8 of each weight; the sum l is of the unrounded ones).
+//
+// What bounds it.  The cache is read once for all of a key head's query rows, n nodes x G heads of
+// them, 4 D flops for each 4 D bytes of keys and values (bf16): memory up to about 280 rows, the
+// tensor cores and the exponentials beyond.  16 rows of an mma.sync would read the cache again for
+// each 16; here 128 rows are the M of one tcgen05.mma, two such tiles share every staged key.
+//
+// Work.  A sequence is (row, key head, pair of 128-row tiles); its keys are cut into units of one TMA
+// box.  CTAs form groups of HG = sequences per row; a group takes an equal share of all rows' cost
+// and CTA r of it serves sequence r, so that the tiles of one key head stream the same pages at the
+// same time.  A CTA's range is a list of pieces (runs of one sequence); only its first and its last
+// can be part of a sequence that another CTA also touches: at most two partial results a CTA.
+//
+// Roles of a CTA (one per SM):
+//   * warp 0: the K and V tiles of BN tokens into a ring of slots (TMA, 128-byte swizzle);
+//   * warp 1, one thread: the products.  Items alternate between two score buffers x = 0, 1.  With two
+//     tiles an item is (stage, tile x); with one tile the items are the stages in turn, so that the
+//     two softmax groups work on alternate stages of the same rows, each with its own output
+//     columns, and are merged at the end of the piece.  Scores of item i + 1 are issued before the
+//     second product of item i, so the tensor cores work while a group is in its softmax;
+//   * warp 2: looks over V tiles that hold tokens which not every row attends to (the tree, the edge
+//     of a window, the ends of a piece) before they are used: a token that nobody attends to becomes
+//     zero, and infinities and NaN of the others are taken out of the product and handed to the rows
+//     that do attend to them (0 x inf must not reach the ones that do not);
+//   * warp 3: the query tiles of each piece;
+//   * two groups of four warps: one thread per score row.  The scores are read twice from tensor
+//     memory, 32 columns at a time (once for the maximum, once for the weights): a second read is
+//     cheaper than 128 live registers.
+// Tensor memory: scores (then weights) x at BN x, outputs at 256.  At head_dim 256 one output fills the
+// rest: one tile, one softmax group, stages of 64 tokens.
+#pragma once
+
+#include "pa_common.cuh"
+#include "pa_quant.cuh"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+
+enum TreeFmt { TREE_BF16 = 0, TREE_FP8 = 1, TREE_NVFP4 = 2 };
+constexpr int kTreeNodes = 64;   // most nodes of a row: bits of a mask
+constexpr int kTreeRows = 128;   // query rows of a tile
+
+struct TreeArgs {
+  const uint8_t *v_pool;
+  const int32_t *block_table, *context_lens, *query_start;
+  const uint64_t *tree_mask;
+  uint16_t *out;
+  float *lse;           // or null
+  uint32_t *desc;       // [nparts] PA_DEV_* bits of each CTA
+  float *part_o;        // [nparts, 2, QT * 128, D]
+  float *part_lse;      // [nparts, 2, QT * 128], log2 units
+  int32_t *seq_first, *seq_last;  // [batch, hs]: -1 whole; 2 x CTA + slot of the first piece / CTA of the last
+  struct TreeHalf *halves;        // [nparts, 2, 128]: the groups' halves of a one-tile piece
+  int batch, tokens, max_query, Hq, Hkv, G;
+  int gt, qt, nsub;     // a tile: qt nodes x gt heads; nsub tiles for a node's heads (G > 128)
+  int nseqh;            // sequences per key head
+  int log2_page, log2_bh, num_pages, max_pages_per_seq, max_context_len, window;
+  int piece_cost, nparts, hg;
+  float qscale;         // scale * log2(e) (* the keys' scale)
+  float vscale;
+};
+
+struct TreeHalf {  // one row's state in one softmax group, for the merge of a one-tile piece
+  float m, l;
+  uint64_t bad_nodes, bad_edge;
+};
+
+template <int D_, int FMT_, int QT_>
+struct TreeCfg {
+  static constexpr int D = D_, FMT = FMT_, QT = QT_;
+  static constexpr int GROUPS = D <= 128 ? 2 : 1;  // softmax groups, and output regions
+  static constexpr int BN = D <= 128 ? 128 : 64;   // tokens per stage
+  static constexpr int NPL = D / 64;               // 128-byte swizzle planes of a row
+  static constexpr int PLANE = BN * 128, SLOT = NPL * PLANE, QPLANE = kTreeRows * 128;
+  static constexpr int Q_BYTES = QT * NPL * QPLANE;
+  static constexpr int NS_FIT = (229376 - Q_BYTES) / SLOT;
+  // two rings of slots: a K tile is free after the scores of its stage, a V tile later.  (One ring for
+  // both would need an even number of slots: the copies complete out of order, and a wait for the phase
+  // of a slot must not come before the phase before it is known to be complete.)
+  static constexpr int NS = NS_FIT < 10 ? NS_FIT : 10, NK = NS / 2, NV = NS - NK;
+  static constexpr int SOFTMAX_WARPS = 4 * GROUPS;
+  static constexpr int THREADS = (4 + SOFTMAX_WARPS) * 32;
+  static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
+  static constexpr uint32_t IDESC_S = tc_idesc_bf16(kTreeRows, BN, false);
+  static constexpr uint32_t IDESC_PV = tc_idesc_bf16(kTreeRows, D, true);
+  static constexpr float TAU = 8.f;
+  static constexpr int META = 8;  // stage records kept: a record is rewritten eight stages later, once the
+                                  // K tile of at least three stages later is free
+  static_assert(NK >= 2 && NK <= 5 && QT <= GROUPS, "a ring of two stages; two tiles need two groups");
+  static_assert(2 * BN <= 256 && GROUPS * D <= 256, "tensor-memory budget");
+};
+
+struct alignas(16) TreeStage {
+  int32_t end, first, left, masked;  // left: stages of the piece behind this one
+  int32_t b, two, slot, tok0;        // slot: -1 whole sequence, else partial slot
+  int32_t tok_hi, L, n, start;
+  uint32_t badmask;                  // bit k: box k of the stage was not loaded
+  int32_t t0, g, lo_min;             // first tile, key head, first token that any node's window reaches
+};
+static_assert(sizeof(TreeStage) == 64, "stage record is 64 bytes");
+
+struct TreePart {
+  int32_t found_b, pad;
+  long long found_off, x_begin, x_end, warp_part[16];
+};
+
+struct TreeMisc {
+  uint32_t status, tmem;
+  int32_t npieces, pad;
+  TreePart part;
+};
+
+template <class C>
+struct TreeSmem {
+  static constexpr int OFF_RING = C::Q_BYTES;
+  static constexpr int OFF_META = OFF_RING + C::NS * C::SLOT;
+  static constexpr int OFF_NF = OFF_META + C::META * (int)sizeof(TreeStage);  // [META][2] token bits
+  // full[NS], empty[NS], clean[META], q_full, q_empty, s_full[2], p_ready[2], pv_done[2], o_free, half[2], drain
+  static constexpr int OFF_BAR = OFF_NF + C::META * 16;
+  static constexpr int NBAR = 2 * C::NS + C::META + 12;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int BYTES = OFF_MISC + (int)sizeof(TreeMisc) + 1024;
+  static_assert(BYTES <= 232448, "fits the 227 KB opt-in shared memory of one CTA");
+};
+
+// ---------------------------------------------------------------------------------------- rows, tiles
+
+struct TreeRow {
+  int start, n, L;  // n = 0: nothing to do
+};
+
+// Row b, its lengths checked: a bad row has no nodes and sets PA_DEV_BAD_LEN.
+__device__ __forceinline__ TreeRow tree_row(const TreeArgs &a, int b, uint32_t *bad) {
+  TreeRow r;
+  r.start = a.query_start[b];
+  r.L = a.context_lens[b];
+  const int end = a.query_start[b + 1];
+  r.n = end - r.start;
+  if (r.start < 0 || end < r.start || end > a.tokens || r.n > a.max_query || r.L < r.n || r.L < 0 ||
+      r.L > a.max_context_len) {
+    *bad |= PA_DEV_BAD_LEN;
+    r.n = 0;
+  }
+  return r;
+}
+
+// First token that some node of the row can see: a node of depth 0 is at position L - n.
+__device__ __forceinline__ int tree_lo(const TreeArgs &a, const TreeRow &r) {
+  return a.window > 0 ? max(r.L - r.n + 1 - a.window, 0) : 0;
+}
+
+// Units of the row's keys: [*u_lo, *u_lo + the returned number).
+__device__ __forceinline__ int tree_units(const TreeArgs &a, const TreeRow &r, int *u_lo) {
+  *u_lo = tree_lo(a, r) >> a.log2_bh;
+  return r.n > 0 ? ((r.L + (1 << a.log2_bh) - 1) >> a.log2_bh) - *u_lo : 0;
+}
+
+__device__ __forceinline__ int tree_cost(const TreeArgs &a, const TreeRow &r) {
+  int ul;
+  const int n = tree_units(a, r, &ul);
+  return n > 0 ? n + a.piece_cost : 0;
+}
+
+__device__ __forceinline__ int tree_tiles(const TreeArgs &a, int n) {
+  return a.nsub > 1 ? n * a.nsub : (n + a.qt - 1) / a.qt;
+}
+
+// Tile t: nodes [i0, i0 + nq), heads [h0, h0 + nh) of the group; its row r is node i0 + r / gt, head h0 + r % gt.
+struct TreeTile {
+  int i0, nq, h0, nh;
+};
+__device__ __forceinline__ TreeTile tree_tile(const TreeArgs &a, int t, int n) {
+  TreeTile x;
+  if (a.nsub > 1) {
+    x.i0 = t / a.nsub;
+    x.nq = 1;
+    x.h0 = (t % a.nsub) * kTreeRows;
+    x.nh = min(kTreeRows, a.G - x.h0);
+  } else {
+    x.i0 = t * a.qt;
+    x.nq = min(a.qt, n - x.i0);
+    x.h0 = 0;
+    x.nh = a.G;
+  }
+  return x;
+}
+
+// ---------------------------------------------------------------------------------------- partition
+// The rows' costs laid end to end are cut into one equal range per group of HG CTAs (see the top).
+
+template <int THREADS>
+__device__ __forceinline__ long long tree_scan(long long v, long long *excl, long long *part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(FULL, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += part[w];
+    total += part[w];
+  }
+  __syncthreads();
+  *excl = before + x - v;
+  return total;
+}
+
+template <int THREADS>
+__device__ __forceinline__ void tree_partition(const TreeArgs &a, TreePart *ps, uint32_t *status) {
+  const int tid = threadIdx.x;
+  if (tid == 0) ps->found_b = -1;
+  __syncthreads();
+  const int NG = a.nparts / a.hg, grp = (int)blockIdx.x / a.hg;
+  const bool member = grp < NG;
+  uint32_t bad = 0;
+  // up to THREADS rows: one scan gives the total and the place; more: a pass for the total, one for the place
+  const bool once = a.batch <= THREADS;
+  long long W = 0, v = 0, ex = 0;
+  if (once) {
+    if (tid < a.batch) v = tree_cost(a, tree_row(a, tid, &bad));
+    W = tree_scan<THREADS>(v, &ex, ps->warp_part);
+  } else {
+    long long local = 0;
+    for (int b = tid; b < a.batch; b += THREADS) local += tree_cost(a, tree_row(a, b, &bad));
+    W = tree_scan<THREADS>(local, &ex, ps->warp_part);
+  }
+  const long long xb = (long long)grp * W / NG, xe = ((long long)grp + 1) * W / NG;
+  if (member && xb < xe) {
+    long long base = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
+      if (!once) {
+        v = b0 + tid < a.batch ? tree_cost(a, tree_row(a, b0 + tid, &bad)) : 0;
+        const long long total = tree_scan<THREADS>(v, &ex, ps->warp_part);
+        ex += base;
+        base += total;
+      }
+      if (v > 0 && xb >= ex && xb < ex + v) {
+        ps->found_b = b0 + tid;
+        ps->found_off = xb - ex;
+      }
+      __syncthreads();
+      if (ps->found_b >= 0) break;
+    }
+  }
+  if (bad) atomicOr(status, bad);
+  if (tid == 0) {
+    ps->x_begin = member ? xb : 0;
+    ps->x_end = member ? xe : 0;
+  }
+  __syncthreads();
+}
+
+// One piece: units [ub, ue) of sequence hs of row b.
+struct TreePiece {
+  int b, hs, ub, ue, start, n, L, t0, g, two;
+  bool starts, ends;
+};
+
+// A warp's walk over its CTA's pieces (all lanes call together); each walker sees the same pieces.
+struct TreeWalker {
+  const TreeArgs &a;
+  int lane, hs_row, b_first, in_first;
+  long long span, R;
+  int rb, w_start, w_n, w_L;  // lane l holds row rb + l
+  int it_hs, it_b, it_in;
+
+  __device__ TreeWalker(const TreeArgs &args, const TreePart *ps, int lane_) : a(args), lane(lane_) {
+    hs_row = a.Hkv * a.nseqh;
+    b_first = max(ps->found_b, 0);
+    in_first = ps->found_b >= 0 ? (int)ps->found_off : 0;
+    span = ps->found_b >= 0 ? ps->x_end - ps->x_begin : 0;
+    R = span;
+    fill(b_first);
+    it_hs = (int)blockIdx.x % a.hg;
+    it_b = b_first;
+    it_in = in_first;
+  }
+  __device__ void fill(int row) {
+    rb = row;
+    uint32_t ignored = 0;
+    TreeRow r = {0, 0, 0};
+    if (rb + lane < a.batch) r = tree_row(a, rb + lane, &ignored);
+    w_start = r.start;
+    w_n = r.n;
+    w_L = r.L;
+  }
+  __device__ TreeRow row_of(int row) {
+    if (row < rb || row >= rb + 32) fill(row);
+    TreeRow r;
+    r.start = __shfl_sync(FULL, w_start, row - rb);
+    r.n = __shfl_sync(FULL, w_n, row - rb);
+    r.L = __shfl_sync(FULL, w_L, row - rb);
+    return r;
+  }
+
+  template <int QT>
+  __device__ bool take(TreePiece &pc) {
+    while (true) {
+      if (R == 0) {
+        it_hs += a.hg;
+        if (span == 0 || it_hs >= hs_row) return false;
+        R = span;
+        it_b = b_first;
+        it_in = in_first;
+      }
+      const TreeRow r = row_of(it_b);
+      const int w = tree_cost(a, r);
+      const int b = it_b;
+      const int take = (int)min((long long)(w - it_in), R);
+      const int u0 = max(0, it_in - a.piece_cost), u1 = max(0, it_in + take - a.piece_cost);
+      R -= take;
+      it_in += take;
+      if (it_in >= w && R > 0) {
+        it_in = 0;
+        ++it_b;
+        while (it_b < a.batch && tree_cost(a, row_of(it_b)) == 0) ++it_b;
+        if (it_b >= a.batch) R = 0;  // (what is left of the range lies in rows that exist)
+      }
+      const int t0 = (it_hs % a.nseqh) * QT;
+      if (u1 > u0 && t0 < tree_tiles(a, r.n)) {
+        int ul;
+        const int units = tree_units(a, r, &ul);
+        pc.b = b;
+        pc.hs = it_hs;
+        pc.start = r.start;
+        pc.n = r.n;
+        pc.L = r.L;
+        pc.ub = ul + u0;
+        pc.ue = ul + u1;
+        pc.starts = u0 == 0;
+        pc.ends = u1 == units;
+        pc.t0 = t0;
+        pc.g = it_hs / a.nseqh;
+        pc.two = QT == 2 && t0 + 1 < tree_tiles(a, r.n);
+        return true;
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------------------- values, bits
+
+template <int FMT, int D>
+__device__ __forceinline__ constexpr int tree_row_bytes() {
+  return FMT == TREE_BF16 ? 2 * D : FMT == TREE_FP8 ? D : (D / 2 + D / 16 + 15) / 16 * 16;
+}
+
+// Value d of a cache row (without the pool's scale).
+template <int FMT, int D>
+__device__ __forceinline__ float cache_value(const uint8_t *row, int d) {
+  if constexpr (FMT == TREE_BF16) {
+    return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(row)[d] << 16);
+  } else if constexpr (FMT == TREE_FP8) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(row[d], __NV_E4M3);
+    return __half2float(*reinterpret_cast<const __half *>(&h));
+  } else {
+    const uint32_t c = (row[d >> 1] >> (4 * (d & 1))) & 15u;
+    const float mag = (c & 7u) < 2 ? 0.5f * (float)(c & 7u)
+                                   : __uint_as_float((((c & 7u) >> 1) + 126u) << 23 | (c & 1u) << 22);
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(row[D / 2 + (d >> 4)], __NV_E4M3);
+    return (c & 8u ? -mag : mag) * __half2float(*reinterpret_cast<const __half *>(&h));
+  }
+}
+
+// The low k bits (k clamped to [0, 32]).
+__device__ __forceinline__ uint32_t low_bits(int k) { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u; }
+
+// Bits of the 32 tokens from `base` on that lie in [lo, hi).
+__device__ __forceinline__ uint32_t range_bits(int base, int lo, int hi) {
+  return low_bits(hi - base) & ~low_bits(lo - base);
+}
+
+// Bits of the 32 tokens from `base` on of a 64-bit mask whose bit 0 is token `at`.
+__device__ __forceinline__ uint32_t mask_bits(uint64_t m, int at, int base) {
+  const int s = base - at;
+  return s >= 64 || s <= -32 ? 0u : s >= 0 ? (uint32_t)(m >> s) : (uint32_t)(m << -s);
+}
+
+// Bits of the tokens of chunk c (32 tokens of a stage) whose boxes were loaded.
+__device__ __forceinline__ uint32_t loaded_bits(uint32_t badmask, int c, int log2_bh) {
+  if (badmask == 0) return ~0u;
+  if (log2_bh >= 5) return (badmask >> ((32 * c) >> log2_bh)) & 1u ? 0u : ~0u;
+  uint32_t ok = 0;
+  const int per = 32 >> log2_bh;
+  for (int k = 0; k < per; ++k)
+    if (!((badmask >> (c * per + k)) & 1u)) ok |= low_bits(1 << log2_bh) << (k << log2_bh);
+  return ok;
+}
+
+// ---------------------------------------------------------------------------------------- the kernel
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    tree_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CUtensorMap tm_q, const TreeArgs a) {
+  using S = TreeSmem<C>;
+  constexpr int D = C::D, BN = C::BN, NS = C::NS;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR), *empty = full + NS, *clean = empty + NS;
+  uint64_t *q_full = clean + C::META, *q_empty = q_full + 1, *s_full = q_full + 2, *p_ready = s_full + 2,
+           *pv_done = p_ready + 2, *o_free = pv_done + 2, *half_in = o_free + 1, *drain = half_in + 2;
+  TreeStage *meta = reinterpret_cast<TreeStage *>(smem + S::OFF_META);
+  uint64_t *nf = reinterpret_cast<uint64_t *>(smem + S::OFF_NF);
+  TreeMisc *misc = reinterpret_cast<TreeMisc *>(smem + S::OFF_MISC);
+  uint32_t *status = &misc->status;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < C::META; ++s) mbar_init(&clean[s], 1);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 2);  // the scores' commit and the issuing thread's arrive
+      mbar_init(&p_ready[x], 4);
+      mbar_init(&pv_done[x], 1);
+      mbar_init(&half_in[x], 4);
+    }
+    mbar_init(o_free, C::SOFTMAX_WARPS);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    misc->status = 0;
+    misc->npieces = 0;
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+    prefetch_tensormap(&tm_q);
+  }
+  if (warp == 1) tc_alloc(&misc->tmem, C::TM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem;
+  pdl_wait();               // what the stream's previous kernel wrote is visible from here on
+  pdl_launch_dependents();  // the combine kernel may be scheduled; it waits for this grid to finish
+  tree_partition<C::THREADS>(a, &misc->part, status);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ K and V tiles
+    const int nbox = BN >> a.log2_bh, P = 1 << a.log2_page;
+    uint32_t t = 0;
+    int in_flight = 0;  // tiles of stage t whose copies were issued
+    bool ok = true;
+    TreeWalker walker(a, &misc->part, lane);
+    int npieces = 0;
+    auto window_of = [&](const TreePiece &p, int w) {  // block-table entries [32 w, 32 w + 32) of a piece
+      const int pb = (p.ub << a.log2_bh) >> a.log2_page;
+      const int np = ((((p.ue << a.log2_bh) - 1) >> a.log2_page) + 1) - pb;
+      return 32 * w + lane < np ? a.block_table[(size_t)p.b * a.max_pages_per_seq + pb + 32 * w + lane] : 0;
+    };
+    TreePiece cur = {}, nxt = {};
+    bool has = walker.take<C::QT>(cur), has_next = false;
+    int cwin = has ? window_of(cur, 0) : 0, nwin = 0;
+    while (has && ok) {
+      has_next = walker.take<C::QT>(nxt);
+      if (has_next) nwin = window_of(nxt, 0);
+      const int slot = (cur.starts && cur.ends) ? -1 : (npieces == 0 ? 0 : 1);
+      if (lane == 0) {
+        const size_t si = (size_t)cur.b * a.Hkv * a.nseqh + cur.hs;
+        if (cur.starts)
+          a.seq_first[si] = slot < 0 ? -1 : (int32_t)blockIdx.x * 2 + slot;
+        else if (cur.ends)
+          a.seq_last[si] = (int32_t)blockIdx.x;
+      }
+      const int prefix = cur.L - cur.n;
+      const TreeRow row = {cur.start, cur.n, cur.L};
+      const int lo_min = tree_lo(a, row);
+      // every node sees the tokens [lo_max, prefix): depths are below n
+      const int lo_max = a.window > 0 ? max(cur.L - a.window, 0) : 0;
+      const int tok_hi = min(cur.L, cur.ue << a.log2_bh);
+      const int n_stages = (cur.ue - cur.ub + nbox - 1) / nbox;
+      const int pb = (cur.ub << a.log2_bh) >> a.log2_page;
+      int wi = 0, fwin = window_of(cur, 1);
+      for (int st = 0; st < n_stages && ok; ++st) {
+        const int unit0 = cur.ub + st * nbox, tok0 = unit0 << a.log2_bh;
+        // the pages of one stage never straddle a window of 32 (nbox divides 32)
+        const int pwin = ((tok0 >> a.log2_page) - pb) >> 5;
+        while (wi < pwin) {
+          cwin = fwin;
+          ++wi;
+          fwin = window_of(cur, wi + 1);
+        }
+        const int unit = unit0 + lane, btok = unit << a.log2_bh;
+        const int phys = __shfl_sync(FULL, cwin, ((btok >> a.log2_page) - pb) & 31);
+        bool load = false, isbad = false;
+        if (lane < nbox && unit < cur.ue) {
+          load = phys >= 0 && phys < a.num_pages;
+          isbad = !load;
+          if (isbad) atomicOr(status, PA_DEV_BAD_PAGE);
+        }
+        const uint32_t bad = __ballot_sync(FULL, isbad);
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL, load)) * (uint32_t)((C::NPL * 128) << a.log2_bh);
+#pragma unroll
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          const int s = kv ? C::NK + t % C::NV : t % C::NK;
+          const uint32_t u = kv ? t / C::NV : t / C::NK;
+          if (u > 0) ok = mbar_wait(&empty[s], (u - 1) & 1, status);
+          ok = __all_sync(FULL, ok);
+          if (!ok) break;
+          in_flight = kv + 1;
+          if (lane == 0) {
+            if (kv == 0) {
+              TreeStage m;
+              m.end = 0;
+              m.first = st == 0;
+              m.left = n_stages - 1 - st;
+              m.masked = tok0 + BN > min(prefix, tok_hi) || tok0 < lo_max || bad != 0;
+              m.b = cur.b;
+              m.two = cur.two;
+              m.slot = slot;
+              m.tok0 = tok0;
+              m.tok_hi = tok_hi;
+              m.L = cur.L;
+              m.n = cur.n;
+              m.start = cur.start;
+              m.badmask = bad;
+              m.t0 = cur.t0;
+              m.g = cur.g;
+              m.lo_min = lo_min;
+              meta[t % C::META] = m;
+            }
+            mbar_arrive_expect_tx(&full[s], bytes);
+          }
+          __syncwarp();
+          if (load) {
+            uint8_t *dst = smem + S::OFF_RING + s * C::SLOT + (lane << a.log2_bh) * 128;
+#pragma unroll
+            for (int p = 0; p < C::NPL; ++p)
+              tma_load_4d(dst + p * C::PLANE, kv ? &tm_v : &tm_k, p * 64, cur.g, btok & (P - 1), phys, &full[s]);
+          }
+        }
+        if (ok) {
+          ++t;
+          in_flight = 0;
+        }
+      }
+      if (!ok) break;
+      ++npieces;
+      cur = nxt;
+      cwin = nwin;
+      has = has_next;
+    }
+    // the end: a record in the place of the next stage, announced in both of its slots
+    for (int kv = 0; kv < 2 && ok; ++kv) {
+      const int s = kv ? C::NK + t % C::NV : t % C::NK;
+      const uint32_t u = kv ? t / C::NV : t / C::NK;
+      if (u > 0) ok = __all_sync(FULL, mbar_wait(&empty[s], (u - 1) & 1, status));
+      if (ok && lane == 0) {
+        if (kv == 0) meta[t % C::META].end = 1;
+        mbar_arrive(&full[s]);
+      }
+    }
+    if (!ok) {  // copies in flight land before the CTA exits
+      const uint32_t nk = t + (in_flight > 0), nv = t + (in_flight > 1);
+      for (uint32_t i = nk > C::NK ? nk - C::NK : 0u; i < nk; ++i) mbar_wait(&full[i % C::NK], (i / C::NK) & 1, status);
+      for (uint32_t i = nv > C::NV ? nv - C::NV : 0u; i < nv; ++i)
+        mbar_wait(&full[C::NK + i % C::NV], (i / C::NV) & 1, status);
+    }
+    if (lane == 0) misc->npieces = npieces;
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products (one thread)
+    if (lane == 0) {
+      const uint32_t ring = smem_u32(smem + S::OFF_RING), qb = smem_u32(smem);
+      uint32_t t = 0, kq = 0;
+      uint32_t cnt[2] = {0, 0};  // items issued with each score buffer
+      uint32_t started = 0;      // pieces whose first second product was issued
+      uint32_t fresh = 0;        // bit o: output region o has had no product in this piece
+      bool piece_open = false;
+      bool ok = true;
+      // scores of one item: query tile qx, stage tt, score buffer x
+      auto scores = [&](int x, int qx, uint32_t tt) {
+        const uint64_t qd = tc_sdesc_sw128(qb + qx * (C::NPL * C::QPLANE), 16, 1024);
+        const uint64_t kd = tc_sdesc_sw128(ring + (tt % C::NK) * C::SLOT, 16, 1024);
+#pragma unroll
+        for (int p = 0; p < C::NPL; ++p)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_ss(tmem + C::TM_S + x * BN, qd + (uint64_t)((p * C::QPLANE + 32 * kk) >> 4),
+                      kd + (uint64_t)((p * C::PLANE + 32 * kk) >> 4), C::IDESC_S, (p | kk) != 0 ? 1u : 0u);
+        tc_commit(&s_full[x]);
+        mbar_arrive(&s_full[x]);
+      };
+      // the second product of one item; `release`: the V tile is free behind it
+      auto weighted = [&](int x, uint32_t tt, uint32_t pair, bool release) -> bool {
+        const uint32_t vs = C::NK + tt % C::NV;  // the V tile's slot
+        if (!mbar_wait(&p_ready[x], pair & 1, status)) return false;
+        if (!mbar_wait(&full[vs], (tt / C::NV) & 1, status)) return false;
+        if (!mbar_wait(&clean[tt % C::META], (tt / C::META) & 1, status)) return false;
+        if (piece_open) {  // the piece's first: the previous piece's outputs have been read
+          if (started > 0 && !mbar_wait(o_free, (started - 1) & 1, status)) return false;
+          ++started;
+          piece_open = false;
+        }
+        tc_fence_after();
+        const int o = C::GROUPS == 2 ? x : 0;
+        const uint64_t vd = tc_sdesc_sw128(ring + vs * C::SLOT, C::PLANE, 1024);
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          tc_mma_ts(tmem + C::TM_O + o * D, tmem + C::TM_S + x * BN + 8 * kk, vd + (uint64_t)((kk * 16 * 128) >> 4),
+                    C::IDESC_PV, ((fresh >> o) & 1u) && kk == 0 ? 0u : 1u);
+        fresh &= ~(1u << o);
+        if (release) tc_commit(&empty[vs]);
+        tc_commit(&pv_done[x]);
+        ++cnt[x];
+        return true;
+      };
+      int pend = 0;  // an item of buffer 1 whose second product is due
+      uint32_t pend_t = 0;
+      for (uint32_t pair = 0; ok; ++pair) {
+        ok = mbar_wait(&full[t % C::NK], (t / C::NK) & 1, status);
+        if (!ok) break;
+        const TreeStage &m = meta[t % C::META];
+        const bool end = m.end, first = m.first, two = m.two;
+        const int left = m.left;
+        if (end) {
+          for (int x = 0; x < 2; ++x) {  // the softmax groups stop here
+            mbar_arrive(&s_full[x]);
+            mbar_arrive(&s_full[x]);
+          }
+          break;
+        }
+        if (first) {
+          ok = mbar_wait(q_full, kq & 1, status);
+          if (!ok) break;
+          ++kq;
+          fresh = 3u;
+          piece_open = true;
+        }
+        const bool last = two ? left == 0 : left <= 1;
+        const bool second = two || left >= 1;
+        const uint32_t t1 = two ? t : t + 1;
+        if (cnt[0] > 0) ok = mbar_wait(&pv_done[0], (cnt[0] - 1) & 1, status);
+        if (!ok) break;
+        tc_fence_after();
+        scores(0, 0, t);
+        if (!two) tc_commit(&empty[t % C::NK]);
+        if (pend) {
+          ok = weighted(1, pend_t, pair - 1, true);
+          pend = 0;
+          if (!ok) break;
+        }
+        if (second) {
+          if (!two) ok = mbar_wait(&full[t1 % C::NK], (t1 / C::NK) & 1, status);
+          if (ok && cnt[1] > 0) ok = mbar_wait(&pv_done[1], (cnt[1] - 1) & 1, status);
+          if (!ok) break;
+          tc_fence_after();
+          scores(1, two ? 1 : 0, t1);
+          tc_commit(&empty[t1 % C::NK]);
+        } else {  // no such stage: the record alone
+          mbar_arrive(&s_full[1]);
+          mbar_arrive(&s_full[1]);
+        }
+        if (last) tc_commit(q_empty);
+        ok = weighted(0, t, pair, !two);
+        if (!ok) break;
+        pend = second;
+        pend_t = t1;
+        if (last) {  // nothing is left open between two pieces
+          ok = second ? weighted(1, t1, pair, true) : mbar_wait(&p_ready[1], pair & 1, status);
+          pend = 0;
+        }
+        t += second && !two ? 2 : 1;
+      }
+      // every operation of this thread has completed before the tensor memory is released
+      tc_commit(drain);
+      mbar_wait(drain, 0, status);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ tokens that not everyone attends to
+    for (uint32_t t = 0;; ++t) {
+      const int s = C::NK + t % C::NV;
+      if (!__all_sync(FULL, mbar_wait(&full[s], (t / C::NV) & 1, status))) break;
+      const TreeStage &m = meta[t % C::META];
+      if (m.end) break;
+      if (m.masked) {
+        const int prefix = m.L - m.n, lo_max = a.window > 0 ? max(m.L - a.window, 0) : 0;
+        uint64_t bad_nodes = 0, bad_edge = 0;
+        uint8_t *v = smem + S::OFF_RING + s * C::SLOT;
+        for (int r = lane; r < BN; r += 32) {
+          const int tok = m.tok0 + r;
+          const bool any = tok >= m.lo_min && tok < m.tok_hi && ((loaded_bits(m.badmask, r >> 5, a.log2_bh) >> (r & 31)) & 1u);
+          const bool some = tok >= prefix || tok < lo_max;  // seen by some nodes and not by others
+          if (any && !some) continue;
+          bool found = false;
+#pragma unroll 4
+          for (int c = 0; c < C::NPL * 8; ++c) {
+            uint4 *p = reinterpret_cast<uint4 *>(v + (c >> 3) * C::PLANE + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            if (!any) {
+              *p = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 x = *p;
+            uint32_t w[4] = {x.x, x.y, x.z, x.w}, hit = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // exponents of all ones: infinities and NaN
+              const uint32_t bits = ((w[e] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w[e] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+              hit |= bits;
+              w[e] &= ~bits;
+            }
+            if (hit) {
+              found = true;
+              *p = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          if (found) {
+            if (tok >= prefix) bad_nodes |= 1ull << (tok - prefix);
+            else bad_edge |= 1ull << (tok - m.lo_min);
+          }
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+          bad_nodes |= __shfl_xor_sync(FULL, bad_nodes, o);
+          bad_edge |= __shfl_xor_sync(FULL, bad_edge, o);
+        }
+        if (lane == 0) {
+          nf[(t % C::META) * 2] = bad_nodes;
+          nf[(t % C::META) * 2 + 1] = bad_edge;
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&clean[t % C::META]);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ query tiles
+    TreeWalker walker(a, &misc->part, lane);
+    TreePiece pc;
+    uint32_t k = 0;
+    while (walker.take<C::QT>(pc)) {
+      if (k > 0 && !__all_sync(FULL, mbar_wait(q_empty, (k - 1) & 1, status))) break;
+      if (lane == 0) {
+        const int boxes = min(a.qt, a.max_query) * a.gt * 128;  // bytes of one plane's box
+        mbar_arrive_expect_tx(q_full, (uint32_t)(C::NPL * boxes * (pc.two ? 2 : 1)));
+        for (int x = 0; x < (pc.two ? 2 : 1); ++x) {
+          const TreeTile tl = tree_tile(a, pc.t0 + x, pc.n);
+#pragma unroll
+          for (int p = 0; p < C::NPL; ++p)
+            tma_load_3d(smem + (x * C::NPL + p) * C::QPLANE, &tm_q, p * 64, pc.g * a.G + tl.h0, pc.start + tl.i0, q_full);
+        }
+      }
+      __syncwarp();
+      ++k;
+    }
+    if (k > 0) mbar_wait(q_full, (k - 1) & 1, status);  // no copy is in flight when the CTA exits
+  } else {
+    // ------------------------------------------------------------ softmax and output
+    const int grp = (warp - 4) >> 2;              // softmax group
+    const int row = 32 * (warp & 3) + lane;       // row of the tile, lane of the tensor memory
+    const uint32_t tl_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    float m_run = -INFINITY, l_run = 0.f;
+    uint64_t eff = 0, bad_nodes = 0, bad_edge = 0;
+    int lo_row = 0, prefix = 0, node_tok = 0, head = 0, start = 0, n = 0, lo_min = 0, b = 0, slot = -1, g = 0, prow = 0;
+    bool real = false, warp_real = false, had = false;  // had: this group's output has had a product in the piece
+    uint32_t cnt[2] = {0, 0}, k_half = 0;
+    uint32_t t = 0;
+    bool ok = true;
+
+    auto item = [&](int x, uint32_t tt) -> bool {
+      const TreeStage &m = meta[tt % C::META];
+      const uint32_t tS = tl_base + C::TM_S + x * BN;
+      const int o = C::GROUPS == 2 ? grp : 0;
+      const uint32_t tO = tl_base + C::TM_O + o * D;
+      if (warp_real) {
+        const bool masked = m.masked;
+        uint32_t vis[BN / 32];
+        if (masked) {
+          if (!mbar_wait(&clean[tt % C::META], (tt / C::META) & 1, status)) return false;
+          __syncwarp();
+          bad_nodes |= nf[(tt % C::META) * 2];
+          bad_edge |= nf[(tt % C::META) * 2 + 1];
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) {
+            const int base = m.tok0 + 32 * c;
+            vis[c] = (range_bits(base, lo_row, prefix) | mask_bits(eff, prefix, base)) & range_bits(base, 0, m.tok_hi) &
+                     loaded_bits(m.badmask, c, a.log2_bh);
+          }
+        }
+        // the largest score (the smallest under a negative scale) of the row
+        float mx = -INFINITY;
+        const float sgn = a.qscale < 0.f ? -1.f : 1.f;
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          float s[32];
+          tc_ld32(tS + 32 * c, s);
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], (vis[c] >> i) & 1u ? s[i] * sgn : -INFINITY);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], s[i] * sgn);
+          }
+          mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+        }
+        mx = mx == -INFINITY ? mx : mx * fabsf(a.qscale);
+        if (!had) {
+          m_run = mx;
+        } else if (__any_sync(FULL, real && m_run != -INFINITY && mx > m_run + C::TAU)) {
+          // raise the maximum: the output so far is scaled, once its products are complete
+          const int px = C::GROUPS == 2 ? x : x ^ 1;  // the buffer of the output's previous item
+          if (!mbar_wait(&pv_done[px], (cnt[px] - 1) & 1, status)) return false;
+          __syncwarp();
+          tc_fence_after();
+          const float mn = fmaxf(m_run, mx);
+          const float al = m_run == -INFINITY ? 1.f : fast_exp2(m_run - mn);
+          m_run = mn;
+          l_run *= al;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float v[32];
+            tc_ld32(tO + c, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= al;
+            tc_st32(tO + c, v);
+          }
+          tc_wait_st();
+        } else if (m_run == -INFINITY) {
+          m_run = mx;  // nothing attended to so far: the output is zero
+        }
+        const float sub = m_run == -INFINITY ? 0.f : m_run;
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          float s[32];
+          tc_ld32(tS + 32 * c, s);
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float p0 = fast_exp2(fmaf(s[i], a.qscale, -sub)), p1 = fast_exp2(fmaf(s[i + 1], a.qscale, -sub));
+            if (masked) {
+              p0 = (vis[c] >> i) & 1u ? p0 : 0.f;
+              p1 = (vis[c] >> (i + 1)) & 1u ? p1 : 0.f;
+            }
+            l4[(i >> 1) & 3] += p0 + p1;
+            w[i >> 1] = pack_bf16x2(p0, p1);
+          }
+          tc_st16(tS + 16 * c, w);
+        }
+        l_run += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        tc_wait_st();
+      }
+      had = true;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_ready[x]);
+      return true;
+    };
+
+    for (uint32_t p = 0; ok; ++p) {
+      bool last = false, two = false;
+      uint32_t step = 1;
+#pragma unroll
+      for (int xi = 0; xi < 2; ++xi) {
+        if (C::GROUPS == 2 && xi != grp) continue;
+        if (!mbar_wait(&s_full[xi], p & 1, status)) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        const TreeStage &m = meta[t % C::META];
+        if (m.end) {
+          ok = false;
+          break;
+        }
+        two = m.two;
+        const int left = m.left;
+        last = two ? left == 0 : left <= 1;
+        step = two ? 1 : left >= 1 ? 2 : 1;
+        if (m.first && (C::GROUPS == 2 || xi == 0)) {
+          // a new piece: this thread's row
+          b = m.b;
+          start = m.start;
+          n = m.n;
+          prefix = m.L - n;
+          lo_min = m.lo_min;
+          slot = m.slot;
+          g = m.g;
+          const int tx = two ? grp : 0;
+          const TreeTile tile = tree_tile(a, m.t0 + tx, n);
+          const int pos = row / a.gt, h = row - pos * a.gt;
+          real = pos < tile.nq && h < tile.nh;
+          warp_real = __any_sync(FULL, real);
+          prow = tx * kTreeRows + row;
+          head = g * a.G + tile.h0 + h;
+          node_tok = start + tile.i0 + pos;
+          eff = 0;
+          lo_row = 0;
+          if (real) {
+            const uint64_t keep = n < 64 ? (1ull << n) - 1 : ~0ull;
+            const int node = tile.i0 + pos;
+            eff = a.tree_mask[node_tok] & keep;
+            if (a.window > 0) {
+              const int depth = __popcll(eff & ~(1ull << node));
+              lo_row = max(prefix + depth - a.window + 1, 0);
+              for (uint64_t rest = eff; rest; rest &= rest - 1) {
+                const int j = __ffsll((long long)rest) - 1;
+                const uint64_t mj = a.tree_mask[start + j] & keep;
+                if (depth - __popcll(mj & ~(1ull << j)) >= a.window) eff &= ~(1ull << j);
+              }
+            }
+          }
+          m_run = -INFINITY;
+          l_run = 0.f;
+          bad_nodes = bad_edge = 0;
+          had = false;
+        }
+        if (two || xi == 0 || left >= 1) {
+          if (!item(xi, two ? t : t + xi)) {
+            ok = false;
+            break;
+          }
+        } else {  // no such stage: only that the record was read
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[xi]);
+        }
+        if (C::GROUPS == 1 && (xi == 0 || left >= 1)) ++cnt[xi];
+        if (C::GROUPS == 2) {  // both buffers' items are counted: the merge waits for the other's too
+          ++cnt[0];
+          if (two || left >= 1) ++cnt[1];
+        }
+      }
+      if (!ok) break;
+      t += step;
+      if (!last) continue;
+
+      // ---- end of a piece
+      TreeHalf other = {-INFINITY, 0.f, 0, 0};
+      const bool merge = C::GROUPS == 2 && !two;
+      if (merge) {
+        TreeHalf *mine = a.halves + ((size_t)blockIdx.x * 2 + grp) * kTreeRows + row;
+        *mine = TreeHalf{m_run, l_run, bad_nodes, bad_edge};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&half_in[grp]);
+        if (!mbar_wait(&half_in[grp ^ 1], k_half & 1, status)) break;
+        ++k_half;
+        other = a.halves[((size_t)blockIdx.x * 2 + (grp ^ 1)) * kTreeRows + row];
+        bad_nodes |= other.bad_nodes;
+        bad_edge |= other.bad_edge;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (cnt[x] > 0 && (C::GROUPS == 1 || merge || x == grp) && !mbar_wait(&pv_done[x], (cnt[x] - 1) & 1, status))
+          ok = false;
+      if (!ok) break;
+      __syncwarp();
+      tc_fence_after();
+      // weights of this group's output and of the other's; a sum of zero: nothing was attended to
+      const float M = fmaxf(m_run, other.m);
+      const float w_own = l_run == 0.f ? 0.f : fast_exp2(m_run - M), w_oth = other.l == 0.f ? 0.f : fast_exp2(other.m - M);
+      const float Z = (l_run == 0.f ? 0.f : l_run * w_own) + (other.l == 0.f ? 0.f : other.l * w_oth);
+      const float inv = Z == 0.f ? 0.f : a.vscale / Z;
+      const float s_own = w_own * inv, s_oth = w_oth * inv;
+      const bool use_own = l_run != 0.f, use_oth = merge && other.l != 0.f;
+      const float lse2 = Z == 0.f ? -INFINITY : M + __log2f(Z);
+      const int o = C::GROUPS == 2 ? grp : 0;
+      const int c0 = merge ? grp * (D / 2) : 0, c1 = merge ? c0 + D / 2 : D;
+      const size_t pi = ((size_t)blockIdx.x * 2 + (slot > 0 ? 1 : 0)) * (C::QT * kTreeRows) + prow;
+      uint16_t *orow = a.out + ((size_t)node_tok * a.Hq + head) * D;
+      float *po = a.part_o + pi * D;
+      // tokens with infinities or NaN that this row attends to
+      uint64_t hit_nodes = bad_nodes & eff, hit_edge = bad_edge;
+      if (hit_edge) hit_edge = lo_row - lo_min >= 64 ? 0 : hit_edge >> (lo_row - lo_min) << (lo_row - lo_min);
+      if (warp_real) {
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 32) {
+          float v[32];
+          tc_ld32(tl_base + C::TM_O + o * D + c, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = use_own ? v[i] * s_own : 0.f;
+          if (merge) {
+            float u[32];
+            tc_ld32(tl_base + C::TM_O + (o ^ 1) * D + c, u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = use_oth ? fmaf(u[i], s_oth, v[i]) : v[i];
+          }
+          if (real) {
+            if (hit_nodes | hit_edge) {
+              for (int half = 0; half < 2; ++half) {
+                for (uint64_t rest = half ? hit_edge : hit_nodes; rest; rest &= rest - 1) {
+                  const int tok = (half ? lo_min : prefix) + __ffsll((long long)rest) - 1;
+                  const size_t page = (size_t)a.block_table[(size_t)b * a.max_pages_per_seq + (tok >> a.log2_page)];
+                  const uint8_t *vr = a.v_pool + (((page << a.log2_page) + (tok & ((1 << a.log2_page) - 1))) * a.Hkv + g) *
+                                                     (size_t)tree_row_bytes<C::FMT, D>();
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) {
+                    const float x = cache_value<C::FMT, D>(vr, c + i);
+                    if (!isfinite(x)) v[i] += x;
+                  }
+                }
+              }
+            }
+            if (slot < 0) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4 *>(orow + c + i) =
+                    make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]), pack_bf16x2(v[i + 4], v[i + 5]),
+                               pack_bf16x2(v[i + 6], v[i + 7]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4 *>(po + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+          }
+        }
+        if (real && c0 == 0) {
+          if (slot >= 0) a.part_lse[pi] = lse2;
+          else if (a.lse) a.lse[(size_t)node_tok * a.Hq + head] = lse2 * LN2;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tc_dealloc(tmem, C::TM_COLS);
+  if (tid == 0) a.desc[blockIdx.x] = misc->status;
+  if (misc->npieces == 0) {
+    // a range that held no key can still lie between two pieces of a sequence: its slot 0 weighs nothing
+    for (int h = tid; h < C::QT * kTreeRows; h += C::THREADS)
+      a.part_lse[(size_t)blockIdx.x * 2 * C::QT * kTreeRows + h] = -INFINITY;
+  }
+}
+
+// ---------------------------------------------------------------------------------------- combine
+// A warp per query row of a sequence that several CTAs share: their partial results in ascending order of
+// the keys, up to four loaded together.  Grid: (batch * hs, rows / kCombineRows).
+
+constexpr int kCombineRows = 32;
+
+template <int D, int QT>
+__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, uint32_t *status) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hs_row = a.Hkv * a.nseqh;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
+    uint32_t st = 0;
+    for (int i = lane; i < a.nparts; i += 32) st |= a.desc[i];
+    st = __reduce_or_sync(FULL, st);
+    if (lane == 0) *status = st;
+  }
+  const int b = (int)blockIdx.x / hs_row, q = (int)blockIdx.x % hs_row;
+  uint32_t ignored = 0;
+  const TreeRow r = tree_row(a, b, &ignored);
+  const int t0 = (q % a.nseqh) * QT;
+  if (r.n == 0 || t0 >= tree_tiles(a, r.n)) return;
+  const size_t si = (size_t)blockIdx.x;
+  const int f = a.seq_first[si], cl = a.seq_last[si], c0 = f >> 1;
+  // written whole, or (only where the split kernel gave up) a stale entry
+  if (f < 0 || c0 >= a.nparts || cl < c0 || cl >= a.nparts || (cl - c0) % a.hg != 0) return;
+  const int k = (cl - c0) / a.hg + 1, g = q / a.nseqh;
+  constexpr int RS = QT * kTreeRows, PER = D / 32, CHUNK = 4;
+  for (int e = warp; e < kCombineRows; e += 8) {
+    const int pr = (int)blockIdx.y * kCombineRows + e, t = t0 + pr / kTreeRows, row = pr % kTreeRows;
+    if (t >= tree_tiles(a, r.n)) break;
+    const TreeTile tl = tree_tile(a, t, r.n);
+    const int pos = row / a.gt, h = row - pos * a.gt;
+    if (pos >= tl.nq || h >= tl.nh) continue;
+    float M = -INFINITY, Z = 0.f, acc[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+    for (int i0 = 0; i0 < k; i0 += CHUNK) {
+      float lc[CHUNK], x[CHUNK][PER];
+#pragma unroll
+      for (int u = 0; u < CHUNK; ++u) {
+        const int i = i0 + u;
+        lc[u] = -INFINITY;
+        if (i < k) {
+          const size_t pi = (i == 0 ? (size_t)f : (size_t)(c0 + i * a.hg) * 2) * RS + pr;
+          lc[u] = a.part_lse[pi];
+#pragma unroll
+          for (int d = 0; d < PER; d += 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(a.part_o + pi * D + lane * PER + d);
+            x[u][d] = v.x;
+            x[u][d + 1] = v.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < CHUNK; ++u) {
+        if (lc[u] != -INFINITY) {  // (an empty slot's values are not written)
+          const float mn = fmaxf(M, lc[u]), sc = M == -INFINITY ? 0.f : fast_exp2(M - mn), wc = fast_exp2(lc[u] - mn);
+          M = mn;
+          Z = Z * sc + wc;
+#pragma unroll
+          for (int d = 0; d < PER; ++d) acc[d] = acc[d] * sc + wc * x[u][d];
+        }
+      }
+    }
+    const float inv = Z == 0.f ? 0.f : 1.f / Z;
+    const size_t at = (size_t)(r.start + tl.i0 + pos) * a.Hq + g * a.G + tl.h0 + h;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + at * D + lane * PER);
+#pragma unroll
+    for (int d = 0; d < PER; d += 2) dst[d / 2] = pack_bf16x2(acc[d] * inv, acc[d + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[at] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * LN2;
+  }
+}
+
+}  // namespace pa
