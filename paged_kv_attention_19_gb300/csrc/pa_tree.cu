@@ -9,81 +9,11 @@
 
 #include "pa_decode.h"
 #include "pa_launch.h"
-#include "pa_tree.cuh"
+#include "pa_tree_launch.cuh"
 
 namespace pa {
 
 namespace {
-
-struct PlainArgs {
-  const uint16_t *q;
-  const uint8_t *k_pool, *v_pool;
-  const int32_t *block_table, *context_lens, *query_start;
-  const uint64_t *tree_mask;
-  uint16_t *out;
-  float *lse;  // or null
-  uint32_t *status;
-  int batch, tokens, max_query, Hq, Hkv, G, page_size, num_pages, max_pages_per_seq, max_context_len, window;
-  float qscale, kscale, vscale;  // scale * log2(e); the pools' scales
-};
-
-// One block per (token, query head), a warp per fourth key.
-template <int FMT, int D>
-__global__ void __launch_bounds__(128) tree_plain_kernel(const PlainArgs a) {
-  constexpr int PER = D / 32, W = 4;
-  constexpr int ROW = FMT == TREE_BF16 ? 2 * D : FMT == TREE_FP8 ? D : (D / 2 + D / 16 + 15) / 16 * 16;
-  __shared__ float so[W][D], sm[W], sl[W];
-  const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int b = 0;
-  while (b < a.batch && !(a.query_start[b] <= t && t < a.query_start[b + 1])) ++b;
-  if (b == a.batch) return;
-  const int start = a.query_start[b], n = a.query_start[b + 1] - start, i = t - start, L = a.context_lens[b];
-  if (n > a.max_query || L < n || L > a.max_context_len) {
-    if (threadIdx.x == 0) atomicOr(a.status, PA_DEV_BAD_LEN);
-    return;
-  }
-  const int prefix = L - n;
-  const uint64_t mask = a.tree_mask[t] & (n < 64 ? (1ull << n) - 1 : ~0ull);
-  const int depth = __popcll(mask & ~(1ull << i));
-  float q[PER], acc[PER] = {}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < PER; ++e) q[e] = __uint_as_float((uint32_t)a.q[((size_t)t * a.Hq + h) * D + e * 32 + lane] << 16);
-  for (int j = warp; j < L; j += W) {
-    int back = prefix + depth - j;
-    if (j >= prefix) {
-      if (!((mask >> (j - prefix)) & 1)) continue;
-      const uint64_t mj = a.tree_mask[start + j - prefix] & (n < 64 ? (1ull << n) - 1 : ~0ull);
-      back = depth - __popcll(mj & ~(1ull << (j - prefix)));
-    }
-    if (a.window > 0 && back >= a.window) continue;
-    const int page = a.block_table[(size_t)b * a.max_pages_per_seq + j / a.page_size];
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) atomicOr(a.status, PA_DEV_BAD_PAGE);
-      continue;
-    }
-    const size_t row = (((size_t)page * a.page_size + j % a.page_size) * a.Hkv + h / a.G) * ROW;
-    float s = 0.f;
-    for (int e = 0; e < PER; ++e) s += q[e] * cache_value<FMT, D>(a.k_pool + row, e * 32 + lane);
-    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-    s *= a.qscale * a.kscale;
-    const float mn = fmaxf(m, s), al = m == -INFINITY ? 0.f : exp2f(m - mn), p = exp2f(s - mn);
-    m = mn;
-    l = l * al + p;
-    for (int e = 0; e < PER; ++e) acc[e] = acc[e] * al + p * cache_value<FMT, D>(a.v_pool + row, e * 32 + lane);
-  }
-  for (int e = 0; e < PER; ++e) so[warp][e * 32 + lane] = acc[e];
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-  __syncthreads();
-  float M = -INFINITY, Z = 0.f;
-  for (int w = 0; w < W; ++w) M = fmaxf(M, sm[w]);
-  for (int w = 0; w < W; ++w) Z += sl[w] == 0.f ? 0.f : sl[w] * exp2f(sm[w] - M);  // a NaN stays one
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float o = 0.f;
-    for (int w = 0; w < W; ++w)
-      if (sl[w] != 0.f) o += so[w][d] * exp2f(sm[w] - M);
-    a.out[((size_t)t * a.Hq + h) * D + d] = (uint16_t)(pack_bf16x2(Z != 0.f ? o * a.vscale / Z : 0.f, 0.f) & 0xffffu);
-  }
-  if (threadIdx.x == 0 && a.lse) a.lse[(size_t)t * a.Hq + h] = Z != 0.f ? (M + log2f(Z)) * LN2 : -INFINITY;
-}
 
 constexpr int kMaxSplits = 4096, kAutoParts = 256;
 // Fixed cost of a piece of work in the partition, as the bytes of cache that an SM streams meanwhile.
@@ -147,19 +77,20 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// A dense map of `rank` dimensions of bf16 values (the first one contiguous), 128-byte swizzle.
+// A dense map of RANK dimensions (the first one contiguous): bf16 values with the 128-byte swizzle, or bytes.
 template <int RANK>
-bool encode_map(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[RANK], const cuuint32_t (&box)[RANK]) {
+bool encode_map(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[RANK], const cuuint32_t (&box)[RANK], bool bytes) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t strides[RANK - 1], s = 2;
+  cuuint64_t strides[RANK - 1], s = bytes ? 1 : 2;
   cuuint32_t ones[RANK];
   for (int i = 0; i < RANK; ++i) {
     ones[i] = 1u;
     if (i < RANK - 1) strides[i] = s = s * dims[i];
   }
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, RANK, const_cast<void *>(base), dims, strides, box, ones,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, RANK, const_cast<void *>(base),
+            dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -168,34 +99,6 @@ int sm_count() {
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return -1;
   return n;
-}
-
-template <typename K, typename... A>
-cudaError_t launch_pdl(K kernel, dim3 grid, int threads, int smem, cudaStream_t stream, A &&...args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-template <int D, int FMT, int QT>
-cudaError_t launch_tree(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CUtensorMap &tm_q, const TreeArgs &a,
-                        uint32_t *status, cudaStream_t stream) {
-  using C = TreeCfg<D, FMT, QT>;
-  // (made at every call: the attribute is the device's, and costs less than to remember where it is set)
-  cudaError_t e = cudaFuncSetAttribute(tree_split_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeSmem<C>::BYTES);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(tree_split_kernel<C>, dim3((unsigned)a.nparts), C::THREADS, TreeSmem<C>::BYTES, stream, tm_k, tm_v, tm_q, a);
-  if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(a.batch * a.Hkv * a.nseqh), QT * kTreeRows / kCombineRows);
-  return launch_pdl(tree_combine_kernel<D, QT>, grid, 256, 0, stream, a, status);
 }
 
 int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
@@ -223,32 +126,19 @@ int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32
     if (!aligned_to(p, 4)) return PA_ERR_MISALIGNED;
   if (!aligned_to(tree_mask, 8)) return PA_ERR_MISALIGNED;
   if (workspace_bytes < pl.total) return PA_ERR_WORKSPACE_TOO_SMALL;
-  if (fmt != TREE_BF16) {
-    PlainArgs p = {static_cast<const uint16_t *>(q), static_cast<const uint8_t *>(k_pool), static_cast<const uint8_t *>(v_pool),
-                   block_table, context_lens, query_start, tree_mask, static_cast<uint16_t *>(out), lse,
-                   &static_cast<WsHeader *>(workspace)->status, batch, tokens, max_query, Hq, Hkv, Hq / Hkv, P, num_pages,
-                   max_pages, max_ctx, window > 0 ? window : 0, scale * LOG2E, k_scale, v_scale};
-    if (const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(WsHeader), stream); e != cudaSuccess) return cuda_fail(e);
-    const dim3 grid((unsigned)tokens, (unsigned)Hq);
-    auto run = [&](auto kernel) { kernel<<<grid, 128, 0, stream>>>(p); };
-    if (fmt == TREE_FP8)
-      D == 64 ? run(tree_plain_kernel<TREE_FP8, 64>) : D == 128 ? run(tree_plain_kernel<TREE_FP8, 128>) : run(tree_plain_kernel<TREE_FP8, 256>);
-    else
-      D == 64 ? run(tree_plain_kernel<TREE_NVFP4, 64>) : D == 128 ? run(tree_plain_kernel<TREE_NVFP4, 128>) : run(tree_plain_kernel<TREE_NVFP4, 256>);
-    if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return cuda_fail(e);
-    note_launches(1);
-    return PA_OK;
-  }
   const int BN = D <= 128 ? 128 : 64;  // tokens per stage (TreeCfg::BN)
   const int BH = P < BN ? P : BN;      // tokens per TMA box: a unit
   const int sms = sm_count();
   if (sms <= 0) return cuda_fail(cudaSuccess);
   CUtensorMap tm_k, tm_v, tm_q;
-  const cuuint64_t pool[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)P, (cuuint64_t)num_pages};
-  const cuuint32_t pbox[4] = {64u, 1u, (cuuint32_t)BH, 1u};
+  const bool codes = fmt != TREE_BF16;
+  const int rowb = tree_row_bytes(fmt, D);
+  const cuuint64_t pool[4] = {(cuuint64_t)(codes ? rowb : D), (cuuint64_t)Hkv, (cuuint64_t)P, (cuuint64_t)num_pages};
+  const cuuint32_t pbox[4] = {codes ? (cuuint32_t)rowb : 64u, 1u, (cuuint32_t)BH, 1u};
   const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)tokens};
   const cuuint32_t qbox[3] = {64u, (cuuint32_t)pl.gt, (cuuint32_t)(pl.qt < max_query ? pl.qt : max_query)};
-  if (!encode_map(&tm_k, k_pool, pool, pbox) || !encode_map(&tm_v, v_pool, pool, pbox) || !encode_map(&tm_q, q, qd, qbox))
+  if (!encode_map(&tm_k, k_pool, pool, pbox, codes) || !encode_map(&tm_v, v_pool, pool, pbox, codes) ||
+      !encode_map(&tm_q, q, qd, qbox, false))
     return PA_ERR_UNSUPPORTED;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   TreeArgs a;
@@ -281,20 +171,18 @@ int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32
   a.max_pages_per_seq = max_pages;
   a.max_context_len = max_ctx;
   a.window = window > 0 ? window : 0;
-  const long long unit_bytes = (long long)BH * D * 4;
+  const long long unit_bytes = (long long)BH * rowb * 2;
   a.piece_cost = (int)((kPieceCostBytes + unit_bytes - 1) / unit_bytes);
   a.nparts = num_splits > 0 ? num_splits : sms < kAutoParts ? sms : kAutoParts;
   const int hs = Hkv * pl.nseqh;
   a.hg = hs < a.nparts ? hs : a.nparts;
-  a.qscale = scale * LOG2E;
-  a.vscale = 1.f;
+  a.qscale = scale * LOG2E * (codes ? k_scale : 1.f);
+  a.vscale = codes ? v_scale : 1.f;
   uint32_t *status = &reinterpret_cast<WsHeader *>(ws)->status;
-  cudaError_t e;
-  if (D == 256) e = launch_tree<256, TREE_BF16, 1>(tm_k, tm_v, tm_q, a, status, stream);
-  else if (D == 128) e = pl.QT == 2 ? launch_tree<128, TREE_BF16, 2>(tm_k, tm_v, tm_q, a, status, stream)
-                                    : launch_tree<128, TREE_BF16, 1>(tm_k, tm_v, tm_q, a, status, stream);
-  else e = pl.QT == 2 ? launch_tree<64, TREE_BF16, 2>(tm_k, tm_v, tm_q, a, status, stream)
-                      : launch_tree<64, TREE_BF16, 1>(tm_k, tm_v, tm_q, a, status, stream);
+  const TreeLaunch l = {tm_k, tm_v, tm_q, a, status, D, pl.QT};
+  const cudaError_t e = fmt == TREE_BF16  ? launch_tree_bf16(l, stream)
+                        : fmt == TREE_FP8 ? launch_tree_fp8(l, stream)
+                                          : launch_tree_nvfp4(l, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   note_launches(2);
   return PA_OK;

@@ -33,6 +33,9 @@
 //     zero, and infinities and NaN of the others are taken out of the product and handed to the rows
 //     that do attend to them (0 x inf must not reach the ones that do not);
 //   * warp 3: the query tiles of each piece;
+//   * FP8 and NVFP4 pools: the tiles of codes land in a ring of their own, and four more warps convert
+//     them to f16 operands (exact), and the query rows, scaled by a power of two each, in place; they
+//     then do warp 2's work too.  The weights are rounded to f16 (2^-11);
 //   * two groups of four warps: one thread per score row.  The scores are read twice from tensor
 //     memory, 32 columns at a time (once for the maximum, once for the weights): a second read is
 //     cheaper than 128 live registers.
@@ -75,28 +78,46 @@ struct TreeHalf {  // one row's state in one softmax group, for the merge of a o
   uint64_t bad_nodes, bad_edge;
 };
 
+// Bytes of one head's row of a token in the cache.
+__host__ __device__ constexpr int tree_row_bytes(int fmt, int D) {
+  return fmt == TREE_BF16 ? 2 * D : fmt == TREE_FP8 ? D : (D / 2 + D / 16 + 15) / 16 * 16;
+}
+
 template <int D_, int FMT_, int QT_>
 struct TreeCfg {
   static constexpr int D = D_, FMT = FMT_, QT = QT_;
+  static constexpr bool QUANT = FMT != TREE_BF16;  // codes in the cache, f16 operands
+  static constexpr int ROWB = tree_row_bytes(FMT, D);
   static constexpr int GROUPS = D <= 128 ? 2 : 1;  // softmax groups, and output regions
   static constexpr int BN = D <= 128 ? 128 : 64;   // tokens per stage
   static constexpr int NPL = D / 64;               // 128-byte swizzle planes of a row
   static constexpr int PLANE = BN * 128, SLOT = NPL * PLANE, QPLANE = kTreeRows * 128;
   static constexpr int Q_BYTES = QT * NPL * QPLANE;
-  static constexpr int NS_FIT = (229376 - Q_BYTES) / SLOT;
+  static constexpr int ROOM = 229376 - Q_BYTES;
+  // codes: up to eight slots of a tile each, copied in order K, V, K, V...; operands converted from them
+  static constexpr int RAW_SLOT = QUANT ? (BN * ROWB + 1023) / 1024 * 1024 : 0;
+  static constexpr int NS_QUANT = D == 64 ? 5 : ROOM >= 4 * SLOT + 4 * RAW_SLOT ? 4 : 3;
+  static constexpr int NR_FIT = QUANT ? (ROOM - NS_QUANT * SLOT) / (RAW_SLOT > 0 ? RAW_SLOT : 1) : 0;
+  static constexpr int NR = NR_FIT < 8 ? NR_FIT : 8;
+  static constexpr int NS_FIT = QUANT ? NS_QUANT : ROOM / SLOT;
   // two rings of slots: a K tile is free after the scores of its stage, a V tile later.  (One ring for
   // both would need an even number of slots: the copies complete out of order, and a wait for the phase
   // of a slot must not come before the phase before it is known to be complete.)
   static constexpr int NS = NS_FIT < 10 ? NS_FIT : 10, NK = NS / 2, NV = NS - NK;
   static constexpr int SOFTMAX_WARPS = 4 * GROUPS;
-  static constexpr int THREADS = (4 + SOFTMAX_WARPS) * 32;
+  static constexpr int CONVERT_WARPS = QUANT ? 4 : 0;
+  static constexpr int CLEAN_WARPS = QUANT ? CONVERT_WARPS : 1;  // warps that look over the V tiles
+  static constexpr int THREADS = (4 + SOFTMAX_WARPS + CONVERT_WARPS) * 32;
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
-  static constexpr uint32_t IDESC_S = tc_idesc_bf16(kTreeRows, BN, false);
-  static constexpr uint32_t IDESC_PV = tc_idesc_bf16(kTreeRows, D, true);
+  // (formats 0: f16 operands)
+  static constexpr uint32_t IDESC_F16 = QUANT ? (1u << 7) | (1u << 10) : 0u;
+  static constexpr uint32_t IDESC_S = tc_idesc_bf16(kTreeRows, BN, false) & ~IDESC_F16;
+  static constexpr uint32_t IDESC_PV = tc_idesc_bf16(kTreeRows, D, true) & ~IDESC_F16;
   static constexpr float TAU = 8.f;
   static constexpr int META = 8;  // stage records kept: a record is rewritten eight stages later, once the
                                   // K tile of at least three stages later is free
-  static_assert(NK >= 2 && NK <= 5 && QT <= GROUPS, "a ring of two stages; two tiles need two groups");
+  static_assert(QUANT ? NR >= 4 && NK >= 1 && NR / 2 + NK <= 6 : NK >= 2 && NK <= 5, "rings of two stages, within the records");
+  static_assert(QT <= GROUPS, "two tiles need two groups");
   static_assert(2 * BN <= 256 && GROUPS * D <= 256, "tensor-memory budget");
 };
 
@@ -123,12 +144,15 @@ struct TreeMisc {
 template <class C>
 struct TreeSmem {
   static constexpr int OFF_RING = C::Q_BYTES;
-  static constexpr int OFF_META = OFF_RING + C::NS * C::SLOT;
-  static constexpr int OFF_NF = OFF_META + C::META * (int)sizeof(TreeStage);  // [META][2] token bits
-  // full[NS], empty[NS], clean[META], q_full, q_empty, s_full[2], p_ready[2], pv_done[2], o_free, half[2], drain
-  static constexpr int OFF_BAR = OFF_NF + C::META * 16;
-  static constexpr int NBAR = 2 * C::NS + C::META + 12;
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int OFF_RAW = OFF_RING + C::NS * C::SLOT;
+  static constexpr int OFF_META = OFF_RAW + C::NR * C::RAW_SLOT;
+  static constexpr int OFF_NF = OFF_META + C::META * (int)sizeof(TreeStage);  // [META][CLEAN_WARPS][2] token bits
+  // full[NS], empty[NS], clean[META], q_full, q_empty, s_full[2], p_ready[2], pv_done[2], o_free, half[2], drain,
+  // q_conv, raw_full[NR], raw_empty[NR]
+  static constexpr int OFF_BAR = OFF_NF + C::META * C::CLEAN_WARPS * 16;
+  static constexpr int NBAR = 2 * C::NS + C::META + 13 + 2 * C::NR;
+  static constexpr int OFF_SHIFT = OFF_BAR + NBAR * 8;  // int8 [2][QT * 128]: exponents of the query rows' scales
+  static constexpr int OFF_MISC = OFF_SHIFT + (C::QUANT ? 2 * C::QT * kTreeRows : 0);
   static constexpr int BYTES = OFF_MISC + (int)sizeof(TreeMisc) + 1024;
   static_assert(BYTES <= 232448, "fits the 227 KB opt-in shared memory of one CTA");
 };
@@ -355,11 +379,6 @@ struct TreeWalker {
 
 // ---------------------------------------------------------------------------------------- values, bits
 
-template <int FMT, int D>
-__device__ __forceinline__ constexpr int tree_row_bytes() {
-  return FMT == TREE_BF16 ? 2 * D : FMT == TREE_FP8 ? D : (D / 2 + D / 16 + 15) / 16 * 16;
-}
-
 // Value d of a cache row (without the pool's scale).
 template <int FMT, int D>
 __device__ __forceinline__ float cache_value(const uint8_t *row, int d) {
@@ -374,6 +393,37 @@ __device__ __forceinline__ float cache_value(const uint8_t *row, int d) {
                                    : __uint_as_float((((c & 7u) >> 1) + 126u) << 23 | (c & 1u) << 22);
     const __half_raw h = __nv_cvt_fp8_to_halfraw(row[D / 2 + (d >> 4)], __NV_E4M3);
     return (c & 8u ? -mag : mag) * __half2float(*reinterpret_cast<const __half *>(&h));
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Values 16 pc .. 16 pc + 15 of a row of codes as f16 pairs, without the pool's scale: exact (an E2M1 value
+// times an E4M3 block scale has at most six significant bits and lies in [2^-10, 2688]).
+template <int FMT, int D>
+__device__ __forceinline__ void convert16(const uint8_t *row, int pc, uint32_t (&h)[8]) {
+  if constexpr (FMT == TREE_FP8) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(row + 16 * pc);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
+      h[e] = (uint32_t)r.x | ((uint32_t)r.y << 16);
+    }
+  } else if constexpr (FMT == TREE_NVFP4) {
+    const uint2 x = *reinterpret_cast<const uint2 *>(row + 8 * pc);
+    const __half_raw b = __nv_cvt_fp8_to_halfraw(row[D / 2 + pc], __NV_E4M3);
+    const __half2 by = __half2half2(*reinterpret_cast<const __half *>(&b));
+    const uint32_t w[2] = {x.x, x.y};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const __half2_raw r = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[e >> 2] >> (8 * (e & 3))), __NV_E2M1);
+      const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&r), by);
+      h[e] = *reinterpret_cast<const uint32_t *>(&v);
+    }
   }
 }
 
@@ -414,7 +464,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR), *empty = full + NS, *clean = empty + NS;
   uint64_t *q_full = clean + C::META, *q_empty = q_full + 1, *s_full = q_full + 2, *p_ready = s_full + 2,
-           *pv_done = p_ready + 2, *o_free = pv_done + 2, *half_in = o_free + 1, *drain = half_in + 2;
+           *pv_done = p_ready + 2, *o_free = pv_done + 2, *half_in = o_free + 1, *drain = half_in + 2, *q_conv = drain + 1,
+           *raw_full = q_conv + 1, *raw_empty = raw_full + C::NR;
   TreeStage *meta = reinterpret_cast<TreeStage *>(smem + S::OFF_META);
   uint64_t *nf = reinterpret_cast<uint64_t *>(smem + S::OFF_NF);
   TreeMisc *misc = reinterpret_cast<TreeMisc *>(smem + S::OFF_MISC);
@@ -423,10 +474,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], C::QUANT ? C::CONVERT_WARPS : 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < C::META; ++s) mbar_init(&clean[s], 1);
+    for (int s = 0; s < C::META; ++s) mbar_init(&clean[s], C::CLEAN_WARPS);
+    for (int s = 0; s < C::NR; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], C::CONVERT_WARPS);
+    }
+    mbar_init(q_conv, C::QUANT ? C::CONVERT_WARPS : 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (int x = 0; x < 2; ++x) {
@@ -460,6 +516,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int nbox = BN >> a.log2_bh, P = 1 << a.log2_page;
     uint32_t t = 0;
     int in_flight = 0;  // tiles of stage t whose copies were issued
+    // where tile kv of stage t goes: slot, its phase, and the barriers of the ring
+    auto place = [&](int kv, uint32_t &u) -> int {
+      if constexpr (C::QUANT) {
+        u = (2 * t + kv) / C::NR;
+        return (2 * t + kv) % C::NR;
+      } else {
+        u = kv ? t / C::NV : t / C::NK;
+        return kv ? C::NK + t % C::NV : t % C::NK;
+      }
+    };
+    uint64_t *const r_full = C::QUANT ? raw_full : full, *const r_empty = C::QUANT ? raw_empty : empty;
     bool ok = true;
     TreeWalker walker(a, &misc->part, lane);
     int npieces = 0;
@@ -509,12 +576,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (isbad) atomicOr(status, PA_DEV_BAD_PAGE);
         }
         const uint32_t bad = __ballot_sync(FULL, isbad);
-        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL, load)) * (uint32_t)((C::NPL * 128) << a.log2_bh);
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL, load)) * (uint32_t)(C::ROWB << a.log2_bh);
 #pragma unroll
         for (int kv = 0; kv < 2 && ok; ++kv) {
-          const int s = kv ? C::NK + t % C::NV : t % C::NK;
-          const uint32_t u = kv ? t / C::NV : t / C::NK;
-          if (u > 0) ok = mbar_wait(&empty[s], (u - 1) & 1, status);
+          uint32_t u;
+          const int s = place(kv, u);
+          if (u > 0) ok = mbar_wait(&r_empty[s], (u - 1) & 1, status);
           ok = __all_sync(FULL, ok);
           if (!ok) break;
           in_flight = kv + 1;
@@ -539,14 +606,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               m.lo_min = lo_min;
               meta[t % C::META] = m;
             }
-            mbar_arrive_expect_tx(&full[s], bytes);
+            mbar_arrive_expect_tx(&r_full[s], bytes);
           }
           __syncwarp();
           if (load) {
-            uint8_t *dst = smem + S::OFF_RING + s * C::SLOT + (lane << a.log2_bh) * 128;
+            if constexpr (C::QUANT) {  // whole rows of codes, one after the other
+              tma_load_4d(smem + S::OFF_RAW + s * C::RAW_SLOT + (lane << a.log2_bh) * C::ROWB, kv ? &tm_v : &tm_k, 0, cur.g,
+                          btok & (P - 1), phys, &r_full[s]);
+            } else {
+              uint8_t *dst = smem + S::OFF_RING + s * C::SLOT + (lane << a.log2_bh) * 128;
 #pragma unroll
-            for (int p = 0; p < C::NPL; ++p)
-              tma_load_4d(dst + p * C::PLANE, kv ? &tm_v : &tm_k, p * 64, cur.g, btok & (P - 1), phys, &full[s]);
+              for (int p = 0; p < C::NPL; ++p)
+                tma_load_4d(dst + p * C::PLANE, kv ? &tm_v : &tm_k, p * 64, cur.g, btok & (P - 1), phys, &full[s]);
+            }
           }
         }
         if (ok) {
@@ -562,19 +634,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     // the end: a record in the place of the next stage, announced in both of its slots
     for (int kv = 0; kv < 2 && ok; ++kv) {
-      const int s = kv ? C::NK + t % C::NV : t % C::NK;
-      const uint32_t u = kv ? t / C::NV : t / C::NK;
-      if (u > 0) ok = __all_sync(FULL, mbar_wait(&empty[s], (u - 1) & 1, status));
+      uint32_t u;
+      const int s = place(kv, u);
+      if (u > 0) ok = __all_sync(FULL, mbar_wait(&r_empty[s], (u - 1) & 1, status));
       if (ok && lane == 0) {
         if (kv == 0) meta[t % C::META].end = 1;
-        mbar_arrive(&full[s]);
+        mbar_arrive(&r_full[s]);
       }
     }
     if (!ok) {  // copies in flight land before the CTA exits
-      const uint32_t nk = t + (in_flight > 0), nv = t + (in_flight > 1);
-      for (uint32_t i = nk > C::NK ? nk - C::NK : 0u; i < nk; ++i) mbar_wait(&full[i % C::NK], (i / C::NK) & 1, status);
-      for (uint32_t i = nv > C::NV ? nv - C::NV : 0u; i < nv; ++i)
-        mbar_wait(&full[C::NK + i % C::NV], (i / C::NV) & 1, status);
+      if constexpr (C::QUANT) {
+        const uint32_t nf_ = 2 * t + (uint32_t)in_flight;
+        for (uint32_t i = nf_ > C::NR ? nf_ - C::NR : 0u; i < nf_; ++i)
+          mbar_wait(&raw_full[i % C::NR], (i / C::NR) & 1, status);
+      } else {
+        const uint32_t nk = t + (in_flight > 0), nv = t + (in_flight > 1);
+        for (uint32_t i = nk > C::NK ? nk - C::NK : 0u; i < nk; ++i) mbar_wait(&full[i % C::NK], (i / C::NK) & 1, status);
+        for (uint32_t i = nv > C::NV ? nv - C::NV : 0u; i < nv; ++i)
+          mbar_wait(&full[C::NK + i % C::NV], (i / C::NV) & 1, status);
+      }
     }
     if (lane == 0) misc->npieces = npieces;
   } else if (warp == 1) {
@@ -640,7 +718,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           break;
         }
         if (first) {
-          ok = mbar_wait(q_full, kq & 1, status);
+          ok = mbar_wait(C::QUANT ? q_conv : q_full, kq & 1, status);
           if (!ok) break;
           ++kq;
           fresh = 3u;
@@ -686,7 +764,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_wait(drain, 0, status);
     }
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (warp == 2 && !C::QUANT) {
     // ------------------------------------------------------------ tokens that not everyone attends to
     for (uint32_t t = 0;; ++t) {
       const int s = C::NK + t % C::NV;
@@ -742,6 +820,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&clean[t % C::META]);
     }
+  } else if (warp == 2) {
+    // (idle: the converting warps look over the V tiles)
   } else if (warp == 3) {
     // ------------------------------------------------------------ query tiles
     TreeWalker walker(a, &misc->part, lane);
@@ -763,12 +843,134 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       ++k;
     }
     if (k > 0) mbar_wait(q_full, (k - 1) & 1, status);  // no copy is in flight when the CTA exits
+  } else if (warp >= 4 + C::SOFTMAX_WARPS) {
+    // ------------------------------------------------------------ codes to f16 operands
+    // Each thread takes 16 codes at a time; a row's threads read one run of bytes, and write the two
+    // 16-byte chunks of the swizzled f16 row in opposite orders in odd planes, so that neither the
+    // reads nor the writes of eight lanes meet in a bank.
+    if constexpr (C::QUANT) {
+      const int ct = tid - (4 + C::SOFTMAX_WARPS) * 32, cw = ct >> 5;
+      constexpr int TPR = D / 16, NTASK = BN * TPR, STEP = C::CONVERT_WARPS * 32;
+      uint32_t kp = 0;  // pieces begun
+      for (uint32_t t = 0;; ++t) {
+        bool end = false, ok = true;
+        for (int kv = 0; kv < 2 && ok && !end; ++kv) {
+          const uint32_t f = 2 * t + kv;
+          const int rs = f % C::NR;
+          ok = __all_sync(FULL, mbar_wait(&raw_full[rs], (f / C::NR) & 1, status));
+          if (!ok) break;
+          const TreeStage &m = meta[t % C::META];
+          end = m.end;
+          if (kv == 0 && !end && m.first) {
+            // the piece's query rows: times 2^s (largest magnitude in [2^14, 2^15)) to f16, in place
+            ok = __all_sync(FULL, mbar_wait(q_full, kp & 1, status));
+            if (!ok) break;
+            int8_t *shift = reinterpret_cast<int8_t *>(smem + S::OFF_SHIFT) + (kp & 1) * (C::QT * kTreeRows);
+            for (int r = ct; r < (m.two ? 2 : 1) * kTreeRows; r += STEP) {
+              uint8_t *row = smem + (r >> 7) * (C::NPL * C::QPLANE) + (r & 127) * 128;
+              float amax = 0.f;
+#pragma unroll 4
+              for (int c = 0; c < C::NPL * 8; ++c) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(row + (c >> 3) * C::QPLANE + (((c & 7) ^ (r & 7)) << 4));
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+              }
+              const int sh = min(max(14 - ((int)(__float_as_uint(amax) >> 23) - 127), -100), 100);
+              const float p2 = __uint_as_float((uint32_t)(sh + 127) << 23);
+              shift[r] = (int8_t)sh;
+#pragma unroll 4
+              for (int c = 0; c < C::NPL * 8; ++c) {
+                uint4 *px = reinterpret_cast<uint4 *>(row + (c >> 3) * C::QPLANE + (((c & 7) ^ (r & 7)) << 4));
+                const uint4 x = *px;
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  h[e] = pack_f16x2(__uint_as_float(w[e] << 16) * p2, __uint_as_float(w[e] & 0xffff0000u) * p2);
+                *px = make_uint4(h[0], h[1], h[2], h[3]);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_conv);
+            ++kp;
+          }
+          const int s = kv ? C::NK + t % C::NV : t % C::NK;
+          const uint32_t u = kv ? t / C::NV : t / C::NK;
+          if (u > 0) ok = __all_sync(FULL, mbar_wait(&empty[s], (u - 1) & 1, status));
+          if (!ok) break;
+          if (end) {  // handed on to the issuing thread
+            if (lane == 0) mbar_arrive(&full[s]);
+            break;
+          }
+          const uint8_t *raw = smem + S::OFF_RAW + rs * C::RAW_SLOT;
+          uint8_t *op = smem + S::OFF_RING + s * C::SLOT;
+          const bool look = kv == 1 && m.masked;
+          const int prefix = m.L - m.n, lo_max = a.window > 0 ? max(m.L - a.window, 0) : 0;
+          uint64_t bad_nodes = 0, bad_edge = 0;
+#pragma unroll 2
+          for (int i = ct; i < NTASK; i += STEP) {
+            const int r = i / TPR, pc = i % TPR;
+            uint32_t h[8];
+            convert16<C::FMT, D>(raw + r * C::ROWB, pc, h);
+            if (look) {
+              const int tok = m.tok0 + r;
+              const bool any = tok >= m.lo_min && tok < m.tok_hi && ((loaded_bits(m.badmask, r >> 5, a.log2_bh) >> (r & 31)) & 1u);
+              if (!any) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[e] = 0u;
+              } else if (tok >= prefix || tok < lo_max) {
+                uint32_t hit = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const uint32_t bits = ((h[e] & 0x7c00u) == 0x7c00u ? 0xffffu : 0u) |
+                                        ((h[e] & 0x7c000000u) == 0x7c000000u ? 0xffff0000u : 0u);
+                  hit |= bits;
+                  h[e] &= ~bits;
+                }
+                if (hit) {
+                  if (tok >= prefix) bad_nodes |= 1ull << (tok - prefix);
+                  else bad_edge |= 1ull << (tok - m.lo_min);
+                }
+              }
+            }
+            uint8_t *row = op + (pc >> 2) * C::PLANE + r * 128;
+            const int c0 = 2 * (pc & 3), sw = (pc >> 2) & 1;
+            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+            *reinterpret_cast<uint4 *>(row + (((c0 + sw) ^ (r & 7)) << 4)) = sw ? hi : lo;
+            *reinterpret_cast<uint4 *>(row + (((c0 + 1 - sw) ^ (r & 7)) << 4)) = sw ? lo : hi;
+          }
+          if (look) {
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) {
+              bad_nodes |= __shfl_xor_sync(FULL, bad_nodes, o);
+              bad_edge |= __shfl_xor_sync(FULL, bad_edge, o);
+            }
+            if (lane == 0) {
+              nf[((t % C::META) * C::CLEAN_WARPS + cw) * 2] = bad_nodes;
+              nf[((t % C::META) * C::CLEAN_WARPS + cw) * 2 + 1] = bad_edge;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full[s]);
+            mbar_arrive(&raw_empty[rs]);
+            if (kv == 1) mbar_arrive(&clean[t % C::META]);
+          }
+        }
+        if (end || !ok) break;
+      }
+    }
   } else {
     // ------------------------------------------------------------ softmax and output
     const int grp = (warp - 4) >> 2;              // softmax group
     const int row = 32 * (warp & 3) + lane;       // row of the tile, lane of the tensor memory
     const uint32_t tl_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    float m_run = -INFINITY, l_run = 0.f;
+    float m_run = -INFINITY, l_run = 0.f, qs = a.qscale;
+    uint32_t kp = 0;  // pieces begun
     uint64_t eff = 0, bad_nodes = 0, bad_edge = 0;
     int lo_row = 0, prefix = 0, node_tok = 0, head = 0, start = 0, n = 0, lo_min = 0, b = 0, slot = -1, g = 0, prow = 0;
     bool real = false, warp_real = false, had = false;  // had: this group's output has had a product in the piece
@@ -787,8 +989,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (masked) {
           if (!mbar_wait(&clean[tt % C::META], (tt / C::META) & 1, status)) return false;
           __syncwarp();
-          bad_nodes |= nf[(tt % C::META) * 2];
-          bad_edge |= nf[(tt % C::META) * 2 + 1];
+#pragma unroll
+          for (int w = 0; w < C::CLEAN_WARPS; ++w) {
+            bad_nodes |= nf[((tt % C::META) * C::CLEAN_WARPS + w) * 2];
+            bad_edge |= nf[((tt % C::META) * C::CLEAN_WARPS + w) * 2 + 1];
+          }
 #pragma unroll
           for (int c = 0; c < BN / 32; ++c) {
             const int base = m.tok0 + 32 * c;
@@ -798,7 +1003,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         // the largest score (the smallest under a negative scale) of the row
         float mx = -INFINITY;
-        const float sgn = a.qscale < 0.f ? -1.f : 1.f;
+        const float sgn = qs < 0.f ? -1.f : 1.f;
 #pragma unroll
         for (int c = 0; c < BN / 32; ++c) {
           float s[32];
@@ -813,7 +1018,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
         }
-        mx = mx == -INFINITY ? mx : mx * fabsf(a.qscale);
+        mx = mx == -INFINITY ? mx : mx * fabsf(qs);
         if (!had) {
           m_run = mx;
         } else if (__any_sync(FULL, real && m_run != -INFINITY && mx > m_run + C::TAU)) {
@@ -847,13 +1052,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            float p0 = fast_exp2(fmaf(s[i], a.qscale, -sub)), p1 = fast_exp2(fmaf(s[i + 1], a.qscale, -sub));
+            float p0 = fast_exp2(fmaf(s[i], qs, -sub)), p1 = fast_exp2(fmaf(s[i + 1], qs, -sub));
             if (masked) {
               p0 = (vis[c] >> i) & 1u ? p0 : 0.f;
               p1 = (vis[c] >> (i + 1)) & 1u ? p1 : 0.f;
             }
             l4[(i >> 1) & 3] += p0 + p1;
-            w[i >> 1] = pack_bf16x2(p0, p1);
+            w[i >> 1] = C::QUANT ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
           }
           tc_st16(tS + 16 * c, w);
         }
@@ -903,6 +1108,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           real = pos < tile.nq && h < tile.nh;
           warp_real = __any_sync(FULL, real);
           prow = tx * kTreeRows + row;
+          if constexpr (C::QUANT) {  // the scores are 2^s times too large
+            const int sh = reinterpret_cast<const int8_t *>(smem + S::OFF_SHIFT)[(kp & 1) * (C::QT * kTreeRows) + prow];
+            qs = a.qscale * __uint_as_float((uint32_t)(127 - sh) << 23);
+          }
+          ++kp;
           head = g * a.G + tile.h0 + h;
           node_tok = start + tile.i0 + pos;
           eff = 0;
@@ -1002,7 +1212,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                   const int tok = (half ? lo_min : prefix) + __ffsll((long long)rest) - 1;
                   const size_t page = (size_t)a.block_table[(size_t)b * a.max_pages_per_seq + (tok >> a.log2_page)];
                   const uint8_t *vr = a.v_pool + (((page << a.log2_page) + (tok & ((1 << a.log2_page) - 1))) * a.Hkv + g) *
-                                                     (size_t)tree_row_bytes<C::FMT, D>();
+                                                     (size_t)C::ROWB;
 #pragma unroll
                   for (int i = 0; i < 32; ++i) {
                     const float x = cache_value<C::FMT, D>(vr, c + i);
