@@ -36,9 +36,8 @@
 //   * FP8 and NVFP4 pools: the tiles of codes land in a ring of their own, and four more warps convert
 //     them to f16 operands (exact), and the query rows, scaled by a power of two each, in place; they
 //     then do warp 2's work too.  The weights are rounded to f16 (2^-11);
-//   * two groups of four warps: one thread per score row.  The scores are read twice from tensor
-//     memory, 32 columns at a time (once for the maximum, once for the weights): a second read is
-//     cheaper than 128 live registers.
+//   * two groups of four warps: one thread per score row.  64 columns of the row are in registers at a
+//     time, the ones behind them are read from tensor memory again once the maximum is known.
 // Tensor memory: scores (then weights) x at BN x, outputs at 256.  At head_dim 256 one output fills the
 // rest: one tile, one softmax group, stages of 64 tokens.
 #pragma once
@@ -114,6 +113,13 @@ struct TreeCfg {
   static constexpr uint32_t IDESC_S = tc_idesc_bf16(kTreeRows, BN, false) & ~IDESC_F16;
   static constexpr uint32_t IDESC_PV = tc_idesc_bf16(kTreeRows, D, true) & ~IDESC_F16;
   static constexpr float TAU = 8.f;
+  // registers a thread: the softmax warps' 64 scores and their row's state do not fit the launch's share
+  // (384 x 168 or 512 x 128), so the other warps hand some over
+  static constexpr bool REG_SPLIT = GROUPS == 2;
+  static constexpr int REGS = QUANT ? 128 : 168;
+  static constexpr int REGS_CONTROL = QUANT ? 80 : 88, REGS_SOFTMAX = QUANT ? 160 : 208, REGS_CONVERT = 104;
+  static_assert(!REG_SPLIT || 128 * REGS_CONTROL + 256 * REGS_SOFTMAX + (QUANT ? 128 * REGS_CONVERT : 0) <= THREADS * REGS,
+                "the register split stays within the launch's registers");
   static constexpr int META = 8;  // stage records kept: a record is rewritten eight stages later, once the
                                   // K tile of at least three stages later is free
   static_assert(QUANT ? NR >= 4 && NK >= 1 && NR / 2 + NK <= 6 : NK >= 2 && NK <= 5, "rings of two stages, within the records");
@@ -404,28 +410,36 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // Values 16 pc .. 16 pc + 15 of a row of codes as f16 pairs, without the pool's scale: exact (an E2M1 value
 // times an E4M3 block scale has at most six significant bits and lies in [2^-10, 2688]).
 template <int FMT, int D>
-__device__ __forceinline__ void convert16(const uint8_t *row, int pc, uint32_t (&h)[8]) {
-  if constexpr (FMT == TREE_FP8) {
-    const uint4 x = *reinterpret_cast<const uint4 *>(row + 16 * pc);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
-      h[e] = (uint32_t)r.x | ((uint32_t)r.y << 16);
-    }
-  } else if constexpr (FMT == TREE_NVFP4) {
-    const uint2 x = *reinterpret_cast<const uint2 *>(row + 8 * pc);
-    const __half_raw b = __nv_cvt_fp8_to_halfraw(row[D / 2 + pc], __NV_E4M3);
-    const __half2 by = __half2half2(*reinterpret_cast<const __half *>(&b));
-    const uint32_t w[2] = {x.x, x.y};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const __half2_raw r = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[e >> 2] >> (8 * (e & 3))), __NV_E2M1);
-      const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&r), by);
-      h[e] = *reinterpret_cast<const uint32_t *>(&v);
+struct Codes16 {
+  uint4 x;
+  __device__ __forceinline__ void load(const uint8_t *row, int pc) {
+    if constexpr (FMT == TREE_FP8) {
+      x = *reinterpret_cast<const uint4 *>(row + 16 * pc);
+    } else {
+      const uint2 c = *reinterpret_cast<const uint2 *>(row + 8 * pc);
+      x = make_uint4(c.x, c.y, row[D / 2 + pc], 0u);
     }
   }
-}
+  __device__ __forceinline__ void convert(uint32_t (&h)[8]) const {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if constexpr (FMT == TREE_FP8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
+        h[e] = (uint32_t)r.x | ((uint32_t)r.y << 16);
+      }
+    } else {
+      const __half_raw b = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)w[2], __NV_E4M3);
+      const __half2 by = __half2half2(*reinterpret_cast<const __half *>(&b));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const __half2_raw r = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[e >> 2] >> (8 * (e & 3))), __NV_E2M1);
+        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&r), by);
+        h[e] = *reinterpret_cast<const uint32_t *>(&v);
+      }
+    }
+  }
+};
 
 // The low k bits (k clamped to [0, 32]).
 __device__ __forceinline__ uint32_t low_bits(int k) { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u; }
@@ -450,6 +464,70 @@ __device__ __forceinline__ uint32_t loaded_bits(uint32_t badmask, int c, int log
   for (int k = 0; k < per; ++k)
     if (!((badmask >> (c * per + k)) & 1u)) ok |= low_bits(1 << log2_bh) << (k << log2_bh);
   return ok;
+}
+
+// ---------------------------------------------------------------------------------------- tensor memory
+// Warp-wide: lane l reads consecutive columns of tensor-memory lane (taddr.lane + l).  The wait is part of
+// the statement: no use of the values can be moved before it.
+__device__ __forceinline__ void tree_ld(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64+32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 32 columns at each of two addresses.
+__device__ __forceinline__ void tree_ld_pair(uint32_t ta, uint32_t tb, float (&v)[32], float (&u)[32]) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(ta), "r"(tb));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v[i] = __uint_as_float(r[i]);
+    u[i] = __uint_as_float(r[32 + i]);
+  }
+}
+// Pairs of fp32 in one instruction: a * b + c, and a + b.
+__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 // ---------------------------------------------------------------------------------------- the kernel
@@ -511,6 +589,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   pdl_launch_dependents();  // the combine kernel may be scheduled; it waits for this grid to finish
   tree_partition<C::THREADS>(a, &misc->part, status);
 
+  if (warp < 4) {
+  if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_CONTROL>();
   if (warp == 0) {
     // ------------------------------------------------------------ K and V tiles
     const int nbox = BN >> a.log2_bh, P = 1 << a.log2_page;
@@ -843,7 +923,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       ++k;
     }
     if (k > 0) mbar_wait(q_full, (k - 1) & 1, status);  // no copy is in flight when the CTA exits
+  }
   } else if (warp >= 4 + C::SOFTMAX_WARPS) {
+    if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_CONVERT>();
     // ------------------------------------------------------------ codes to f16 operands
     // Each thread takes 16 codes at a time; a row's threads read one run of bytes, and write the two
     // 16-byte chunks of the swizzled f16 row in opposite orders in odd planes, so that neither the
@@ -851,6 +933,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if constexpr (C::QUANT) {
       const int ct = tid - (4 + C::SOFTMAX_WARPS) * 32, cw = ct >> 5;
       constexpr int TPR = D / 16, NTASK = BN * TPR, STEP = C::CONVERT_WARPS * 32;
+      static_assert(NTASK % (4 * STEP) == 0 && STEP % TPR == 0, "whole rounds of four tasks");
       uint32_t kp = 0;  // pieces begun
       for (uint32_t t = 0;; ++t) {
         bool end = false, ok = true;
@@ -910,13 +993,36 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const bool look = kv == 1 && m.masked;
           const int prefix = m.L - m.n, lo_max = a.window > 0 ? max(m.L - a.window, 0) : 0;
           uint64_t bad_nodes = 0, bad_edge = 0;
-#pragma unroll 2
-          for (int i = ct; i < NTASK; i += STEP) {
-            const int r = i / TPR, pc = i % TPR;
-            uint32_t h[8];
-            convert16<C::FMT, D>(raw + r * C::ROWB, pc, h);
-            if (look) {
-              const int tok = m.tok0 + r;
+          auto put = [&](int r, int pc, const uint32_t (&h)[8]) {
+            uint8_t *row = op + (pc >> 2) * C::PLANE + r * 128;
+            const int c0 = 2 * (pc & 3), sw = (pc >> 2) & 1;
+            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+            *reinterpret_cast<uint4 *>(row + (((c0 + sw) ^ (r & 7)) << 4)) = sw ? hi : lo;
+            *reinterpret_cast<uint4 *>(row + (((c0 + 1 - sw) ^ (r & 7)) << 4)) = sw ? lo : hi;
+          };
+          // a thread's tasks lie STEP / TPR rows apart, at the same place of the row; four loads in flight
+          const int pc = ct % TPR, r0 = ct / TPR;
+          if (!look) {
+#pragma unroll 1
+            for (int i0 = 0; i0 < NTASK / STEP; i0 += 4) {
+              Codes16<C::FMT, D> x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e].load(raw + (r0 + (i0 + e) * (STEP / TPR)) * C::ROWB, pc);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t h[8];
+                x[e].convert(h);
+                put(r0 + (i0 + e) * (STEP / TPR), pc, h);
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < NTASK / STEP; ++i) {
+              const int r = r0 + i * (STEP / TPR), tok = m.tok0 + r;
+              Codes16<C::FMT, D> x;
+              uint32_t h[8];
+              x.load(raw + r * C::ROWB, pc);
+              x.convert(h);
               const bool any = tok >= m.lo_min && tok < m.tok_hi && ((loaded_bits(m.badmask, r >> 5, a.log2_bh) >> (r & 31)) & 1u);
               if (!any) {
 #pragma unroll
@@ -935,12 +1041,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                   else bad_edge |= 1ull << (tok - m.lo_min);
                 }
               }
+              put(r, pc, h);
             }
-            uint8_t *row = op + (pc >> 2) * C::PLANE + r * 128;
-            const int c0 = 2 * (pc & 3), sw = (pc >> 2) & 1;
-            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-            *reinterpret_cast<uint4 *>(row + (((c0 + sw) ^ (r & 7)) << 4)) = sw ? hi : lo;
-            *reinterpret_cast<uint4 *>(row + (((c0 + 1 - sw) ^ (r & 7)) << 4)) = sw ? lo : hi;
           }
           if (look) {
 #pragma unroll
@@ -965,11 +1067,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
     }
   } else {
+    if constexpr (C::REG_SPLIT) setmaxnreg_inc<C::REGS_SOFTMAX>();
     // ------------------------------------------------------------ softmax and output
     const int grp = (warp - 4) >> 2;              // softmax group
     const int row = 32 * (warp & 3) + lane;       // row of the tile, lane of the tensor memory
     const uint32_t tl_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    float m_run = -INFINITY, l_run = 0.f, qs = a.qscale;
+    // scores s to exponents s' * qs - m with qs > 0: s' = s * flip
+    const float flip = a.qscale > 0.f ? 1.f : a.qscale < 0.f ? -1.f : 0.f, scale = a.qscale != 0.f ? fabsf(a.qscale) : 1.f;
+    float m_run = -INFINITY, l_run = 0.f, qs = scale;
     uint32_t kp = 0;  // pieces begun
     uint64_t eff = 0, bad_nodes = 0, bad_edge = 0;
     int lo_row = 0, prefix = 0, node_tok = 0, head = 0, start = 0, n = 0, lo_min = 0, b = 0, slot = -1, g = 0, prow = 0;
@@ -1001,24 +1106,28 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                      loaded_bits(m.badmask, c, a.log2_bh);
           }
         }
-        // the largest score (the smallest under a negative scale) of the row
-        float mx = -INFINITY;
-        const float sgn = qs < 0.f ? -1.f : 1.f;
+        // 64 columns of the row (those from 64 h on): read, turned, masked; returns their maximum
+        auto read = [&](int h, float (&s)[64]) -> float {
+          tree_ld(tS + 64 * h, s);
+          if (flip != 1.f) {  // a scale that is not positive
 #pragma unroll
-        for (int c = 0; c < BN / 32; ++c) {
-          float s[32];
-          tc_ld32(tS + 32 * c, s);
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            for (int i = 0; i < 64; ++i) s[i] *= flip;
+          }
           if (masked) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], (vis[c] >> i) & 1u ? s[i] * sgn : -INFINITY);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], s[i] * sgn);
+            for (int i = 0; i < 64; ++i) s[i] = (vis[2 * h + i / 32] >> (i % 32)) & 1u ? s[i] : -INFINITY;
           }
-          mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-        }
-        mx = mx == -INFINITY ? mx : mx * fabsf(qs);
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 64; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(s[i + e], s[i + 4 + e]));
+          return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        };
+        float s[64], mx = -INFINITY;
+        if constexpr (BN == 128) mx = read(1, s);
+        mx = fmaxf(mx, read(0, s));
+        mx *= qs;
         if (!had) {
           m_run = mx;
         } else if (__any_sync(FULL, real && m_run != -INFINITY && mx > m_run + C::TAU)) {
@@ -1044,25 +1153,29 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           m_run = mx;  // nothing attended to so far: the output is zero
         }
         const float sub = m_run == -INFINITY ? 0.f : m_run;
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 q2 = make_float2(qs, qs), sub2 = make_float2(-sub, -sub);
+        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        auto weigh = [&](int h) {  // the weights of the columns in s, packed, over the columns from 32 h on
 #pragma unroll
-        for (int c = 0; c < BN / 32; ++c) {
-          float s[32];
-          tc_ld32(tS + 32 * c, s);
-          uint32_t w[16];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float p0 = fast_exp2(fmaf(s[i], qs, -sub)), p1 = fast_exp2(fmaf(s[i + 1], qs, -sub));
-            if (masked) {
-              p0 = (vis[c] >> i) & 1u ? p0 : 0.f;
-              p1 = (vis[c] >> (i + 1)) & 1u ? p1 : 0.f;
+            for (int i = 0; i < 32; i += 2) {
+              const float2 y = fma_pair(make_float2(s[32 * c + i], s[32 * c + i + 1]), q2, sub2);
+              const float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+              l2[(i >> 1) & 1] = add_pair(l2[(i >> 1) & 1], pr);
+              w[i >> 1] = C::QUANT ? pack_f16x2(pr.x, pr.y) : pack_bf16x2(pr.x, pr.y);
             }
-            l4[(i >> 1) & 3] += p0 + p1;
-            w[i >> 1] = C::QUANT ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+            tc_st16(tS + 32 * h + 16 * c, w);
           }
-          tc_st16(tS + 16 * c, w);
+        };
+        weigh(0);
+        if constexpr (BN == 128) {
+          read(1, s);
+          weigh(1);
         }
-        l_run += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        l2[0] = add_pair(l2[0], l2[1]);
+        l_run += l2[0].x + l2[0].y;
         tc_wait_st();
       }
       had = true;
@@ -1110,7 +1223,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           prow = tx * kTreeRows + row;
           if constexpr (C::QUANT) {  // the scores are 2^s times too large
             const int sh = reinterpret_cast<const int8_t *>(smem + S::OFF_SHIFT)[(kp & 1) * (C::QT * kTreeRows) + prow];
-            qs = a.qscale * __uint_as_float((uint32_t)(127 - sh) << 23);
+            qs = scale * __uint_as_float((uint32_t)(127 - sh) << 23);
           }
           ++kp;
           head = g * a.G + tile.h0 + h;
@@ -1195,32 +1308,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (warp_real) {
 #pragma unroll 1
         for (int c = c0; c < c1; c += 32) {
-          float v[32];
-          tc_ld32(tl_base + C::TM_O + o * D + c, v);
+          float v[32], u[32];
+          if (merge) {
+            tree_ld_pair(tl_base + C::TM_O + o * D + c, tl_base + C::TM_O + (o ^ 1) * D + c, v, u);
+          } else {
+            tc_ld32(tl_base + C::TM_O + o * D + c, v);
+          }
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = use_own ? v[i] * s_own : 0.f;
           if (merge) {
-            float u[32];
-            tc_ld32(tl_base + C::TM_O + (o ^ 1) * D + c, u);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = use_oth ? fmaf(u[i], s_oth, v[i]) : v[i];
           }
           if (real) {
-            if (hit_nodes | hit_edge) {
-              for (int half = 0; half < 2; ++half) {
-                for (uint64_t rest = half ? hit_edge : hit_nodes; rest; rest &= rest - 1) {
-                  const int tok = (half ? lo_min : prefix) + __ffsll((long long)rest) - 1;
-                  const size_t page = (size_t)a.block_table[(size_t)b * a.max_pages_per_seq + (tok >> a.log2_page)];
-                  const uint8_t *vr = a.v_pool + (((page << a.log2_page) + (tok & ((1 << a.log2_page) - 1))) * a.Hkv + g) *
-                                                     (size_t)C::ROWB;
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) {
-                    const float x = cache_value<C::FMT, D>(vr, c + i);
-                    if (!isfinite(x)) v[i] += x;
-                  }
-                }
-              }
-            }
             if (slot < 0) {
 #pragma unroll
               for (int i = 0; i < 32; i += 8)
@@ -1231,6 +1331,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
                 *reinterpret_cast<float4 *>(po + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+          }
+        }
+        if (real && (hit_nodes | hit_edge)) {
+          // (rare) their infinities and NaN, added to what this thread has just written
+          for (int half = 0; half < 2; ++half) {
+            for (uint64_t rest = half ? hit_edge : hit_nodes; rest; rest &= rest - 1) {
+              const int tok = (half ? lo_min : prefix) + __ffsll((long long)rest) - 1;
+              const size_t page = (size_t)a.block_table[(size_t)b * a.max_pages_per_seq + (tok >> a.log2_page)];
+              const uint8_t *vr =
+                  a.v_pool + (((page << a.log2_page) + (tok & ((1 << a.log2_page) - 1))) * a.Hkv + g) * (size_t)C::ROWB;
+#pragma unroll 1
+              for (int d = c0; d < c1; ++d) {
+                const float x = cache_value<C::FMT, D>(vr, d);
+                if (isfinite(x)) continue;
+                if (slot < 0) orow[d] = (uint16_t)pack_bf16x2(__uint_as_float((uint32_t)orow[d] << 16) + x, 0.f);
+                else po[d] += x;
+              }
             }
           }
         }
