@@ -11,7 +11,8 @@ Names follow the C ABI: ``pa_workspace_size``, ``pa_decode_gqa``,
 ``pa_qk_norm_rope_write``, ``pa_qk_norm_rope_write_fp8``, ``pa_qk_norm_rope_write_nvfp4``, ``pa_tree_gqa``, ``pa_tree_gqa_fp8``,
 ``pa_tree_gqa_nvfp4``, ``pa_tree_workspace_size``, ``pa_kv_compact``, ``pa_status_string``, ``pa_read_device_status``,
 ``pa_set_profile_events``, ``pa_last_launch_count``, ``pa_set_wait_limit_ns``, ``pa_last_cuda_error``,
-``pa_last_cuda_error_string``.  The tensor-taking
+``pa_last_cuda_error_string``.  The operators of tree drafting are called through a compiled module that
+checks their tensors (``csrc/pa_binding.cpp``).  The tensor-taking
 functions accept torch tensors (device memory, the layouts of the header) and
 infer every size from their shapes.
 """
@@ -22,6 +23,7 @@ import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libpa_decode.so")
+BINDING_PATH = os.path.join(_HERE, "_lib", "pa_binding.so")
 
 PA_OK = 0
 PA_ERR_INVALID_ARGUMENT = -1
@@ -281,29 +283,31 @@ def _refuse(what: str, why: str):
     raise err
 
 
-def _arrays(what: str, device, **arrays):
-    """Refuses (PaError) an array argument that is not (tensor, dtype, shape): a dense tensor of that
-    type and shape on `device`.  None stands for an optional argument that was not given."""
-    for name, want in arrays.items():
-        if want is None:
-            continue
-        t, dtype, shape = want
-        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
-            _refuse(what, f"{name} has to be a dense {dtype} tensor of shape {tuple(shape)} on {device}; it is "
-                          f"{t.dtype} {tuple(t.shape)}, strides {tuple(t.stride())}, on {t.device}")
+_native_module = None
 
 
-def _launch(what: str, device, stream, call) -> None:
-    """`call(stream handle)` with the tensors' device current (a stream that is not given is that
-    device's current one)."""
-    import torch
-    if device.type != "cuda":
-        _refuse(what, f"the tensors are on {device}, not on a GPU")
-    if device.index == torch.cuda.current_device():
-        _check(call(_stream(stream)), what)
-    else:
-        with torch.cuda.device(device):
-            _check(call(_stream(stream)), what)
+def _native():
+    """The compiled calls (csrc/pa_binding.cpp), loaded at the first one: they need torch."""
+    global _native_module
+    if _native_module is None:
+        import importlib.machinery
+        import importlib.util
+        import torch  # noqa: F401  (its libraries are the module's)
+        if not os.path.exists(BINDING_PATH):
+            raise ImportError(f"{BINDING_PATH} is not built; run `python paged_kv_attention_19_gb300/build.py`")
+        loader = importlib.machinery.ExtensionFileLoader("pa_binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("pa_binding", loader))
+        loader.exec_module(module)
+        _native_module = module
+    return _native_module
+
+
+def _done(what: str, answer) -> None:
+    """The answer of a compiled call: None, a status, or what is wrong with an argument."""
+    if answer is not None:
+        if isinstance(answer, str):
+            _refuse(what, answer)
+        raise PaError(answer, what)
 
 
 def pa_plan_step(context_lens, new_lens, held_pages, free_list, free_count, block_table, query_start, slot_mapping,
@@ -316,56 +320,12 @@ def pa_plan_step(context_lens, new_lens, held_pages, free_list, free_count, bloc
     int32 and tree_mask [max_tokens] int64 (the 64 mask bits) go together: drafted trees.  The _out
     arrays default to their inputs (updated in place).  status: optional int32 device word that gets
     PA_DEV_* bits (rows that found no pages: PA_DEV_NO_PAGES, their slots are -1)."""
-    import torch
-    i32, what, dev = torch.int32, "pa_plan_step", context_lens.device
-    B, T, N = context_lens.shape[0], positions.shape[0], free_list.shape[0]
-    lens_out = context_lens if context_lens_out is None else context_lens_out
-    held_out = held_pages if held_pages_out is None else held_pages_out
-    count_out = free_count if free_count_out is None else free_count_out
-    if block_table.dim() != 2:
-        _refuse(what, "block_table has to have two dimensions")
-    W = block_table.shape[1]
-    _arrays(what, dev, context_lens=(context_lens, i32, (B,)), new_lens=(new_lens, i32, (B,)),
-            held_pages=(held_pages, i32, (B,)), free_list=(free_list, i32, (N,)), free_count=(free_count, i32, (1,)),
-            block_table=(block_table, i32, (B, W)), context_lens_out=(lens_out, i32, (B,)),
-            held_pages_out=(held_out, i32, (B,)), free_count_out=(count_out, i32, (1,)),
-            query_start=(query_start, i32, (B + 1,)), slot_mapping=(slot_mapping, torch.int64, (T,)),
-            positions=(positions, i32, (T,)), parents=parents is not None and (parents, i32, (T,)) or None,
-            tree_mask=tree_mask is not None and (tree_mask, torch.int64, (T,)) or None,
-            status=status is not None and (status, i32, (1,)) or None)
-    _launch(what, dev, stream, lambda st: lib.pa_plan_step(
-        _ptr(context_lens), _ptr(new_lens), _ptr(held_pages), _ptr(free_list), _ptr(free_count), _ptr(parents),
-        _ptr(block_table), _ptr(lens_out), _ptr(held_out), _ptr(count_out), _ptr(query_start), _ptr(slot_mapping),
-        _ptr(positions), _ptr(tree_mask), B, page_size, N, W, T, _ptr(status), st))
-
-
-def _qk_norm_rope_write(what, q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping, q_out, k_pool, v_pool, eps,
-                        interleaved, kind, width, scales, status, stream):
-    import torch
-    bf16, dev = torch.bfloat16, q.device
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    for name, t, heads in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
-        if t.dtype is not bf16 or t.shape != (T, heads, D) or t.device != dev or t.stride(2) != 1 or t.stride(1) != D:
-            _refuse(what, f"{name} has to be a bfloat16 tensor of shape {(T, heads, D)} on {dev} whose heads are dense; "
-                          f"it is {t.dtype} {tuple(t.shape)}, strides {tuple(t.stride())}, on {t.device}")
-    N, P, rot, R = k_pool.shape[0], k_pool.shape[1], cos_sin.shape[1], width(D)
-    _arrays(what, dev, q_weight=q_weight is not None and (q_weight, bf16, (D,)) or None,
-            k_weight=k_weight is not None and (k_weight, bf16, (D,)) or None,
-            cos_sin=(cos_sin, torch.float32, (cos_sin.shape[0], rot)), positions=(positions, torch.int32, (T,)),
-            slot_mapping=(slot_mapping, torch.int64, (T,)), q_out=(q_out, bf16, (T, Hq, D)),
-            k_pool=(k_pool, kind, (N, P, Hkv, R)), v_pool=(v_pool, kind, (N, P, Hkv, R)),
-            status=status is not None and (status, torch.int32, (1,)) or None)
-    call = getattr(lib, what)
-    _launch(what, dev, stream, lambda st: call(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), _ptr(positions), _ptr(slot_mapping),
-        _ptr(q_out), _ptr(k_pool), _ptr(v_pool), T, Hq, Hkv, D, _step(q, Hq * D), _step(k, Hkv * D), _step(v, Hkv * D),
-        rot, 1 if interleaved else 0, cos_sin.shape[0], eps, *scales, P, N, _ptr(status), st))
-
-
-def _step(t, dense: int) -> int:
-    """Values from one token to the next (a single token's stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else dense
+    _done("pa_plan_step", (_native_module or _native()).plan_step(
+        context_lens, new_lens, held_pages, free_list, free_count, block_table,
+        context_lens if context_lens_out is None else context_lens_out,
+        held_pages if held_pages_out is None else held_pages_out,
+        free_count if free_count_out is None else free_count_out, query_start, slot_mapping, positions, parents,
+        tree_mask, status, page_size, stream))
 
 
 def pa_qk_norm_rope_write(q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping, q_out, k_pool, v_pool, *,
@@ -375,56 +335,33 @@ def pa_qk_norm_rope_write(q, k, v, q_weight, k_weight, cos_sin, positions, slot_
     norm); cos_sin [max_position, rot_dim] fp32 (cosines, then sines); positions [T] int32; slot_mapping
     [T] int64 (negative: padding, nothing written); q_out [T, Hq, D] bf16; pools [pages, P, Hkv, D] bf16;
     status: optional int32 device word for PA_DEV_* bits."""
-    import torch
-    _qk_norm_rope_write("pa_qk_norm_rope_write", q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping, q_out,
-                        k_pool, v_pool, eps, interleaved, torch.bfloat16, int, (), status, stream)
+    _done("pa_qk_norm_rope_write", (_native_module or _native()).qk_norm_rope_write(
+        0, q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping, q_out, k_pool, v_pool, status, eps,
+        interleaved, 1.0, 1.0, stream))
 
 
 def pa_qk_norm_rope_write_fp8(q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping, q_out, k_pool, v_pool, *,
                               k_scale: float, v_scale: float, eps: float = 1e-6, interleaved: bool = False,
                               status=None, stream=None) -> None:
     """The same into FP8 pools [pages, P, Hkv, D] uint8 (E4M3 codes of value / scale)."""
-    import torch
-    _qk_norm_rope_write("pa_qk_norm_rope_write_fp8", q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping,
-                        q_out, k_pool, v_pool, eps, interleaved, torch.uint8, int, (k_scale, v_scale), status, stream)
+    _done("pa_qk_norm_rope_write_fp8", (_native_module or _native()).qk_norm_rope_write(
+        1, q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping, q_out, k_pool, v_pool, status, eps,
+        interleaved, k_scale, v_scale, stream))
 
 
 def pa_qk_norm_rope_write_nvfp4(q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping, q_out, k_pool, v_pool,
                                 *, k_scale: float, v_scale: float, eps: float = 1e-6, interleaved: bool = False,
                                 status=None, stream=None) -> None:
     """The same into NVFP4 pools [pages, P, Hkv, nvfp4_row_bytes(D)] uint8."""
-    import torch
-    _qk_norm_rope_write("pa_qk_norm_rope_write_nvfp4", q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping,
-                        q_out, k_pool, v_pool, eps, interleaved, torch.uint8, nvfp4_row_bytes, (k_scale, v_scale),
-                        status, stream)
+    _done("pa_qk_norm_rope_write_nvfp4", (_native_module or _native()).qk_norm_rope_write(
+        2, q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping, q_out, k_pool, v_pool, status, eps,
+        interleaved, k_scale, v_scale, stream))
 
 
 def pa_tree_workspace_size(batch: int, max_query: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                            max_context_len: int, page_size: int, num_splits: int = 0) -> int:
     return int(lib.pa_tree_workspace_size(batch, max_query, num_q_heads, num_kv_heads, head_dim, max_context_len,
                                           page_size, num_splits))
-
-
-def _tree(what, q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, max_query, scale, kind,
-          width, scales, workspace, window, num_splits, max_context_len, stream):
-    import torch
-    dev, i32 = q.device, torch.int32
-    T, Hq, D = q.shape
-    N, P, Hkv, _ = k_pool.shape
-    B, W = block_table.shape
-    R = width(D)
-    _arrays(what, dev, q=(q, torch.bfloat16, (T, Hq, D)), k_pool=(k_pool, kind, (N, P, Hkv, R)),
-            v_pool=(v_pool, kind, (N, P, Hkv, R)), block_table=(block_table, i32, (B, W)),
-            context_lens=(context_lens, i32, (B,)), query_start=(query_start, i32, (B + 1,)),
-            tree_mask=(tree_mask, torch.int64, (T,)), out=(out, torch.bfloat16, (T, Hq, D)),
-            lse=lse is not None and (lse, torch.float32, (T, Hq)) or None,
-            workspace=(workspace, workspace.dtype, workspace.shape))
-    call = getattr(lib, what)
-    most = W * P if max_context_len is None else max_context_len
-    _launch(what, dev, stream, lambda st: call(
-        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(context_lens), _ptr(query_start), _ptr(tree_mask),
-        _ptr(out), _ptr(lse), B, T, max_query, Hq, Hkv, D, P, N, W, most, scale, *scales, window, num_splits,
-        _ptr(workspace), workspace.numel() * workspace.element_size(), st))
 
 
 def pa_tree_gqa(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse=None, *, max_query: int,
@@ -435,28 +372,27 @@ def pa_tree_gqa(q, k_pool, v_pool, block_table, context_lens, query_start, tree_
     int64: bit j set if the node attends to its row's node j; context_lens [B] int32 count the nodes;
     out [T, Hq, D] bf16 and lse [T, Hq] fp32 or None (tokens behind the last row stay as they were);
     pools and block_table as for pa_decode_gqa; workspace: workspace_for_tree(...)."""
-    import torch
-    _tree("pa_tree_gqa", q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, max_query,
-          scale, torch.bfloat16, int, (), workspace, window, num_splits, max_context_len, stream)
+    _done("pa_tree_gqa", (_native_module or _native()).tree_gqa(
+        0, q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, workspace, max_query,
+        scale, 1.0, 1.0, window, num_splits, max_context_len, stream))
 
 
 def pa_tree_gqa_fp8(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse=None, *,
                     max_query: int, scale: float, k_scale: float, v_scale: float, workspace, window: int = 0,
                     num_splits: int = 0, max_context_len=None, stream=None) -> None:
     """The same over FP8 E4M3 pools [pages, P, Hkv, D] uint8."""
-    import torch
-    _tree("pa_tree_gqa_fp8", q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, max_query,
-          scale, torch.uint8, int, (k_scale, v_scale), workspace, window, num_splits, max_context_len, stream)
+    _done("pa_tree_gqa_fp8", (_native_module or _native()).tree_gqa(
+        1, q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, workspace, max_query,
+        scale, k_scale, v_scale, window, num_splits, max_context_len, stream))
 
 
 def pa_tree_gqa_nvfp4(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse=None, *,
                       max_query: int, scale: float, k_scale: float, v_scale: float, workspace, window: int = 0,
                       num_splits: int = 0, max_context_len=None, stream=None) -> None:
     """The same over NVFP4 pools [pages, P, Hkv, nvfp4_row_bytes(D)] uint8."""
-    import torch
-    _tree("pa_tree_gqa_nvfp4", q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse,
-          max_query, scale, torch.uint8, nvfp4_row_bytes, (k_scale, v_scale), workspace, window, num_splits,
-          max_context_len, stream)
+    _done("pa_tree_gqa_nvfp4", (_native_module or _native()).tree_gqa(
+        2, q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, workspace, max_query,
+        scale, k_scale, v_scale, window, num_splits, max_context_len, stream))
 
 
 def pa_kv_compact(k_pool, v_pool, block_table, context_lens, query_start, accepted, num_accepted, *, context_lens_out,
@@ -465,22 +401,9 @@ def pa_kv_compact(k_pool, v_pool, block_table, context_lens, query_start, accept
     L - n_b + i, in every layer.  Pools [pages, P, Hkv, R] or [layers, pages, P, Hkv, R] of any format;
     accepted [B, max_accepted] int32 ascending; num_accepted [B] int32; context_lens_out [B] int32 (not
     context_lens itself) gets L - n_b + num_accepted."""
-    import torch
-    what, dev, i32 = "pa_kv_compact", k_pool.device, torch.int32
-    if k_pool.dim() not in (4, 5) or accepted.dim() != 2 or block_table.dim() != 2:
-        _refuse(what, "pools have four or five dimensions, accepted and block_table two")
-    N, P, Hkv, R = k_pool.shape[-4:]
-    B, W = block_table.shape
-    M = accepted.shape[1]
-    _arrays(what, dev, k_pool=(k_pool, k_pool.dtype, k_pool.shape), v_pool=(v_pool, k_pool.dtype, k_pool.shape),
-            block_table=(block_table, i32, (B, W)), context_lens=(context_lens, i32, (B,)),
-            query_start=(query_start, i32, (B + 1,)), accepted=(accepted, i32, (B, M)),
-            num_accepted=(num_accepted, i32, (B,)), context_lens_out=(context_lens_out, i32, (B,)),
-            status=status is not None and (status, i32, (1,)) or None)
-    _launch(what, dev, stream, lambda st: lib.pa_kv_compact(
-        _ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(context_lens), _ptr(query_start), _ptr(accepted),
-        _ptr(num_accepted), _ptr(context_lens_out), k_pool.shape[0] if k_pool.dim() == 5 else 1, B, M,
-        Hkv * R * k_pool.element_size(), P, N, W, _ptr(status), st))
+    _done("pa_kv_compact", (_native_module or _native()).kv_compact(
+        k_pool, v_pool, block_table, context_lens, query_start, accepted, num_accepted, context_lens_out, status,
+        stream))
 
 
 def pa_read_device_status(workspace, stream=None) -> int:

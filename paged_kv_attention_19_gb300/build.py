@@ -1,5 +1,6 @@
 """Build step of the CUDA library: compiles csrc/*.cu for sm_103a in parallel and
-links them into paged_kv_attention_19_gb300/_lib/libpa_decode.so (in-tree).
+links them into paged_kv_attention_19_gb300/_lib/libpa_decode.so (in-tree), and
+csrc/pa_binding.cpp (torch tensors) into _lib/pa_binding.so beside it.
 
 Run ``python paged_kv_attention_19_gb300/build.py`` (a script: importing the package
 needs the library to exist) or call ``build()``.  The
@@ -22,6 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIB_DIR, "libpa_decode.so")
+BINDING_SRC = os.path.join(CSRC, "pa_binding.cpp")
+BINDING = os.path.join(LIB_DIR, "pa_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", INCLUDE, "-I", CSRC]
@@ -43,15 +46,44 @@ def _sources():
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return _sources() + [BINDING_SRC] + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
                                + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _compile_binding() -> str:
+    """Object of the tensor binding; the include paths come from the torch it is built for."""
+    import importlib.util
+    import sysconfig
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    obj = os.path.join(OBJ_DIR, "pa_binding.o")
+    cuda_include = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-isystem", cuda_include, "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(BINDING_SRC)}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import importlib.util
+    torch_lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", LIB_DIR, "-l:libpa_decode.so", "-Wl,-rpath,$ORIGIN", "-L", torch_lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -72,14 +104,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout, r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 
