@@ -58,10 +58,10 @@ struct TreeArgs {
   const uint64_t *tree_mask;
   uint16_t *out;
   float *lse;           // or null
-  uint32_t *desc;       // [nparts] PA_DEV_* bits of each CTA
+  struct TreeDesc *desc;  // [nparts]
   float *part_o;        // [nparts, 2, QT * 128, D]
   float *part_lse;      // [nparts, 2, QT * 128], log2 units
-  int32_t *seq_first, *seq_last;  // [batch, hs]: -1 whole; 2 x CTA + slot of the first piece / CTA of the last
+  int32_t *seq_last;    // [batch, hs]: CTA of the last piece of a sequence that several share
   struct TreeHalf *halves;        // [nparts, 2, 128]: the groups' halves of a one-tile piece
   int batch, tokens, max_query, Hq, Hkv, G;
   int gt, qt, nsub;     // a tile: qt nodes x gt heads; nsub tiles for a node's heads (G > 128)
@@ -70,6 +70,12 @@ struct TreeArgs {
   int piece_cost, nparts, hg;
   float qscale;         // scale * log2(e) (* the keys' scale)
   float vscale;
+};
+
+struct alignas(16) TreeDesc {  // what a CTA leaves for the combine kernel
+  uint32_t status;   // PA_DEV_* bits
+  int32_t b, hs;     // the sequence that its last piece begins and does not end; b = -1: none
+  int32_t slot;      // the partial slot of that piece
 };
 
 struct TreeHalf {  // one row's state in one softmax group, for the merge of a one-tile piece
@@ -143,7 +149,7 @@ struct TreePart {
 
 struct TreeMisc {
   uint32_t status, tmem;
-  int32_t npieces, pad;
+  int32_t npieces, open_b, open_hs, open_slot;
   TreePart part;
 };
 
@@ -574,6 +580,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     fence_mbar_init();
     misc->status = 0;
     misc->npieces = 0;
+    misc->open_b = -1;
   }
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tm_k);
@@ -623,11 +630,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (has_next) nwin = window_of(nxt, 0);
       const int slot = (cur.starts && cur.ends) ? -1 : (npieces == 0 ? 0 : 1);
       if (lane == 0) {
-        const size_t si = (size_t)cur.b * a.Hkv * a.nseqh + cur.hs;
-        if (cur.starts)
-          a.seq_first[si] = slot < 0 ? -1 : (int32_t)blockIdx.x * 2 + slot;
-        else if (cur.ends)
-          a.seq_last[si] = (int32_t)blockIdx.x;
+        // where the combine kernel finds a sequence that several CTAs share: its first CTA names it
+        if (cur.starts && !cur.ends) {
+          misc->open_b = cur.b;
+          misc->open_hs = cur.hs;
+          misc->open_slot = slot;
+        } else if (cur.ends && !cur.starts) {
+          a.seq_last[(size_t)cur.b * a.Hkv * a.nseqh + cur.hs] = (int32_t)blockIdx.x;
+        }
       }
       const int prefix = cur.L - cur.n;
       const TreeRow row = {cur.start, cur.n, cur.L};
@@ -1367,7 +1377,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tc_dealloc(tmem, C::TM_COLS);
-  if (tid == 0) a.desc[blockIdx.x] = misc->status;
+  if (tid == 0) a.desc[blockIdx.x] = TreeDesc{misc->status, misc->open_b, misc->open_hs, misc->open_slot};
   if (misc->npieces == 0) {
     // a range that held no key can still lie between two pieces of a sequence: its slot 0 weighs nothing
     for (int h = tid; h < C::QT * kTreeRows; h += C::THREADS)
@@ -1376,77 +1386,86 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------------------- combine
-// A warp per query row of a sequence that several CTAs share: their partial results in ascending order of
-// the keys, up to four loaded together.  Grid: (batch * hs, rows / kCombineRows).
+// Grid (CTAs of the split kernel, rows / 8): a block for 8 rows of the sequence that CTA x begins and does not
+// end (at most one), a warp per row.  Its pieces lie in CTAs x, x + HG, ..., in ascending order of the keys.
+// All pieces' log-sum-exps are read at once, a piece per lane, and with them the weights are known before any
+// value is read: the values are then loads that wait for nothing.
 
-constexpr int kCombineRows = 32;
+constexpr int kCombineRows = 8;
 
 template <int D, int QT>
-__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, uint32_t *status) {
+__global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const TreeArgs a, uint32_t *status) {
   pdl_wait();
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hs_row = a.Hkv * a.nseqh;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = (int)blockIdx.x;
+  if (cta == 0 && blockIdx.y == 0 && warp == 0) {
     uint32_t st = 0;
-    for (int i = lane; i < a.nparts; i += 32) st |= a.desc[i];
+    for (int i = lane; i < a.nparts; i += 32) st |= a.desc[i].status;
     st = __reduce_or_sync(FULL, st);
     if (lane == 0) *status = st;
   }
-  const int b = (int)blockIdx.x / hs_row, q = (int)blockIdx.x % hs_row;
+  const TreeDesc d = a.desc[cta];
+  if (d.b < 0) return;
   uint32_t ignored = 0;
-  const TreeRow r = tree_row(a, b, &ignored);
-  const int t0 = (q % a.nseqh) * QT;
-  if (r.n == 0 || t0 >= tree_tiles(a, r.n)) return;
-  const size_t si = (size_t)blockIdx.x;
-  const int f = a.seq_first[si], cl = a.seq_last[si], c0 = f >> 1;
-  // written whole, or (only where the split kernel gave up) a stale entry
-  if (f < 0 || c0 >= a.nparts || cl < c0 || cl >= a.nparts || (cl - c0) % a.hg != 0) return;
-  const int k = (cl - c0) / a.hg + 1, g = q / a.nseqh;
-  constexpr int RS = QT * kTreeRows, PER = D / 32, CHUNK = 4;
-  for (int e = warp; e < kCombineRows; e += 8) {
-    const int pr = (int)blockIdx.y * kCombineRows + e, t = t0 + pr / kTreeRows, row = pr % kTreeRows;
-    if (t >= tree_tiles(a, r.n)) break;
-    const TreeTile tl = tree_tile(a, t, r.n);
-    const int pos = row / a.gt, h = row - pos * a.gt;
-    if (pos >= tl.nq || h >= tl.nh) continue;
-    float M = -INFINITY, Z = 0.f, acc[PER];
+  const TreeRow r = tree_row(a, d.b, &ignored);
+  const int last = a.seq_last[(size_t)d.b * a.Hkv * a.nseqh + d.hs];
+  constexpr int RS = QT * kTreeRows, PER = D / 32, CHUNK = D <= 128 ? 8 : 4;
+  const int pr = (int)blockIdx.y * kCombineRows + warp, t = (d.hs % a.nseqh) * QT + pr / kTreeRows, row = pr % kTreeRows;
+  // (a stale entry only where the split kernel gave up)
+  if (r.n == 0 || t >= tree_tiles(a, r.n) || last <= cta || last >= a.nparts || (last - cta) % a.hg != 0) return;
+  const TreeTile tl = tree_tile(a, t, r.n);
+  const int pos = row / a.gt, h = row - pos * a.gt, k = (last - cta) / a.hg + 1;
+  if (pos >= tl.nq || h >= tl.nh) return;
+  auto place = [&](int i) { return ((size_t)(cta + i * a.hg) * 2 + (i == 0 ? d.slot : 0)) * RS + pr; };
+  float M = -INFINITY, Z = 0.f, acc[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-    for (int i0 = 0; i0 < k; i0 += CHUNK) {
-      float lc[CHUNK], x[CHUNK][PER];
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+  for (int i0 = 0; i0 < k; i0 += 32) {
+    // an empty piece (lse -inf) weighs nothing and its values are not read: they were not written
+    const float lc = i0 + lane < k ? a.part_lse[place(i0 + lane)] : -INFINITY;
+    float mn = lc;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(FULL, mn, o));
+    mn = fmaxf(mn, M);
+    const float w = lc == -INFINITY ? 0.f : fast_exp2(lc - mn), sc = M == -INFINITY ? 0.f : fast_exp2(M - mn);
+    M = mn;
+    float zs = w;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) zs += __shfl_xor_sync(FULL, zs, o);
+    Z = Z * sc + zs;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= sc;
+    for (int j0 = 0; j0 < 32 && i0 + j0 < k; j0 += CHUNK) {
+      float wj[CHUNK], x[CHUNK][PER];
 #pragma unroll
       for (int u = 0; u < CHUNK; ++u) {
-        const int i = i0 + u;
-        lc[u] = -INFINITY;
-        if (i < k) {
-          const size_t pi = (i == 0 ? (size_t)f : (size_t)(c0 + i * a.hg) * 2) * RS + pr;
-          lc[u] = a.part_lse[pi];
+        wj[u] = __shfl_sync(FULL, w, (j0 + u) & 31);
+        if (j0 + u < 32 && i0 + j0 + u < k && wj[u] != 0.f) {
+          const float *src = a.part_o + place(i0 + j0 + u) * D + lane * PER;
 #pragma unroll
-          for (int d = 0; d < PER; d += 2) {
-            const float2 v = *reinterpret_cast<const float2 *>(a.part_o + pi * D + lane * PER + d);
-            x[u][d] = v.x;
-            x[u][d + 1] = v.y;
+          for (int e = 0; e < PER; e += 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(src + e);
+            x[u][e] = v.x;
+            x[u][e + 1] = v.y;
           }
+        } else {
+          wj[u] = 0.f;
+#pragma unroll
+          for (int e = 0; e < PER; ++e) x[u][e] = 0.f;
         }
       }
 #pragma unroll
-      for (int u = 0; u < CHUNK; ++u) {
-        if (lc[u] != -INFINITY) {  // (an empty slot's values are not written)
-          const float mn = fmaxf(M, lc[u]), sc = M == -INFINITY ? 0.f : fast_exp2(M - mn), wc = fast_exp2(lc[u] - mn);
-          M = mn;
-          Z = Z * sc + wc;
+      for (int u = 0; u < CHUNK; ++u)
 #pragma unroll
-          for (int d = 0; d < PER; ++d) acc[d] = acc[d] * sc + wc * x[u][d];
-        }
-      }
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(wj[u], x[u][e], acc[e]);
     }
-    const float inv = Z == 0.f ? 0.f : 1.f / Z;
-    const size_t at = (size_t)(r.start + tl.i0 + pos) * a.Hq + g * a.G + tl.h0 + h;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + at * D + lane * PER);
-#pragma unroll
-    for (int d = 0; d < PER; d += 2) dst[d / 2] = pack_bf16x2(acc[d] * inv, acc[d + 1] * inv);
-    if (lane == 0 && a.lse) a.lse[at] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * LN2;
   }
+  const float inv = Z == 0.f ? 0.f : 1.f / Z;
+  const size_t at = (size_t)(r.start + tl.i0 + pos) * a.Hq + (d.hs / a.nseqh) * a.G + tl.h0 + h;
+  uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + at * D + lane * PER);
+#pragma unroll
+  for (int e = 0; e < PER; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0 && a.lse) a.lse[at] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * LN2;
 }
 
 }  // namespace pa

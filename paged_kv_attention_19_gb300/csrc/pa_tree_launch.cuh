@@ -42,8 +42,10 @@ cudaError_t launch_tree(const TreeLaunch &l, cudaStream_t stream) {
   e = launch_pdl(tree_split_kernel<C>, dim3((unsigned)a.nparts), C::THREADS, TreeSmem<C>::BYTES, stream,
                  l.tm_k, l.tm_v, l.tm_q, a);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(a.batch * a.Hkv * a.nseqh), QT * kTreeRows / kCombineRows);
-  return launch_pdl(tree_combine_kernel<D, QT>, grid, 256, 0, stream, a, l.status);
+  // the rows that a sequence can have: of a single tile those that it holds
+  const int rows = a.nseqh * QT > 1 ? QT * kTreeRows : a.gt * (a.qt < a.max_query ? a.qt : a.max_query);
+  const dim3 grid((unsigned)a.nparts, (unsigned)((rows + kCombineRows - 1) / kCombineRows));
+  return launch_pdl(tree_combine_kernel<D, QT>, grid, kCombineRows * 32, 0, stream, a, l.status);
 }
 
 template <int FMT>
