@@ -29,174 +29,193 @@ struct PlanArgs {
   int batch, page_size, num_pages, max_pages_per_seq, max_tokens;
 };
 
-// What a CTA keeps of a row, in shared memory.  need: pages to take; PLAN_REFUSED: a row with bad
-// lengths; PLAN_ENDED: its pages are given back (first: where they start among the given ones).
+// What a CTA keeps of a row, in shared memory.  need: pages to take; PLAN_REFUSED: a row with bad lengths;
+// PLAN_ENDED: its pages are given back.
 struct PlanRow {
-  int32_t ctx, held, start, need, first;
+  int32_t ctx, held, start, need;
+  int32_t first;  // pages needed by the rows before it
+  int32_t given;  // pages given back by the rows before it
 };
 constexpr int32_t PLAN_REFUSED = -1, PLAN_ENDED = -2;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 // All threads of the cluster's CTAs; global writes before it are visible to all of them behind it.
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Exclusive scan over the CTA's threads of two 64-bit values; the totals in *ta, *tb.
-__device__ __forceinline__ void block_scan2(long long &a, long long &b, long long *ta, long long *tb,
-                                            long long (*part)[2]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  long long x = a, y = b;
+// Exclusive scan over the CTA's threads of three 64-bit values; the totals in sum.
+__device__ __forceinline__ void block_scan3(long long (&v)[3], long long (&sum)[3], long long (*part)[3]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x[3];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(FULL, x, o), v = __shfl_up_sync(FULL, y, o);
-    if (lane >= o) {
-      x += u;
-      y += v;
+  for (int k = 0; k < 3; ++k) {
+    x[k] = v[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(FULL, x[k], o);
+      if (lane >= o) x[k] += u;
     }
-  }
-  if (lane == 31) {
-    part[warp][0] = x;
-    part[warp][1] = y;
+    if (lane == 31) part[warp][k] = x[k];
   }
   __syncthreads();
-  long long pa = 0, pb = 0;
-  *ta = *tb = 0;
-  for (int w = 0; w < nw; ++w) {
-    if (w == warp) {
-      pa = *ta;
-      pb = *tb;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    // the warps' sums: lane w has warp w's
+    long long s = lane < kPlanThreads / 32 ? part[lane][k] : 0, p = s;
+#pragma unroll
+    for (int o = 1; o < kPlanThreads / 32; o <<= 1) {
+      const long long u = __shfl_up_sync(FULL, p, o);
+      if (lane >= o) p += u;
     }
-    *ta += part[w][0];
-    *tb += part[w][1];
+    sum[k] = __shfl_sync(FULL, p, kPlanThreads / 32 - 1);
+    v[k] = __shfl_sync(FULL, p - s, warp) + x[k] - v[k];
   }
   __syncthreads();
-  a = pa + x - a;
-  b = pb + y - b;
 }
 
-// One cluster of CTAs plans the step: a few thousand integers in and out, bound by the launch and by
-// the few dependent trips to memory.  Every CTA scans all rows (the lengths are read by each, which
-// costs no more than handing the sums over), keeps them in shared memory, and after one barrier of
-// the cluster writes its share of the rows and tokens.  Nothing that may be updated in place is
-// written before that barrier, and every CTA has read all of its inputs by then.  The page of a
-// token comes from the free list where it is a new one, so tokens need not wait for the table's
-// new entries.
+struct PlanTotals {
+  int count, top, total;  // free pages before; with the given ones; tokens
+};
+
+// All rows into shared memory, with the sums before each (every CTA of the plan does this for itself: the
+// lengths are few, and to hand the sums over would take a launch).
+__device__ __forceinline__ PlanTotals plan_rows(const PlanArgs &a, PlanRow *rows, long long (*part)[3], uint32_t &bad) {
+  const int tid = threadIdx.x, P = a.page_size;
+  const int free0 = *a.free_count;
+  long long sums[3] = {0, 0, 0};  // tokens, pages given, pages needed
+  // a row's need is 0 where its tokens pass max_tokens, which only the sum of the tokens tells: the first pass
+  // takes that as not so, and a second follows in the rare call where it is
+  for (int pass = 0; pass < 2; ++pass) {
+    sums[0] = sums[1] = sums[2] = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
+      const int b = b0 + tid;
+      int ctx = 0, n = 0, held = 0;
+      if (b < a.batch) {
+        ctx = a.context_lens[b];
+        n = a.new_lens[b];
+        held = a.held_pages[b];
+      }
+      const bool ended = n < 0, held_ok = held >= 0 && held <= a.max_pages_per_seq;
+      const long long add = max(n, 0), pages = ((long long)ctx + add + P - 1) / P;  // pages behind this step
+      bool ok = ctx >= 0 && held_ok && pages <= a.max_pages_per_seq;
+      if (pass > 0) ok = ok && b < a.batch && rows[b].start + add <= a.max_tokens;
+      if (ended ? !held_ok : !ok) bad |= PA_DEV_BAD_LEN;
+      const long long need = ok && n > 0 ? max(pages - held, 0ll) : 0;
+      long long v[3] = {add, ended && held_ok ? held : 0, need}, all[3];
+      block_scan3(v, all, part);
+      if (b < a.batch) {
+        PlanRow r;
+        r.ctx = ctx;
+        r.held = held_ok ? held : 0;
+        r.start = (int)min(sums[0] + v[0], (long long)INT_MAX);
+        r.need = ended ? PLAN_ENDED : ok ? (int)need : PLAN_REFUSED;
+        r.first = (int)min(sums[2] + v[2], (long long)INT_MAX);
+        r.given = (int)min(sums[1] + v[1], (long long)INT_MAX);
+        rows[b] = r;
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k) sums[k] += all[k];
+    }
+    if (sums[0] <= a.max_tokens) break;
+  }
+  PlanTotals t;
+  t.count = min(max(free0, 0), a.num_pages);
+  if (free0 != t.count) bad |= PA_DEV_BAD_LEN;
+  if (t.count + sums[1] > a.num_pages) bad |= PA_DEV_BAD_LEN;  // more pages than there are: the ones past the list are lost
+  t.top = (int)min(t.count + sums[1], (long long)a.num_pages);
+  t.total = (int)min(sums[0], (long long)INT_MAX);
+  if (tid == 0) rows[a.batch].start = t.total;
+  __syncthreads();
+  return t;
+}
+
+__device__ __forceinline__ bool plan_granted(const PlanRow &r, int top) {
+  return r.need == 0 || (r.need > 0 && (long long)r.first + r.need <= top);
+}
+
+// Page j of the step: entry top - 1 - j of the list with the given pages on it.  Those are taken from the ended
+// rows' own table entries, so that no CTA waits for another to have pushed them.
+__device__ __forceinline__ int plan_page(const PlanArgs &a, const PlanRow *rows, const PlanTotals &t, int j) {
+  const int s = t.top - 1 - j;
+  if (s < t.count) return a.free_list[s];
+  const int r = s - t.count;
+  int lo = 0, hi = a.batch - 1;  // the last row with at most r pages given before it
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (rows[mid].given <= r) lo = mid;
+    else hi = mid - 1;
+  }
+  return a.block_table[(size_t)lo * a.max_pages_per_seq + (r - rows[lo].given)];
+}
+
+// The rows' state after the step (one CTA): what may be updated in place.
+__device__ __forceinline__ void plan_state(const PlanArgs &a, const PlanRow *rows, const PlanTotals &t, long long (*part)[3]) {
+  const int tid = threadIdx.x;
+  long long taken = 0;  // the needs are granted up to the first that passes the list, in row order
+  for (int b = tid; b < a.batch; b += kPlanThreads) {
+    const PlanRow r = rows[b];
+    const bool ok = plan_granted(r, t.top), ended = r.need == PLAN_ENDED;
+    a.context_lens_out[b] = ended ? 0 : ok ? r.ctx + (rows[b + 1].start - r.start) : r.ctx;
+    // (a refused row keeps what it said, a bad count included)
+    if (ended) a.held_pages_out[b] = 0;
+    else if (ok) a.held_pages_out[b] = r.held + r.need;
+    else if (a.held_pages_out != a.held_pages) a.held_pages_out[b] = a.held_pages[b];
+    if (ok && r.need > 0) taken = max(taken, (long long)r.first + r.need);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) taken = max(taken, __shfl_xor_sync(FULL, taken, o));
+  if ((tid & 31) == 0) part[tid >> 5][0] = taken;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kPlanThreads / 32; ++w) taken = max(taken, part[w][0]);
+    *a.free_count_out = t.top - (int)taken;
+  }
+}
+
+// A few thousand integers in and out, bound by the launch and by the few dependent trips to memory.  STATE: the
+// grid is one cluster, whose CTAs meet once, when all have read all of their inputs, before the state that may
+// be updated in place is written (the smaller steps).  Otherwise (more than kPlanMaxCluster chunks of tokens) the
+// CTAs are independent and plan_state_kernel follows.  Each CTA writes its share of the rows' table entries and
+// of the tokens; what it reads of the table and of the list is what no CTA writes.
+template <bool STATE>
 __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs a) {
   extern __shared__ PlanRow rows[];  // [batch + 1]: the last one holds the total of the tokens
-  __shared__ long long part[kPlanThreads / 32][2];
+  __shared__ long long part[kPlanThreads / 32][3];
   __shared__ int8_t up[kTreeNodes - 1 + kPlanThreads];  // parents of the chunk's tokens and 63 before it
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
-  const int rank = (int)cluster_rank(), nranks = (int)gridDim.x;  // one cluster is the grid
+  const int rank = (int)blockIdx.x, nranks = (int)gridDim.x;
   const int P = a.page_size;
   uint32_t bad = 0;
+  const PlanTotals tot = plan_rows(a, rows, part, bad);
+  const int total = tot.total;
+  if constexpr (STATE) cluster_barrier();
 
-  long long tokens = 0, given = 0, needed = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    int ctx = 0, n = 0, held = 0;
-    if (b < a.batch) {
-      ctx = a.context_lens[b];
-      n = a.new_lens[b];
-      held = a.held_pages[b];
-    }
-    const bool ended = n < 0;
-    const bool held_ok = held >= 0 && held <= a.max_pages_per_seq;
-    if (ended && !held_ok) bad |= PA_DEV_BAD_LEN;
-    long long t = ended ? 0 : n, g = ended && held_ok ? held : 0, tt, tg;
-    block_scan2(t, g, &tt, &tg, part);
-    t += tokens;
-    g += given;
-    tokens += tt;
-    given += tg;
-    // pages the row holds behind this step
-    const long long pages = ((long long)ctx + max(n, 0) + P - 1) / P;
-    const bool ok = ctx >= 0 && held_ok && pages <= a.max_pages_per_seq && t + max(n, 0) <= a.max_tokens;
-    if (!ended && !ok) bad |= PA_DEV_BAD_LEN;
-    const long long need = ok && !ended && n > 0 ? max(pages - held, 0ll) : 0;
-    long long f = need, z = 0, tf, tz;
-    block_scan2(f, z, &tf, &tz, part);
-    f += needed;
-    needed += tf;
-    if (b < a.batch) {
-      PlanRow r;
-      r.ctx = ctx;
-      r.held = held_ok ? held : 0;
-      r.start = (int)min(t, (long long)INT_MAX);
-      r.need = ended ? PLAN_ENDED : ok ? (int)need : PLAN_REFUSED;
-      r.first = (int)min(ended ? g : f, (long long)INT_MAX);
-      rows[b] = r;
-    }
-  }
-  const int count = min(max(*a.free_count, 0), a.num_pages);
-  if (*a.free_count != count) bad |= PA_DEV_BAD_LEN;
-  long long top_ = count + given;
-  if (top_ > a.num_pages) {  // more pages than there are: the ones past the list are lost
-    bad |= PA_DEV_BAD_LEN;
-    top_ = a.num_pages;
-  }
-  const int top = (int)top_;
-  const int total = (int)min(tokens, (long long)INT_MAX);
-  if (tid == 0) rows[a.batch].start = total;
-  __syncthreads();
-
-  // the ended rows' pages, one warp a row
+  // rows, one warp each: the ended ones' pages go onto the list, new pages into the table
   const int nwarps = nranks * (kPlanThreads / 32), warp = rank * (kPlanThreads / 32) + (tid >> 5);
   for (int b = warp; b < a.batch; b += nwarps) {
     const PlanRow r = rows[b];
-    if (r.need != PLAN_ENDED) continue;
-    const int32_t *bt = a.block_table + (size_t)b * a.max_pages_per_seq;
-    for (int j = lane; j < r.held; j += 32) {
-      const long long to = (long long)count + r.first + j;
-      if (to < top) a.free_list[to] = bt[j];
-    }
-  }
-  cluster_barrier();
-
-  // rows: new table entries and state.  Page j of the step is entry top - 1 - j of the list.
-  auto granted = [&](const PlanRow &r) { return r.need == 0 || (r.need > 0 && (long long)r.first + r.need <= top); };
-  for (int b = warp; b < a.batch; b += nwarps) {
-    const PlanRow r = rows[b];
-    const bool ok = granted(r);
-    if (r.need > 0 && !ok) bad |= PA_DEV_NO_PAGES;
-    if (ok) {
-      int32_t *bt = a.block_table + (size_t)b * a.max_pages_per_seq + r.held;
-      for (int j = lane; j < r.need; j += 32) {
-        const int page = a.free_list[top - 1 - r.first - j];
-        if (page < 0 || page >= a.num_pages) bad |= PA_DEV_BAD_PAGE;
-        bt[j] = page;
+    int32_t *bt = a.block_table + (size_t)b * a.max_pages_per_seq;
+    if (lane == 0) a.query_start[b] = r.start;
+    if (r.need == PLAN_ENDED) {
+      for (int j = lane; j < r.held; j += 32) {
+        const long long to = (long long)tot.count + r.given + j;
+        if (to < tot.top) a.free_list[to] = bt[j];
+      }
+    } else if (r.need > 0) {
+      if (plan_granted(r, tot.top)) {
+        for (int j = lane; j < r.need; j += 32) {
+          const int page = plan_page(a, rows, tot, r.first + j);
+          if (page < 0 || page >= a.num_pages) bad |= PA_DEV_BAD_PAGE;
+          bt[r.held + j] = page;
+        }
+      } else {
+        bad |= PA_DEV_NO_PAGES;
       }
     }
-    if (lane == 0) {
-      const bool ended = r.need == PLAN_ENDED;
-      a.context_lens_out[b] = ended ? 0 : ok ? r.ctx + (rows[b + 1].start - r.start) : r.ctx;
-      a.held_pages_out[b] = ended ? 0 : ok ? r.held + r.need : r.held;
-      a.query_start[b] = r.start;
-    }
   }
-  if (rank == 0) {
-    // pages taken: the needs are granted up to the first that passes the list, in row order
-    long long taken = 0;
-    for (int b = tid; b < a.batch; b += kPlanThreads) {
-      const PlanRow r = rows[b];
-      if (r.need > 0 && granted(r)) taken = max(taken, (long long)r.first + r.need);
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) taken = max(taken, __shfl_xor_sync(FULL, taken, o));
-    if (lane == 0) part[tid >> 5][0] = taken;
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < kPlanThreads / 32; ++w) taken = max(taken, part[w][0]);
-      *a.free_count_out = top - (int)taken;
-      a.query_start[a.batch] = total;
-    }
-  }
+  if (rank == 0 && tid == 0) a.query_start[a.batch] = total;
 
   // tokens, a chunk of kPlanThreads at a time
   for (int t0 = rank * kPlanThreads; t0 < a.max_tokens; t0 += nranks * kPlanThreads) {
@@ -223,6 +242,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
       }
       const PlanRow r = rows[lo];
       const int i = t - r.start, n = rows[lo + 1].start - r.start;
+      const long long at = (long long)r.ctx + i;
+      int page = 0;
+      unsigned k = 0;
+      const bool ok = plan_granted(r, tot.top);
+      if (ok) {  // then at < max_pages_per_seq * P, which the host keeps below 2^31
+        k = (unsigned)at / (unsigned)P;
+        page = (int)k < r.held ? a.block_table[(size_t)lo * a.max_pages_per_seq + k]
+                               : plan_page(a, rows, tot, r.first + ((int)k - r.held));
+      }
       int depth = i;
       if (a.parents && n <= kTreeNodes) {
         for (int j = i;;) {  // up the ancestors: each step goes to a smaller index
@@ -236,12 +264,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
         }
         depth = __popcll(mask) - 1;
       }
-      const long long at = (long long)r.ctx + i;
       pos = (int)min((long long)r.ctx + depth, (long long)INT_MAX);
-      if (granted(r)) {  // then at < max_pages_per_seq * P, which the host keeps below 2^31
-        const unsigned k = (unsigned)at / (unsigned)P;
-        const int page = (int)k < r.held ? a.block_table[(size_t)lo * a.max_pages_per_seq + k]
-                                         : a.free_list[top - 1 - r.first - ((int)k - r.held)];
+      if (ok) {
         if (page < 0 || page >= a.num_pages) bad |= PA_DEV_BAD_PAGE;
         else slot = (int64_t)page * P + ((unsigned)at - k * (unsigned)P);
       }
@@ -251,6 +275,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
     if (a.tree_mask) a.tree_mask[t] = mask;
   }
   if (bad && a.status) atomicOr(a.status, bad);
+  if constexpr (STATE) {
+    if (rank == 0) {
+      __syncthreads();  // (the sums' scratch was last read before the barrier)
+      plan_state(a, rows, tot, part);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_state_kernel(const PlanArgs a) {
+  extern __shared__ PlanRow rows[];
+  __shared__ long long part[kPlanThreads / 32][3];
+  pdl_wait();  // for the step kernel, which reads what is written here
+  pdl_launch_dependents();
+  uint32_t bad = 0;  // (said by the step kernel)
+  const PlanTotals tot = plan_rows(a, rows, part, bad);
+  plan_state(a, rows, tot, part);
 }
 
 // Accepted paths.  Block (x, y) moves 256 16-byte columns of row y: a column is one 16-byte piece of
@@ -277,6 +317,9 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const Compa
   pdl_launch_dependents();
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   if (tid < 32) {
+    // the path's first 64 entries, the lengths and the count: loads that wait for nothing
+    const int32_t *path = a.accepted + (size_t)b * a.max_accepted;
+    const int p0 = lane < a.max_accepted ? path[lane] : 0, p1 = lane + 32 < a.max_accepted ? path[lane + 32] : 0;
     uint32_t bad = 0;
     const int L = a.context_lens[b], n = a.query_start[b + 1] - a.query_start[b];
     int m = a.num_accepted[b];
@@ -289,13 +332,11 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const Compa
     const int prefix = L - n;
     int good = 0;  // entries before the first bad one
     bool stop = false;
+    int tail = -1;  // the entry before this round's first
     for (int i0 = 0; i0 < m && !stop; i0 += 32) {
-      const int i = i0 + lane;
-      int p = 0, before = -1;
-      if (i < m) {
-        p = a.accepted[(size_t)b * a.max_accepted + i];
-        before = i > 0 ? a.accepted[(size_t)b * a.max_accepted + i - 1] : -1;
-      }
+      const int i = i0 + lane, p = i0 == 0 ? p0 : p1;
+      const int up = __shfl_up_sync(FULL, p, 1), before = lane == 0 ? tail : up;
+      tail = __shfl_sync(FULL, p, 31);
       const uint32_t wrong = __ballot_sync(FULL, i < m && (p <= before || p < 0 || p >= n));
       stop = wrong != 0;
       good = stop ? i0 + __ffs((int)wrong) - 1 : min(m, i0 + 32);
@@ -412,17 +453,27 @@ extern "C" int pa_plan_step(const int32_t *context_lens, const int32_t *new_lens
                 held_pages_out, free_count_out, query_start, slot_mapping, positions, tree_mask, status, batch,
                 page_size, num_pages, max_pages_per_seq, max_tokens};
   const size_t smem = (size_t)(batch + 1) * sizeof(PlanRow);
+  const int chunks = (max_tokens + kPlanThreads - 1) / kPlanThreads;
+  // One cluster of as many CTAs as there are chunks of tokens; from more than eight chunks on a CTA each, up to two
+  // on an SM, and a second launch for the state: at 72000 tokens of 512 rows 12 us, where one cluster takes 38; at
+  // 4000 tokens the second launch costs more than it gives.
+  const bool one = chunks <= kPlanMaxCluster;
+  int cluster = 1;
+  while (one && cluster < chunks) cluster *= 2;
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(plan_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (kPlanMaxBatch + 1) * (int)sizeof(PlanRow));
+    constexpr int most = (kPlanMaxBatch + 1) * (int)sizeof(PlanRow);
+    cudaError_t e = cudaFuncSetAttribute(one ? plan_step_kernel<true> : plan_step_kernel<false>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess && !one) e = cudaFuncSetAttribute(plan_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  const int chunks = (max_tokens + kPlanThreads - 1) / kPlanThreads;
-  const int cluster = chunks <= 1 && batch <= 64 ? 1 : kPlanMaxCluster;
-  if (const cudaError_t e = launch(plan_step_kernel, dim3((unsigned)cluster), kPlanThreads, smem, cluster, a, stream);
-      e != cudaSuccess)
-    return cuda_fail(e);
-  note_launches(1);
+  constexpr int kPlanMostCtas = 304;
+  cudaError_t e = one ? launch(plan_step_kernel<true>, dim3((unsigned)cluster), kPlanThreads, smem, cluster, a, stream)
+                      : launch(plan_step_kernel<false>, dim3((unsigned)(chunks < kPlanMostCtas ? chunks : kPlanMostCtas)),
+                               kPlanThreads, smem, 0, a, stream);
+  if (e == cudaSuccess && !one) e = launch(plan_state_kernel, dim3(1), kPlanThreads, smem, 0, a, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  note_launches(one ? 1 : 2);
   return PA_OK;
 }
 

@@ -5,12 +5,15 @@
 // pairs (u, v) of the first rot values become (u cos - v sin, v cos + u sin) by the angles of row p
 // of a table; one rounding to the output's type at the end.  Values of v are stored as they are.
 //
-// A pass over the data, bound by HBM: each value is read once and written once.  A lane holds 8
-// consecutive values (one 16-byte load), D / 8 lanes a head row, so the sum of squares is a few
-// shuffles, an adjacent pair lies in one lane, and a pair rot / 2 apart is one shuffle away (rot is a
-// multiple of 16, so whole lanes face each other).  A warp takes one token and IT x (256 / D) of its
-// heads: the token's position, slot and angles are loaded once for all of them, and the IT rows'
-// loads are in flight together.
+// A pass over the data, bound by HBM: each value is read once and written once.  D / 8 lanes hold a head
+// row, 8 values each, so the sum of squares is a few shuffles.  Where a pair lies rot / 2 apart, a lane's
+// values are two pieces of 4 that far apart (and from rot on 8 in a row): both values of a pair are in one
+// lane, at the price of 8-byte accesses.  A warp takes a segment of a token's heads, 256 / D head rows at a
+// time (a group): the token's position, slot and angles are loaded once for the segment, and the next three
+// groups' loads are in flight while three are worked on (two, or four, with as many blocks on an SM as the
+// registers allow: 5 to 11% slower).  The warps of one wave stride over the (token,
+// segment) pairs.
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -29,7 +32,7 @@ enum RopeFmt { ROPE_BF16 = 0, ROPE_FP8 = 1, ROPE_NVFP4 = 2 };
 
 struct RopeArgs {
   const uint16_t *q, *k, *v;    // token strides below; heads dense
-  const uint4 *q_weight, *k_weight;  // [D] bf16 or null
+  const uint16_t *q_weight, *k_weight;  // [D] bf16 or null
   const float *cos_sin;         // [max_position, rot]
   const int32_t *positions;
   const int64_t *slots;
@@ -37,10 +40,27 @@ struct RopeArgs {
   uint8_t *k_pool, *v_pool;
   uint32_t *status;             // or null
   long long q_stride, k_stride, v_stride, n_slots;
-  int tokens, Hq, Hkv, rot, max_position, chunks;  // chunks: warps per token
+  int tokens, Hq, Hkv, rot, max_position;
+  int groups, segs, per_seg;  // groups of head rows per token, segments of them, groups per segment
   float eps;
   Fp8Scale k_scale, v_scale;
 };
+
+__device__ __forceinline__ float2 pair_mul(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 pair_fma(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
 
 __device__ __forceinline__ void unpack8(uint4 x, float (&f)[8]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -55,167 +75,284 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// E4M3 codes of f / s, nearest with ties to even, saturated.
-__device__ __forceinline__ uint2 fp8_codes8(const float (&f)[8], Fp8Scale s) {
+// f / s, correctly rounded; the way of dividing (see Fp8Scale) is the same for the whole launch.
+__device__ __forceinline__ void quot8(const float (&f)[8], Fp8Scale s, float (&q)[8]) {
+  if (s.rcp != 0.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = f[i] * s.rcp;
+  } else if (s.rcpn != 0.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = markstein_quot(f[i], s.sc, s.rcpn);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(f[i], s.sc);
+  }
+}
+
+// E4M3 codes of quotients, nearest with ties to even, saturated.
+__device__ __forceinline__ uint2 fp8_codes8(const float (&q)[8]) {
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(quot(f[2 * i], s), quot(f[2 * i + 1], s)), __NV_SATFINITE, __NV_E4M3);
+  for (int i = 0; i < 4; ++i) c[i] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * i], q[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
   return make_uint2((c[0] & 0xffffu) | (c[1] << 16), (c[2] & 0xffffu) | (c[3] << 16));
 }
 
-// NVFP4 codes of this lane's 8 values and the scale code of its block of 16, which it shares with the
-// lane beside it (all lanes of the warp): the scale code of (amax / s) / 6, then each value's code of
-// (f / s) / E4M3(scale code), every step correctly rounded; a NaN in the block gives the NaN scale
-// code and zero codes.
-__device__ __forceinline__ uint32_t nvfp4_codes8(const float (&f)[8], Fp8Scale s, uint32_t *scale_code) {
-  float amax = 0.f;
-  bool nan = false;
+// NVFP4: this lane's 8 quotients f / s, whose block of 16 it shares with the lane beside it (all lanes of the
+// warp): the scale code of amax / 6, then each value's code of its quotient over E4M3(scale code), every
+// step correctly rounded; a NaN in the block gives the NaN scale code and zero codes.
+__device__ __forceinline__ uint32_t nvfp4_codes8(const float (&q)[8], uint32_t *scale_code) {
+  float amax = 0.f;  // of the quotients: the division is monotone, so it is the quotient of the largest
+  int nan = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    amax = fmaxf(amax, fabsf(f[i]));
-    nan = nan || f[i] != f[i];
+    amax = fmaxf(amax, fabsf(q[i]));
+    nan |= q[i] != q[i];
   }
   // every lane takes part in both exchanges
-  const float both = fmaxf(amax, __shfl_xor_sync(FULL, amax, 1));
-  const int other_nan = __shfl_xor_sync(FULL, (int)nan, 1);
-  const bool any_nan = nan || other_nan != 0;
+  amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 1));
+  nan |= __shfl_xor_sync(FULL, nan, 1);
   *scale_code = 0x7Fu;
-  if (any_nan) return 0u;
-  *scale_code = (uint32_t)__nv_cvt_float_to_fp8(markstein_quot(quot(both, s), 6.f, 1.f / 6.f), __NV_SATFINITE, __NV_E4M3);
+  if (nan) return 0u;
+  *scale_code = (uint32_t)__nv_cvt_float_to_fp8(markstein_quot(amax, 6.f, 1.f / 6.f), __NV_SATFINITE, __NV_E4M3);
   const float ds = e4m3_value(*scale_code);
   if (ds == 0.f) return 0u;
   const float r = __frcp_rn(ds);
   uint32_t c = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c |= e2m1_pair(markstein_quot(quot(f[2 * i], s), ds, r), markstein_quot(quot(f[2 * i + 1], s), ds, r)) << (8 * i);
+  for (int i = 0; i < 4; ++i) c |= e2m1_pair(markstein_quot(q[2 * i], ds, r), markstein_quot(q[2 * i + 1], ds, r)) << (8 * i);
   return c;
 }
 
-template <int D, int FMT, bool IL, int IT>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_write_kernel(const RopeArgs a) {
+template <int D, int FMT, bool IL>
+__global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(const RopeArgs a) {
   constexpr int LPH = D / 8;     // lanes per head row
-  constexpr int HPI = 32 / LPH;  // head rows per warp and iteration
+  constexpr int HPG = 32 / LPH;  // head rows per group
+  constexpr int AHEAD = 3;       // groups loaded together
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, l = lane % LPH, g = lane / LPH;
-  const int item = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  const int t = item / a.chunks, h0 = (item - t * a.chunks) * (HPI * IT);
-  if (t >= a.tokens) return;
-  const long long slot = a.slots[t];
-  const int pos = a.positions[t];
-  const int H = a.Hq + 2 * a.Hkv;
-  uint4 raw[IT];
-#pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int h = h0 + i * HPI + g;
-    const uint16_t *row = h < a.Hq          ? a.q + t * a.q_stride + h * D
-                          : h < a.Hq + a.Hkv ? a.k + t * a.k_stride + (h - a.Hq) * D
-                                             : a.v + t * a.v_stride + (h - a.Hq - a.Hkv) * D;
-    raw[i] = h < H ? *reinterpret_cast<const uint4 *>(row + l * 8) : make_uint4(0, 0, 0, 0);
-  }
-  if (slot < 0) return;  // padding
-  if (slot >= a.n_slots || pos < 0 || pos >= a.max_position) {
-    if (a.status && lane == 0) atomicOr(a.status, slot >= a.n_slots ? PA_DEV_BAD_SLOT : PA_DEV_BAD_POS);
-    return;
-  }
-  // this lane's angles: those of its 8 values (or 4 adjacent pairs)
-  const int half = a.rot >> 1;
+  const int H = a.Hq + 2 * a.Hkv, half = a.rot >> 1;
+  constexpr bool PIECES = !IL;
   const bool turned = l * 8 < a.rot;
-  float co[IL ? 4 : 8], si[IL ? 4 : 8];
-  {
-    const int e0 = IL ? l * 4 : (l * 8 < half ? l * 8 : l * 8 - half);
-    const float *cs = a.cos_sin + (size_t)pos * a.rot + (turned ? e0 : 0);
-#pragma unroll
-    for (int i = 0; i < (IL ? 4 : 8); i += 4) {
-      const float4 c = *reinterpret_cast<const float4 *>(cs + i);
-      const float4 s = *reinterpret_cast<const float4 *>(cs + half + i);
-      co[i] = c.x, co[i + 1] = c.y, co[i + 2] = c.z, co[i + 3] = c.w;
-      si[i] = s.x, si[i + 1] = s.y, si[i + 2] = s.z, si[i + 3] = s.w;
+  // where this lane's two pieces of 4 values start (8 in a row where pairs are adjacent, and from rot on)
+  const int at0 = PIECES && turned ? l * 4 : l * 8, at1 = PIECES && turned ? half + l * 4 : l * 8 + 4;
+  const int e0 = turned ? l * 4 : 0;  // the first angle of this lane's 4 pairs
+  // 16 bytes of bf16 values of a row: one access, or one of each piece
+  auto load8 = [&](const uint16_t *row) {
+    if constexpr (!PIECES) return *reinterpret_cast<const uint4 *>(row + at0);
+    const uint2 lo = *reinterpret_cast<const uint2 *>(row + at0), hi = *reinterpret_cast<const uint2 *>(row + at1);
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+  };
+  auto store8 = [&](uint16_t *row, uint4 v) {
+    if constexpr (!PIECES) {
+      *reinterpret_cast<uint4 *>(row + at0) = v;
+    } else {
+      *reinterpret_cast<uint2 *>(row + at0) = make_uint2(v.x, v.y);
+      *reinterpret_cast<uint2 *>(row + at1) = make_uint2(v.z, v.w);
     }
-  }
-  // pairs half a turn apart: this lane's partner, and the sign of the sine for its side
-  const int partner = !turned ? lane : l * 8 < half ? lane + half / 8 : lane - half / 8;
-  const float side = l * 8 < half ? -1.f : 1.f;
+  };
+  const bool norm_q = a.q_weight != nullptr, norm_k = a.k_weight != nullptr;
+  const uint4 wq = norm_q ? load8(a.q_weight) : make_uint4(0, 0, 0, 0), wk = norm_k ? load8(a.k_weight) : make_uint4(0, 0, 0, 0);
+  const int items = a.tokens * a.segs, stride = (int)gridDim.x * (kRopeThreads / 32);
+  int item = (int)blockIdx.x * (kRopeThreads / 32) + (int)(threadIdx.x >> 5);
+  long long next_slot = item < items ? a.slots[item / a.segs] : 0;
+  int next_pos = item < items ? a.positions[item / a.segs] : 0;
+  for (; item < items; item += stride) {
+    const int t = item / a.segs, g0 = (item - t * a.segs) * a.per_seg, g1 = min(g0 + a.per_seg, a.groups);
+    const long long slot = next_slot;
+    const int pos = next_pos;
+    auto fetch = [&](int grp) {  // this lane's values of a group's rows
+      const int h = grp * HPG + g;
+      const uint16_t *row = h < a.Hq           ? a.q + t * a.q_stride + h * D
+                            : h < a.Hq + a.Hkv ? a.k + t * a.k_stride + (h - a.Hq) * D
+                                               : a.v + t * a.v_stride + (h - a.Hq - a.Hkv) * D;
+      if (FMT == ROPE_NVFP4 && PIECES && h >= a.Hq + a.Hkv)  // (see the keys' exchange below)
+        return grp < g1 && h < H ? *reinterpret_cast<const uint4 *>(row + l * 8) : make_uint4(0, 0, 0, 0);
+      return grp < g1 && h < H ? load8(row) : make_uint4(0, 0, 0, 0);
+    };
+    uint4 raw[AHEAD];
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int hw = h0 + i * HPI;  // the warp's first row of this iteration
-    if (hw >= H) break;
-    const int h = hw + g;
-    const bool is_v = h >= a.Hq + a.Hkv;
-    float x[8];
-    unpack8(raw[i], x);
-    if (hw < a.Hq + a.Hkv) {  // some row of the warp is a query's or a key's
-      const uint4 *weight = h < a.Hq ? a.q_weight : a.k_weight;
-      float ss = 0.f;
+    for (int i = 0; i < AHEAD; ++i) raw[i] = fetch(g0 + i);
+    if (item + stride < items) {
+      next_slot = a.slots[(item + stride) / a.segs];
+      next_pos = a.positions[(item + stride) / a.segs];
+    }
+    if (slot < 0) continue;  // padding
+    if (slot >= a.n_slots || pos < 0 || pos >= a.max_position) {
+      if (a.status && lane == 0) atomicOr(a.status, slot >= a.n_slots ? PA_DEV_BAD_SLOT : PA_DEV_BAD_POS);
+      continue;
+    }
+    float co[4], si[4];
+    {
+      const float *cs = a.cos_sin + (size_t)pos * a.rot + e0;
+      const float4 c = *reinterpret_cast<const float4 *>(cs), s = *reinterpret_cast<const float4 *>(cs + half);
+      co[0] = c.x, co[1] = c.y, co[2] = c.z, co[3] = c.w;
+      si[0] = s.x, si[1] = s.y, si[2] = s.z, si[3] = s.w;
+    }
+    // norm and rotation of one lane's values of a row (all lanes of the warp; sums: some row has a norm;
+    // norm, on: this row has one, is turned)
+    auto turn = [&](float (&x)[8], bool sums, uint4 weight, bool norm, bool on) {
+      if (sums) {
+        float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+        for (int e = 0; e < 8; e += 2) s2 = pair_fma(make_float2(x[e], x[e + 1]), make_float2(x[e], x[e + 1]), s2);
+        float ss = s2.x + s2.y;
 #pragma unroll
-      for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(FULL, ss, o);
-      if (!is_v && weight) {
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
-        float w[8];
-        unpack8(weight[l], w);
+        for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(FULL, ss, o);
+        if (norm) {
+          const float r = rsqrtf(ss * (1.f / D) + a.eps);
+          float w[8];
+          unpack8(weight, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
+          for (int e = 0; e < 8; e += 2) {
+            const float2 y = pair_mul(pair_mul(make_float2(x[e], x[e + 1]), make_float2(r, r)), make_float2(w[e], w[e + 1]));
+            x[e] = y.x, x[e + 1] = y.y;
+          }
+        }
       }
-      if constexpr (IL) {
-        if (!is_v && turned) {
+      if (on && turned) {
+        if constexpr (IL) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float u = x[2 * e], v = x[2 * e + 1];
             x[2 * e] = u * co[e] - v * si[e];
             x[2 * e + 1] = v * co[e] + u * si[e];
           }
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float y = __shfl_sync(FULL, x[e], partner);
-          if (!is_v && turned) x[e] = x[e] * co[e] + side * y * si[e];
+          for (int e = 0; e < 4; e += 2) {
+            const float2 u = make_float2(x[e], x[e + 1]), v = make_float2(x[4 + e], x[5 + e]), c = make_float2(co[e], co[e + 1]),
+                         s = make_float2(si[e], si[e + 1]);
+            const float2 p = pair_fma(make_float2(-v.x, -v.y), s, pair_mul(u, c)), q = pair_fma(u, s, pair_mul(v, c));
+            x[e] = p.x, x[e + 1] = p.y, x[4 + e] = q.x, x[5 + e] = q.y;
+          }
         }
       }
-    }
-    if (h < a.Hq) *reinterpret_cast<uint4 *>(a.q_out + ((size_t)t * a.Hq + h) * D + l * 8) = pack8(x);
-    if (hw + HPI > a.Hq) {  // some row of the warp goes into a pool
-      const bool store = h >= a.Hq && h < H;
-      uint8_t *pool = is_v ? a.v_pool : a.k_pool;
-      const Fp8Scale sc = is_v ? a.v_scale : a.k_scale;
-      const size_t row = (size_t)slot * a.Hkv + (is_v ? h - a.Hq - a.Hkv : h - a.Hq);
-      if constexpr (FMT == ROPE_BF16) {
-        if (store) *reinterpret_cast<uint4 *>(pool + row * (2 * D) + l * 16) = pack8(x);
-      } else if constexpr (FMT == ROPE_FP8) {
-        if (store) *reinterpret_cast<uint2 *>(pool + row * D + l * 8) = fp8_codes8(x, sc);
-      } else {
-        constexpr int CODES = D / 2, SCALES = D / 16, ROW = (CODES + SCALES + 15) / 16 * 16;
-        uint32_t sb;
-        const uint32_t codes = nvfp4_codes8(x, sc, &sb);
-        // four blocks' scales to the first of their eight lanes
-        const uint32_t s1 = __shfl_down_sync(FULL, sb, 2), s2 = __shfl_down_sync(FULL, sb, 4),
-                       s3 = __shfl_down_sync(FULL, sb, 6);
-        if (store) {
-          uint8_t *p = pool + row * ROW;
-          *reinterpret_cast<uint32_t *>(p + l * 4) = codes;
-          if (l % 8 == 0) *reinterpret_cast<uint32_t *>(p + CODES + l / 2) = sb | (s1 << 8) | (s2 << 16) | (s3 << 24);
-          if (l > 0 && l <= (ROW - CODES - SCALES) / 4)
-            *reinterpret_cast<uint32_t *>(p + CODES + SCALES + (l - 1) * 4) = 0u;
+    };
+    for (int grp = g0; grp < g1; grp += AHEAD) {
+      uint4 cur[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        cur[i] = raw[i];
+        raw[i] = fetch(grp + AHEAD + i);
+      }
+      if ((grp + AHEAD) * HPG <= a.Hq) {  // queries only
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          if (grp + i >= g1) break;
+          float x[8];
+          unpack8(cur[i], x);
+          turn(x, norm_q, wq, norm_q, true);
+          store8(a.q_out + ((size_t)t * a.Hq + (grp + i) * HPG + g) * D, pack8(x));
+        }
+        continue;
+      }
+#pragma unroll 1
+      for (int i = 0; i < AHEAD && grp + i < g1; ++i) {
+        const int h = (grp + i) * HPG + g, hw = h - g;  // hw: the warp's first row
+        const bool is_v = h >= a.Hq + a.Hkv, is_q = h < a.Hq;
+        float x[8];
+        unpack8(cur[0], x);
+#pragma unroll
+        for (int e = 0; e + 1 < AHEAD; ++e) cur[e] = cur[e + 1];
+        if (hw < a.Hq + a.Hkv)   // some row is a query's or a key's
+          turn(x, norm_q || norm_k, is_q ? wq : wk, is_q ? norm_q : norm_k && !is_v, !is_v);
+        if (is_q) store8(a.q_out + ((size_t)t * a.Hq + h) * D, pack8(x));
+        if (hw + HPG <= a.Hq) continue;
+        // some row of the warp goes into a pool
+        const bool store = !is_q && h < H;
+        uint8_t *pool = is_v ? a.v_pool : a.k_pool;
+        const size_t row = (size_t)slot * a.Hkv + (is_v ? h - a.Hq - a.Hkv : h - a.Hq);
+        if constexpr (FMT == ROPE_BF16) {
+          if (store) store8(reinterpret_cast<uint16_t *>(pool) + row * D, pack8(x));
+        } else {
+          if constexpr (FMT == ROPE_NVFP4 && PIECES) {
+            // keys: from two pieces to 8 values in a row, so that a block is two lanes' (values were read so)
+            const bool first = l * 8 < half;
+            float y[8];
+            const int src = lane - l + (turned ? 2 * (first ? l : l - half / 8) : l);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = x[e];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int nb = turned ? src + 1 : lane;
+              const float a0 = __shfl_sync(FULL, y[e], src), a1 = __shfl_sync(FULL, y[e], nb),
+                          b0 = __shfl_sync(FULL, y[4 + e], src), b1 = __shfl_sync(FULL, y[4 + e], nb);
+              if (turned && !is_v) {
+                x[e] = first ? a0 : b0;
+                x[4 + e] = first ? a1 : b1;
+              }
+            }
+          }
+          float q[8];
+          quot8(x, is_v ? a.v_scale : a.k_scale, q);
+          if constexpr (FMT == ROPE_FP8) {
+            const uint2 c = fp8_codes8(q);
+            if (store) {
+              uint8_t *p = pool + row * D;
+              if constexpr (PIECES) {
+                *reinterpret_cast<uint32_t *>(p + at0) = c.x;
+                *reinterpret_cast<uint32_t *>(p + at1) = c.y;
+              } else {
+                *reinterpret_cast<uint2 *>(p + at0) = c;
+              }
+            }
+          } else {
+            constexpr int CODES = D / 2, SCALES = D / 16, ROW = (CODES + SCALES + 15) / 16 * 16;
+            uint8_t *p = pool + row * ROW;
+            uint32_t sb;
+            const uint32_t codes = nvfp4_codes8(q, &sb);
+            // four blocks' scales to the first of their eight lanes
+            const uint32_t s1 = __shfl_down_sync(FULL, sb, 2), s2 = __shfl_down_sync(FULL, sb, 4),
+                           s3 = __shfl_down_sync(FULL, sb, 6);
+            if (store) {
+              *reinterpret_cast<uint32_t *>(p + l * 4) = codes;
+              if (l % 8 == 0) *reinterpret_cast<uint32_t *>(p + CODES + l / 2) = sb | (s1 << 8) | (s2 << 16) | (s3 << 24);
+              if (l > 0 && l <= (ROW - CODES - SCALES) / 4)
+                *reinterpret_cast<uint32_t *>(p + CODES + SCALES + (l - 1) * 4) = 0u;
+            }
+          }
         }
       }
     }
   }
 }
 
-template <int D, int FMT, bool IL, int IT>
+// Blocks of one wave: the device's SMs times the kernel's resident blocks (asked once per device).
+template <auto kernel>
+int wave_blocks() {
+  static std::atomic<int> known[64];
+  int dev = 0, sms = 0, per_sm = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+  if (const int n = known[dev].load(std::memory_order_relaxed)) return n;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kRopeThreads, 0) != cudaSuccess)
+    return -1;
+  known[dev].store(sms * per_sm, std::memory_order_relaxed);
+  return sms * per_sm;
+}
+
+template <int D, int FMT, bool IL>
 cudaError_t launch_rope(RopeArgs &a, cudaStream_t stream) {
-  constexpr int ROWS = 256 / D * IT;
-  const int H = a.Hq + 2 * a.Hkv;
-  a.chunks = (H + ROWS - 1) / ROWS;
-  const long long items = (long long)a.tokens * a.chunks;
-  const long long grid = (items + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  if (grid > INT_MAX / (kRopeThreads / 32)) return cudaErrorInvalidConfiguration;
+  constexpr int HPG = 256 / D, WARPS = kRopeThreads / 32;
+  constexpr auto kernel = qk_norm_rope_write_kernel<D, FMT, IL>;
+  const int wave = wave_blocks<kernel>();
+  if (wave <= 0) return cudaErrorUnknown;
+  a.groups = (a.Hq + 2 * a.Hkv + HPG - 1) / HPG;
+  // Segments per token, by the time of the longest warp: rounds of (token, segment) pairs, each the segment's
+  // groups and a start (position, slot, angles and first rows from memory) worth about four of them.  (One
+  // group a segment everywhere takes 117 us where this takes 65, 8192 tokens of 64 + 8 + 8 heads of 128.)
+  const long long warps = (long long)wave * WARPS;
+  long long best = LLONG_MAX;
+  for (int per = a.groups; per >= 1; per = per > 1 ? per * 3 / 4 : 0) {
+    const int segs = (a.groups + per - 1) / per;
+    const long long cost = ((long long)a.tokens * segs + warps - 1) / warps * (per + 4);
+    if (cost < best) best = cost, a.per_seg = per, a.segs = segs;
+  }
+  const long long items = (long long)a.tokens * a.segs, blocks = (items + WARPS - 1) / WARPS;
+  if (items > INT_MAX - wave * WARPS) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)(blocks < wave ? blocks : wave));
   cfg.blockDim = dim3(kRopeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -223,12 +360,12 @@ cudaError_t launch_rope(RopeArgs &a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, qk_norm_rope_write_kernel<D, FMT, IL, IT>, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 template <int D, int FMT>
 cudaError_t launch_rope_any(RopeArgs &a, bool interleaved, cudaStream_t stream) {
-  return interleaved ? launch_rope<D, FMT, true, 1>(a, stream) : launch_rope<D, FMT, false, 1>(a, stream);
+  return interleaved ? launch_rope<D, FMT, true>(a, stream) : launch_rope<D, FMT, false>(a, stream);
 }
 
 template <int FMT>
@@ -287,8 +424,8 @@ int rope_call(const void *q, const void *k, const void *v, const void *q_weight,
   a.q = static_cast<const uint16_t *>(q);
   a.k = static_cast<const uint16_t *>(k);
   a.v = static_cast<const uint16_t *>(v);
-  a.q_weight = static_cast<const uint4 *>(q_weight);
-  a.k_weight = static_cast<const uint4 *>(k_weight);
+  a.q_weight = static_cast<const uint16_t *>(q_weight);
+  a.k_weight = static_cast<const uint16_t *>(k_weight);
   a.cos_sin = cos_sin;
   a.positions = positions;
   a.slots = slot_mapping;
@@ -305,7 +442,7 @@ int rope_call(const void *q, const void *k, const void *v, const void *q_weight,
   a.Hkv = Hkv;
   a.rot = rot;
   a.max_position = max_position;
-  a.chunks = 0;
+  a.groups = a.segs = a.per_seg = 0;
   a.eps = eps;
   a.k_scale = fp8_scale(k_scale);
   a.v_scale = fp8_scale(v_scale);
