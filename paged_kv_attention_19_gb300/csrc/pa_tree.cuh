@@ -23,23 +23,24 @@
 //
 // Roles of a CTA (one per SM):
 //   * warp 0: the K and V tiles of BN tokens into a ring of slots (TMA, 128-byte swizzle);
-//   * warp 1, one thread: the products.  Items alternate between two score buffers x = 0, 1.  With two
-//     tiles an item is (stage, tile x); with one tile the items are the stages in turn, so that the
-//     two softmax groups work on alternate stages of the same rows, each with its own output
-//     columns, and are merged at the end of the piece.  Scores of item i + 1 are issued before the
-//     second product of item i, so the tensor cores work while a group is in its softmax;
-//   * warp 2: looks over V tiles that hold tokens which not every row attends to (the tree, the edge
-//     of a window, the ends of a piece) before they are used: a token that nobody attends to becomes
-//     zero, and infinities and NaN of the others are taken out of the product and handed to the rows
-//     that do attend to them (0 x inf must not reach the ones that do not);
-//   * warp 3: the query tiles of each piece;
+//   * warps 1 and 2, one thread each: the products.  Score buffer, softmax group and output columns x = 0, 1
+//     belong to thread x.  With two tiles thread x takes tile x of every stage; with one tile the threads
+//     take alternate stages of the same rows, and the two outputs are merged at the end of the piece.  (One
+//     thread for both spent more time on its waits and commits than the products took.)  A piece has an
+//     even number of stages, so that a stage's parity says whose it is; the last may be without tokens;
+//   * warp 3: the query tiles of each piece; and looks over V tiles that hold tokens which not every row
+//     attends to (the tree, the edge of a window, the ends of a piece) before they are used: a token that
+//     nobody attends to becomes zero, and infinities and NaN of the others are taken out of the product and
+//     handed to the rows that do attend to them (0 x inf must not reach the ones that do not);
 //   * FP8 and NVFP4 pools: the tiles of codes land in a ring of their own, and four more warps convert
-//     them to f16 operands (exact), and the query rows, scaled by a power of two each, in place; they
-//     then do warp 2's work too.  The weights are rounded to f16 (2^-11);
+//     them to f16 operands (exact; two warps K tiles, two V tiles), and the query rows, scaled by a
+//     power of two each, in place; those of the V tiles then look them over.  The weights are rounded to
+//     f16 (2^-11);
 //   * two groups of four warps: one thread per score row.  64 columns of the row are in registers at a
 //     time, the ones behind them are read from tensor memory again once the maximum is known.
 // Tensor memory: scores (then weights) x at BN x, outputs at 256.  At head_dim 256 one output fills the
-// rest: one tile, one softmax group, stages of 64 tokens.
+// rest: one tile, stages of 64 tokens, one softmax group and one issuing thread, which has the scores of a
+// stage issued before the second product of the one before it.
 #pragma once
 
 #include "pa_common.cuh"
@@ -101,17 +102,19 @@ struct TreeCfg {
   static constexpr int ROOM = 229376 - Q_BYTES;
   // codes: up to eight slots of a tile each, copied in order K, V, K, V...; operands converted from them
   static constexpr int RAW_SLOT = QUANT ? (BN * ROWB + 1023) / 1024 * 1024 : 0;
-  static constexpr int NS_QUANT = D == 64 ? 5 : ROOM >= 4 * SLOT + 4 * RAW_SLOT ? 4 : 3;
+  static constexpr int NS_QUANT = D == 64 ? 6 : D == 128 ? 4 : 3;
   static constexpr int NR_FIT = QUANT ? (ROOM - NS_QUANT * SLOT) / (RAW_SLOT > 0 ? RAW_SLOT : 1) : 0;
-  static constexpr int NR = NR_FIT < 8 ? NR_FIT : 8;
+  static constexpr int NR = (NR_FIT < 6 ? NR_FIT : 6) & ~1;  // (even: a slot holds tiles of one kind)
   static constexpr int NS_FIT = QUANT ? NS_QUANT : ROOM / SLOT;
-  // two rings of slots: a K tile is free after the scores of its stage, a V tile later.  (One ring for
-  // both would need an even number of slots: the copies complete out of order, and a wait for the phase
-  // of a slot must not come before the phase before it is known to be complete.)
-  static constexpr int NS = NS_FIT < 10 ? NS_FIT : 10, NK = NS / 2, NV = NS - NK;
+  // Two rings of slots: a K tile is free after the scores of its stage, a V tile later.  Copies complete out of order,
+  // and a wait for a phase of a slot must not come before the phase before it is known to be complete, so whoever
+  // waits for the tiles of one kind, or of one parity of the stages, needs slots that hold those only.
+  static constexpr int NK = GROUPS == 1 ? NS_FIT / 2 : D == 64 ? (NS_FIT >= 10 ? 4 : 2) : 2;
+  static constexpr int NV = GROUPS == 1 ? NS_FIT - NK : (NS_FIT - NK < 4 ? 2 : 4), NS = NK + NV;
   static constexpr int SOFTMAX_WARPS = 4 * GROUPS;
   static constexpr int CONVERT_WARPS = QUANT ? 4 : 0;
-  static constexpr int CLEAN_WARPS = QUANT ? CONVERT_WARPS : 1;  // warps that look over the V tiles
+  static constexpr int TILE_WARPS = CONVERT_WARPS / 2;           // half of them for K tiles, half for V tiles
+  static constexpr int CLEAN_WARPS = QUANT ? TILE_WARPS : 1;     // warps that look over the V tiles
   static constexpr int THREADS = (4 + SOFTMAX_WARPS + CONVERT_WARPS) * 32;
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
   // (formats 0: f16 operands)
@@ -126,21 +129,25 @@ struct TreeCfg {
   static constexpr int REGS_CONTROL = QUANT ? 80 : 88, REGS_SOFTMAX = QUANT ? 160 : 208, REGS_CONVERT = 104;
   static_assert(!REG_SPLIT || 128 * REGS_CONTROL + 256 * REGS_SOFTMAX + (QUANT ? 128 * REGS_CONVERT : 0) <= THREADS * REGS,
                 "the register split stays within the launch's registers");
-  static constexpr int META = 8;  // stage records kept: a record is rewritten eight stages later, once the
-                                  // K tile of at least three stages later is free
-  static_assert(QUANT ? NR >= 4 && NK >= 1 && NR / 2 + NK <= 6 : NK >= 2 && NK <= 5, "rings of two stages, within the records");
+  static constexpr int META = 8;  // stage records kept: a record is rewritten eight stages later, once the K tile of a
+                                  // stage at least four later is free, and with that its own softmax long done
+  static_assert(NK >= 1 && NK + NR / 2 <= (QUANT ? 5 : 4) && (GROUPS == 1 || NK % 2 + NV % 2 == 0), "rings within the records");
   static_assert(QT <= GROUPS, "two tiles need two groups");
   static_assert(2 * BN <= 256 && GROUPS * D <= 256, "tensor-memory budget");
 };
 
+enum : int32_t { STAGE_MASKED = 1, STAGE_ABSENT = 2 };
 struct alignas(16) TreeStage {
-  int32_t end, first, left, masked;  // left: stages of the piece behind this one
-  int32_t b, two, slot, tok0;        // slot: -1 whole sequence, else partial slot
-  int32_t tok_hi, L, n, start;
-  uint32_t badmask;                  // bit k: box k of the stage was not loaded
-  int32_t t0, g, lo_min;             // first tile, key head, first token that any node's window reaches
+  int32_t flags;     // MASKED: not every row attends to every token; ABSENT: no tokens
+  int32_t tok0, tok_hi;
+  uint32_t badmask;  // bit k: box k of the stage was not loaded
 };
-static_assert(sizeof(TreeStage) == 64, "stage record is 64 bytes");
+struct alignas(16) TreePieceRec {  // written by the query warp before the piece's query is announced
+  int32_t end, stages, two, slot;  // stages with tokens; slot: -1 whole sequence, else partial slot
+  int32_t b, L, n, start;
+  int32_t t0, g, lo_min, pad;      // first tile, key head, first token that any node's window reaches
+};
+static_assert(sizeof(TreeStage) == 16 && sizeof(TreePieceRec) == 48, "records of 16-byte words");
 
 struct TreePart {
   int32_t found_b, pad;
@@ -158,11 +165,12 @@ struct TreeSmem {
   static constexpr int OFF_RING = C::Q_BYTES;
   static constexpr int OFF_RAW = OFF_RING + C::NS * C::SLOT;
   static constexpr int OFF_META = OFF_RAW + C::NR * C::RAW_SLOT;
-  static constexpr int OFF_NF = OFF_META + C::META * (int)sizeof(TreeStage);  // [META][CLEAN_WARPS][2] token bits
-  // full[NS], empty[NS], clean[META], q_full, q_empty, s_full[2], p_ready[2], pv_done[2], o_free, half[2], drain,
+  static constexpr int OFF_PIECE = OFF_META + C::META * (int)sizeof(TreeStage);       // [2]
+  static constexpr int OFF_NF = OFF_PIECE + 2 * (int)sizeof(TreePieceRec);            // [META][CLEAN_WARPS][2] token bits
+  // full[NS], empty[NS], clean[META], q_full, q_empty, s_full[2], p_ready[2], pv_done[2], o_free, half[2], drain[2],
   // q_conv, raw_full[NR], raw_empty[NR]
   static constexpr int OFF_BAR = OFF_NF + C::META * C::CLEAN_WARPS * 16;
-  static constexpr int NBAR = 2 * C::NS + C::META + 13 + 2 * C::NR;
+  static constexpr int NBAR = 2 * C::NS + C::META + 14 + 2 * C::NR;
   static constexpr int OFF_SHIFT = OFF_BAR + NBAR * 8;  // int8 [2][QT * 128]: exponents of the query rows' scales
   static constexpr int OFF_MISC = OFF_SHIFT + (C::QUANT ? 2 * C::QT * kTreeRows : 0);
   static constexpr int BYTES = OFF_MISC + (int)sizeof(TreeMisc) + 1024;
@@ -306,6 +314,9 @@ struct TreePiece {
   int b, hs, ub, ue, start, n, L, t0, g, two;
   bool starts, ends;
 };
+
+// Where a piece's results go: -1 the outputs (it is a whole sequence), else the partial slot (its number in the CTA).
+__device__ __forceinline__ int tree_slot(const TreePiece &p, int number) { return p.starts && p.ends ? -1 : number == 0 ? 0 : 1; }
 
 // A warp's walk over its CTA's pieces (all lanes call together); each walker sees the same pieces.
 struct TreeWalker {
@@ -548,9 +559,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR), *empty = full + NS, *clean = empty + NS;
   uint64_t *q_full = clean + C::META, *q_empty = q_full + 1, *s_full = q_full + 2, *p_ready = s_full + 2,
-           *pv_done = p_ready + 2, *o_free = pv_done + 2, *half_in = o_free + 1, *drain = half_in + 2, *q_conv = drain + 1,
+           *pv_done = p_ready + 2, *o_free = pv_done + 2, *half_in = o_free + 1, *drain = half_in + 2, *q_conv = drain + 2,
            *raw_full = q_conv + 1, *raw_empty = raw_full + C::NR;
   TreeStage *meta = reinterpret_cast<TreeStage *>(smem + S::OFF_META);
+  TreePieceRec *prec = reinterpret_cast<TreePieceRec *>(smem + S::OFF_PIECE);
   uint64_t *nf = reinterpret_cast<uint64_t *>(smem + S::OFF_NF);
   TreeMisc *misc = reinterpret_cast<TreeMisc *>(smem + S::OFF_MISC);
   uint32_t *status = &misc->status;
@@ -558,17 +570,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], C::QUANT ? C::CONVERT_WARPS : 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&full[s], C::QUANT ? C::TILE_WARPS : 1);
+      mbar_init(&empty[s], C::GROUPS);  // an arrival of each issuing thread (both of one where the stage is its own)
     }
     for (int s = 0; s < C::META; ++s) mbar_init(&clean[s], C::CLEAN_WARPS);
     for (int s = 0; s < C::NR; ++s) {
       mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], C::CONVERT_WARPS);
+      mbar_init(&raw_empty[s], C::TILE_WARPS);
     }
     mbar_init(q_conv, C::QUANT ? C::CONVERT_WARPS : 1);
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, C::GROUPS);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 2);  // the scores' commit and the issuing thread's arrive
       mbar_init(&p_ready[x], 4);
@@ -576,7 +588,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(&half_in[x], 4);
     }
     mbar_init(o_free, C::SOFTMAX_WARPS);
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     fence_mbar_init();
     misc->status = 0;
     misc->npieces = 0;
@@ -628,7 +641,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     while (has && ok) {
       has_next = walker.take<C::QT>(nxt);
       if (has_next) nwin = window_of(nxt, 0);
-      const int slot = (cur.starts && cur.ends) ? -1 : (npieces == 0 ? 0 : 1);
+      const int slot = tree_slot(cur, npieces);
       if (lane == 0) {
         // where the combine kernel finds a sequence that several CTAs share: its first CTA names it
         if (cur.starts && !cur.ends) {
@@ -640,15 +653,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
       const int prefix = cur.L - cur.n;
-      const TreeRow row = {cur.start, cur.n, cur.L};
-      const int lo_min = tree_lo(a, row);
       // every node sees the tokens [lo_max, prefix): depths are below n
       const int lo_max = a.window > 0 ? max(cur.L - a.window, 0) : 0;
       const int tok_hi = min(cur.L, cur.ue << a.log2_bh);
       const int n_stages = (cur.ue - cur.ub + nbox - 1) / nbox;
       const int pb = (cur.ub << a.log2_bh) >> a.log2_page;
       int wi = 0, fwin = window_of(cur, 1);
-      for (int st = 0; st < n_stages && ok; ++st) {
+      for (int st = 0; st < ((n_stages + 1) & ~1) && ok; ++st) {  // (the last one may be without tokens)
         const int unit0 = cur.ub + st * nbox, tok0 = unit0 << a.log2_bh;
         // the pages of one stage never straddle a window of 32 (nbox divides 32)
         const int pwin = ((tok0 >> a.log2_page) - pb) >> 5;
@@ -678,22 +689,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (lane == 0) {
             if (kv == 0) {
               TreeStage m;
-              m.end = 0;
-              m.first = st == 0;
-              m.left = n_stages - 1 - st;
-              m.masked = tok0 + BN > min(prefix, tok_hi) || tok0 < lo_max || bad != 0;
-              m.b = cur.b;
-              m.two = cur.two;
-              m.slot = slot;
+              m.flags = st >= n_stages ? STAGE_ABSENT
+                                       : (tok0 + BN > min(prefix, tok_hi) || tok0 < lo_max || bad != 0 ? STAGE_MASKED : 0);
               m.tok0 = tok0;
               m.tok_hi = tok_hi;
-              m.L = cur.L;
-              m.n = cur.n;
-              m.start = cur.start;
               m.badmask = bad;
-              m.t0 = cur.t0;
-              m.g = cur.g;
-              m.lo_min = lo_min;
               meta[t % C::META] = m;
             }
             mbar_arrive_expect_tx(&r_full[s], bytes);
@@ -722,15 +722,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       cwin = nwin;
       has = has_next;
     }
-    // the end: a record in the place of the next stage, announced in both of its slots
-    for (int kv = 0; kv < 2 && ok; ++kv) {
+    // the end, for the converting warps: the next stage's tiles, which are none
+    for (int kv = 0; C::QUANT && kv < 2 && ok; ++kv) {
       uint32_t u;
       const int s = place(kv, u);
       if (u > 0) ok = __all_sync(FULL, mbar_wait(&r_empty[s], (u - 1) & 1, status));
-      if (ok && lane == 0) {
-        if (kv == 0) meta[t % C::META].end = 1;
-        mbar_arrive(&r_full[s]);
-      }
+      if (ok && lane == 0) mbar_arrive(&r_full[s]);
     }
     if (!ok) {  // copies in flight land before the CTA exits
       if constexpr (C::QUANT) {
@@ -745,181 +742,117 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
     }
     if (lane == 0) misc->npieces = npieces;
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ products (one thread)
+  } else if (warp == 1 || (warp == 2 && C::GROUPS == 2)) {
+    // ------------------------------------------------------------ products (one thread of the warp)
     if (lane == 0) {
+      const int x = warp - 1;  // (one group: the stages alternate between the score buffers)
       const uint32_t ring = smem_u32(smem + S::OFF_RING), qb = smem_u32(smem);
-      uint32_t t = 0, kq = 0;
-      uint32_t cnt[2] = {0, 0};  // items issued with each score buffer
-      uint32_t started = 0;      // pieces whose first second product was issued
-      uint32_t fresh = 0;        // bit o: output region o has had no product in this piece
-      bool piece_open = false;
+      uint32_t t0 = 0, c = 0, d = 0;  // the piece's first stage; items begun and finished
       bool ok = true;
-      // scores of one item: query tile qx, stage tt, score buffer x
-      auto scores = [&](int x, int qx, uint32_t tt) {
-        const uint64_t qd = tc_sdesc_sw128(qb + qx * (C::NPL * C::QPLANE), 16, 1024);
-        const uint64_t kd = tc_sdesc_sw128(ring + (tt % C::NK) * C::SLOT, 16, 1024);
-#pragma unroll
-        for (int p = 0; p < C::NPL; ++p)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_ss(tmem + C::TM_S + x * BN, qd + (uint64_t)((p * C::QPLANE + 32 * kk) >> 4),
-                      kd + (uint64_t)((p * C::PLANE + 32 * kk) >> 4), C::IDESC_S, (p | kk) != 0 ? 1u : 0u);
-        tc_commit(&s_full[x]);
-        mbar_arrive(&s_full[x]);
+      auto buf = [&](uint32_t i) { return C::GROUPS == 2 ? (uint32_t)x : i & 1; };
+      auto par = [&](uint32_t i) { return C::GROUPS == 2 ? i & 1 : (i >> 1) & 1; };
+      // the slot of a tile is free for whoever shares it: with this thread's operations, or at once
+      auto release = [&](uint64_t *bar, bool read, bool alone) {
+        if (read) tc_commit(bar);
+        else mbar_arrive(bar);
+        if (C::GROUPS == 2 && alone) mbar_arrive(bar);
       };
-      // the second product of one item; `release`: the V tile is free behind it
-      auto weighted = [&](int x, uint32_t tt, uint32_t pair, bool release) -> bool {
-        const uint32_t vs = C::NK + tt % C::NV;  // the V tile's slot
-        if (!mbar_wait(&p_ready[x], pair & 1, status)) return false;
-        if (!mbar_wait(&full[vs], (tt / C::NV) & 1, status)) return false;
-        if (!mbar_wait(&clean[tt % C::META], (tt / C::META) & 1, status)) return false;
-        if (piece_open) {  // the piece's first: the previous piece's outputs have been read
-          if (started > 0 && !mbar_wait(o_free, (started - 1) & 1, status)) return false;
-          ++started;
-          piece_open = false;
-        }
-        tc_fence_after();
-        const int o = C::GROUPS == 2 ? x : 0;
-        const uint64_t vd = tc_sdesc_sw128(ring + vs * C::SLOT, C::PLANE, 1024);
+      // the scores of the next item: query tile qx, stage t
+      auto begin = [&](uint32_t t, int qx, bool present, bool alone) -> bool {
+        const uint32_t b = buf(c);
+        constexpr uint32_t BACK = C::GROUPS == 2 ? 1 : 2;  // items since this buffer's last
+        if (!mbar_wait(&full[t % C::NK], (t / C::NK) & 1, status)) return false;
+        if (c >= BACK && !mbar_wait(&pv_done[b], par(c - BACK), status)) return false;
+        if (present) {
+          tc_fence_after();
+          const uint64_t qd = tc_sdesc_sw128(qb + qx * (C::NPL * C::QPLANE), 16, 1024);
+          const uint64_t kd = tc_sdesc_sw128(ring + (t % C::NK) * C::SLOT, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          tc_mma_ts(tmem + C::TM_O + o * D, tmem + C::TM_S + x * BN + 8 * kk, vd + (uint64_t)((kk * 16 * 128) >> 4),
-                    C::IDESC_PV, ((fresh >> o) & 1u) && kk == 0 ? 0u : 1u);
-        fresh &= ~(1u << o);
-        if (release) tc_commit(&empty[vs]);
-        tc_commit(&pv_done[x]);
-        ++cnt[x];
+          for (int p = 0; p < C::NPL; ++p)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_ss(tmem + C::TM_S + b * BN, qd + (uint64_t)((p * C::QPLANE + 32 * kk) >> 4),
+                        kd + (uint64_t)((p * C::PLANE + 32 * kk) >> 4), C::IDESC_S, (p | kk) != 0 ? 1u : 0u);
+          tc_commit(&s_full[b]);
+        } else {
+          mbar_arrive(&s_full[b]);  // no scores: the record alone
+        }
+        mbar_arrive(&s_full[b]);
+        release(&empty[t % C::NK], present, alone);
+        ++c;
         return true;
       };
-      int pend = 0;  // an item of buffer 1 whose second product is due
-      uint32_t pend_t = 0;
-      for (uint32_t pair = 0; ok; ++pair) {
-        ok = mbar_wait(&full[t % C::NK], (t / C::NK) & 1, status);
+      // the second product of the oldest item; first: of this thread in the piece
+      auto finish = [&](uint32_t t, uint32_t piece, bool first, bool present, bool alone) -> bool {
+        const uint32_t b = buf(d), vs = C::NK + t % C::NV;
+        if (!mbar_wait(&p_ready[b], par(d), status)) return false;
+        // the previous piece's outputs have been read, and all its V tiles with that
+        if (first && piece > 0 && !mbar_wait(o_free, (piece - 1) & 1, status)) return false;
+        // (bf16: whoever looked it over has waited for it)
+        if (C::QUANT ? !mbar_wait(&full[vs], (t / C::NV) & 1, status)
+                     : !mbar_wait(&clean[t % C::META], (t / C::META) & 1, status))
+          return false;
+        if (present) {
+          tc_fence_after();
+          const int o = C::GROUPS == 2 ? x : 0;
+          const uint64_t vd = tc_sdesc_sw128(ring + vs * C::SLOT, C::PLANE, 1024);
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            tc_mma_ts(tmem + C::TM_O + o * D, tmem + C::TM_S + b * BN + 8 * kk, vd + (uint64_t)((kk * 16 * 128) >> 4),
+                      C::IDESC_PV, first && kk == 0 ? 0u : 1u);
+        }
+        tc_commit(&pv_done[b]);
+        release(&empty[vs], present, alone);
+        ++d;
+        return true;
+      };
+      for (uint32_t piece = 0; ok; ++piece) {
+        ok = mbar_wait(C::QUANT ? q_conv : q_full, piece & 1, status);
         if (!ok) break;
-        const TreeStage &m = meta[t % C::META];
-        const bool end = m.end, first = m.first, two = m.two;
-        const int left = m.left;
-        if (end) {
-          for (int x = 0; x < 2; ++x) {  // the softmax groups stop here
-            mbar_arrive(&s_full[x]);
-            mbar_arrive(&s_full[x]);
-          }
+        const int4 r = *reinterpret_cast<const int4 *>(&prec[piece & 1]);  // end, stages, two, slot
+        if (r.x) {
+          for (int k = 0; k < 2; ++k) mbar_arrive(&s_full[buf(c)]);  // the softmax groups stop here
           break;
         }
-        if (first) {
-          ok = mbar_wait(C::QUANT ? q_conv : q_full, kq & 1, status);
-          if (!ok) break;
-          ++kq;
-          fresh = 3u;
-          piece_open = true;
+        const uint32_t n = (uint32_t)r.y, even = (n + 1) & ~1u;
+        const bool two = r.z != 0, alone = !two;
+        // this thread's stages: all of them, or every other one
+        const uint32_t j0 = C::GROUPS == 2 && !two ? (uint32_t)x : 0, dj = C::GROUPS == 2 && !two ? 2 : 1;
+        if constexpr (C::GROUPS == 2) {
+          for (uint32_t j = j0; j < even && ok; j += dj) {
+            ok = begin(t0 + j, two ? x : 0, j < n, alone);
+            if (j + dj >= even) tc_commit(q_empty);
+            if (ok) ok = finish(t0 + j, piece, j == j0, j < n, alone);
+          }
+        } else {
+          for (uint32_t j = 0; j <= even && ok; ++j) {
+            if (j < even) ok = begin(t0 + j, 0, j < n, alone);
+            if (j + 1 == even) tc_commit(q_empty);
+            if (ok && j > 0) ok = finish(t0 + j - 1, piece, j == 1, j - 1 < n, alone);
+          }
         }
-        const bool last = two ? left == 0 : left <= 1;
-        const bool second = two || left >= 1;
-        const uint32_t t1 = two ? t : t + 1;
-        if (cnt[0] > 0) ok = mbar_wait(&pv_done[0], (cnt[0] - 1) & 1, status);
-        if (!ok) break;
-        tc_fence_after();
-        scores(0, 0, t);
-        if (!two) tc_commit(&empty[t % C::NK]);
-        if (pend) {
-          ok = weighted(1, pend_t, pair - 1, true);
-          pend = 0;
-          if (!ok) break;
-        }
-        if (second) {
-          if (!two) ok = mbar_wait(&full[t1 % C::NK], (t1 / C::NK) & 1, status);
-          if (ok && cnt[1] > 0) ok = mbar_wait(&pv_done[1], (cnt[1] - 1) & 1, status);
-          if (!ok) break;
-          tc_fence_after();
-          scores(1, two ? 1 : 0, t1);
-          tc_commit(&empty[t1 % C::NK]);
-        } else {  // no such stage: the record alone
-          mbar_arrive(&s_full[1]);
-          mbar_arrive(&s_full[1]);
-        }
-        if (last) tc_commit(q_empty);
-        ok = weighted(0, t, pair, !two);
-        if (!ok) break;
-        pend = second;
-        pend_t = t1;
-        if (last) {  // nothing is left open between two pieces
-          ok = second ? weighted(1, t1, pair, true) : mbar_wait(&p_ready[1], pair & 1, status);
-          pend = 0;
-        }
-        t += second && !two ? 2 : 1;
+        t0 += even;
       }
       // every operation of this thread has completed before the tensor memory is released
-      tc_commit(drain);
-      mbar_wait(drain, 0, status);
+      tc_commit(&drain[x]);
+      mbar_wait(&drain[x], 0, status);
     }
     __syncwarp();
-  } else if (warp == 2 && !C::QUANT) {
-    // ------------------------------------------------------------ tokens that not everyone attends to
-    for (uint32_t t = 0;; ++t) {
-      const int s = C::NK + t % C::NV;
-      if (!__all_sync(FULL, mbar_wait(&full[s], (t / C::NV) & 1, status))) break;
-      const TreeStage &m = meta[t % C::META];
-      if (m.end) break;
-      if (m.masked) {
-        const int prefix = m.L - m.n, lo_max = a.window > 0 ? max(m.L - a.window, 0) : 0;
-        uint64_t bad_nodes = 0, bad_edge = 0;
-        uint8_t *v = smem + S::OFF_RING + s * C::SLOT;
-        for (int r = lane; r < BN; r += 32) {
-          const int tok = m.tok0 + r;
-          const bool any = tok >= m.lo_min && tok < m.tok_hi && ((loaded_bits(m.badmask, r >> 5, a.log2_bh) >> (r & 31)) & 1u);
-          const bool some = tok >= prefix || tok < lo_max;  // seen by some nodes and not by others
-          if (any && !some) continue;
-          bool found = false;
-#pragma unroll 4
-          for (int c = 0; c < C::NPL * 8; ++c) {
-            uint4 *p = reinterpret_cast<uint4 *>(v + (c >> 3) * C::PLANE + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-            if (!any) {
-              *p = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 x = *p;
-            uint32_t w[4] = {x.x, x.y, x.z, x.w}, hit = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {  // exponents of all ones: infinities and NaN
-              const uint32_t bits = ((w[e] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w[e] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
-              hit |= bits;
-              w[e] &= ~bits;
-            }
-            if (hit) {
-              found = true;
-              *p = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          if (found) {
-            if (tok >= prefix) bad_nodes |= 1ull << (tok - prefix);
-            else bad_edge |= 1ull << (tok - m.lo_min);
-          }
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-          bad_nodes |= __shfl_xor_sync(FULL, bad_nodes, o);
-          bad_edge |= __shfl_xor_sync(FULL, bad_edge, o);
-        }
-        if (lane == 0) {
-          nf[(t % C::META) * 2] = bad_nodes;
-          nf[(t % C::META) * 2 + 1] = bad_edge;
-        }
-        fence_proxy_async_smem();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&clean[t % C::META]);
-    }
-  } else if (warp == 2) {
-    // (idle: the converting warps look over the V tiles)
   } else if (warp == 3) {
-    // ------------------------------------------------------------ query tiles
+    // ------------------------------------------------------------ query tiles; V tiles looked over (bf16)
     TreeWalker walker(a, &misc->part, lane);
     TreePiece pc;
-    uint32_t k = 0;
-    while (walker.take<C::QT>(pc)) {
-      if (k > 0 && !__all_sync(FULL, mbar_wait(q_empty, (k - 1) & 1, status))) break;
+    uint32_t k = 0, t = 0;
+    const int nbox = BN >> a.log2_bh;
+    bool ok = true;
+    while (ok && walker.take<C::QT>(pc)) {
+      if (k > 0) ok = __all_sync(FULL, mbar_wait(q_empty, (k - 1) & 1, status));
+      if (!ok) break;
+      const int stages = (pc.ue - pc.ub + nbox - 1) / nbox;
+      const TreeRow row = {pc.start, pc.n, pc.L};
+      const int prefix = pc.L - pc.n, lo_min = tree_lo(a, row), lo_max = a.window > 0 ? max(pc.L - a.window, 0) : 0;
       if (lane == 0) {
+        prec[k & 1] = TreePieceRec{0, stages, pc.two, tree_slot(pc, (int)k), pc.b, pc.L, pc.n, pc.start, pc.t0, pc.g, lo_min, 0};
         const int boxes = min(a.qt, a.max_query) * a.gt * 128;  // bytes of one plane's box
         mbar_arrive_expect_tx(q_full, (uint32_t)(C::NPL * boxes * (pc.two ? 2 : 1)));
         for (int x = 0; x < (pc.two ? 2 : 1); ++x) {
@@ -931,8 +864,71 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
       __syncwarp();
       ++k;
+      if constexpr (!C::QUANT) {
+        for (int st = 0; st < ((stages + 1) & ~1) && ok; ++st, ++t) {
+          const int s = C::NK + t % C::NV;
+          ok = __all_sync(FULL, mbar_wait(&full[s], (t / C::NV) & 1, status));
+          if (!ok) break;
+          const int4 m = *reinterpret_cast<const int4 *>(&meta[t % C::META]);  // flags, tok0, tok_hi, badmask
+          if (m.x & STAGE_MASKED) {
+            uint64_t bad_nodes = 0, bad_edge = 0;
+            uint8_t *v = smem + S::OFF_RING + s * C::SLOT;
+            for (int r = lane; r < BN; r += 32) {
+              const int tok = m.y + r;
+              const bool any = tok >= lo_min && tok < m.z && ((loaded_bits((uint32_t)m.w, r >> 5, a.log2_bh) >> (r & 31)) & 1u);
+              const bool some = tok >= prefix || tok < lo_max;  // seen by some nodes and not by others
+              if (any && !some) continue;
+              bool found = false;
+#pragma unroll 4
+              for (int c = 0; c < C::NPL * 8; ++c) {
+                uint4 *p = reinterpret_cast<uint4 *>(v + (c >> 3) * C::PLANE + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                if (!any) {
+                  *p = make_uint4(0, 0, 0, 0);
+                  continue;
+                }
+                uint4 x = *p;
+                uint32_t w[4] = {x.x, x.y, x.z, x.w}, hit = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {  // exponents of all ones: infinities and NaN
+                  const uint32_t bits = ((w[e] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w[e] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+                  hit |= bits;
+                  w[e] &= ~bits;
+                }
+                if (hit) {
+                  found = true;
+                  *p = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
+              if (found) {
+                if (tok >= prefix) bad_nodes |= 1ull << (tok - prefix);
+                else bad_edge |= 1ull << (tok - lo_min);
+              }
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) {
+              bad_nodes |= __shfl_xor_sync(FULL, bad_nodes, o);
+              bad_edge |= __shfl_xor_sync(FULL, bad_edge, o);
+            }
+            if (lane == 0) {
+              nf[(t % C::META) * 2] = bad_nodes;
+              nf[(t % C::META) * 2 + 1] = bad_edge;
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&clean[t % C::META]);
+        }
+      }
     }
-    if (k > 0) mbar_wait(q_full, (k - 1) & 1, status);  // no copy is in flight when the CTA exits
+    // no copy is in flight when the CTA exits, and the issuing threads learn of the end
+    if (k > 0) {
+      mbar_wait(q_full, (k - 1) & 1, status);
+      if (ok) ok = __all_sync(FULL, mbar_wait(q_empty, (k - 1) & 1, status));
+    }
+    if (ok && lane == 0) {
+      prec[k & 1].end = 1;
+      mbar_arrive(q_full);
+    }
   }
   } else if (warp >= 4 + C::SOFTMAX_WARPS) {
     if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_CONVERT>();
@@ -942,24 +938,35 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // reads nor the writes of eight lanes meet in a bank.
     if constexpr (C::QUANT) {
       const int ct = tid - (4 + C::SOFTMAX_WARPS) * 32, cw = ct >> 5;
-      constexpr int TPR = D / 16, NTASK = BN * TPR, STEP = C::CONVERT_WARPS * 32;
-      static_assert(NTASK % (4 * STEP) == 0 && STEP % TPR == 0, "whole rounds of four tasks");
-      uint32_t kp = 0;  // pieces begun
+      constexpr int TPR = D / 16, NTASK = BN * TPR, STEP = C::TILE_WARPS * 32, ROUND = 8;
+      static_assert(NTASK % (ROUND * STEP) == 0 && STEP % TPR == 0, "whole rounds of tasks");
+      const int kv = cw / C::TILE_WARPS, tt = ct % STEP;  // this warp's kind of tile; the thread among its warps'
+      uint32_t kp = 0, left = 0;  // pieces begun; stages left of the current one
+      int prefix = 0, lo_min = 0, lo_max = 0;
       for (uint32_t t = 0;; ++t) {
-        bool end = false, ok = true;
-        for (int kv = 0; kv < 2 && ok && !end; ++kv) {
-          const uint32_t f = 2 * t + kv;
-          const int rs = f % C::NR;
-          ok = __all_sync(FULL, mbar_wait(&raw_full[rs], (f / C::NR) & 1, status));
-          if (!ok) break;
-          const TreeStage &m = meta[t % C::META];
-          end = m.end;
-          if (kv == 0 && !end && m.first) {
-            // the piece's query rows: times 2^s (largest magnitude in [2^14, 2^15)) to f16, in place
+        const uint32_t f = 2 * t + kv;
+        const int rs = f % C::NR;
+        bool ok = __all_sync(FULL, mbar_wait(&raw_full[rs], (f / C::NR) & 1, status));
+        if (!ok) break;
+        const int4 m = *reinterpret_cast<const int4 *>(&meta[t % C::META]);  // flags, tok0, tok_hi, badmask
+        {
+          if (left == 0) {
+            // a new piece, or the end
             ok = __all_sync(FULL, mbar_wait(q_full, kp & 1, status));
             if (!ok) break;
+            const TreePieceRec &r = prec[kp & 1];
+            if (r.end) {
+              if (lane == 0) mbar_arrive(q_conv);
+              break;
+            }
+            left = (uint32_t)(r.stages + 1) & ~1u;
+            prefix = r.L - r.n;
+            lo_min = r.lo_min;
+            lo_max = a.window > 0 ? max(r.L - a.window, 0) : 0;
+            const bool two = r.two != 0;
+            // the piece's query rows: times 2^s (largest magnitude in [2^14, 2^15)) to f16, in place
             int8_t *shift = reinterpret_cast<int8_t *>(smem + S::OFF_SHIFT) + (kp & 1) * (C::QT * kTreeRows);
-            for (int r = ct; r < (m.two ? 2 : 1) * kTreeRows; r += STEP) {
+            for (int r = ct; r < (two ? 2 : 1) * kTreeRows; r += C::CONVERT_WARPS * 32) {
               uint8_t *row = smem + (r >> 7) * (C::NPL * C::QPLANE) + (r & 127) * 128;
               float amax = 0.f;
 #pragma unroll 4
@@ -994,14 +1001,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const uint32_t u = kv ? t / C::NV : t / C::NK;
           if (u > 0) ok = __all_sync(FULL, mbar_wait(&empty[s], (u - 1) & 1, status));
           if (!ok) break;
-          if (end) {  // handed on to the issuing thread
-            if (lane == 0) mbar_arrive(&full[s]);
-            break;
-          }
+          --left;
           const uint8_t *raw = smem + S::OFF_RAW + rs * C::RAW_SLOT;
           uint8_t *op = smem + S::OFF_RING + s * C::SLOT;
-          const bool look = kv == 1 && m.masked;
-          const int prefix = m.L - m.n, lo_max = a.window > 0 ? max(m.L - a.window, 0) : 0;
+          const bool look = kv == 1 && (m.x & STAGE_MASKED);
           uint64_t bad_nodes = 0, bad_edge = 0;
           auto put = [&](int r, int pc, const uint32_t (&h)[8]) {
             uint8_t *row = op + (pc >> 2) * C::PLANE + r * 128;
@@ -1010,16 +1013,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             *reinterpret_cast<uint4 *>(row + (((c0 + sw) ^ (r & 7)) << 4)) = sw ? hi : lo;
             *reinterpret_cast<uint4 *>(row + (((c0 + 1 - sw) ^ (r & 7)) << 4)) = sw ? lo : hi;
           };
-          // a thread's tasks lie STEP / TPR rows apart, at the same place of the row; four loads in flight
-          const int pc = ct % TPR, r0 = ct / TPR;
-          if (!look) {
+          // a thread's tasks lie STEP / TPR rows apart, at the same place of the row; eight loads in flight
+          const int pc = tt % TPR, r0 = tt / TPR;
+          if (m.x & STAGE_ABSENT) {
+            // nothing is there
+          } else if (!look) {
 #pragma unroll 1
-            for (int i0 = 0; i0 < NTASK / STEP; i0 += 4) {
-              Codes16<C::FMT, D> x[4];
+            for (int i0 = 0; i0 < NTASK / STEP; i0 += ROUND) {
+              Codes16<C::FMT, D> x[ROUND];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[e].load(raw + (r0 + (i0 + e) * (STEP / TPR)) * C::ROWB, pc);
+              for (int e = 0; e < ROUND; ++e) x[e].load(raw + (r0 + (i0 + e) * (STEP / TPR)) * C::ROWB, pc);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
+              for (int e = 0; e < ROUND; ++e) {
                 uint32_t h[8];
                 x[e].convert(h);
                 put(r0 + (i0 + e) * (STEP / TPR), pc, h);
@@ -1028,12 +1033,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           } else {
 #pragma unroll 1
             for (int i = 0; i < NTASK / STEP; ++i) {
-              const int r = r0 + i * (STEP / TPR), tok = m.tok0 + r;
+              const int r = r0 + i * (STEP / TPR), tok = m.y + r;
               Codes16<C::FMT, D> x;
               uint32_t h[8];
               x.load(raw + r * C::ROWB, pc);
               x.convert(h);
-              const bool any = tok >= m.lo_min && tok < m.tok_hi && ((loaded_bits(m.badmask, r >> 5, a.log2_bh) >> (r & 31)) & 1u);
+              const bool any = tok >= lo_min && tok < m.z && ((loaded_bits((uint32_t)m.w, r >> 5, a.log2_bh) >> (r & 31)) & 1u);
               if (!any) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) h[e] = 0u;
@@ -1048,7 +1053,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 if (hit) {
                   if (tok >= prefix) bad_nodes |= 1ull << (tok - prefix);
-                  else bad_edge |= 1ull << (tok - m.lo_min);
+                  else bad_edge |= 1ull << (tok - lo_min);
                 }
               }
               put(r, pc, h);
@@ -1061,8 +1066,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               bad_edge |= __shfl_xor_sync(FULL, bad_edge, o);
             }
             if (lane == 0) {
-              nf[((t % C::META) * C::CLEAN_WARPS + cw) * 2] = bad_nodes;
-              nf[((t % C::META) * C::CLEAN_WARPS + cw) * 2 + 1] = bad_edge;
+              const int w = cw % C::TILE_WARPS;
+              nf[((t % C::META) * C::CLEAN_WARPS + w) * 2] = bad_nodes;
+              nf[((t % C::META) * C::CLEAN_WARPS + w) * 2 + 1] = bad_edge;
             }
           }
           fence_proxy_async_smem();
@@ -1073,7 +1079,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (kv == 1) mbar_arrive(&clean[t % C::META]);
           }
         }
-        if (end || !ok) break;
       }
     }
   } else {
@@ -1089,17 +1094,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint64_t eff = 0, bad_nodes = 0, bad_edge = 0;
     int lo_row = 0, prefix = 0, node_tok = 0, head = 0, start = 0, n = 0, lo_min = 0, b = 0, slot = -1, g = 0, prow = 0;
     bool real = false, warp_real = false, had = false;  // had: this group's output has had a product in the piece
-    uint32_t cnt[2] = {0, 0}, k_half = 0;
-    uint32_t t = 0;
+    uint32_t c = 0, k_half = 0;  // items done; merges
+    uint32_t t0 = 0;             // the piece's first stage
     bool ok = true;
+    auto buf = [&](uint32_t i) { return C::GROUPS == 2 ? (uint32_t)grp : i & 1; };
+    auto par = [&](uint32_t i) { return C::GROUPS == 2 ? i & 1 : (i >> 1) & 1; };
 
-    auto item = [&](int x, uint32_t tt) -> bool {
-      const TreeStage &m = meta[tt % C::META];
-      const uint32_t tS = tl_base + C::TM_S + x * BN;
+    // the group's next item: stage tt, whose record is m (flags, tok0, tok_hi, badmask)
+    auto item = [&](uint32_t tt, int4 m) -> bool {
+      const uint32_t tS = tl_base + C::TM_S + buf(c) * BN;
       const int o = C::GROUPS == 2 ? grp : 0;
       const uint32_t tO = tl_base + C::TM_O + o * D;
-      if (warp_real) {
-        const bool masked = m.masked;
+      if (warp_real && !(m.x & STAGE_ABSENT)) {
+        const bool masked = m.x & STAGE_MASKED;
         uint32_t vis[BN / 32];
         if (masked) {
           if (!mbar_wait(&clean[tt % C::META], (tt / C::META) & 1, status)) return false;
@@ -1111,9 +1118,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
 #pragma unroll
           for (int c = 0; c < BN / 32; ++c) {
-            const int base = m.tok0 + 32 * c;
-            vis[c] = (range_bits(base, lo_row, prefix) | mask_bits(eff, prefix, base)) & range_bits(base, 0, m.tok_hi) &
-                     loaded_bits(m.badmask, c, a.log2_bh);
+            const int base = m.y + 32 * c;
+            vis[c] = (range_bits(base, lo_row, prefix) | mask_bits(eff, prefix, base)) & range_bits(base, 0, m.z) &
+                     loaded_bits((uint32_t)m.w, c, a.log2_bh);
           }
         }
         // 64 columns of the row (those from 64 h on): read, turned, masked; returns their maximum
@@ -1142,8 +1149,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           m_run = mx;
         } else if (__any_sync(FULL, real && m_run != -INFINITY && mx > m_run + C::TAU)) {
           // raise the maximum: the output so far is scaled, once its products are complete
-          const int px = C::GROUPS == 2 ? x : x ^ 1;  // the buffer of the output's previous item
-          if (!mbar_wait(&pv_done[px], (cnt[px] - 1) & 1, status)) return false;
+          if (!mbar_wait(&pv_done[buf(c - 1)], par(c - 1), status)) return false;
           __syncwarp();
           tc_fence_after();
           const float mn = fmaxf(m_run, mx);
@@ -1187,96 +1193,79 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         l2[0] = add_pair(l2[0], l2[1]);
         l_run += l2[0].x + l2[0].y;
         tc_wait_st();
+        had = true;
       }
-      had = true;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_ready[x]);
+      if (lane == 0) mbar_arrive(&p_ready[buf(c)]);
+      ++c;
       return true;
     };
 
-    for (uint32_t p = 0; ok; ++p) {
-      bool last = false, two = false;
-      uint32_t step = 1;
-#pragma unroll
-      for (int xi = 0; xi < 2; ++xi) {
-        if (C::GROUPS == 2 && xi != grp) continue;
-        if (!mbar_wait(&s_full[xi], p & 1, status)) {
-          ok = false;
-          break;
+    while (ok) {
+      // a new piece: its record comes with its first item
+      if (!mbar_wait(&s_full[buf(c)], par(c), status)) break;
+      __syncwarp();
+      tc_fence_after();
+      const int4 *rp = reinterpret_cast<const int4 *>(&prec[kp & 1]);
+      const int4 r0 = rp[0], r1 = rp[1], r2 = rp[2];
+      if (r0.x) break;
+      const uint32_t stages = (uint32_t)r0.y, even = (stages + 1) & ~1u;
+      const bool two = r0.z != 0;
+      slot = r0.w;
+      b = r1.x;
+      n = r1.z;
+      prefix = r1.y - n;
+      start = r1.w;
+      g = r2.y;
+      lo_min = r2.z;
+      {
+        const int tx = two ? grp : 0;
+        const TreeTile tile = tree_tile(a, r2.x + tx, n);
+        const int pos = row / a.gt, h = row - pos * a.gt;
+        real = pos < tile.nq && h < tile.nh;
+        warp_real = __any_sync(FULL, real);
+        prow = tx * kTreeRows + row;
+        if constexpr (C::QUANT) {  // the scores are 2^s times too large
+          const int sh = reinterpret_cast<const int8_t *>(smem + S::OFF_SHIFT)[(kp & 1) * (C::QT * kTreeRows) + prow];
+          qs = scale * __uint_as_float((uint32_t)(127 - sh) << 23);
         }
-        __syncwarp();
-        tc_fence_after();
-        const TreeStage &m = meta[t % C::META];
-        if (m.end) {
-          ok = false;
-          break;
-        }
-        two = m.two;
-        const int left = m.left;
-        last = two ? left == 0 : left <= 1;
-        step = two ? 1 : left >= 1 ? 2 : 1;
-        if (m.first && (C::GROUPS == 2 || xi == 0)) {
-          // a new piece: this thread's row
-          b = m.b;
-          start = m.start;
-          n = m.n;
-          prefix = m.L - n;
-          lo_min = m.lo_min;
-          slot = m.slot;
-          g = m.g;
-          const int tx = two ? grp : 0;
-          const TreeTile tile = tree_tile(a, m.t0 + tx, n);
-          const int pos = row / a.gt, h = row - pos * a.gt;
-          real = pos < tile.nq && h < tile.nh;
-          warp_real = __any_sync(FULL, real);
-          prow = tx * kTreeRows + row;
-          if constexpr (C::QUANT) {  // the scores are 2^s times too large
-            const int sh = reinterpret_cast<const int8_t *>(smem + S::OFF_SHIFT)[(kp & 1) * (C::QT * kTreeRows) + prow];
-            qs = scale * __uint_as_float((uint32_t)(127 - sh) << 23);
-          }
-          ++kp;
-          head = g * a.G + tile.h0 + h;
-          node_tok = start + tile.i0 + pos;
-          eff = 0;
-          lo_row = 0;
-          if (real) {
-            const uint64_t keep = n < 64 ? (1ull << n) - 1 : ~0ull;
-            const int node = tile.i0 + pos;
-            eff = a.tree_mask[node_tok] & keep;
-            if (a.window > 0) {
-              const int depth = __popcll(eff & ~(1ull << node));
-              lo_row = max(prefix + depth - a.window + 1, 0);
-              for (uint64_t rest = eff; rest; rest &= rest - 1) {
-                const int j = __ffsll((long long)rest) - 1;
-                const uint64_t mj = a.tree_mask[start + j] & keep;
-                if (depth - __popcll(mj & ~(1ull << j)) >= a.window) eff &= ~(1ull << j);
-              }
+        head = g * a.G + tile.h0 + h;
+        node_tok = start + tile.i0 + pos;
+        eff = 0;
+        lo_row = 0;
+        if (real) {
+          const uint64_t keep = n < 64 ? (1ull << n) - 1 : ~0ull;
+          const int node = tile.i0 + pos;
+          eff = a.tree_mask[node_tok] & keep;
+          if (a.window > 0) {
+            const int depth = __popcll(eff & ~(1ull << node));
+            lo_row = max(prefix + depth - a.window + 1, 0);
+            for (uint64_t rest = eff; rest; rest &= rest - 1) {
+              const int j = __ffsll((long long)rest) - 1;
+              const uint64_t mj = a.tree_mask[start + j] & keep;
+              if (depth - __popcll(mj & ~(1ull << j)) >= a.window) eff &= ~(1ull << j);
             }
           }
-          m_run = -INFINITY;
-          l_run = 0.f;
-          bad_nodes = bad_edge = 0;
-          had = false;
-        }
-        if (two || xi == 0 || left >= 1) {
-          if (!item(xi, two ? t : t + xi)) {
-            ok = false;
-            break;
-          }
-        } else {  // no such stage: only that the record was read
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_ready[xi]);
-        }
-        if (C::GROUPS == 1 && (xi == 0 || left >= 1)) ++cnt[xi];
-        if (C::GROUPS == 2) {  // both buffers' items are counted: the merge waits for the other's too
-          ++cnt[0];
-          if (two || left >= 1) ++cnt[1];
         }
       }
+      ++kp;
+      m_run = -INFINITY;
+      l_run = 0.f;
+      bad_nodes = bad_edge = 0;
+      had = false;
+      const uint32_t j0 = C::GROUPS == 2 && !two ? (uint32_t)grp : 0, dj = C::GROUPS == 2 && !two ? 2 : 1;
+      for (uint32_t j = j0; j < even && ok; j += dj) {
+        if (j != j0) {
+          ok = mbar_wait(&s_full[buf(c)], par(c), status);
+          if (!ok) break;
+          __syncwarp();
+          tc_fence_after();
+        }
+        ok = item(t0 + j, *reinterpret_cast<const int4 *>(&meta[(t0 + j) % C::META]));
+      }
       if (!ok) break;
-      t += step;
-      if (!last) continue;
+      t0 += even;
 
       // ---- end of a piece
       TreeHalf other = {-INFINITY, 0.f, 0, 0};
@@ -1292,10 +1281,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         bad_nodes |= other.bad_nodes;
         bad_edge |= other.bad_edge;
       }
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (cnt[x] > 0 && (C::GROUPS == 1 || merge || x == grp) && !mbar_wait(&pv_done[x], (cnt[x] - 1) & 1, status))
-          ok = false;
+      // the products of the last items, and with them all before, are complete; both groups have as many items
+      ok = mbar_wait(&pv_done[buf(c - 1)], par(c - 1), status);
+      if (merge && ok) ok = mbar_wait(&pv_done[grp ^ 1], par(c - 1), status);
       if (!ok) break;
       __syncwarp();
       tc_fence_after();
