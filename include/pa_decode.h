@@ -413,7 +413,7 @@ int pa_mla_cache_write(const void *c_lat, const void *k_rope, const int64_t *slo
  * with held_pages out of range gives nothing back and sets PA_DEV_BAD_LEN.  A
  * parent out of order sets PA_DEV_BAD_TREE and counts as -1; a page outside
  * [0, num_pages) sets PA_DEV_BAD_PAGE and gives slot -1.
- * batch in [0, 8192] and max_pages_per_seq * page_size below 2^31 (more:
+ * batch in [0, 8192], max_pages_per_seq * page_size and * batch below 2^31 (more:
  * PA_ERR_UNSUPPORTED); page_size >= 1; status: a device word or NULL, whose bits
  * are only ever set.  batch == 0 writes query_start[0],
  * the padding and free_count_out.

@@ -43,50 +43,50 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Exclusive scan over the CTA's threads of three 64-bit values; the totals in sum.
-__device__ __forceinline__ void block_scan3(long long (&v)[3], long long (&sum)[3], long long (*part)[3]) {
+// Exclusive scan over the CTA's threads of a 64-bit and two 32-bit values; the totals in *sum.
+struct PlanSums {
+  long long tokens;
+  int given, need;
+};
+template <typename T>
+__device__ __forceinline__ T lanes_scan(T x) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T u = __shfl_up_sync(FULL, x, o);
+    if ((int)(threadIdx.x & 31) >= o) x += u;
+  }
+  return x;
+}
+__device__ __forceinline__ PlanSums block_scan(PlanSums v, PlanSums *sum, PlanSums *part) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x[3];
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    x[k] = v[k];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(FULL, x[k], o);
-      if (lane >= o) x[k] += u;
-    }
-    if (lane == 31) part[warp][k] = x[k];
-  }
+  const PlanSums x = {lanes_scan(v.tokens), lanes_scan(v.given), lanes_scan(v.need)};
+  if (lane == 31) part[warp] = x;
   __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    // the warps' sums: lane w has warp w's
-    long long s = lane < kPlanThreads / 32 ? part[lane][k] : 0, p = s;
-#pragma unroll
-    for (int o = 1; o < kPlanThreads / 32; o <<= 1) {
-      const long long u = __shfl_up_sync(FULL, p, o);
-      if (lane >= o) p += u;
-    }
-    sum[k] = __shfl_sync(FULL, p, kPlanThreads / 32 - 1);
-    v[k] = __shfl_sync(FULL, p - s, warp) + x[k] - v[k];
-  }
+  // the warps' sums: lane w has warp w's
+  const PlanSums s = lane < kPlanThreads / 32 ? part[lane] : PlanSums{0, 0, 0};
+  const PlanSums p = {lanes_scan(s.tokens), lanes_scan(s.given), lanes_scan(s.need)};
+  *sum = {__shfl_sync(FULL, p.tokens, 31), __shfl_sync(FULL, p.given, 31), __shfl_sync(FULL, p.need, 31)};
+  const PlanSums before = {__shfl_sync(FULL, p.tokens - s.tokens, warp), __shfl_sync(FULL, p.given - s.given, warp),
+                           __shfl_sync(FULL, p.need - s.need, warp)};
   __syncthreads();
+  return {before.tokens + x.tokens - v.tokens, before.given + x.given - v.given, before.need + x.need - v.need};
 }
 
 struct PlanTotals {
   int count, top, total;  // free pages before; with the given ones; tokens
+  int need;               // pages needed by all rows
 };
 
 // All rows into shared memory, with the sums before each (every CTA of the plan does this for itself: the
 // lengths are few, and to hand the sums over would take a launch).
-__device__ __forceinline__ PlanTotals plan_rows(const PlanArgs &a, PlanRow *rows, long long (*part)[3], uint32_t &bad) {
+__device__ __forceinline__ PlanTotals plan_rows(const PlanArgs &a, PlanRow *rows, PlanSums *part, uint32_t &bad) {
   const int tid = threadIdx.x, P = a.page_size;
   const int free0 = *a.free_count;
-  long long sums[3] = {0, 0, 0};  // tokens, pages given, pages needed
+  PlanSums sums;
   // a row's need is 0 where its tokens pass max_tokens, which only the sum of the tokens tells: the first pass
   // takes that as not so, and a second follows in the rare call where it is
   for (int pass = 0; pass < 2; ++pass) {
-    sums[0] = sums[1] = sums[2] = 0;
+    sums = {0, 0, 0};
     for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
       const int b = b0 + tid;
       int ctx = 0, n = 0, held = 0;
@@ -96,34 +96,36 @@ __device__ __forceinline__ PlanTotals plan_rows(const PlanArgs &a, PlanRow *rows
         held = a.held_pages[b];
       }
       const bool ended = n < 0, held_ok = held >= 0 && held <= a.max_pages_per_seq;
-      const long long add = max(n, 0), pages = ((long long)ctx + add + P - 1) / P;  // pages behind this step
-      bool ok = ctx >= 0 && held_ok && pages <= a.max_pages_per_seq;
+      const long long add = max(n, 0);
+      bool ok = ctx >= 0 && held_ok && ctx + add <= INT_MAX - P;
+      const int pages = ok ? (int)(((unsigned)ctx + (unsigned)add + (unsigned)P - 1u) / (unsigned)P) : 0;  // behind this step
+      ok = ok && pages <= a.max_pages_per_seq;
       if (pass > 0) ok = ok && b < a.batch && rows[b].start + add <= a.max_tokens;
       if (ended ? !held_ok : !ok) bad |= PA_DEV_BAD_LEN;
-      const long long need = ok && n > 0 ? max(pages - held, 0ll) : 0;
-      long long v[3] = {add, ended && held_ok ? held : 0, need}, all[3];
-      block_scan3(v, all, part);
+      const int need = ok && n > 0 ? max(pages - held, 0) : 0;
+      PlanSums all;
+      const PlanSums v = block_scan({add, ended && held_ok ? held : 0, need}, &all, part);
       if (b < a.batch) {
         PlanRow r;
         r.ctx = ctx;
         r.held = held_ok ? held : 0;
-        r.start = (int)min(sums[0] + v[0], (long long)INT_MAX);
-        r.need = ended ? PLAN_ENDED : ok ? (int)need : PLAN_REFUSED;
-        r.first = (int)min(sums[2] + v[2], (long long)INT_MAX);
-        r.given = (int)min(sums[1] + v[1], (long long)INT_MAX);
+        r.start = (int)min(sums.tokens + v.tokens, (long long)INT_MAX);
+        r.need = ended ? PLAN_ENDED : ok ? need : PLAN_REFUSED;
+        r.first = sums.need + v.need;
+        r.given = sums.given + v.given;
         rows[b] = r;
       }
-#pragma unroll
-      for (int k = 0; k < 3; ++k) sums[k] += all[k];
+      sums = {sums.tokens + all.tokens, sums.given + all.given, sums.need + all.need};
     }
-    if (sums[0] <= a.max_tokens) break;
+    if (sums.tokens <= a.max_tokens) break;
   }
   PlanTotals t;
   t.count = min(max(free0, 0), a.num_pages);
   if (free0 != t.count) bad |= PA_DEV_BAD_LEN;
-  if (t.count + sums[1] > a.num_pages) bad |= PA_DEV_BAD_LEN;  // more pages than there are: the ones past the list are lost
-  t.top = (int)min(t.count + sums[1], (long long)a.num_pages);
-  t.total = (int)min(sums[0], (long long)INT_MAX);
+  if ((long long)t.count + sums.given > a.num_pages) bad |= PA_DEV_BAD_LEN;  // more pages than there are: the ones past the list are lost
+  t.top = (int)min((long long)t.count + sums.given, (long long)a.num_pages);
+  t.total = (int)min(sums.tokens, (long long)INT_MAX);
+  t.need = sums.need;
   if (tid == 0) rows[a.batch].start = t.total;
   __syncthreads();
   return t;
@@ -133,100 +135,105 @@ __device__ __forceinline__ bool plan_granted(const PlanRow &r, int top) {
   return r.need == 0 || (r.need > 0 && (long long)r.first + r.need <= top);
 }
 
-// Page j of the step: entry top - 1 - j of the list with the given pages on it.  Those are taken from the ended
-// rows' own table entries, so that no CTA waits for another to have pushed them.
-__device__ __forceinline__ int plan_page(const PlanArgs &a, const PlanRow *rows, const PlanTotals &t, int j) {
-  const int s = t.top - 1 - j;
-  if (s < t.count) return a.free_list[s];
-  const int r = s - t.count;
-  int lo = 0, hi = a.batch - 1;  // the last row with at most r pages given before it
+// The last row with key at most x.
+template <int32_t PlanRow::*key>
+__device__ __forceinline__ int plan_find(const PlanRow *rows, int batch, int x) {
+  int lo = 0, hi = batch - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (rows[mid].given <= r) lo = mid;
+    if (rows[mid].*key <= x) lo = mid;
     else hi = mid - 1;
   }
-  return a.block_table[(size_t)lo * a.max_pages_per_seq + (r - rows[lo].given)];
+  return lo;
 }
 
-// The rows' state after the step (one CTA): what may be updated in place.
-__device__ __forceinline__ void plan_state(const PlanArgs &a, const PlanRow *rows, const PlanTotals &t, long long (*part)[3]) {
-  const int tid = threadIdx.x;
-  long long taken = 0;  // the needs are granted up to the first that passes the list, in row order
-  for (int b = tid; b < a.batch; b += kPlanThreads) {
-    const PlanRow r = rows[b];
-    const bool ok = plan_granted(r, t.top), ended = r.need == PLAN_ENDED;
-    a.context_lens_out[b] = ended ? 0 : ok ? r.ctx + (rows[b + 1].start - r.start) : r.ctx;
-    // (a refused row keeps what it said, a bad count included)
-    if (ended) a.held_pages_out[b] = 0;
-    else if (ok) a.held_pages_out[b] = r.held + r.need;
-    else if (a.held_pages_out != a.held_pages) a.held_pages_out[b] = a.held_pages[b];
-    if (ok && r.need > 0) taken = max(taken, (long long)r.first + r.need);
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) taken = max(taken, __shfl_xor_sync(FULL, taken, o));
-  if ((tid & 31) == 0) part[tid >> 5][0] = taken;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kPlanThreads / 32; ++w) taken = max(taken, part[w][0]);
-    *a.free_count_out = t.top - (int)taken;
-  }
+// Page r of those given back, from its ended row's own table entries.
+__device__ __forceinline__ int plan_given(const PlanArgs &a, const PlanRow *rows, int r) {
+  const int b = plan_find<&PlanRow::given>(rows, a.batch, r);
+  return a.block_table[(size_t)b * a.max_pages_per_seq + (r - rows[b].given)];
 }
 
-// A few thousand integers in and out, bound by the launch and by the few dependent trips to memory.  STATE: the
-// grid is one cluster, whose CTAs meet once, when all have read all of their inputs, before the state that may
-// be updated in place is written (the smaller steps).  Otherwise (more than kPlanMaxCluster chunks of tokens) the
-// CTAs are independent and plan_state_kernel follows.  Each CTA writes its share of the rows' table entries and
-// of the tokens; what it reads of the table and of the list is what no CTA writes.
-template <bool STATE>
+// Page j of the step: entry top - 1 - j of the list with the given pages on it, without waiting for anyone to have
+// put them there.
+__device__ __forceinline__ int plan_page(const PlanArgs &a, const PlanRow *rows, const PlanTotals &t, int j) {
+  const int s = t.top - 1 - j;
+  return s < t.count ? a.free_list[s] : plan_given(a, rows, s - t.count);
+}
+
+// Row b's state after the step, and with it (one row's) the count of the free pages: what may be updated in place.
+// The needs are granted, in row order, up to the first that passes the list; of the refused rows only that one has
+// no more than the list before it.
+__device__ __forceinline__ void plan_state(const PlanArgs &a, const PlanRow *rows, const PlanTotals &t, int b) {
+  const PlanRow r = rows[b];
+  const bool ok = plan_granted(r, t.top), ended = r.need == PLAN_ENDED;
+  a.context_lens_out[b] = ended ? 0 : ok ? r.ctx + (rows[b + 1].start - r.start) : r.ctx;
+  // (a refused row keeps what it said, a bad count included)
+  if (ended) a.held_pages_out[b] = 0;
+  else if (ok) a.held_pages_out[b] = r.held + r.need;
+  else if (a.held_pages_out != a.held_pages) a.held_pages_out[b] = a.held_pages[b];
+  if (r.need > 0 && !ok && r.first <= t.top) *a.free_count_out = t.top - r.first;
+}
+__device__ __forceinline__ void plan_state_all_granted(const PlanArgs &a, const PlanTotals &t) {
+  if (t.need <= t.top) *a.free_count_out = t.top - (int)t.need;
+}
+
+// A few thousand integers in and out, bound by the launch and by the few dependent trips to memory.  The CTAs are
+// independent: each has all rows' sums, writes its share of the rows' table entries and of the tokens, and reads of
+// the table and the list what no CTA writes.  Only state that is updated in place makes them meet: with few CTAs
+// (PLAN_CLUSTER) at a barrier of the one cluster that they form, when all have read all of their inputs, with many
+// (PLAN_AFTER) in a launch of its own behind this one.
+enum PlanMode { PLAN_APART = 0, PLAN_CLUSTER = 1, PLAN_AFTER = 2 };
+template <int MODE>
 __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs a) {
   extern __shared__ PlanRow rows[];  // [batch + 1]: the last one holds the total of the tokens
-  __shared__ long long part[kPlanThreads / 32][3];
+  __shared__ PlanSums part[kPlanThreads / 32];
   __shared__ int8_t up[kTreeNodes - 1 + kPlanThreads];  // parents of the chunk's tokens and 63 before it
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x;
   const int rank = (int)blockIdx.x, nranks = (int)gridDim.x;
   const int P = a.page_size;
   uint32_t bad = 0;
+  // the chunk's parents, whose loads go along with the lengths' (entries behind the last row are not looked at)
+  auto load_parents = [&](int t0) {
+    for (int e = tid; e < kTreeNodes - 1 + kPlanThreads; e += kPlanThreads) {
+      const int s = t0 - (kTreeNodes - 1) + e;
+      const int p = s >= 0 && s < a.max_tokens ? a.parents[s] : -1;
+      up[e] = (int8_t)(p < -1 || p >= kTreeNodes ? -2 : p);
+    }
+  };
+  if (a.parents) load_parents(rank * kPlanThreads);
   const PlanTotals tot = plan_rows(a, rows, part, bad);
   const int total = tot.total;
-  if constexpr (STATE) cluster_barrier();
+  if constexpr (MODE == PLAN_CLUSTER) cluster_barrier();
 
-  // rows, one warp each: the ended ones' pages go onto the list, new pages into the table
-  const int nwarps = nranks * (kPlanThreads / 32), warp = rank * (kPlanThreads / 32) + (tid >> 5);
-  for (int b = warp; b < a.batch; b += nwarps) {
-    const PlanRow r = rows[b];
-    int32_t *bt = a.block_table + (size_t)b * a.max_pages_per_seq;
-    if (lane == 0) a.query_start[b] = r.start;
-    if (r.need == PLAN_ENDED) {
-      for (int j = lane; j < r.held; j += 32) {
-        const long long to = (long long)tot.count + r.given + j;
-        if (to < tot.top) a.free_list[to] = bt[j];
-      }
-    } else if (r.need > 0) {
-      if (plan_granted(r, tot.top)) {
-        for (int j = lane; j < r.need; j += 32) {
-          const int page = plan_page(a, rows, tot, r.first + j);
-          if (page < 0 || page >= a.num_pages) bad |= PA_DEV_BAD_PAGE;
-          bt[r.held + j] = page;
-        }
-      } else {
-        bad |= PA_DEV_NO_PAGES;
-      }
-    }
+  // rows, then the pages given back onto the list and the step's pages into the table, each a thread's
+  const int first = rank * kPlanThreads + tid, stride = nranks * kPlanThreads;
+  for (int b = first; b < a.batch; b += stride) {
+    a.query_start[b] = rows[b].start;
+    if (rows[b].need > 0 && !plan_granted(rows[b], tot.top)) bad |= PA_DEV_NO_PAGES;
+    if constexpr (MODE != PLAN_AFTER) plan_state(a, rows, tot, b);
   }
-  if (rank == 0 && tid == 0) a.query_start[a.batch] = total;
+  if (first == 0) {
+    a.query_start[a.batch] = total;
+    if constexpr (MODE != PLAN_AFTER) plan_state_all_granted(a, tot);
+  }
+  for (int r = first; r < tot.top - tot.count; r += stride) a.free_list[tot.count + r] = plan_given(a, rows, r);
+  for (int j = first; j < min(tot.need, tot.top); j += stride) {
+    const int b = plan_find<&PlanRow::first>(rows, a.batch, j);
+    const PlanRow r = rows[b];
+    if (r.need <= 0 || !plan_granted(r, tot.top)) continue;  // behind the last page that was granted
+    const int page = plan_page(a, rows, tot, j);
+    if (page < 0 || page >= a.num_pages) bad |= PA_DEV_BAD_PAGE;
+    a.block_table[(size_t)b * a.max_pages_per_seq + r.held + (j - r.first)] = page;
+  }
 
   // tokens, a chunk of kPlanThreads at a time
   for (int t0 = rank * kPlanThreads; t0 < a.max_tokens; t0 += nranks * kPlanThreads) {
     const int t = t0 + tid;
-    if (a.parents) {
+    if (a.parents && t0 != rank * kPlanThreads) {
       __syncthreads();
-      for (int e = tid; e < kTreeNodes - 1 + kPlanThreads; e += kPlanThreads) {
-        const int s = t0 - (kTreeNodes - 1) + e;
-        const int p = s >= 0 && s < total && s < a.max_tokens ? a.parents[s] : -1;
-        up[e] = (int8_t)(p < -1 || p >= kTreeNodes ? -2 : p);
-      }
+      load_parents(t0);
       __syncthreads();
     }
     if (t >= a.max_tokens) continue;
@@ -234,12 +241,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
     int pos = 0;
     uint64_t mask = 0;
     if (t < total) {
-      int lo = 0, hi = a.batch - 1;  // the last row that starts at or before t
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (rows[mid].start <= t) lo = mid;
-        else hi = mid - 1;
-      }
+      const int lo = plan_find<&PlanRow::start>(rows, a.batch, t);
       const PlanRow r = rows[lo];
       const int i = t - r.start, n = rows[lo + 1].start - r.start;
       const long long at = (long long)r.ctx + i;
@@ -275,27 +277,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
     if (a.tree_mask) a.tree_mask[t] = mask;
   }
   if (bad && a.status) atomicOr(a.status, bad);
-  if constexpr (STATE) {
-    if (rank == 0) {
-      __syncthreads();  // (the sums' scratch was last read before the barrier)
-      plan_state(a, rows, tot, part);
-    }
-  }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_state_kernel(const PlanArgs a) {
   extern __shared__ PlanRow rows[];
-  __shared__ long long part[kPlanThreads / 32][3];
+  __shared__ PlanSums part[kPlanThreads / 32];
   pdl_wait();  // for the step kernel, which reads what is written here
   pdl_launch_dependents();
   uint32_t bad = 0;  // (said by the step kernel)
   const PlanTotals tot = plan_rows(a, rows, part, bad);
-  plan_state(a, rows, tot, part);
+  for (int b = threadIdx.x; b < a.batch; b += kPlanThreads) plan_state(a, rows, tot, b);
+  if (threadIdx.x == 0) plan_state_all_granted(a, tot);
 }
 
 // Accepted paths.  Block (x, y) moves 256 16-byte columns of row y: a column is one 16-byte piece of
 // a token in one pool of one layer, and each thread moves its column's accepted nodes in ascending
-// order, eight loads in flight.  A node's target lies at or before its source and behind every
+// order, eight loads in flight (sixteen: 14.0 us for 12.2, fewer threads fit an SM).  A node's target lies at or before its source and behind every
 // earlier source, so no source is overwritten before it is read.
 constexpr int kCompactThreads = 256;
 
@@ -418,7 +415,9 @@ extern "C" int pa_plan_step(const int32_t *context_lens, const int32_t *new_lens
   note_launches(0);
   if (batch < 0 || page_size <= 0 || num_pages <= 0 || max_pages_per_seq <= 0 || max_tokens < 0)
     return PA_ERR_INVALID_ARGUMENT;
-  if (batch > kPlanMaxBatch || (long long)max_pages_per_seq * page_size > INT_MAX) return PA_ERR_UNSUPPORTED;
+  if (batch > kPlanMaxBatch || (long long)max_pages_per_seq * page_size > INT_MAX ||
+      (long long)max_pages_per_seq * batch > INT_MAX)
+    return PA_ERR_UNSUPPORTED;
   if (!free_list || !free_count || !free_count_out || !query_start) return PA_ERR_INVALID_ARGUMENT;
   if (batch > 0 && (!context_lens || !new_lens || !held_pages || !block_table || !context_lens_out || !held_pages_out))
     return PA_ERR_INVALID_ARGUMENT;
@@ -454,26 +453,29 @@ extern "C" int pa_plan_step(const int32_t *context_lens, const int32_t *new_lens
                 page_size, num_pages, max_pages_per_seq, max_tokens};
   const size_t smem = (size_t)(batch + 1) * sizeof(PlanRow);
   const int chunks = (max_tokens + kPlanThreads - 1) / kPlanThreads;
-  // One cluster of as many CTAs as there are chunks of tokens; from more than eight chunks on a CTA each, up to two
-  // on an SM, and a second launch for the state: at 72000 tokens of 512 rows 12 us, where one cluster takes 38; at
-  // 4000 tokens the second launch costs more than it gives.
-  const bool one = chunks <= kPlanMaxCluster;
-  int cluster = 1;
-  while (one && cluster < chunks) cluster *= 2;
+  // A CTA for each chunk of tokens and for 64 rows.  State in place: up to eight of them in one cluster, more with
+  // a second launch for the state.
+  const bool in_place = context_lens_out == context_lens || held_pages_out == held_pages || free_count_out == free_count;
+  constexpr int kPlanMostCtas = 304;  // two on each SM
+  int ctas = chunks > (batch + 63) / 64 ? chunks : (batch + 63) / 64;
+  ctas = ctas < 1 ? 1 : ctas < kPlanMostCtas ? ctas : kPlanMostCtas;
+  int cluster = 0;
+  if (in_place && chunks <= kPlanMaxCluster) {
+    for (cluster = 1; cluster < kPlanMaxCluster && cluster < ctas;) cluster *= 2;
+    ctas = cluster;
+  }
+  auto kernel = !in_place ? plan_step_kernel<PLAN_APART> : cluster ? plan_step_kernel<PLAN_CLUSTER> : plan_step_kernel<PLAN_AFTER>;
+  const bool after = in_place && !cluster;
   if (smem > 40 * 1024) {
     constexpr int most = (kPlanMaxBatch + 1) * (int)sizeof(PlanRow);
-    cudaError_t e = cudaFuncSetAttribute(one ? plan_step_kernel<true> : plan_step_kernel<false>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e == cudaSuccess && !one) e = cudaFuncSetAttribute(plan_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess && after) e = cudaFuncSetAttribute(plan_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  constexpr int kPlanMostCtas = 304;
-  cudaError_t e = one ? launch(plan_step_kernel<true>, dim3((unsigned)cluster), kPlanThreads, smem, cluster, a, stream)
-                      : launch(plan_step_kernel<false>, dim3((unsigned)(chunks < kPlanMostCtas ? chunks : kPlanMostCtas)),
-                               kPlanThreads, smem, 0, a, stream);
-  if (e == cudaSuccess && !one) e = launch(plan_state_kernel, dim3(1), kPlanThreads, smem, 0, a, stream);
+  cudaError_t e = launch(kernel, dim3((unsigned)ctas), kPlanThreads, smem, cluster, a, stream);
+  if (e == cudaSuccess && after) e = launch(plan_state_kernel, dim3(1), kPlanThreads, smem, 0, a, stream);
   if (e != cudaSuccess) return cuda_fail(e);
-  note_launches(one ? 1 : 2);
+  note_launches(after ? 2 : 1);
   return PA_OK;
 }
 
