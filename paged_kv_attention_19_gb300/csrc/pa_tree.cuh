@@ -60,7 +60,7 @@ struct TreeArgs {
   uint16_t *out;
   float *lse;           // or null
   struct TreeDesc *desc;  // [nparts]
-  float *part_o;        // [nparts, 2, QT * 128, D]
+  float *part_o;        // [nparts, 2, D / 4, QT * 128, 4]: rows beside each other, so that a warp's stores are whole lines
   float *part_lse;      // [nparts, 2, QT * 128], log2 units
   int32_t *seq_last;    // [batch, hs]: CTA of the last piece of a sequence that several share
   struct TreeHalf *halves;        // [nparts, 2, 128]: the groups' halves of a one-tile piece
@@ -422,6 +422,19 @@ __device__ __forceinline__ float cache_value(const uint8_t *row, int d) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Of 8 bf16 values: the largest magnitude (NaN aside); a pair times a power of two as an f16 pair.
+__device__ __forceinline__ float absmax8(uint4 x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+  return m;
+}
+__device__ __forceinline__ uint32_t scaled_f16x2(uint32_t pair, float p2) {
+  return pack_f16x2(__uint_as_float(pair << 16) * p2, __uint_as_float(pair & 0xffff0000u) * p2);
 }
 
 // Values 16 pc .. 16 pc + 15 of a row of codes as f16 pairs, without the pool's scale: exact (an E2M1 value
@@ -933,9 +946,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   } else if (warp >= 4 + C::SOFTMAX_WARPS) {
     if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_CONVERT>();
     // ------------------------------------------------------------ codes to f16 operands
-    // Each thread takes 16 codes at a time; a row's threads read one run of bytes, and write the two
-    // 16-byte chunks of the swizzled f16 row in opposite orders in odd planes, so that neither the
-    // reads nor the writes of eight lanes meet in a bank.
+    // Each thread takes 16 codes at a time: two 16-byte chunks of a swizzled f16 row.  Eight lanes take a plane
+    // (64 values) of one row and the plane beside it of the next row: in the swizzled rows one half's chunks are
+    // then the even and the other's the odd ones, and the codes are in different banks too.
     if constexpr (C::QUANT) {
       const int ct = tid - (4 + C::SOFTMAX_WARPS) * 32, cw = ct >> 5;
       constexpr int TPR = D / 16, NTASK = BN * TPR, STEP = C::TILE_WARPS * 32, ROUND = 8;
@@ -968,28 +981,32 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             int8_t *shift = reinterpret_cast<int8_t *>(smem + S::OFF_SHIFT) + (kp & 1) * (C::QT * kTreeRows);
             for (int r = ct; r < (two ? 2 : 1) * kTreeRows; r += C::CONVERT_WARPS * 32) {
               uint8_t *row = smem + (r >> 7) * (C::NPL * C::QPLANE) + (r & 127) * 128;
+              auto chunk = [&](int c) {
+                return reinterpret_cast<uint4 *>(row + (c >> 3) * C::QPLANE + (((c & 7) ^ (r & 7)) << 4));
+              };
+              constexpr int CH = 8;  // chunks of the row in registers at a time
+              uint4 w[CH];
               float amax = 0.f;
-#pragma unroll 4
-              for (int c = 0; c < C::NPL * 8; ++c) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(row + (c >> 3) * C::QPLANE + (((c & 7) ^ (r & 7)) << 4));
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 1
+              for (int c0 = 0; c0 < C::NPL * 8; c0 += CH) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+                for (int c = 0; c < CH; ++c) w[c] = *chunk(c0 + c);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) amax = fmaxf(amax, absmax8(w[c]));
               }
               const int sh = min(max(14 - ((int)(__float_as_uint(amax) >> 23) - 127), -100), 100);
               const float p2 = __uint_as_float((uint32_t)(sh + 127) << 23);
               shift[r] = (int8_t)sh;
-#pragma unroll 4
-              for (int c = 0; c < C::NPL * 8; ++c) {
-                uint4 *px = reinterpret_cast<uint4 *>(row + (c >> 3) * C::QPLANE + (((c & 7) ^ (r & 7)) << 4));
-                const uint4 x = *px;
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                uint32_t h[4];
+#pragma unroll 1
+              for (int c0 = C::NPL * 8 - CH; c0 >= 0; c0 -= CH) {  // (the last ones read are still there)
+                if (c0 != C::NPL * 8 - CH) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  h[e] = pack_f16x2(__uint_as_float(w[e] << 16) * p2, __uint_as_float(w[e] & 0xffff0000u) * p2);
-                *px = make_uint4(h[0], h[1], h[2], h[3]);
+                  for (int c = 0; c < CH; ++c) w[c] = *chunk(c0 + c);
+                }
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+                  *chunk(c0 + c) = make_uint4(scaled_f16x2(w[c].x, p2), scaled_f16x2(w[c].y, p2), scaled_f16x2(w[c].z, p2),
+                                              scaled_f16x2(w[c].w, p2));
               }
             }
             fence_proxy_async_smem();
@@ -1008,13 +1025,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           uint64_t bad_nodes = 0, bad_edge = 0;
           auto put = [&](int r, int pc, const uint32_t (&h)[8]) {
             uint8_t *row = op + (pc >> 2) * C::PLANE + r * 128;
-            const int c0 = 2 * (pc & 3), sw = (pc >> 2) & 1;
-            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-            *reinterpret_cast<uint4 *>(row + (((c0 + sw) ^ (r & 7)) << 4)) = sw ? hi : lo;
-            *reinterpret_cast<uint4 *>(row + (((c0 + 1 - sw) ^ (r & 7)) << 4)) = sw ? lo : hi;
+            const int c0 = 2 * (pc & 3);
+            *reinterpret_cast<uint4 *>(row + ((c0 ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(row + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
           };
-          // a thread's tasks lie STEP / TPR rows apart, at the same place of the row; eight loads in flight
-          const int pc = tt % TPR, r0 = tt / TPR;
+          // this thread's place: 16 codes pc of row r0, and of every (STEP / TPR)-th row from there; eight loads in flight
+          const int pl = (tt >> 3) % C::NPL, odd = (tt >> 2) & 1;
+          const int pc = (C::NPL > 1 ? pl ^ odd : pl) * 4 + (tt & 3), r0 = (tt >> 3) / C::NPL * 2 + odd;
           if (m.x & STAGE_ABSENT) {
             // nothing is there
           } else if (!look) {
@@ -1141,8 +1158,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(s[i + e], s[i + 4 + e]));
           return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         };
-        float s[64], mx = -INFINITY;
-        if constexpr (BN == 128) mx = read(1, s);
+        constexpr bool HOLD = !C::QUANT;  // registers for all 128
+        float s[64], s1[64], mx = -INFINITY;
+        if constexpr (BN == 128) mx = read(1, HOLD ? s1 : s);
         mx = fmaxf(mx, read(0, s));
         mx *= qs;
         if (!had) {
@@ -1171,7 +1189,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const float sub = m_run == -INFINITY ? 0.f : m_run;
         const float2 q2 = make_float2(qs, qs), sub2 = make_float2(-sub, -sub);
         float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        auto weigh = [&](int h) {  // the weights of the columns in s, packed, over the columns from 32 h on
+        auto weigh = [&](int h, const float (&s)[64]) {  // the weights of the columns in s, packed, over the columns from 32 h on
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t w[16];
@@ -1185,10 +1203,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             tc_st16(tS + 32 * h + 16 * c, w);
           }
         };
-        weigh(0);
+        weigh(0, s);
         if constexpr (BN == 128) {
-          read(1, s);
-          weigh(1);
+          if constexpr (!HOLD) read(1, s1);
+          weigh(1, s1);
         }
         l2[0] = add_pair(l2[0], l2[1]);
         l_run += l2[0].x + l2[0].y;
@@ -1299,7 +1317,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int c0 = merge ? grp * (D / 2) : 0, c1 = merge ? c0 + D / 2 : D;
       const size_t pi = ((size_t)blockIdx.x * 2 + (slot > 0 ? 1 : 0)) * (C::QT * kTreeRows) + prow;
       uint16_t *orow = a.out + ((size_t)node_tok * a.Hq + head) * D;
-      float *po = a.part_o + pi * D;
+      constexpr int RS = C::QT * kTreeRows;
+      float *po = a.part_o + (pi - prow) * D + prow * 4;  // value d of the row: po[d / 4 * 4 RS + d % 4]
       // tokens with infinities or NaN that this row attends to
       uint64_t hit_nodes = bad_nodes & eff, hit_edge = bad_edge;
       if (hit_edge) hit_edge = lo_row - lo_min >= 64 ? 0 : hit_edge >> (lo_row - lo_min) << (lo_row - lo_min);
@@ -1328,7 +1347,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             } else {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4 *>(po + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                *reinterpret_cast<float4 *>(po + (size_t)(c + i) * RS) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
           }
         }
@@ -1345,7 +1364,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const float x = cache_value<C::FMT, D>(vr, d);
                 if (isfinite(x)) continue;
                 if (slot < 0) orow[d] = (uint16_t)pack_bf16x2(__uint_as_float((uint32_t)orow[d] << 16) + x, 0.f);
-                else po[d] += x;
+                else po[(size_t)(d & ~3) * RS + (d & 3)] += x;
               }
             }
           }
@@ -1374,15 +1393,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------------------- combine
-// Grid (CTAs of the split kernel, rows / 8): a block for 8 rows of the sequence that CTA x begins and does not
-// end (at most one), a warp per row.  Its pieces lie in CTAs x, x + HG, ..., in ascending order of the keys.
-// All pieces' log-sum-exps are read at once, a piece per lane, and with them the weights are known before any
-// value is read: the values are then loads that wait for nothing.
+// Grid (CTAs of the split kernel, rows / rows per block): a block for some rows of the sequence that CTA x begins
+// and does not end (at most one).  Its pieces lie in CTAs x, x + HG, ..., in ascending order of the keys.  A warp
+// takes 8 rows x 32 columns: the partials of 8 rows lie beside each other, 16 bytes of each.  Eight pieces' log-sum-
+// exps and values are loaded together and merged in order.
 
-constexpr int kCombineRows = 8;
+constexpr int kCombineThreads = 256;
+__host__ __device__ constexpr int combine_rows(int D) { return 8 * (kCombineThreads / 32) / (D / 32); }  // rows of a block
 
 template <int D, int QT>
-__global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const TreeArgs a, uint32_t *status) {
+__global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const TreeArgs a, uint32_t *status) {
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = (int)blockIdx.x;
@@ -1397,63 +1417,64 @@ __global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const T
   uint32_t ignored = 0;
   const TreeRow r = tree_row(a, d.b, &ignored);
   const int last = a.seq_last[(size_t)d.b * a.Hkv * a.nseqh + d.hs];
-  constexpr int RS = QT * kTreeRows, PER = D / 32, CHUNK = D <= 128 ? 8 : 4;
-  const int pr = (int)blockIdx.y * kCombineRows + warp, t = (d.hs % a.nseqh) * QT + pr / kTreeRows, row = pr % kTreeRows;
+  constexpr int RS = QT * kTreeRows, WPR = D / 32, CHUNK = 8;  // warps for one row
+  const int pr = (int)blockIdx.y * combine_rows(D) + warp / WPR * 8 + (lane & 7);
+  const int t = (d.hs % a.nseqh) * QT + pr / kTreeRows, row = pr % kTreeRows;
   // (a stale entry only where the split kernel gave up)
   if (r.n == 0 || t >= tree_tiles(a, r.n) || last <= cta || last >= a.nparts || (last - cta) % a.hg != 0) return;
   const TreeTile tl = tree_tile(a, t, r.n);
   const int pos = row / a.gt, h = row - pos * a.gt, k = (last - cta) / a.hg + 1;
-  if (pos >= tl.nq || h >= tl.nh) return;
-  auto place = [&](int i) { return ((size_t)(cta + i * a.hg) * 2 + (i == 0 ? d.slot : 0)) * RS + pr; };
-  float M = -INFINITY, Z = 0.f, acc[PER];
+  if (pos >= tl.nq || h >= tl.nh) return;  // (nothing below is the whole warp's)
+  const int c0 = warp % WPR * 32 + (lane >> 3) * 4;  // this lane's values: c0 .. c0 + 3 and c0 + 16 .. c0 + 19
+  float M = -INFINITY, Z = 0.f, acc[8];
 #pragma unroll
-  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  for (int i0 = 0; i0 < k; i0 += 32) {
-    // an empty piece (lse -inf) weighs nothing and its values are not read: they were not written
-    const float lc = i0 + lane < k ? a.part_lse[place(i0 + lane)] : -INFINITY;
-    float mn = lc;
+  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  for (int i0 = 0; i0 < k; i0 += CHUNK) {
+    float lc[CHUNK];
+    float4 x[CHUNK][2];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(FULL, mn, o));
-    mn = fmaxf(mn, M);
-    const float w = lc == -INFINITY ? 0.f : fast_exp2(lc - mn), sc = M == -INFINITY ? 0.f : fast_exp2(M - mn);
+    for (int u = 0; u < CHUNK; ++u) {
+      lc[u] = -INFINITY;
+      x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + u < k) {
+        const size_t slot = (size_t)(cta + (i0 + u) * a.hg) * 2 + (i0 + u == 0 ? d.slot : 0);
+        lc[u] = a.part_lse[slot * RS + pr];
+        const float *src = a.part_o + slot * RS * D + (size_t)c0 * RS + pr * 4;
+        x[u][0] = *reinterpret_cast<const float4 *>(src);
+        x[u][1] = *reinterpret_cast<const float4 *>(src + 16 * RS);
+      }
+    }
+    float mn = M;
+#pragma unroll
+    for (int u = 0; u < CHUNK; ++u) mn = fmaxf(mn, lc[u]);
+    const float sc = M == -INFINITY ? 0.f : fast_exp2(M - mn);
     M = mn;
-    float zs = w;
+    Z *= sc;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) zs += __shfl_xor_sync(FULL, zs, o);
-    Z = Z * sc + zs;
+    for (int e = 0; e < 8; ++e) acc[e] *= sc;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] *= sc;
-    for (int j0 = 0; j0 < 32 && i0 + j0 < k; j0 += CHUNK) {
-      float wj[CHUNK], x[CHUNK][PER];
+    for (int u = 0; u < CHUNK; ++u) {
+      // an empty piece (lse -inf) weighs nothing, and what lies in its place is not looked at: it was not written
+      const float w = lc[u] == -INFINITY ? 0.f : fast_exp2(lc[u] - mn);
+      if (w != 0.f) {
+        Z += w;
 #pragma unroll
-      for (int u = 0; u < CHUNK; ++u) {
-        wj[u] = __shfl_sync(FULL, w, (j0 + u) & 31);
-        if (j0 + u < 32 && i0 + j0 + u < k && wj[u] != 0.f) {
-          const float *src = a.part_o + place(i0 + j0 + u) * D + lane * PER;
-#pragma unroll
-          for (int e = 0; e < PER; e += 2) {
-            const float2 v = *reinterpret_cast<const float2 *>(src + e);
-            x[u][e] = v.x;
-            x[u][e + 1] = v.y;
-          }
-        } else {
-          wj[u] = 0.f;
-#pragma unroll
-          for (int e = 0; e < PER; ++e) x[u][e] = 0.f;
+        for (int v = 0; v < 2; ++v) {
+          acc[4 * v] = fmaf(w, x[u][v].x, acc[4 * v]);
+          acc[4 * v + 1] = fmaf(w, x[u][v].y, acc[4 * v + 1]);
+          acc[4 * v + 2] = fmaf(w, x[u][v].z, acc[4 * v + 2]);
+          acc[4 * v + 3] = fmaf(w, x[u][v].w, acc[4 * v + 3]);
         }
       }
-#pragma unroll
-      for (int u = 0; u < CHUNK; ++u)
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = fmaf(wj[u], x[u][e], acc[e]);
     }
   }
   const float inv = Z == 0.f ? 0.f : 1.f / Z;
   const size_t at = (size_t)(r.start + tl.i0 + pos) * a.Hq + (d.hs / a.nseqh) * a.G + tl.h0 + h;
-  uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + at * D + lane * PER);
 #pragma unroll
-  for (int e = 0; e < PER; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0 && a.lse) a.lse[at] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * LN2;
+  for (int v = 0; v < 2; ++v)
+    *reinterpret_cast<uint2 *>(a.out + at * D + c0 + 16 * v) =
+        make_uint2(pack_bf16x2(acc[4 * v] * inv, acc[4 * v + 1] * inv), pack_bf16x2(acc[4 * v + 2] * inv, acc[4 * v + 3] * inv));
+  if (c0 == 0 && a.lse) a.lse[at] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * LN2;
 }
 
 }  // namespace pa

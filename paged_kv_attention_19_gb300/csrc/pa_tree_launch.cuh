@@ -44,8 +44,8 @@ cudaError_t launch_tree(const TreeLaunch &l, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // the rows that a sequence can have: of a single tile those that it holds
   const int rows = a.nseqh * QT > 1 ? QT * kTreeRows : a.gt * (a.qt < a.max_query ? a.qt : a.max_query);
-  const dim3 grid((unsigned)a.nparts, (unsigned)((rows + kCombineRows - 1) / kCombineRows));
-  return launch_pdl(tree_combine_kernel<D, QT>, grid, kCombineRows * 32, 0, stream, a, l.status);
+  const dim3 grid((unsigned)a.nparts, (unsigned)((rows + combine_rows(D) - 1) / combine_rows(D)));
+  return launch_pdl(tree_combine_kernel<D, QT>, grid, kCombineThreads, 0, stream, a, l.status);
 }
 
 template <int FMT>
