@@ -126,7 +126,7 @@ int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32
     if (!aligned_to(p, 4)) return PA_ERR_MISALIGNED;
   if (!aligned_to(tree_mask, 8)) return PA_ERR_MISALIGNED;
   if (workspace_bytes < pl.total) return PA_ERR_WORKSPACE_TOO_SMALL;
-  const int BN = D <= 128 ? 128 : 64;  // tokens per stage (TreeCfg::BN)
+  const int BN = 64;                   // tokens per stage (TreeCfg::BN)
   const int BH = P < BN ? P : BN;      // tokens per TMA box: a unit
   const int sms = sm_count();
   if (sms <= 0) return cuda_fail(cudaSuccess);

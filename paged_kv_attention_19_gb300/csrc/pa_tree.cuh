@@ -22,12 +22,14 @@
 // can be part of a sequence that another CTA also touches: at most two partial results a CTA.
 //
 // Roles of a CTA (one per SM):
-//   * warp 0: the K and V tiles of BN tokens into a ring of slots (TMA, 128-byte swizzle);
-//   * warps 1 and 2, one thread each: the products.  Score buffer, softmax group and output columns x = 0, 1
-//     belong to thread x.  With two tiles thread x takes tile x of every stage; with one tile the threads
-//     take alternate stages of the same rows, and the two outputs are merged at the end of the piece.  (One
-//     thread for both spent more time on its waits and commits than the products took.)  A piece has an
-//     even number of stages, so that a stage's parity says whose it is; the last may be without tokens;
+//   * warp 0: the K and V tiles of 64 tokens into two rings of slots (TMA, 128-byte swizzle);
+//   * warps 1 and 2, one thread each: the products.  Softmax group and output columns x = 0, 1 and two score
+//     buffers each belong to thread x: it issues the scores of an item before the second product of the
+//     one before it, so that the group has its next scores while its weights are being used.  With two tiles
+//     thread x takes tile x of every stage; with one tile the threads take alternate stages of the same
+//     rows, and the two outputs are merged at the end of the piece.  (One thread for both spent more time
+//     on its waits and commits than the products took.)  A piece has an even number of stages, so that a
+//     stage's parity says whose it is; the last may be without tokens;
 //   * warp 3: the query tiles of each piece; and looks over V tiles that hold tokens which not every row
 //     attends to (the tree, the edge of a window, the ends of a piece) before they are used: a token that
 //     nobody attends to becomes zero, and infinities and NaN of the others are taken out of the product and
@@ -36,11 +38,9 @@
 //     them to f16 operands (exact; two warps K tiles, two V tiles), and the query rows, scaled by a
 //     power of two each, in place; those of the V tiles then look them over.  The weights are rounded to
 //     f16 (2^-11);
-//   * two groups of four warps: one thread per score row.  64 columns of the row are in registers at a
-//     time, the ones behind them are read from tensor memory again once the maximum is known.
-// Tensor memory: scores (then weights) x at BN x, outputs at 256.  At head_dim 256 one output fills the
-// rest: one tile, stages of 64 tokens, one softmax group and one issuing thread, which has the scores of a
-// stage issued before the second product of the one before it.
+//   * two groups of four warps: one thread per score row, its 64 scores of the item in registers.
+// Tensor memory: score buffer b (the weights over its first half) at 64 b, outputs at 256.  At head_dim 256 one
+// output fills the rest: one tile, one softmax group and one issuing thread.
 #pragma once
 
 #include "pa_common.cuh"
@@ -95,22 +95,23 @@ struct TreeCfg {
   static constexpr bool QUANT = FMT != TREE_BF16;  // codes in the cache, f16 operands
   static constexpr int ROWB = tree_row_bytes(FMT, D);
   static constexpr int GROUPS = D <= 128 ? 2 : 1;  // softmax groups, and output regions
-  static constexpr int BN = D <= 128 ? 128 : 64;   // tokens per stage
+  static constexpr int BN = 64;                    // tokens per stage
+  static constexpr int NB = 4;                     // score buffers
   static constexpr int NPL = D / 64;               // 128-byte swizzle planes of a row
   static constexpr int PLANE = BN * 128, SLOT = NPL * PLANE, QPLANE = kTreeRows * 128;
   static constexpr int Q_BYTES = QT * NPL * QPLANE;
-  static constexpr int ROOM = 229376 - Q_BYTES;
+  static constexpr int ROOM = (QUANT ? 228352 : 229376) - Q_BYTES;
   // codes: up to eight slots of a tile each, copied in order K, V, K, V...; operands converted from them
   static constexpr int RAW_SLOT = QUANT ? (BN * ROWB + 1023) / 1024 * 1024 : 0;
-  static constexpr int NS_QUANT = D == 64 ? 6 : D == 128 ? 4 : 3;
+  static constexpr int NS_QUANT = D == 64 ? 10 : D == 128 ? (QT == 1 ? 8 : 6) : 3;
   static constexpr int NR_FIT = QUANT ? (ROOM - NS_QUANT * SLOT) / (RAW_SLOT > 0 ? RAW_SLOT : 1) : 0;
-  static constexpr int NR = (NR_FIT < 6 ? NR_FIT : 6) & ~1;  // (even: a slot holds tiles of one kind)
-  static constexpr int NS_FIT = QUANT ? NS_QUANT : ROOM / SLOT;
+  static constexpr int NR = (NR_FIT < 8 ? NR_FIT : 8) & ~1;  // (even: a slot holds tiles of one kind)
+  static constexpr int NS_FIT = QUANT ? NS_QUANT : ROOM / SLOT < 12 ? ROOM / SLOT : 12;
   // Two rings of slots: a K tile is free after the scores of its stage, a V tile later.  Copies complete out of order,
   // and a wait for a phase of a slot must not come before the phase before it is known to be complete, so whoever
   // waits for the tiles of one kind, or of one parity of the stages, needs slots that hold those only.
-  static constexpr int NK = GROUPS == 1 ? NS_FIT / 2 : D == 64 ? (NS_FIT >= 10 ? 4 : 2) : 2;
-  static constexpr int NV = GROUPS == 1 ? NS_FIT - NK : (NS_FIT - NK < 4 ? 2 : 4), NS = NK + NV;
+  static constexpr int NK = GROUPS == 1 ? NS_FIT / 2 : NS_FIT / 4 * 2;
+  static constexpr int NV = GROUPS == 1 ? NS_FIT - NK : (NS_FIT - NK) / 2 * 2, NS = NK + NV;
   static constexpr int SOFTMAX_WARPS = 4 * GROUPS;
   static constexpr int CONVERT_WARPS = QUANT ? 4 : 0;
   static constexpr int TILE_WARPS = CONVERT_WARPS / 2;           // half of them for K tiles, half for V tiles
@@ -122,6 +123,11 @@ struct TreeCfg {
   static constexpr uint32_t IDESC_S = tc_idesc_bf16(kTreeRows, BN, false) & ~IDESC_F16;
   static constexpr uint32_t IDESC_PV = tc_idesc_bf16(kTreeRows, D, true) & ~IDESC_F16;
   static constexpr float TAU = 8.f;
+  // score buffer of item i of group (issuing thread) x, and the parity of its use
+  __host__ __device__ static constexpr uint32_t buffer(int x, uint32_t i) {
+    return GROUPS == 2 ? (uint32_t)x + 2 * (i & 1) : i & 3;
+  }
+  __host__ __device__ static constexpr uint32_t buffer_phase(uint32_t i) { return GROUPS == 2 ? (i >> 1) & 1 : (i >> 2) & 1; }
   // registers a thread: the softmax warps' 64 scores and their row's state do not fit the launch's share
   // (384 x 168 or 512 x 128), so the other warps hand some over
   static constexpr bool REG_SPLIT = GROUPS == 2;
@@ -129,11 +135,11 @@ struct TreeCfg {
   static constexpr int REGS_CONTROL = QUANT ? 80 : 88, REGS_SOFTMAX = QUANT ? 160 : 208, REGS_CONVERT = 104;
   static_assert(!REG_SPLIT || 128 * REGS_CONTROL + 256 * REGS_SOFTMAX + (QUANT ? 128 * REGS_CONVERT : 0) <= THREADS * REGS,
                 "the register split stays within the launch's registers");
-  static constexpr int META = 8;  // stage records kept: a record is rewritten eight stages later, once the K tile of a
-                                  // stage at least four later is free, and with that its own softmax long done
-  static_assert(NK >= 1 && NK + NR / 2 <= (QUANT ? 5 : 4) && (GROUPS == 1 || NK % 2 + NV % 2 == 0), "rings within the records");
+  static constexpr int META = 16;  // stage records kept: a record is rewritten sixteen stages later, once the K tile of a
+                                   // stage at least six later is free, and with that its own softmax long done
+  static_assert(NK >= 1 && NK + NR / 2 <= 10 && (GROUPS == 1 || NK % 2 + NV % 2 == 0), "rings within the records");
   static_assert(QT <= GROUPS, "two tiles need two groups");
-  static_assert(2 * BN <= 256 && GROUPS * D <= 256, "tensor-memory budget");
+  static_assert(NB * BN <= 256 && GROUPS * D <= 256, "tensor-memory budget");
 };
 
 enum : int32_t { STAGE_MASKED = 1, STAGE_ABSENT = 2 };
@@ -167,10 +173,10 @@ struct TreeSmem {
   static constexpr int OFF_META = OFF_RAW + C::NR * C::RAW_SLOT;
   static constexpr int OFF_PIECE = OFF_META + C::META * (int)sizeof(TreeStage);       // [2]
   static constexpr int OFF_NF = OFF_PIECE + 2 * (int)sizeof(TreePieceRec);            // [META][CLEAN_WARPS][2] token bits
-  // full[NS], empty[NS], clean[META], q_full, q_empty, s_full[2], p_ready[2], pv_done[2], o_free, half[2], drain[2],
+  // full[NS], empty[NS], clean[META], q_full, q_empty, s_full[NB], p_ready[NB], pv_done[NB], o_free, half[2], drain[2],
   // q_conv, raw_full[NR], raw_empty[NR]
   static constexpr int OFF_BAR = OFF_NF + C::META * C::CLEAN_WARPS * 16;
-  static constexpr int NBAR = 2 * C::NS + C::META + 14 + 2 * C::NR;
+  static constexpr int NBAR = 2 * C::NS + C::META + 8 + 3 * C::NB + 2 * C::NR;
   static constexpr int OFF_SHIFT = OFF_BAR + NBAR * 8;  // int8 [2][QT * 128]: exponents of the query rows' scales
   static constexpr int OFF_MISC = OFF_SHIFT + (C::QUANT ? 2 * C::QT * kTreeRows : 0);
   static constexpr int BYTES = OFF_MISC + (int)sizeof(TreeMisc) + 1024;
@@ -571,8 +577,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR), *empty = full + NS, *clean = empty + NS;
-  uint64_t *q_full = clean + C::META, *q_empty = q_full + 1, *s_full = q_full + 2, *p_ready = s_full + 2,
-           *pv_done = p_ready + 2, *o_free = pv_done + 2, *half_in = o_free + 1, *drain = half_in + 2, *q_conv = drain + 2,
+  uint64_t *q_full = clean + C::META, *q_empty = q_full + 1, *s_full = q_full + 2, *p_ready = s_full + C::NB,
+           *pv_done = p_ready + C::NB, *o_free = pv_done + C::NB, *half_in = o_free + 1, *drain = half_in + 2, *q_conv = drain + 2,
            *raw_full = q_conv + 1, *raw_empty = raw_full + C::NR;
   TreeStage *meta = reinterpret_cast<TreeStage *>(smem + S::OFF_META);
   TreePieceRec *prec = reinterpret_cast<TreePieceRec *>(smem + S::OFF_PIECE);
@@ -594,12 +600,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     mbar_init(q_conv, C::QUANT ? C::CONVERT_WARPS : 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, C::GROUPS);
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&s_full[x], 2);  // the scores' commit and the issuing thread's arrive
-      mbar_init(&p_ready[x], 4);
-      mbar_init(&pv_done[x], 1);
-      mbar_init(&half_in[x], 4);
+    for (int b = 0; b < C::NB; ++b) {
+      mbar_init(&s_full[b], 2);  // the scores' commit and the issuing thread's arrive
+      mbar_init(&p_ready[b], 4);
+      mbar_init(&pv_done[b], 1);
     }
+    mbar_init(&half_in[0], 4);
+    mbar_init(&half_in[1], 4);
     mbar_init(o_free, C::SOFTMAX_WARPS);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
@@ -758,12 +765,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   } else if (warp == 1 || (warp == 2 && C::GROUPS == 2)) {
     // ------------------------------------------------------------ products (one thread of the warp)
     if (lane == 0) {
-      const int x = warp - 1;  // (one group: the stages alternate between the score buffers)
+      const int x = warp - 1;
       const uint32_t ring = smem_u32(smem + S::OFF_RING), qb = smem_u32(smem);
       uint32_t t0 = 0, c = 0, d = 0;  // the piece's first stage; items begun and finished
       bool ok = true;
-      auto buf = [&](uint32_t i) { return C::GROUPS == 2 ? (uint32_t)x : i & 1; };
-      auto par = [&](uint32_t i) { return C::GROUPS == 2 ? i & 1 : (i >> 1) & 1; };
+      auto buf = [&](uint32_t i) { return C::buffer(x, i); };
+      auto par = [&](uint32_t i) { return C::buffer_phase(i); };
       // the slot of a tile is free for whoever shares it: with this thread's operations, or at once
       auto release = [&](uint64_t *bar, bool read, bool alone) {
         if (read) tc_commit(bar);
@@ -773,7 +780,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // the scores of the next item: query tile qx, stage t
       auto begin = [&](uint32_t t, int qx, bool present, bool alone) -> bool {
         const uint32_t b = buf(c);
-        constexpr uint32_t BACK = C::GROUPS == 2 ? 1 : 2;  // items since this buffer's last
+        constexpr uint32_t BACK = C::NB / C::GROUPS;  // items since this buffer's last
         if (!mbar_wait(&full[t % C::NK], (t / C::NK) & 1, status)) return false;
         if (c >= BACK && !mbar_wait(&pv_done[b], par(c - BACK), status)) return false;
         if (present) {
@@ -831,18 +838,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const bool two = r.z != 0, alone = !two;
         // this thread's stages: all of them, or every other one
         const uint32_t j0 = C::GROUPS == 2 && !two ? (uint32_t)x : 0, dj = C::GROUPS == 2 && !two ? 2 : 1;
-        if constexpr (C::GROUPS == 2) {
-          for (uint32_t j = j0; j < even && ok; j += dj) {
-            ok = begin(t0 + j, two ? x : 0, j < n, alone);
-            if (j + dj >= even) tc_commit(q_empty);
-            if (ok) ok = finish(t0 + j, piece, j == j0, j < n, alone);
-          }
-        } else {
-          for (uint32_t j = 0; j <= even && ok; ++j) {
-            if (j < even) ok = begin(t0 + j, 0, j < n, alone);
-            if (j + 1 == even) tc_commit(q_empty);
-            if (ok && j > 0) ok = finish(t0 + j - 1, piece, j == 1, j - 1 < n, alone);
-          }
+        // the second product of an item behind the scores of the next one
+        for (uint32_t j = j0; j < even + dj && ok; j += dj) {
+          if (j < even) ok = begin(t0 + j, two ? x : 0, j < n, alone);
+          if (j < even && j + dj >= even) tc_commit(q_empty);
+          if (ok && j > j0) ok = finish(t0 + j - dj, piece, j == j0 + dj, j - dj < n, alone);
         }
         t0 += even;
       }
@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // then the even and the other's the odd ones, and the codes are in different banks too.
     if constexpr (C::QUANT) {
       const int ct = tid - (4 + C::SOFTMAX_WARPS) * 32, cw = ct >> 5;
-      constexpr int TPR = D / 16, NTASK = BN * TPR, STEP = C::TILE_WARPS * 32, ROUND = 8;
+      constexpr int TPR = D / 16, NTASK = BN * TPR, STEP = C::TILE_WARPS * 32, ROUND = NTASK / STEP < 8 ? NTASK / STEP : 8;
       static_assert(NTASK % (ROUND * STEP) == 0 && STEP % TPR == 0, "whole rounds of tasks");
       const int kv = cw / C::TILE_WARPS, tt = ct % STEP;  // this warp's kind of tile; the thread among its warps'
       uint32_t kp = 0, left = 0;  // pieces begun; stages left of the current one
@@ -1114,8 +1114,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint32_t c = 0, k_half = 0;  // items done; merges
     uint32_t t0 = 0;             // the piece's first stage
     bool ok = true;
-    auto buf = [&](uint32_t i) { return C::GROUPS == 2 ? (uint32_t)grp : i & 1; };
-    auto par = [&](uint32_t i) { return C::GROUPS == 2 ? i & 1 : (i >> 1) & 1; };
+    auto buf = [&](uint32_t i) { return C::buffer(grp, i); };
+    auto par = [&](uint32_t i) { return C::buffer_phase(i); };
+    int seen = -1;  // the stage of the item before, if its V tile was looked over: what was found is not taken up yet
+    auto take_up = [&]() {  // (its second product is complete)
+      if (seen < 0 || !mbar_wait(&clean[seen % C::META], (seen / C::META) & 1, status)) return;
+#pragma unroll
+      for (int w = 0; w < C::CLEAN_WARPS; ++w) {
+        bad_nodes |= nf[((seen % C::META) * C::CLEAN_WARPS + w) * 2];
+        bad_edge |= nf[((seen % C::META) * C::CLEAN_WARPS + w) * 2 + 1];
+      }
+      seen = -1;
+    };
 
     // the group's next item: stage tt, whose record is m (flags, tok0, tok_hi, badmask)
     auto item = [&](uint32_t tt, int4 m) -> bool {
@@ -1123,16 +1133,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int o = C::GROUPS == 2 ? grp : 0;
       const uint32_t tO = tl_base + C::TM_O + o * D;
       if (warp_real && !(m.x & STAGE_ABSENT)) {
+        if (seen >= 0) {  // of the item before, whose record is soon another's
+          if (!mbar_wait(&pv_done[buf(c - 1)], par(c - 1), status)) return false;
+          __syncwarp();
+          take_up();
+        }
         const bool masked = m.x & STAGE_MASKED;
         uint32_t vis[BN / 32];
         if (masked) {
-          if (!mbar_wait(&clean[tt % C::META], (tt / C::META) & 1, status)) return false;
-          __syncwarp();
-#pragma unroll
-          for (int w = 0; w < C::CLEAN_WARPS; ++w) {
-            bad_nodes |= nf[((tt % C::META) * C::CLEAN_WARPS + w) * 2];
-            bad_edge |= nf[((tt % C::META) * C::CLEAN_WARPS + w) * 2 + 1];
-          }
+          seen = (int)tt;
 #pragma unroll
           for (int c = 0; c < BN / 32; ++c) {
             const int base = m.y + 32 * c;
@@ -1140,28 +1149,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                      loaded_bits((uint32_t)m.w, c, a.log2_bh);
           }
         }
-        // 64 columns of the row (those from 64 h on): read, turned, masked; returns their maximum
-        auto read = [&](int h, float (&s)[64]) -> float {
-          tree_ld(tS + 64 * h, s);
-          if (flip != 1.f) {  // a scale that is not positive
+        float s[BN];
+        tree_ld(tS, s);
+        if (flip != 1.f) {  // a scale that is not positive
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] *= flip;
-          }
-          if (masked) {
+          for (int i = 0; i < BN; ++i) s[i] *= flip;
+        }
+        if (masked) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = (vis[2 * h + i / 32] >> (i % 32)) & 1u ? s[i] : -INFINITY;
-          }
+          for (int i = 0; i < BN; ++i) s[i] = (vis[i / 32] >> (i % 32)) & 1u ? s[i] : -INFINITY;
+        }
+        float mx;
+        {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 64; i += 8)
+          for (int i = 0; i < BN; i += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(s[i + e], s[i + 4 + e]));
-          return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        };
-        constexpr bool HOLD = !C::QUANT;  // registers for all 128
-        float s[64], s1[64], mx = -INFINITY;
-        if constexpr (BN == 128) mx = read(1, HOLD ? s1 : s);
-        mx = fmaxf(mx, read(0, s));
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        }
         mx *= qs;
         if (!had) {
           m_run = mx;
@@ -1189,24 +1195,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const float sub = m_run == -INFINITY ? 0.f : m_run;
         const float2 q2 = make_float2(qs, qs), sub2 = make_float2(-sub, -sub);
         float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        auto weigh = [&](int h, const float (&s)[64]) {  // the weights of the columns in s, packed, over the columns from 32 h on
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t w[16];
+        for (int k = 0; k < BN / 32; ++k) {
+          uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 y = fma_pair(make_float2(s[32 * c + i], s[32 * c + i + 1]), q2, sub2);
-              const float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-              l2[(i >> 1) & 1] = add_pair(l2[(i >> 1) & 1], pr);
-              w[i >> 1] = C::QUANT ? pack_f16x2(pr.x, pr.y) : pack_bf16x2(pr.x, pr.y);
-            }
-            tc_st16(tS + 32 * h + 16 * c, w);
+          for (int i = 0; i < 32; i += 2) {
+            const float2 y = fma_pair(make_float2(s[32 * k + i], s[32 * k + i + 1]), q2, sub2);
+            const float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            l2[(i >> 1) & 1] = add_pair(l2[(i >> 1) & 1], pr);
+            w[i >> 1] = C::QUANT ? pack_f16x2(pr.x, pr.y) : pack_bf16x2(pr.x, pr.y);
           }
-        };
-        weigh(0, s);
-        if constexpr (BN == 128) {
-          if constexpr (!HOLD) read(1, s1);
-          weigh(1, s1);
+          tc_st16(tS + 16 * k, w);
         }
         l2[0] = add_pair(l2[0], l2[1]);
         l_run += l2[0].x + l2[0].y;
@@ -1285,24 +1284,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (!ok) break;
       t0 += even;
 
-      // ---- end of a piece
+      // ---- end of a piece: the products of the last item, and with them all before, are complete
+      ok = mbar_wait(&pv_done[buf(c - 1)], par(c - 1), status);
+      if (!ok) break;
+      __syncwarp();
+      take_up();
       TreeHalf other = {-INFINITY, 0.f, 0, 0};
       const bool merge = C::GROUPS == 2 && !two;
-      if (merge) {
+      if (merge) {  // both groups have had as many items
         TreeHalf *mine = a.halves + ((size_t)blockIdx.x * 2 + grp) * kTreeRows + row;
         *mine = TreeHalf{m_run, l_run, bad_nodes, bad_edge};
         __syncwarp();
         if (lane == 0) mbar_arrive(&half_in[grp]);
-        if (!mbar_wait(&half_in[grp ^ 1], k_half & 1, status)) break;
+        ok = mbar_wait(&half_in[grp ^ 1], k_half & 1, status) && mbar_wait(&pv_done[C::buffer(grp ^ 1, c - 1)], par(c - 1), status);
+        if (!ok) break;
         ++k_half;
         other = a.halves[((size_t)blockIdx.x * 2 + (grp ^ 1)) * kTreeRows + row];
         bad_nodes |= other.bad_nodes;
         bad_edge |= other.bad_edge;
       }
-      // the products of the last items, and with them all before, are complete; both groups have as many items
-      ok = mbar_wait(&pv_done[buf(c - 1)], par(c - 1), status);
-      if (merge && ok) ok = mbar_wait(&pv_done[grp ^ 1], par(c - 1), status);
-      if (!ok) break;
       __syncwarp();
       tc_fence_after();
       // weights of this group's output and of the other's; a sum of zero: nothing was attended to
