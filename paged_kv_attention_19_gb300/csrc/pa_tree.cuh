@@ -142,9 +142,9 @@ struct TreeCfg {
   static_assert(NB * BN <= 256 && GROUPS * D <= 256, "tensor-memory budget");
 };
 
-enum : int32_t { STAGE_MASKED = 1, STAGE_ABSENT = 2 };
+enum : int32_t { STAGE_MASKED = 1, STAGE_ABSENT = 2, STAGE_FIRST = 4, STAGE_END = 8 };
 struct alignas(16) TreeStage {
-  int32_t flags;     // MASKED: not every row attends to every token; ABSENT: no tokens
+  int32_t flags;     // MASKED: not every row attends to every token; ABSENT: no tokens; FIRST: of a piece; END: none follows
   int32_t tok0, tok_hi;
   uint32_t badmask;  // bit k: box k of the stage was not loaded
 };
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], C::TILE_WARPS);
     }
-    mbar_init(q_conv, C::QUANT ? C::CONVERT_WARPS : 1);
+    mbar_init(q_conv, C::QUANT ? C::TILE_WARPS : 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, C::GROUPS);
     for (int b = 0; b < C::NB; ++b) {
@@ -711,6 +711,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               TreeStage m;
               m.flags = st >= n_stages ? STAGE_ABSENT
                                        : (tok0 + BN > min(prefix, tok_hi) || tok0 < lo_max || bad != 0 ? STAGE_MASKED : 0);
+              if (st == 0) m.flags |= STAGE_FIRST;
               m.tok0 = tok0;
               m.tok_hi = tok_hi;
               m.badmask = bad;
@@ -747,7 +748,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       uint32_t u;
       const int s = place(kv, u);
       if (u > 0) ok = __all_sync(FULL, mbar_wait(&r_empty[s], (u - 1) & 1, status));
-      if (ok && lane == 0) mbar_arrive(&r_full[s]);
+      if (ok && lane == 0) {
+        if (kv == 0) meta[t % C::META].flags = STAGE_END;
+        mbar_arrive(&r_full[s]);
+      }
     }
     if (!ok) {  // copies in flight land before the CTA exits
       if constexpr (C::QUANT) {
@@ -954,7 +958,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       constexpr int TPR = D / 16, NTASK = BN * TPR, STEP = C::TILE_WARPS * 32, ROUND = NTASK / STEP < 8 ? NTASK / STEP : 8;
       static_assert(NTASK % (ROUND * STEP) == 0 && STEP % TPR == 0, "whole rounds of tasks");
       const int kv = cw / C::TILE_WARPS, tt = ct % STEP;  // this warp's kind of tile; the thread among its warps'
-      uint32_t kp = 0, left = 0;  // pieces begun; stages left of the current one
+      uint32_t kp = 0;  // pieces begun
       int prefix = 0, lo_min = 0, lo_max = 0;
       for (uint32_t t = 0;; ++t) {
         const uint32_t f = 2 * t + kv;
@@ -962,24 +966,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         bool ok = __all_sync(FULL, mbar_wait(&raw_full[rs], (f / C::NR) & 1, status));
         if (!ok) break;
         const int4 m = *reinterpret_cast<const int4 *>(&meta[t % C::META]);  // flags, tok0, tok_hi, badmask
-        {
-          if (left == 0) {
-            // a new piece, or the end
-            ok = __all_sync(FULL, mbar_wait(q_full, kp & 1, status));
-            if (!ok) break;
-            const TreePieceRec &r = prec[kp & 1];
-            if (r.end) {
-              if (lane == 0) mbar_arrive(q_conv);
-              break;
-            }
-            left = (uint32_t)(r.stages + 1) & ~1u;
+        // a new piece, or the end: the warps of the V tiles, which are needed later, take the query rows
+        if (kv == 1 && (m.x & (STAGE_FIRST | STAGE_END))) {
+          ok = __all_sync(FULL, mbar_wait(q_full, kp & 1, status));
+          if (!ok) break;
+          const TreePieceRec &r = prec[kp & 1];
+          if (!(m.x & STAGE_END)) {
             prefix = r.L - r.n;
             lo_min = r.lo_min;
             lo_max = a.window > 0 ? max(r.L - a.window, 0) : 0;
             const bool two = r.two != 0;
-            // the piece's query rows: times 2^s (largest magnitude in [2^14, 2^15)) to f16, in place
+            // times 2^s (largest magnitude in [2^14, 2^15)) to f16, in place
             int8_t *shift = reinterpret_cast<int8_t *>(smem + S::OFF_SHIFT) + (kp & 1) * (C::QT * kTreeRows);
-            for (int r = ct; r < (two ? 2 : 1) * kTreeRows; r += C::CONVERT_WARPS * 32) {
+            for (int r = tt; r < (two ? 2 : 1) * kTreeRows; r += STEP) {
               uint8_t *row = smem + (r >> 7) * (C::NPL * C::QPLANE) + (r & 127) * 128;
               auto chunk = [&](int c) {
                 return reinterpret_cast<uint4 *>(row + (c >> 3) * C::QPLANE + (((c & 7) ^ (r & 7)) << 4));
@@ -1011,14 +1010,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(q_conv);
-            ++kp;
           }
+          if (lane == 0) mbar_arrive(q_conv);
+          ++kp;
+        }
+        if (m.x & STAGE_END) break;
+        {
           const int s = kv ? C::NK + t % C::NV : t % C::NK;
           const uint32_t u = kv ? t / C::NV : t / C::NK;
           if (u > 0) ok = __all_sync(FULL, mbar_wait(&empty[s], (u - 1) & 1, status));
           if (!ok) break;
-          --left;
           const uint8_t *raw = smem + S::OFF_RAW + rs * C::RAW_SLOT;
           uint8_t *op = smem + S::OFF_RING + s * C::SLOT;
           const bool look = kv == 1 && (m.x & STAGE_MASKED);
