@@ -16,8 +16,8 @@ namespace pa {
 namespace {
 
 constexpr int kMaxSplits = 4096, kAutoParts = 256;
-// Fixed cost of a piece of work in the partition, as the bytes of cache that an SM streams meanwhile.
-constexpr long long kPieceCostBytes = 160 << 10;
+// Fixed cost of a piece of work in the partition, as the tokens that a CTA passes meanwhile.
+constexpr int kPieceCost = 512;
 
 bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
@@ -170,8 +170,7 @@ int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32
   a.max_pages_per_seq = max_pages;
   a.max_context_len = max_ctx;
   a.window = window > 0 ? window : 0;
-  const long long unit_bytes = (long long)BH * rowb * 2;
-  a.piece_cost = (int)((kPieceCostBytes + unit_bytes - 1) / unit_bytes);
+  a.piece_cost = kPieceCost / BH;
   a.nparts = num_splits > 0 ? num_splits : sms < kAutoParts ? sms : kAutoParts;
   const int hs = Hkv * pl.nseqh;
   a.hg = hs < a.nparts ? hs : a.nparts;

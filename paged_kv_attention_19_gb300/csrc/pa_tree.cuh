@@ -955,7 +955,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // then the even and the other's the odd ones, and the codes are in different banks too.
     if constexpr (C::QUANT) {
       const int ct = tid - (4 + C::SOFTMAX_WARPS) * 32, cw = ct >> 5;
-      constexpr int TPR = D / 16, NTASK = BN * TPR, STEP = C::TILE_WARPS * 32, ROUND = NTASK / STEP < 8 ? NTASK / STEP : 8;
+      constexpr int TPR = D / 16, NTASK = BN * TPR, STEP = C::TILE_WARPS * 32, ROUND = NTASK / STEP < 4 ? NTASK / STEP : 4;
       static_assert(NTASK % (ROUND * STEP) == 0 && STEP % TPR == 0, "whole rounds of tasks");
       const int kv = cw / C::TILE_WARPS, tt = ct % STEP;  // this warp's kind of tile; the thread among its warps'
       uint32_t kp = 0;  // pieces begun
@@ -1030,7 +1030,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             *reinterpret_cast<uint4 *>(row + ((c0 ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
             *reinterpret_cast<uint4 *>(row + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
           };
-          // this thread's place: 16 codes pc of row r0, and of every (STEP / TPR)-th row from there; eight loads in flight
+          // this thread's place: 16 codes pc of row r0, and of every (STEP / TPR)-th row from there; four loads in flight
           const int pl = (tt >> 3) % C::NPL, odd = (tt >> 2) & 1;
           const int pc = (C::NPL > 1 ? pl ^ odd : pl) * 4 + (tt & 3), r0 = (tt >> 3) / C::NPL * 2 + odd;
           if (m.x & STAGE_ABSENT) {
