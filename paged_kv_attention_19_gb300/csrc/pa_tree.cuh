@@ -122,7 +122,9 @@ struct TreeCfg {
   static constexpr uint32_t IDESC_F16 = QUANT ? (1u << 7) | (1u << 10) : 0u;
   static constexpr uint32_t IDESC_S = tc_idesc_bf16(kTreeRows, BN, false) & ~IDESC_F16;
   static constexpr uint32_t IDESC_PV = tc_idesc_bf16(kTreeRows, D, true) & ~IDESC_F16;
-  static constexpr float TAU = 8.f;
+  // the maximum is raised when it grows by more than 2^TAU; f16 weights are 2^LIFT times as large: below 2^15, and one of
+  // 2^-21 of the largest still has all its bits (its step is 2^-24, so none is off by more than 2^-32 of the largest)
+  static constexpr float TAU = 8.f, LIFT = QUANT ? 7.f : 0.f;
   // score buffer of item i of group (issuing thread) x, and the parity of its use
   __host__ __device__ static constexpr uint32_t buffer(int x, uint32_t i) {
     return GROUPS == 2 ? (uint32_t)x + 2 * (i & 1) : i & 3;
@@ -1169,7 +1171,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(s[i + e], s[i + 4 + e]));
           mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         }
-        mx *= qs;
+        mx = mx * qs - C::LIFT;
         if (!had) {
           m_run = mx;
         } else if (__any_sync(FULL, real && m_run != -INFINITY && mx > m_run + C::TAU)) {

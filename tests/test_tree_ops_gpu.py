@@ -133,8 +133,17 @@ class Tree:
         torch.cuda.synchronize()
         assert pa.pa_read_device_status(ws) == 0
         assert bool((out[self.T:] == 7.0).all()) and bool((lse[self.T:] == 7.0).all()), "tokens behind the last row"
-        R.check_tree(f64(out[:self.T]), f64(lse[:self.T]), *self.reference(window), self.D)
+        R.check_tree(f64(out[:self.T]), f64(lse[:self.T]), *self.reference(window), self.D, self.lost())
         return out, lse
+
+    def lost(self):
+        """f16 weights (8- and 4-bit pools): a weight below 2^-14 is off by at most half of f16's smallest step, 2^-25.
+        The largest weight of a row is at least 2^7, so their sum is too, and an output sum(w v) / sum(w) is off by at
+        most 2^-25 / 2^7 sum(|v|) = 2^-32 sum(|v|) <= 2^-32 L max |v|.  bf16 weights have fp32's range: nothing."""
+        if self.fmt == "bf16":
+            return 0.0
+        v = R.pool_values(raw(self.v), self.fmt, self.D, self.scales[1])
+        return 2.0 ** -32 * max(L for L, _ in self.rows) * float(np.nanmax(np.abs(v)))
 
 
 LADDER = [(1, 1), (2, 2), (3, 1), (31, 7), (32, 5), (33, 33), (64, 16), (100, 0), (129, 12), (685, 20), (1000, 3)]
@@ -350,6 +359,74 @@ def test_tree_bad_rows_are_reported(pa):
     call(lambda a: a[5].__setitem__(2, 1), pa.PA_DEV_BAD_LEN)        # descending
     call(lambda a: a[3][1].__setitem__(2, 1 << 20), pa.PA_DEV_BAD_PAGE)
     call(lambda a: a[3][2].__setitem__(0, -1), pa.PA_DEV_BAD_PAGE)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("hq,hkv,D,page", [(16, 4, 256, 32), (8, 2, 128, 16), (64, 2, 128, 64), (4, 2, 64, 8)])
+@pytest.mark.parametrize("splits", [1, 7])
+def test_tree_long_pieces_in_a_window(pa, fmt, hq, hkv, D, page, splits):
+    """Pieces of many tiles that not every node attends to at both their ends, and at neither in between."""
+    Tree(97 + D, [(5000, 13), (2300, 1), (700, 9), (4100, 30)], hq, hkv, D, page, fmt).check(pa, window=2500, num_splits=splits)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("hq,hkv,D", [(16, 4, 256), (8, 2, 128), (64, 1, 128)])
+def test_tree_bad_token_at_the_edge_of_a_window(pa, fmt, hq, hkv, D):
+    """A token that the root attends to and deeper nodes no longer do, tens of tiles before the tree, holds NaN:
+    the root's outputs are not finite, the deeper nodes' are as before."""
+    L, n, window = 3600, 12, 2200
+    t = Tree(99, [(L, n)], hq, hkv, D, 16, fmt, chain=True)
+    want, want_l, _ = t.call(pa, window=window, num_splits=1)
+    edge = L - n + 1 - window  # the first token of the root (depth 0)
+    for p in (t.k, t.v):
+        x = p[int(t.table[0, edge // 16]), edge % 16]
+        x[:] = math.nan if fmt == "bf16" else 0x7F
+    out, lse, ws = t.call(pa, window=window, num_splits=1)
+    torch.cuda.synchronize()
+    assert pa.pa_read_device_status(ws) == 0
+    assert torch.equal(out[1:n], want[1:n]) and torch.equal(lse[1:n], want_l[1:n])
+    assert bool((~torch.isfinite(out[0].float())).any(-1).all())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("hq,hkv,D", [(16, 4, 256), (8, 2, 128)])
+def test_tree_bad_page_within_a_long_piece(pa, fmt, hq, hkv, D):
+    """A page that is not there, far from both ends: its tokens are skipped and it is reported, with nothing else."""
+    t = Tree(98, [(4000, 10), (90, 4)], hq, hkv, D, 16, fmt)
+    good = t.reference()
+    args = list(t.args())
+    args[3][0, 60] = 1 << 20
+    out, lse, ws = t.call(pa, args=args, num_splits=2)
+    torch.cuda.synchronize()
+    assert pa.pa_read_device_status(ws) == pa.PA_DEV_BAD_PAGE
+    s = slice(10, 14)
+    R.check_tree(f64(out[s]), f64(lse[s]), *(x[s] for x in good), D)
+    assert bool(torch.isfinite(out[:10].float()).all())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("scale", [0.0, -0.09, 1.5])
+def test_tree_scales(pa, fmt, scale):
+    t = Tree(100, [(300, 9), (70, 70 - 6), (1, 1)], 8, 2, 128, 16, fmt)
+    t.scale = scale
+    t.check(pa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+def test_tree_most_splits_and_most_nodes_announced(pa, fmt):
+    """More shares than there is work, and room for more nodes than any row has."""
+    t = Tree(101, [(200, 3), (40, 1)], 8, 2, 128, 16, fmt)
+    t.check(pa, num_splits=4096, max_query=64)
+
+
+@pytest.mark.parametrize("D,fmt", [(256, "bf16"), (128, "fp8"), (128, "bf16"), (64, "nvfp4")])
+def test_tree_on_memory_that_was_not_read_before(pa, D, fmt):
+    """Copies that come back in any order: every call ends by itself."""
+    for seed in range(12):
+        t = Tree(200 + seed, [(2000 + 97 * seed, 5 + seed), (300, 9)], 8, 2, D, 32, fmt)
+        _, _, ws = t.call(pa, num_splits=1 + seed)
+        torch.cuda.synchronize()
+        assert pa.pa_read_device_status(ws) == 0
 
 
 # ------------------------------------------------------------------------------------------ plan

@@ -90,13 +90,14 @@ def tree_attention(q, keys, values, masks, L, scale, window):
     return out, lse, spread, size
 
 
-def check_tree(got_o, got_l, out, lse, spread, size, D):
+def check_tree(got_o, got_l, out, lse, spread, size, D, lost=0.0):
     """The bounds: products of two 8-bit-significand values are exact in fp32 and a sum of D of them
     is off by at most D steps of 2^-23 of the sum of magnitudes, so a score by es = 2 (D + 16) 2^-23 size (two
     for the scaling and the exponential's own error); a weight by a factor e^es and, as a matrix operand,
-    half a bf16 step (2^-8); their sum is normalised in fp32; the output is rounded once (2^-8)."""
+    half a bf16 step (2^-8); their sum is normalised in fp32; the output is rounded once (2^-8).
+    lost: what weights too small for their operand's type leave out (0 with bf16 operands)."""
     es = 2 * (D + 16) * 2.0 ** -23 * size + 2.0 ** -18
-    tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2 * es[..., None]) * 1.01 * spread + 1e-30
+    tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2 * es[..., None]) * 1.01 * spread + lost + 1e-30
     err = np.abs(got_o - out)
     assert np.all(np.isfinite(got_o)), "not finite"
     worst = np.unravel_index(np.argmax(err / tol), err.shape)
