@@ -31,7 +31,7 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // How a call's query rows are tiled, and where its workspace's parts lie.
 struct TreePlan {
   int G, gt, qt, nsub, QT, nseqh, nparts_max;
-  size_t off_desc, off_lse, off_o, off_half, off_seq, total;
+  size_t off_status, off_lse, off_o, off_half, total;
 };
 
 int tree_plan(int batch, int max_query, int Hq, int Hkv, int D, int max_ctx, int P, int num_splits, TreePlan *pl) {
@@ -50,16 +50,14 @@ int tree_plan(int batch, int max_query, int Hq, int Hkv, int D, int max_ctx, int
   pl->nparts_max = num_splits > 0 ? num_splits : kAutoParts;
   const size_t np = (size_t)pl->nparts_max, rows = np * 2 * pl->QT * kTreeRows;
   size_t off = sizeof(WsHeader);
-  pl->off_desc = off;
-  off = round_up(off + np * sizeof(TreeDesc), 256);
+  pl->off_status = off;
+  off = round_up(off + np * sizeof(uint32_t), 256);
   pl->off_lse = off;
   off = round_up(off + rows * sizeof(float), 256);
   pl->off_o = off;
   off = round_up(off + rows * D * sizeof(float), 256);
   pl->off_half = off;
   off = round_up(off + np * 2 * kTreeRows * sizeof(TreeHalf), 256);
-  pl->off_seq = off;
-  off = round_up(off + (size_t)(batch > 0 ? batch : 1) * Hkv * pl->nseqh * sizeof(int32_t), 256);
   pl->total = off;
   return PA_OK;
 }
@@ -149,11 +147,10 @@ int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32
   a.tree_mask = tree_mask;
   a.out = static_cast<uint16_t *>(out);
   a.lse = lse;
-  a.desc = reinterpret_cast<TreeDesc *>(ws + pl.off_desc);
+  a.cta_status = reinterpret_cast<uint32_t *>(ws + pl.off_status);
   a.part_lse = reinterpret_cast<float *>(ws + pl.off_lse);
   a.part_o = reinterpret_cast<float *>(ws + pl.off_o);
   a.halves = reinterpret_cast<TreeHalf *>(ws + pl.off_half);
-  a.seq_last = reinterpret_cast<int32_t *>(ws + pl.off_seq);
   a.batch = batch;
   a.tokens = tokens;
   a.max_query = max_query;

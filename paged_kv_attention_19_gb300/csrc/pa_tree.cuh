@@ -59,10 +59,9 @@ struct TreeArgs {
   const uint64_t *tree_mask;
   uint16_t *out;
   float *lse;           // or null
-  struct TreeDesc *desc;  // [nparts]
+  uint32_t *cta_status; // [nparts]: PA_DEV_* bits
   float *part_o;        // [nparts, 2, D / 4, QT * 128, 4]: rows beside each other, so that a warp's stores are whole lines
   float *part_lse;      // [nparts, 2, QT * 128], log2 units
-  int32_t *seq_last;    // [batch, hs]: CTA of the last piece of a sequence that several share
   struct TreeHalf *halves;        // [nparts, 2, 128]: the groups' halves of a one-tile piece
   int batch, tokens, max_query, Hq, Hkv, G;
   int gt, qt, nsub;     // a tile: qt nodes x gt heads; nsub tiles for a node's heads (G > 128)
@@ -71,12 +70,6 @@ struct TreeArgs {
   int piece_cost, nparts, hg;
   float qscale;         // scale * log2(e) (* the keys' scale)
   float vscale;
-};
-
-struct alignas(16) TreeDesc {  // what a CTA leaves for the combine kernel
-  uint32_t status;   // PA_DEV_* bits
-  int32_t b, hs;     // the sequence that its last piece begins and does not end; b = -1: none
-  int32_t slot;      // the partial slot of that piece
 };
 
 struct TreeHalf {  // one row's state in one softmax group, for the merge of a one-tile piece
@@ -159,12 +152,12 @@ static_assert(sizeof(TreeStage) == 16 && sizeof(TreePieceRec) == 48, "records of
 
 struct TreePart {
   int32_t found_b, pad;
-  long long found_off, x_begin, x_end, warp_part[16];
+  long long found_x, x_begin, x_end, warp_part[16];
 };
 
 struct TreeMisc {
   uint32_t status, tmem;
-  int32_t npieces, open_b, open_hs, open_slot;
+  int32_t npieces, pad;
   TreePart part;
 };
 
@@ -191,12 +184,13 @@ struct TreeRow {
   int start, n, L;  // n = 0: nothing to do
 };
 
-// Row b, its lengths checked: a bad row has no nodes and sets PA_DEV_BAD_LEN.
+// Row b, its lengths checked: a bad row has no nodes and sets PA_DEV_BAD_LEN.  (From L2: the combine kernel
+// reads them before the grids that come before it are known to it as complete.)
 __device__ __forceinline__ TreeRow tree_row(const TreeArgs &a, int b, uint32_t *bad) {
   TreeRow r;
-  r.start = a.query_start[b];
-  r.L = a.context_lens[b];
-  const int end = a.query_start[b + 1];
+  r.start = __ldcg(a.query_start + b);
+  r.L = __ldcg(a.context_lens + b);
+  const int end = __ldcg(a.query_start + b + 1);
   r.n = end - r.start;
   if (r.start < 0 || end < r.start || end > a.tokens || r.n > a.max_query || r.L < r.n || r.L < 0 ||
       r.L > a.max_context_len) {
@@ -272,47 +266,56 @@ __device__ __forceinline__ long long tree_scan(long long v, long long *excl, lon
   return total;
 }
 
-template <int THREADS>
-__device__ __forceinline__ void tree_partition(const TreeArgs &a, TreePart *ps, uint32_t *status) {
+// The rows' total cost W; and the row for which is(W, x, v) holds (at most one; x: the costs of the rows before it, v: its
+// own) as found_b (-1: none) and found_x = x.
+template <int THREADS, class Is>
+__device__ __forceinline__ long long tree_find(const TreeArgs &a, TreePart *ps, uint32_t *bad, const Is &is) {
   const int tid = threadIdx.x;
   if (tid == 0) ps->found_b = -1;
-  __syncthreads();
-  const int NG = a.nparts / a.hg, grp = (int)blockIdx.x / a.hg;
-  const bool member = grp < NG;
-  uint32_t bad = 0;
   // up to THREADS rows: one scan gives the total and the place; more: a pass for the total, one for the place
   const bool once = a.batch <= THREADS;
   long long W = 0, v = 0, ex = 0;
   if (once) {
-    if (tid < a.batch) v = tree_cost(a, tree_row(a, tid, &bad));
+    if (tid < a.batch) v = tree_cost(a, tree_row(a, tid, bad));
     W = tree_scan<THREADS>(v, &ex, ps->warp_part);
   } else {
     long long local = 0;
-    for (int b = tid; b < a.batch; b += THREADS) local += tree_cost(a, tree_row(a, b, &bad));
+    for (int b = tid; b < a.batch; b += THREADS) local += tree_cost(a, tree_row(a, b, bad));
     W = tree_scan<THREADS>(local, &ex, ps->warp_part);
   }
-  const long long xb = (long long)grp * W / NG, xe = ((long long)grp + 1) * W / NG;
-  if (member && xb < xe) {
-    long long base = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
-      if (!once) {
-        v = b0 + tid < a.batch ? tree_cost(a, tree_row(a, b0 + tid, &bad)) : 0;
-        const long long total = tree_scan<THREADS>(v, &ex, ps->warp_part);
-        ex += base;
-        base += total;
-      }
-      if (v > 0 && xb >= ex && xb < ex + v) {
-        ps->found_b = b0 + tid;
-        ps->found_off = xb - ex;
-      }
-      __syncthreads();
-      if (ps->found_b >= 0) break;
+  long long base = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
+    if (!once) {
+      uint32_t again = 0;
+      v = b0 + tid < a.batch ? tree_cost(a, tree_row(a, b0 + tid, &again)) : 0;
+      const long long total = tree_scan<THREADS>(v, &ex, ps->warp_part);
+      ex += base;
+      base += total;
     }
+    if (v > 0 && is(W, ex, v)) {
+      ps->found_b = b0 + tid;
+      ps->found_x = ex;
+    }
+    __syncthreads();
+    if (ps->found_b >= 0) break;
   }
+  return W;
+}
+
+// This CTA's range [x_begin, x_end) of the rows' costs, and the row that it begins in.
+template <int THREADS>
+__device__ __forceinline__ void tree_partition(const TreeArgs &a, TreePart *ps, uint32_t *status) {
+  const int NG = a.nparts / a.hg, grp = (int)blockIdx.x / a.hg;
+  const bool member = grp < NG;
+  uint32_t bad = 0;
+  const long long W = tree_find<THREADS>(a, ps, &bad, [&](long long W, long long x, long long v) {
+    const long long xb = (long long)grp * W / NG;
+    return member && xb < ((long long)grp + 1) * W / NG && xb >= x && xb < x + v;
+  });
   if (bad) atomicOr(status, bad);
-  if (tid == 0) {
-    ps->x_begin = member ? xb : 0;
-    ps->x_end = member ? xe : 0;
+  if (threadIdx.x == 0) {
+    ps->x_begin = member ? (long long)grp * W / NG : 0;
+    ps->x_end = member ? ((long long)grp + 1) * W / NG : 0;
   }
   __syncthreads();
 }
@@ -323,8 +326,9 @@ struct TreePiece {
   bool starts, ends;
 };
 
-// Where a piece's results go: -1 the outputs (it is a whole sequence), else the partial slot (its number in the CTA).
-__device__ __forceinline__ int tree_slot(const TreePiece &p, int number) { return p.starts && p.ends ? -1 : number == 0 ? 0 : 1; }
+// Where a piece's results go: -1 the outputs (it is a whole sequence); else the CTA's partial slot 1 (it begins a
+// sequence that another CTA ends) or 0.
+__device__ __forceinline__ int tree_slot(const TreePiece &p) { return p.starts ? (p.ends ? -1 : 1) : 0; }
 
 // A warp's walk over its CTA's pieces (all lanes call together); each walker sees the same pieces.
 struct TreeWalker {
@@ -337,7 +341,7 @@ struct TreeWalker {
   __device__ TreeWalker(const TreeArgs &args, const TreePart *ps, int lane_) : a(args), lane(lane_) {
     hs_row = a.Hkv * a.nseqh;
     b_first = max(ps->found_b, 0);
-    in_first = ps->found_b >= 0 ? (int)ps->found_off : 0;
+    in_first = ps->found_b >= 0 ? (int)(ps->x_begin - ps->found_x) : 0;
     span = ps->found_b >= 0 ? ps->x_end - ps->x_begin : 0;
     R = span;
     fill(b_first);
@@ -615,7 +619,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     fence_mbar_init();
     misc->status = 0;
     misc->npieces = 0;
-    misc->open_b = -1;
   }
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tm_k);
@@ -663,17 +666,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     while (has && ok) {
       has_next = walker.take<C::QT>(nxt);
       if (has_next) nwin = window_of(nxt, 0);
-      const int slot = tree_slot(cur, npieces);
-      if (lane == 0) {
-        // where the combine kernel finds a sequence that several CTAs share: its first CTA names it
-        if (cur.starts && !cur.ends) {
-          misc->open_b = cur.b;
-          misc->open_hs = cur.hs;
-          misc->open_slot = slot;
-        } else if (cur.ends && !cur.starts) {
-          a.seq_last[(size_t)cur.b * a.Hkv * a.nseqh + cur.hs] = (int32_t)blockIdx.x;
-        }
-      }
       const int prefix = cur.L - cur.n;
       // every node sees the tokens [lo_max, prefix): depths are below n
       const int lo_max = a.window > 0 ? max(cur.L - a.window, 0) : 0;
@@ -871,7 +863,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const TreeRow row = {pc.start, pc.n, pc.L};
       const int prefix = pc.L - pc.n, lo_min = tree_lo(a, row), lo_max = a.window > 0 ? max(pc.L - a.window, 0) : 0;
       if (lane == 0) {
-        prec[k & 1] = TreePieceRec{0, stages, pc.two, tree_slot(pc, (int)k), pc.b, pc.L, pc.n, pc.start, pc.t0, pc.g, lo_min, 0};
+        prec[k & 1] = TreePieceRec{0, stages, pc.two, tree_slot(pc), pc.b, pc.L, pc.n, pc.start, pc.t0, pc.g, lo_min, 0};
         const int boxes = min(a.qt, a.max_query) * a.gt * 128;  // bytes of one plane's box
         mbar_arrive_expect_tx(q_full, (uint32_t)(C::NPL * boxes * (pc.two ? 2 : 1)));
         for (int x = 0; x < (pc.two ? 2 : 1); ++x) {
@@ -1387,7 +1379,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tc_dealloc(tmem, C::TM_COLS);
-  if (tid == 0) a.desc[blockIdx.x] = TreeDesc{misc->status, misc->open_b, misc->open_hs, misc->open_slot};
+  if (tid == 0) a.cta_status[blockIdx.x] = misc->status;
   if (misc->npieces == 0) {
     // a range that held no key can still lie between two pieces of a sequence: its slot 0 weighs nothing
     for (int h = tid; h < C::QT * kTreeRows; h += C::THREADS)
@@ -1397,87 +1389,108 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
 // ---------------------------------------------------------------------------------------- combine
 // Grid (CTAs of the split kernel, rows / rows per block): a block for some rows of the sequence that CTA x begins
-// and does not end (at most one).  Its pieces lie in CTAs x, x + HG, ..., in ascending order of the keys.  A warp
-// takes 8 rows x 32 columns: the partials of 8 rows lie beside each other, 16 bytes of each.  Eight pieces' log-sum-
-// exps and values are loaded together and merged in order.
+// and does not end (at most one).  Its pieces lie in CTAs x, x + HG, ..., in ascending order of the keys.  Which one
+// that is and where it ends follow from the partition, which a block works out while the split kernel's last CTAs run;
+// behind it only the partial results are loaded.  A warp takes 8 rows x 32 columns: the partials of 8 rows lie beside
+// each other, 16 bytes of each.  Eight pieces' log-sum-exps and values are loaded together and merged in order; of
+// sequences of two tiles, whose many rows want more warps and which are cut into fewer pieces, four (64-node trees
+// 153 -> 149 us; a single request of one tile, cut into 19, would lose 15.8 -> 16.7).  At most four blocks share a
+// sequence's rows (64-node trees: two 152, four 153, sixteen, one for each 16 rows, 158 us; windowed at head_dim 256:
+// 59.5, 57.3, 59.7).
 
-constexpr int kCombineThreads = 256;
+constexpr int kCombineThreads = 256, kCombineBlocks = 4;  // most blocks for one sequence
 __host__ __device__ constexpr int combine_rows(int D) { return 8 * (kCombineThreads / 32) / (D / 32); }  // rows of a block
 
+// The rows that a sequence can have: of a single tile those that it holds.
+__host__ __device__ inline int tree_max_rows(const TreeArgs &a, int QT) {
+  const int nodes = a.qt < a.max_query ? a.qt : a.max_query;
+  return a.nseqh * QT > 1 ? QT * kTreeRows : a.gt * nodes;
+}
+
 template <int D, int QT>
-__global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const TreeArgs a, uint32_t *status) {
+__global__ void __launch_bounds__(kCombineThreads, QT == 2 ? 3 : 2) tree_combine_kernel(const TreeArgs a, uint32_t *status) {
+  __shared__ TreePart part;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = (int)blockIdx.x;
+  const int NG = a.nparts / a.hg, grp = cta / a.hg, hs = cta % a.hg;
+  // the row whose first unit lies in this range, and whose last one does not; k: the ranges that it lies in
+  uint32_t ignored = 0;
+  const long long W = tree_find<kCombineThreads>(a, &part, &ignored, [&](long long W, long long x, long long v) {
+    const long long xb = (long long)grp * W / NG, xe = ((long long)grp + 1) * W / NG, first = x + a.piece_cost;
+    return grp < NG && xb <= first && first < xe && xe < x + v;
+  });
+  const int b = part.found_b;
+  const TreeRow r = b >= 0 ? tree_row(a, b, &ignored) : TreeRow{0, 0, 0};
+  const long long end = b >= 0 ? part.found_x + tree_cost(a, r) : 0;
+  const int k = b >= 0 ? (int)((end * NG + W - 1) / W) - grp : 0;
   pdl_wait();
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = (int)blockIdx.x;
   if (cta == 0 && blockIdx.y == 0 && warp == 0) {
     uint32_t st = 0;
-    for (int i = lane; i < a.nparts; i += 32) st |= a.desc[i].status;
+    for (int i = lane; i < a.nparts; i += 32) st |= a.cta_status[i];
     st = __reduce_or_sync(FULL, st);
     if (lane == 0) *status = st;
   }
-  const TreeDesc d = a.desc[cta];
-  if (d.b < 0) return;
-  uint32_t ignored = 0;
-  const TreeRow r = tree_row(a, d.b, &ignored);
-  const int last = a.seq_last[(size_t)d.b * a.Hkv * a.nseqh + d.hs];
-  constexpr int RS = QT * kTreeRows, WPR = D / 32, CHUNK = 8;  // warps for one row
-  const int pr = (int)blockIdx.y * combine_rows(D) + warp / WPR * 8 + (lane & 7);
-  const int t = (d.hs % a.nseqh) * QT + pr / kTreeRows, row = pr % kTreeRows;
-  // (a stale entry only where the split kernel gave up)
-  if (r.n == 0 || t >= tree_tiles(a, r.n) || last <= cta || last >= a.nparts || (last - cta) % a.hg != 0) return;
-  const TreeTile tl = tree_tile(a, t, r.n);
-  const int pos = row / a.gt, h = row - pos * a.gt, k = (last - cta) / a.hg + 1;
-  if (pos >= tl.nq || h >= tl.nh) return;  // (nothing below is the whole warp's)
-  const int c0 = warp % WPR * 32 + (lane >> 3) * 4;  // this lane's values: c0 .. c0 + 3 and c0 + 16 .. c0 + 19
-  float M = -INFINITY, Z = 0.f, acc[8];
+  if (b < 0) return;
+  constexpr int RS = QT * kTreeRows, WPR = D / 32, CHUNK = QT == 2 ? 4 : 8;  // warps for one row; pieces at a time
+  const int rows = tree_max_rows(a, QT);
+#pragma unroll 1
+  for (int pr = (int)blockIdx.y * combine_rows(D) + warp / WPR * 8 + (lane & 7); pr < rows; pr += (int)gridDim.y * combine_rows(D)) {
+    const int t = (hs % a.nseqh) * QT + pr / kTreeRows, row = pr % kTreeRows;
+    if (t >= tree_tiles(a, r.n)) return;
+    const TreeTile tl = tree_tile(a, t, r.n);
+    const int pos = row / a.gt, h = row - pos * a.gt;
+    if (pos >= tl.nq || h >= tl.nh) continue;  // (nothing below is the whole warp's)
+    const int c0 = warp % WPR * 32 + (lane >> 3) * 4;  // this lane's values: c0 .. c0 + 3 and c0 + 16 .. c0 + 19
+    float M = -INFINITY, Z = 0.f, acc[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  for (int i0 = 0; i0 < k; i0 += CHUNK) {
-    float lc[CHUNK];
-    float4 x[CHUNK][2];
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int i0 = 0; i0 < k; i0 += CHUNK) {
+      float lc[CHUNK];
+      float4 x[CHUNK][2];
 #pragma unroll
-    for (int u = 0; u < CHUNK; ++u) {
-      lc[u] = -INFINITY;
-      x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i0 + u < k) {
-        const size_t slot = (size_t)(cta + (i0 + u) * a.hg) * 2 + (i0 + u == 0 ? d.slot : 0);
-        lc[u] = a.part_lse[slot * RS + pr];
-        const float *src = a.part_o + slot * RS * D + (size_t)c0 * RS + pr * 4;
-        x[u][0] = *reinterpret_cast<const float4 *>(src);
-        x[u][1] = *reinterpret_cast<const float4 *>(src + 16 * RS);
+      for (int u = 0; u < CHUNK; ++u) {
+        lc[u] = -INFINITY;
+        x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + u < k) {
+          const size_t slot = (size_t)(cta + (i0 + u) * a.hg) * 2 + (i0 + u == 0 ? 1 : 0);
+          lc[u] = a.part_lse[slot * RS + pr];
+          const float *src = a.part_o + slot * RS * D + (size_t)c0 * RS + pr * 4;
+          x[u][0] = *reinterpret_cast<const float4 *>(src);
+          x[u][1] = *reinterpret_cast<const float4 *>(src + 16 * RS);
+        }
       }
-    }
-    float mn = M;
+      float mn = M;
 #pragma unroll
-    for (int u = 0; u < CHUNK; ++u) mn = fmaxf(mn, lc[u]);
-    const float sc = M == -INFINITY ? 0.f : fast_exp2(M - mn);
-    M = mn;
-    Z *= sc;
+      for (int u = 0; u < CHUNK; ++u) mn = fmaxf(mn, lc[u]);
+      const float sc = M == -INFINITY ? 0.f : fast_exp2(M - mn);
+      M = mn;
+      Z *= sc;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] *= sc;
+      for (int e = 0; e < 8; ++e) acc[e] *= sc;
 #pragma unroll
-    for (int u = 0; u < CHUNK; ++u) {
-      // an empty piece (lse -inf) weighs nothing, and what lies in its place is not looked at: it was not written
-      const float w = lc[u] == -INFINITY ? 0.f : fast_exp2(lc[u] - mn);
-      if (w != 0.f) {
-        Z += w;
+      for (int u = 0; u < CHUNK; ++u) {
+        // an empty piece (lse -inf) weighs nothing, and what lies in its place is not looked at: it was not written
+        const float w = lc[u] == -INFINITY ? 0.f : fast_exp2(lc[u] - mn);
+        if (w != 0.f) {
+          Z += w;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          acc[4 * v] = fmaf(w, x[u][v].x, acc[4 * v]);
-          acc[4 * v + 1] = fmaf(w, x[u][v].y, acc[4 * v + 1]);
-          acc[4 * v + 2] = fmaf(w, x[u][v].z, acc[4 * v + 2]);
-          acc[4 * v + 3] = fmaf(w, x[u][v].w, acc[4 * v + 3]);
+          for (int v = 0; v < 2; ++v) {
+            acc[4 * v] = fmaf(w, x[u][v].x, acc[4 * v]);
+            acc[4 * v + 1] = fmaf(w, x[u][v].y, acc[4 * v + 1]);
+            acc[4 * v + 2] = fmaf(w, x[u][v].z, acc[4 * v + 2]);
+            acc[4 * v + 3] = fmaf(w, x[u][v].w, acc[4 * v + 3]);
+          }
         }
       }
     }
-  }
-  const float inv = Z == 0.f ? 0.f : 1.f / Z;
-  const size_t at = (size_t)(r.start + tl.i0 + pos) * a.Hq + (d.hs / a.nseqh) * a.G + tl.h0 + h;
+    const float inv = Z == 0.f ? 0.f : 1.f / Z;
+    const size_t at = (size_t)(r.start + tl.i0 + pos) * a.Hq + (hs / a.nseqh) * a.G + tl.h0 + h;
 #pragma unroll
-  for (int v = 0; v < 2; ++v)
-    *reinterpret_cast<uint2 *>(a.out + at * D + c0 + 16 * v) =
-        make_uint2(pack_bf16x2(acc[4 * v] * inv, acc[4 * v + 1] * inv), pack_bf16x2(acc[4 * v + 2] * inv, acc[4 * v + 3] * inv));
-  if (c0 == 0 && a.lse) a.lse[at] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * LN2;
+    for (int v = 0; v < 2; ++v)
+      *reinterpret_cast<uint2 *>(a.out + at * D + c0 + 16 * v) =
+          make_uint2(pack_bf16x2(acc[4 * v] * inv, acc[4 * v + 1] * inv), pack_bf16x2(acc[4 * v + 2] * inv, acc[4 * v + 3] * inv));
+    if (c0 == 0 && a.lse) a.lse[at] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * LN2;
+  }
 }
 
 }  // namespace pa

@@ -42,9 +42,8 @@ cudaError_t launch_tree(const TreeLaunch &l, cudaStream_t stream) {
   e = launch_pdl(tree_split_kernel<C>, dim3((unsigned)a.nparts), C::THREADS, TreeSmem<C>::BYTES, stream,
                  l.tm_k, l.tm_v, l.tm_q, a);
   if (e != cudaSuccess) return e;
-  // the rows that a sequence can have: of a single tile those that it holds
-  const int rows = a.nseqh * QT > 1 ? QT * kTreeRows : a.gt * (a.qt < a.max_query ? a.qt : a.max_query);
-  const dim3 grid((unsigned)a.nparts, (unsigned)((rows + combine_rows(D) - 1) / combine_rows(D)));
+  const int groups = (tree_max_rows(a, QT) + combine_rows(D) - 1) / combine_rows(D);
+  const dim3 grid((unsigned)a.nparts, (unsigned)(groups < kCombineBlocks ? groups : kCombineBlocks));
   return launch_pdl(tree_combine_kernel<D, QT>, grid, kCombineThreads, 0, stream, a, l.status);
 }
 
