@@ -855,11 +855,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     TreePiece pc;
     uint32_t k = 0, t = 0;
     const int nbox = BN >> a.log2_bh;
+    int stages = 0;
     bool ok = true;
+    // the last piece's scores are done: of all the kernel's waits the one that lasts as long as a piece.  65536 stages
+    // take some 60 ms; a second more for each
+    auto scored = [&]() -> bool {
+      const bool r = mbar_wait_warp(q_empty, (k - 1) & 1, WAIT_LIMIT_NS * (1 + ((uint64_t)stages >> 16)));
+      if (!r && lane == 0) atomicOr(status, PA_DEV_TIMEOUT);
+      return r;
+    };
     while (ok && walker.take<C::QT>(pc)) {
-      if (k > 0) ok = __all_sync(FULL, mbar_wait(q_empty, (k - 1) & 1, status));
+      if (k > 0) ok = scored();
       if (!ok) break;
-      const int stages = (pc.ue - pc.ub + nbox - 1) / nbox;
+      stages = (pc.ue - pc.ub + nbox - 1) / nbox;
       const TreeRow row = {pc.start, pc.n, pc.L};
       const int prefix = pc.L - pc.n, lo_min = tree_lo(a, row), lo_max = a.window > 0 ? max(pc.L - a.window, 0) : 0;
       if (lane == 0) {
@@ -934,7 +942,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // no copy is in flight when the CTA exits, and the issuing threads learn of the end
     if (k > 0) {
       mbar_wait(q_full, (k - 1) & 1, status);
-      if (ok) ok = __all_sync(FULL, mbar_wait(q_empty, (k - 1) & 1, status));
+      if (ok) ok = scored();
     }
     if (ok && lane == 0) {
       prec[k & 1].end = 1;
