@@ -514,7 +514,10 @@ int pa_qk_norm_rope_write_nvfp4(const void *q, const void *k, const void *v, con
  * pa_verify_gqa; the workspace is pa_tree_workspace_size bytes, and its status
  * word is read by pa_read_device_status.  For a fixed num_splits results are
  * bitwise reproducible and independent of the physical page order.  batch == 0
- * is a no-op.
+ * or num_tokens == 0 is a no-op (the status word stays as it was).
+ * bf16 pools: products of bf16 operands, weights rounded to bf16.  FP8 and NVFP4
+ * pools: codes as exact f16 values, a query row scaled by a power of two to f16,
+ * weights rounded to f16.  The calls always use the default wait limit.
  */
 int pa_tree_gqa(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
                 const int32_t *context_lens, const int32_t *query_start, const uint64_t *tree_mask,
@@ -612,7 +615,7 @@ int pa_last_launch_count(void);
  * (waiting up to another second), so no CTA ends with a copy in flight or
  * leaves a warp waiting.  The call still returns normally, but its out and
  * lse are unspecified.  The next call with a sufficient limit is
- * unaffected.  The MLA kernels always use the default.  A call at the
+ * unaffected.  The MLA and tree kernels always use the default.  A call at the
  * default limit runs kernels compiled with the 1 s bound fixed; a call with
  * any other limit runs the same kernels compiled with it as an argument.
  * Always returns PA_OK.

@@ -181,7 +181,8 @@ __device__ __forceinline__ void plan_state_all_granted(const PlanArgs &a, const 
 // independent: each has all rows' sums, writes its share of the rows' table entries and of the tokens, and reads of
 // the table and the list what no CTA writes.  Only state that is updated in place makes them meet: with few CTAs
 // (PLAN_CLUSTER) at a barrier of the one cluster that they form, when all have read all of their inputs, with many
-// (PLAN_AFTER) in a launch of its own behind this one.
+// (PLAN_AFTER) in a launch of its own behind this one.  48 rows of trees: 4.8 us; 512 rows of 1 to 1024 tokens: 5.9 us
+// (one cluster of eight CTAs for those, waiting for one another's sums: 38 us).
 enum PlanMode { PLAN_APART = 0, PLAN_CLUSTER = 1, PLAN_AFTER = 2 };
 template <int MODE>
 __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs a) {
@@ -292,8 +293,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_state_kernel(const PlanArgs
 
 // Accepted paths.  Block (x, y) moves 256 16-byte columns of row y: a column is one 16-byte piece of
 // a token in one pool of one layer, and each thread moves its column's accepted nodes in ascending
-// order, eight loads in flight (sixteen: 14.0 us for 12.2, fewer threads fit an SM).  A node's target lies at or before its source and behind every
-// earlier source, so no source is overwritten before it is read.
+// order, eight loads in flight (sixteen: 14.0 us for 12.2, fewer threads fit an SM).  A node's target lies
+// at or before its source and behind every earlier source, so no source is overwritten before it is read.
+// Bound by memory and, before it, by two dependent trips (lengths and path, pages): 48 FP8 layers of 64 rows,
+// 9 nodes of 63 each, 12.2 us (4.0 TB/s read and written); one layer 2.5 us in a graph.
 constexpr int kCompactThreads = 256;
 
 struct CompactArgs {

@@ -59,7 +59,9 @@ def rope(pa, fmt="", **kw):
     (dict(qs=1028), MISALIGNED), (dict(q=0x100008), MISALIGNED), (dict(wq=0x400008), MISALIGNED),
     (dict(cs=0x420004), MISALIGNED), (dict(slots=0x440004), MISALIGNED), (dict(kp=0x600008), MISALIGNED),
     (dict(qo=0x100010), INVALID), (dict(qo=0x100000, qs=2048), INVALID), (dict(qo=0x200000), INVALID),
-    (dict(vp=0x600010), INVALID), (dict(kp=0x300000), INVALID), (dict(vp=0x500000), INVALID)])
+    (dict(vp=0x600010), INVALID), (dict(kp=0x300000), INVALID), (dict(vp=0x500000), INVALID),
+    (dict(qo=0x420010), INVALID), (dict(cs=0x500000), INVALID), (dict(pos=0x600000), INVALID), (dict(slots=0x700008), INVALID),
+    (dict(wq=0x500010), INVALID), (dict(wk=0x600010), INVALID), (dict(status=0x500004), INVALID)])
 def test_rope_write_refuses(pa, fmt, kw, rc):
     assert rope(pa, fmt, **kw) == rc
 
