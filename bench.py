@@ -56,7 +56,7 @@ KERNEL_SOURCES = {"gqa": ("pa_gqa.cuh", "pa_partition.cuh", "pa_common.cuh", "pa
                   "gqa_fp4": ("pa_gqa_fp4.cuh", "pa_gqa.cuh", "pa_partition.cuh", "pa_common.cuh", "pa_api.cu"),
                   "mla": ("pa_mla_tc.cuh", "pa_tcgen05.cuh", "pa_mla.cu", "pa_gqa.cuh", "pa_partition.cuh",
                           "pa_common.cuh"),
-                  "write": ("pa_kv_write.cu", "pa_common.cuh")}
+                  "write": ("pa_kv_write.cu", "pa_quant.cuh", "pa_common.cuh")}
 
 
 def compute_dtype(w):
