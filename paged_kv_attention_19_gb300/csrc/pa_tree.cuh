@@ -575,20 +575,11 @@ __device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
   return d;
 }
 
-// The products, issued by the threads for which `one` holds (the operands are the whole warp's).
-__device__ __forceinline__ void tree_mma_ss(bool one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"((uint32_t)one)
-      : "memory");
-}
-__device__ __forceinline__ void tree_mma_ts(bool one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"((uint32_t)one)
-      : "memory");
+// One thread of a converged warp, the same one at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one != 0;
 }
 
 // ---------------------------------------------------------------------------------------- the kernel
@@ -780,31 +771,28 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     if (lane == 0) misc->npieces = npieces;
   } else if (warp == 1 || (warp == 2 && C::GROUPS == 2)) {
-    // ------------------------------------------------------------ products (the warp's first thread issues them; what
-    // they are made of is the warp's, so that it is worked out once and lies where the instructions want it)
-    {
-      const bool one = lane == 0;
-      const int x = __shfl_sync(FULL, warp - 1, 0);
+    // ------------------------------------------------------------ products (one thread of the warp, elected: with the
+    // first one, which the compiler cannot know to be alone, each instruction's operands take a detour, 64-node trees
+    // 147 -> 133 us)
+    if (elect_one()) {
+      const int x = warp - 1;
       const uint32_t ring = smem_u32(smem + S::OFF_RING), qb = smem_u32(smem);
       uint32_t t0 = 0, c = 0, d = 0;  // the piece's first stage; items begun and finished
       bool ok = true;
-      auto wait = [&](uint64_t *bar, uint32_t parity) { return (bool)__all_sync(FULL, mbar_wait(bar, parity, status)); };
       auto buf = [&](uint32_t i) { return C::buffer(x, i); };
       auto par = [&](uint32_t i) { return C::buffer_phase(i); };
       // the slot of a tile is free for whoever shares it: with this thread's operations, or at once
       auto release = [&](uint64_t *bar, bool read, bool alone) {
-        if (one) {
-          if (read) tc_commit(bar);
-          else mbar_arrive(bar);
-          if (C::GROUPS == 2 && alone) mbar_arrive(bar);
-        }
+        if (read) tc_commit(bar);
+        else mbar_arrive(bar);
+        if (C::GROUPS == 2 && alone) mbar_arrive(bar);
       };
       // the scores of the next item: query tile qx, stage t
       auto begin = [&](uint32_t t, int qx, bool present, bool alone) -> bool {
         const uint32_t b = buf(c);
         constexpr uint32_t BACK = C::NB / C::GROUPS;  // items since this buffer's last
-        if (!wait(&full[t % C::NK], (t / C::NK) & 1)) return false;
-        if (c >= BACK && !wait(&pv_done[b], par(c - BACK))) return false;
+        if (!mbar_wait(&full[t % C::NK], (t / C::NK) & 1, status)) return false;
+        if (c >= BACK && !mbar_wait(&pv_done[b], par(c - BACK), status)) return false;
         if (present) {
           tc_fence_after();
           const uint64_t qd = tc_sdesc_sw128(qb + qx * (C::NPL * C::QPLANE), 16, 1024);
@@ -813,13 +801,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           for (int p = 0; p < C::NPL; ++p)
 #pragma unroll(C::QUANT ? 1 : 4)
             for (int kk = 0; kk < 4; ++kk)
-              tree_mma_ss(one, tmem + C::TM_S + b * BN, qd + (uint64_t)((p * C::QPLANE + 32 * kk) >> 4),
+              tc_mma_ss(tmem + C::TM_S + b * BN, qd + (uint64_t)((p * C::QPLANE + 32 * kk) >> 4),
                         kd + (uint64_t)((p * C::PLANE + 32 * kk) >> 4), C::IDESC_S, (p | kk) != 0 ? 1u : 0u);
-          if (one) tc_commit(&s_full[b]);
+          tc_commit(&s_full[b]);
         } else {
-          if (one) mbar_arrive(&s_full[b]);  // no scores: the record alone
+          mbar_arrive(&s_full[b]);  // no scores: the record alone
         }
-        if (one) mbar_arrive(&s_full[b]);
+        mbar_arrive(&s_full[b]);
         release(&empty[t % C::NK], present, alone);
         ++c;
         return true;
@@ -827,11 +815,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // the second product of the oldest item; first: of this thread in the piece
       auto finish = [&](uint32_t t, uint32_t piece, bool first, bool present, bool alone) -> bool {
         const uint32_t b = buf(d), vs = C::NK + t % C::NV;
-        if (!wait(&p_ready[b], par(d))) return false;
+        if (!mbar_wait(&p_ready[b], par(d), status)) return false;
         // the previous piece's outputs have been read, and all its V tiles with that
-        if (first && piece > 0 && !wait(o_free, (piece - 1) & 1)) return false;
+        if (first && piece > 0 && !mbar_wait(o_free, (piece - 1) & 1, status)) return false;
         // (bf16: whoever looked it over has waited for it)
-        if (!(C::QUANT ? wait(&full[vs], (t / C::NV) & 1) : wait(&clean[t % C::META], (t / C::META) & 1)))
+        if (C::QUANT ? !mbar_wait(&full[vs], (t / C::NV) & 1, status)
+                     : !mbar_wait(&clean[t % C::META], (t / C::META) & 1, status))
           return false;
         if (present) {
           tc_fence_after();
@@ -839,26 +828,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const uint64_t vd = tc_sdesc_sw128(ring + vs * C::SLOT, C::PLANE, 1024);
 #pragma unroll(C::QUANT ? 1 : BN / 16)
           for (int kk = 0; kk < BN / 16; ++kk)
-            tree_mma_ts(one, tmem + C::TM_O + o * D, tmem + C::TM_S + b * BN + 8 * kk, vd + (uint64_t)((kk * 16 * 128) >> 4),
+            tc_mma_ts(tmem + C::TM_O + o * D, tmem + C::TM_S + b * BN + 8 * kk, vd + (uint64_t)((kk * 16 * 128) >> 4),
                       C::IDESC_PV, first && kk == 0 ? 0u : 1u);
         }
-        if (one) tc_commit(&pv_done[b]);
+        tc_commit(&pv_done[b]);
         release(&empty[vs], present, alone);
         ++d;
         return true;
       };
       for (uint32_t piece = 0; ok; ++piece) {
-        ok = wait(C::QUANT ? q_conv : q_full, piece & 1);
+        ok = mbar_wait(C::QUANT ? q_conv : q_full, piece & 1, status);
         if (!ok) break;
-        int4 r = *reinterpret_cast<const int4 *>(&prec[piece & 1]);  // end, stages, two, slot
-        r.x = __shfl_sync(FULL, r.x, 0);
-        r.y = __shfl_sync(FULL, r.y, 0);
-        r.z = __shfl_sync(FULL, r.z, 0);
+        const int4 r = *reinterpret_cast<const int4 *>(&prec[piece & 1]);  // end, stages, two, slot
         if (r.x) {
-          if (one) {
-            mbar_arrive(&s_full[buf(c)]);
-            mbar_arrive(&s_full[buf(c)]);
-          }  // the softmax groups stop here
+          for (int k = 0; k < 2; ++k) mbar_arrive(&s_full[buf(c)]);  // the softmax groups stop here
           break;
         }
         const uint32_t n = (uint32_t)r.y, even = (n + 1) & ~1u;
@@ -868,13 +851,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // the second product of an item behind the scores of the next one
         for (uint32_t j = j0; j < even + dj && ok; j += dj) {
           if (j < even) ok = begin(t0 + j, two ? x : 0, j < n, alone);
-          if (j < even && j + dj >= even && one) tc_commit(q_empty);
+          if (j < even && j + dj >= even) tc_commit(q_empty);
           if (ok && j > j0) ok = finish(t0 + j - dj, piece, j == j0 + dj, j - dj < n, alone);
         }
         t0 += even;
       }
       // every operation of this thread has completed before the tensor memory is released
-      if (one) tc_commit(&drain[x]);
+      tc_commit(&drain[x]);
       mbar_wait(&drain[x], 0, status);
     }
     __syncwarp();
