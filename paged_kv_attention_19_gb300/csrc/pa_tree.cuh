@@ -37,11 +37,17 @@
 //   * FP8 and NVFP4 pools: the tiles of codes land in a ring of their own, and four more warps convert
 //     them to f16 operands (exact; two warps K tiles, two V tiles), and the query rows, scaled by a
 //     power of two each, in place; those of the V tiles then look them over.  The weights are rounded to
-//     f16 (2^-11).  These warps' code and the others' together pass the instruction cache of an SM (13% of its
-//     requests missed, and the misses of an SM wait for those of its neighbours), so the loops of these formats
-//     are rolled up where bf16's are not: FP8 137 -> 116 us, NVFP4 134 -> 110, bf16 would lose 107 -> 114 (32 ragged
-//     trees of up to 16 nodes x 8 heads over 128 to 16384 tokens, 8 key heads of 128);
-//   * two groups of four warps: one thread per score row, its item's 64 scores for the maximum, then 32 at a time.
+//     f16 (2^-11);
+//   * two groups of four warps: one thread per score row, 32 of its item's scores at a time, for the maximum and
+//     then for the weights (read twice: less code than all 64 held, 104 -> 99 us in the case below).
+// Code.  The roles' code together passes the instruction cache of an SM (with codes 13% of its requests missed, and
+// an SM's misses wait for its neighbours'), so what a stage rarely needs is kept out of its path, and with codes the
+// loops over the products' instructions are not unrolled: 32 ragged trees of up to 16 nodes x 8 heads over 128 to
+// 16384 tokens, 8 key heads of 128, FP8 137 -> 111 us, NVFP4 134 -> 104, bf16 107 -> 99.
+// Measured (GB300; bytes: the cache once): a request of 8 nodes x 32 heads over 1000 tokens 15.1 us, start-up and the
+// combine kernel's trips; 16 rows of 64 nodes x 64 heads over 1024 to 8192 tokens 132 us, 874 TFLOP/s, the issue of
+// the products; 16 windowed rows at head_dim 256 56 us, 4.5 TB/s; the ragged trees above 2.05 TB/s of FP8 codes and
+// 1.4 TB/s of NVFP4 ones, the chain from conversion to weights.
 // Tensor memory: score buffer b (the weights over its first half) at 64 b, outputs at 256.  At head_dim 256 one
 // output fills the rest: one tile, one softmax group and one issuing thread.
 #pragma once
@@ -126,7 +132,7 @@ struct TreeCfg {
     return GROUPS == 2 ? (uint32_t)x + 2 * (i & 1) : i & 3;
   }
   __host__ __device__ static constexpr uint32_t buffer_phase(uint32_t i) { return GROUPS == 2 ? (i >> 1) & 1 : (i >> 2) & 1; }
-  // registers a thread: the softmax warps' 64 scores and their row's state do not fit the launch's share
+  // registers a thread: what the softmax warps hold of a row and its output does not fit the launch's share
   // (384 x 168 or 512 x 128), so the other warps hand some over
   static constexpr bool REG_SPLIT = GROUPS == 2;
   static constexpr int REGS = QUANT ? 128 : 168;
@@ -512,29 +518,8 @@ __device__ __forceinline__ uint32_t loaded_bits(uint32_t badmask, int c, int log
 }
 
 // ---------------------------------------------------------------------------------------- tensor memory
-// Warp-wide: lane l reads consecutive columns of tensor-memory lane (taddr.lane + l).  The wait is part of
-// the statement: no use of the values can be moved before it.
-__device__ __forceinline__ void tree_ld(uint32_t taddr, float (&v)[64]) {
-  uint32_t r[64];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64+32];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
-}
-// 32 columns at each of two addresses.
+// Warp-wide: lane l reads 32 consecutive columns of tensor-memory lane (taddr.lane + l) at each of two addresses.
+// The wait is part of the statement: no use of the values can be moved before it.
 __device__ __forceinline__ void tree_ld_pair(uint32_t ta, uint32_t tb, float (&v)[32], float (&u)[32]) {
   uint32_t r[64];
   asm volatile(
@@ -702,7 +687,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         const uint32_t bad = __ballot_sync(FULL, isbad);
         const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL, load)) * (uint32_t)(C::ROWB << a.log2_bh);
-#pragma unroll(C::QUANT ? 1 : 2)
+#pragma unroll
         for (int kv = 0; kv < 2 && ok; ++kv) {
           uint32_t u;
           const int s = place(kv, u);
@@ -1105,7 +1090,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
+          if (elect_one()) {
             mbar_arrive(&full[s]);
             mbar_arrive(&raw_empty[rs]);
             if (kv == 1) mbar_arrive(&clean[t % C::META]);
@@ -1172,16 +1157,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           tc_wait_st();
         }
-        float mx;
-        {
-          float s[BN];
-          tree_ld(tS, s);
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int k = 0; k < BN / 32; ++k) {
+          float v[32];
+          tc_ld32(tS + 32 * k, v);
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < BN; i += 8)
+          for (int i = 0; i < 32; i += 8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(s[i + e], s[i + 4 + e]));
-          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(v[i + e], v[i + 4 + e]));
+          mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
         }
         mx = mx * qs - C::LIFT;
         if (!had) {
@@ -1214,7 +1200,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int k = 0; k < BN / 32; ++k) {
           uint32_t w[16];
           float x[32];
-          tc_ld32(tS + 32 * k, x);  // (again: less code in all than with the halves side by side, 149 -> 147 us)
+          tc_ld32(tS + 32 * k, x);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             const float2 y = fma_pair(make_float2(x[i], x[i + 1]), q2, sub2);
