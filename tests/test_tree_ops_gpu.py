@@ -870,3 +870,82 @@ def test_steps_of_tree_drafting(pa, fmt):
         torch.cuda.synchronize()
         assert lens.tolist() == [len(x) for x in kept]
     assert max(len(x) for x in kept) > 20
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+def test_steps_captured_are_steps_called(pa, fmt):
+    """A whole step, captured in two graphs that share the state and the workspace and are replayed in turn, gives
+    the bits of the same calls made one by one."""
+    hq, hkv, D, P, pages, B, T, steps = 8, 2, 128, 16, 64, 6, 50, 6
+    width, kind = (D, torch.bfloat16) if fmt == "bf16" else (R.row_bytes(fmt, D), torch.uint8)
+    sc = {} if fmt == "bf16" else dict(k_scale=0.02, v_scale=0.02)
+    write = {"bf16": pa.pa_qk_norm_rope_write, "fp8": pa.pa_qk_norm_rope_write_fp8, "nvfp4": pa.pa_qk_norm_rope_write_nvfp4}[fmt]
+    attend = {"bf16": pa.pa_tree_gqa, "fp8": pa.pa_tree_gqa_fp8, "nvfp4": pa.pa_tree_gqa_nvfp4}[fmt]
+    rng, g = np.random.default_rng(5), torch.Generator().manual_seed(5)
+    cs = torch.randn(400, D, generator=g).cuda()
+    w = torch.randn(D, generator=g).to(torch.bfloat16).cuda()
+    order = rng.permutation(pages)
+    inputs = []
+    for step in range(steps):
+        news = [int(rng.integers(0, 9)) for _ in range(B)]
+        if step == 3:
+            news[2] = -1
+        trees = [R.random_tree(rng, max(n, 0)) for n in news]
+        parents = [p for t in trees for p in t[0]]
+        paths, num = np.zeros((B, 8), np.int64), []
+        for b, n in enumerate(news):
+            path = [i for i in range(n) if trees[b][1][n - 1] >> i & 1] if n > 0 else []
+            paths[b, :len(path)] = path
+            num.append(len(path))
+        x = (torch.randn(T, hq + 2 * hkv, D, generator=g) * 2).to(torch.bfloat16).cuda()
+        inputs.append((i32(news), i32(parents + [-1] * (T - len(parents))), x, i32(paths), i32(num)))
+
+    class State:
+        def __init__(self):
+            z = lambda *s, d=torch.int32: torch.zeros(*s, dtype=d, device="cuda")  # noqa: E731
+            self.pools = [z(pages, P, hkv, width, d=kind) for _ in range(2)]
+            self.lens, self.lens2, self.held, self.count, self.fl = z(B), z(B), z(B), i32([pages]), i32(order)
+            self.table, self.start, self.slots, self.pos = z(B, 10), z(B + 1), z(T, d=torch.int64), z(T)
+            self.mask, self.q = z(T, d=torch.int64), z(T, hq, D, d=torch.bfloat16)
+            self.out, self.lse = torch.zeros_like(self.q), z(T, hq, d=torch.float32)
+            self.ws, self.st = pa.workspace_for_tree(self.q, self.pools[0], self.table, 8), z(1)
+
+        def step(self, news, parents, x, paths, num):
+            pa.pa_plan_step(self.lens, news, self.held, self.fl, self.count, self.table, self.start, self.slots, self.pos,
+                            page_size=P, parents=parents, tree_mask=self.mask, status=self.st)
+            write(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], w, w, cs, self.pos, self.slots, self.q, *self.pools,
+                  status=self.st, **sc)
+            attend(self.q, *self.pools, self.table, self.lens, self.start, self.mask, self.out, self.lse, max_query=8,
+                   scale=D ** -0.5, workspace=self.ws, **sc)
+            pa.pa_kv_compact(*self.pools, self.table, self.lens, self.start, paths, num, context_lens_out=self.lens2,
+                             status=self.st)
+            self.lens.copy_(self.lens2)
+
+        def all(self):
+            return [t.clone() for t in (*self.pools, self.lens, self.held, self.count, self.table, self.start, self.slots,
+                                        self.pos, self.mask, self.q, self.out, self.lse, self.st)]
+
+    eager, want = State(), []
+    for i in inputs:
+        eager.step(*i)
+        want.append(eager.all())
+    held = [t.clone() for t in inputs[0]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        State().step(*held)  # (whatever is set up at a first call)
+    torch.cuda.current_stream().wait_stream(side)
+    state, graphs = State(), []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            state.step(*held)
+    for k, i in enumerate(inputs):
+        for a, b in zip(held, i):
+            a.copy_(b)
+        graphs[k % 2].replay()
+        torch.cuda.synchronize()
+        for a, b in zip(state.all(), want[k]):
+            assert torch.equal(a.view(torch.uint8) if a.dtype != torch.float32 else a.view(torch.int32),
+                               b.view(torch.uint8) if b.dtype != torch.float32 else b.view(torch.int32))
+    assert int(state.st[0]) == 0 and int(state.lens.max()) > 8
