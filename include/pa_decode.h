@@ -518,6 +518,7 @@ int pa_qk_norm_rope_write_nvfp4(const void *q, const void *k, const void *v, con
  * bf16 pools: products of bf16 operands, weights rounded to bf16.  FP8 and NVFP4
  * pools: codes as exact f16 values, a query row scaled by a power of two to f16,
  * weights rounded to f16.  The calls always use the default wait limit.
+ * num_splits == 0: no share is made for less than 128 tokens' work.
  */
 int pa_tree_gqa(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
                 const int32_t *context_lens, const int32_t *query_start, const uint64_t *tree_mask,

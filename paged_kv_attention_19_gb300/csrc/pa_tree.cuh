@@ -76,7 +76,7 @@ struct TreeArgs {
   int gt, qt, nsub;     // a tile: qt nodes x gt heads; nsub tiles for a node's heads (G > 128)
   int nseqh;            // sequences per key head
   int log2_page, log2_bh, num_pages, max_pages_per_seq, max_context_len, window;
-  int piece_cost, nparts, hg;
+  int piece_cost, min_share, nparts, hg;  // (costs in units)
   float qscale;         // scale * log2(e) (* the keys' scale)
   float vscale;
 };
@@ -311,20 +311,35 @@ __device__ __forceinline__ long long tree_find(const TreeArgs &a, TreePart *ps, 
   return W;
 }
 
+// a / b, in 32 bits where that will do (a division of 64 bits takes a few hundred cycles).
+__device__ __forceinline__ long long tree_div(long long a, long long b) {
+  return ((unsigned long long)a | (unsigned long long)b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
+// The groups that work on a total cost W: all of them, but none for less than min_share.  Group g has the costs
+// [tree_cut(W, g, NG), tree_cut(W, g + 1, NG)).
+__device__ __forceinline__ int tree_groups(const TreeArgs &a, long long W) {
+  const int all = a.nparts / a.hg;
+  return a.min_share > 0 ? max(1, (int)min((long long)all, tree_div(W, a.min_share))) : all;
+}
+__device__ __forceinline__ long long tree_cut(long long W, int g, int NG) { return tree_div((long long)g * W, NG); }
+
 // This CTA's range [x_begin, x_end) of the rows' costs, and the row that it begins in.
 template <int THREADS>
 __device__ __forceinline__ void tree_partition(const TreeArgs &a, TreePart *ps, uint32_t *status) {
-  const int NG = a.nparts / a.hg, grp = (int)blockIdx.x / a.hg;
-  const bool member = grp < NG;
+  const int grp = (int)blockIdx.x / a.hg;
   uint32_t bad = 0;
   const long long W = tree_find<THREADS>(a, ps, &bad, [&](long long W, long long x, long long v) {
-    const long long xb = (long long)grp * W / NG;
-    return member && xb < ((long long)grp + 1) * W / NG && xb >= x && xb < x + v;
+    const int NG = tree_groups(a, W);
+    if (grp >= NG) return false;
+    const long long xb = tree_cut(W, grp, NG);
+    return xb < tree_cut(W, grp + 1, NG) && xb >= x && xb < x + v;
   });
   if (bad) atomicOr(status, bad);
   if (threadIdx.x == 0) {
-    ps->x_begin = member ? (long long)grp * W / NG : 0;
-    ps->x_end = member ? ((long long)grp + 1) * W / NG : 0;
+    const int NG = tree_groups(a, W);
+    ps->x_begin = grp < NG ? tree_cut(W, grp, NG) : 0;
+    ps->x_end = grp < NG ? tree_cut(W, grp + 1, NG) : 0;
   }
   __syncthreads();
 }
@@ -1419,17 +1434,19 @@ template <int D, int QT>
 __global__ void __launch_bounds__(kCombineThreads, QT == 2 ? 3 : 2) tree_combine_kernel(const TreeArgs a, uint32_t *status) {
   __shared__ TreePart part;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = (int)blockIdx.x;
-  const int NG = a.nparts / a.hg, grp = cta / a.hg, hs = cta % a.hg;
+  const int grp = cta / a.hg, hs = cta % a.hg;
   // the row whose first unit lies in this range, and whose last one does not; k: the ranges that it lies in
   uint32_t ignored = 0;
   const long long W = tree_find<kCombineThreads>(a, &part, &ignored, [&](long long W, long long x, long long v) {
-    const long long xb = (long long)grp * W / NG, xe = ((long long)grp + 1) * W / NG, first = x + a.piece_cost;
-    return grp < NG && xb <= first && first < xe && xe < x + v;
+    const int NG = tree_groups(a, W);
+    if (grp >= NG) return false;
+    const long long xb = tree_cut(W, grp, NG), xe = tree_cut(W, grp + 1, NG), first = x + a.piece_cost;
+    return xb <= first && first < xe && xe < x + v;
   });
   const int b = part.found_b;
   const TreeRow r = b >= 0 ? tree_row(a, b, &ignored) : TreeRow{0, 0, 0};
   const long long end = b >= 0 ? part.found_x + tree_cost(a, r) : 0;
-  const int k = b >= 0 ? (int)((end * NG + W - 1) / W) - grp : 0;
+  const int k = b >= 0 ? (int)tree_div(end * tree_groups(a, W) + W - 1, W) - grp : 0;
   pdl_wait();
   pdl_launch_dependents();
   if (cta == 0 && blockIdx.y == 0 && warp == 0) {
