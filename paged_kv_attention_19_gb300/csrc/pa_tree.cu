@@ -173,7 +173,7 @@ int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32
   a.max_context_len = max_ctx;
   a.window = window > 0 ? window : 0;
   a.piece_cost = kPieceCost / BH;
-  a.min_share = num_splits > 0 ? 0 : kMinShare / BH;
+  a.log2_share = num_splits > 0 ? 0 : ilog2(kMinShare / BH);
   a.nparts = num_splits > 0 ? num_splits : sms < kAutoParts ? sms : kAutoParts;
   const int hs = Hkv * pl.nseqh;
   a.hg = hs < a.nparts ? hs : a.nparts;

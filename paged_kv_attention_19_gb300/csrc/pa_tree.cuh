@@ -76,7 +76,7 @@ struct TreeArgs {
   int gt, qt, nsub;     // a tile: qt nodes x gt heads; nsub tiles for a node's heads (G > 128)
   int nseqh;            // sequences per key head
   int log2_page, log2_bh, num_pages, max_pages_per_seq, max_context_len, window;
-  int piece_cost, min_share, nparts, hg;  // (costs in units)
+  int piece_cost, log2_share, nparts, hg;  // (costs in units)
   float qscale;         // scale * log2(e) (* the keys' scale)
   float vscale;
 };
@@ -283,15 +283,9 @@ __device__ __forceinline__ long long tree_find(const TreeArgs &a, TreePart *ps, 
   if (tid == 0) ps->found_b = -1;
   // up to THREADS rows: one scan gives the total and the place; more: a pass for the total, one for the place
   const bool once = a.batch <= THREADS;
-  long long W = 0, v = 0, ex = 0;
-  if (once) {
-    if (tid < a.batch) v = tree_cost(a, tree_row(a, tid, bad));
-    W = tree_scan<THREADS>(v, &ex, ps->warp_part);
-  } else {
-    long long local = 0;
-    for (int b = tid; b < a.batch; b += THREADS) local += tree_cost(a, tree_row(a, b, bad));
-    W = tree_scan<THREADS>(local, &ex, ps->warp_part);
-  }
+  long long v = 0, ex = 0;
+  for (int b = tid; b < a.batch; b += THREADS) v += tree_cost(a, tree_row(a, b, bad));
+  const long long W = tree_scan<THREADS>(v, &ex, ps->warp_part);
   long long base = 0;
   for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
     if (!once) {
@@ -311,37 +305,43 @@ __device__ __forceinline__ long long tree_find(const TreeArgs &a, TreePart *ps, 
   return W;
 }
 
-// a / b, in 32 bits where that will do (a division of 64 bits takes a few hundred cycles).
-__device__ __forceinline__ long long tree_div(long long a, long long b) {
-  return ((unsigned long long)a | (unsigned long long)b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
-}
-
-// The groups that work on a total cost W: all of them, but none for less than min_share.  Group g has the costs
-// [tree_cut(W, g, NG), tree_cut(W, g + 1, NG)).
-__device__ __forceinline__ int tree_groups(const TreeArgs &a, long long W) {
-  const int all = a.nparts / a.hg;
-  return a.min_share > 0 ? max(1, (int)min((long long)all, tree_div(W, a.min_share))) : all;
-}
-__device__ __forceinline__ long long tree_cut(long long W, int g, int NG) { return tree_div((long long)g * W, NG); }
+// The groups that work on a total cost W, none on less than 2^log2_share, and their shares: group g has the costs
+// [cut(g), cut(g + 1)).
+struct TreeShares {
+  int groups, more;  // the first `more` groups have one unit of cost more than `each`
+  long long each;
+  __device__ __forceinline__ TreeShares(const TreeArgs &a, long long W) {
+    groups = (int)max(1ll, min((long long)(a.nparts / a.hg), W >> a.log2_share));
+    each = W >> 32 ? W / groups : (long long)((uint32_t)W / (uint32_t)groups);
+    more = (int)(W - each * groups);
+  }
+  __device__ __forceinline__ long long cut(int g) const { return g * each + min(g, more); }
+  // the group of cost x, x >= cut(g), counted from g
+  __device__ __forceinline__ int behind(int g, long long x) const {
+    int n = 0;
+    while (g + n + 1 < groups && cut(g + n + 1) <= x) ++n;
+    return n;
+  }
+};
 
 // This CTA's range [x_begin, x_end) of the rows' costs, and the row that it begins in.
 template <int THREADS>
 __device__ __forceinline__ void tree_partition(const TreeArgs &a, TreePart *ps, uint32_t *status) {
   const int grp = (int)blockIdx.x / a.hg;
   uint32_t bad = 0;
-  const long long W = tree_find<THREADS>(a, ps, &bad, [&](long long W, long long x, long long v) {
-    const int NG = tree_groups(a, W);
-    if (grp >= NG) return false;
-    const long long xb = tree_cut(W, grp, NG);
-    return xb < tree_cut(W, grp + 1, NG) && xb >= x && xb < x + v;
+  long long xb = 0, xe = 0;
+  tree_find<THREADS>(a, ps, &bad, [&](long long W, long long x, long long v) {
+    const TreeShares s(a, W);
+    xb = grp < s.groups ? s.cut(grp) : 0;
+    xe = grp < s.groups ? s.cut(grp + 1) : 0;
+    const bool mine = xb < xe && xb >= x && xb < x + v;
+    if (mine) {
+      ps->x_begin = xb;
+      ps->x_end = xe;
+    }
+    return mine;
   });
   if (bad) atomicOr(status, bad);
-  if (threadIdx.x == 0) {
-    const int NG = tree_groups(a, W);
-    ps->x_begin = grp < NG ? tree_cut(W, grp, NG) : 0;
-    ps->x_end = grp < NG ? tree_cut(W, grp + 1, NG) : 0;
-  }
-  __syncthreads();
 }
 
 // One piece: units [ub, ue) of sequence hs of row b.
@@ -401,19 +401,22 @@ struct TreeWalker {
         it_b = b_first;
         it_in = in_first;
       }
+      if (it_b >= a.batch) {
+        R = 0;  // (what is left of the range lies in rows that exist)
+        continue;
+      }
       const TreeRow r = row_of(it_b);
       const int w = tree_cost(a, r);
+      if (it_in >= w) {
+        it_in = 0;
+        ++it_b;
+        continue;
+      }
       const int b = it_b;
       const int take = (int)min((long long)(w - it_in), R);
       const int u0 = max(0, it_in - a.piece_cost), u1 = max(0, it_in + take - a.piece_cost);
       R -= take;
       it_in += take;
-      if (it_in >= w && R > 0) {
-        it_in = 0;
-        ++it_b;
-        while (it_b < a.batch && tree_cost(a, row_of(it_b)) == 0) ++it_b;
-        if (it_b >= a.batch) R = 0;  // (what is left of the range lies in rows that exist)
-      }
       const int t0 = (it_hs % a.nseqh) * QT;
       if (u1 > u0 && t0 < tree_tiles(a, r.n)) {
         int ul;
@@ -671,81 +674,83 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       return 32 * w + lane < np ? a.block_table[(size_t)p.b * a.max_pages_per_seq + pb + 32 * w + lane] : 0;
     };
     TreePiece cur = {}, nxt = {};
-    bool has = walker.take<C::QT>(cur), has_next = false;
-    int cwin = has ? window_of(cur, 0) : 0, nwin = 0;
-    while (has && ok) {
-      has_next = walker.take<C::QT>(nxt);
+    int cwin = 0, nwin = 0;
+    for (bool has = false;;) {  // cur, if there is one, with the piece behind it known
+      const bool has_next = walker.take<C::QT>(nxt);
       if (has_next) nwin = window_of(nxt, 0);
-      const int prefix = cur.L - cur.n;
-      // every node sees the tokens [lo_max, prefix): depths are below n
-      const int lo_max = a.window > 0 ? max(cur.L - a.window, 0) : 0;
-      const int tok_hi = min(cur.L, cur.ue << a.log2_bh);
-      const int n_stages = (cur.ue - cur.ub + nbox - 1) / nbox;
-      const int pb = (cur.ub << a.log2_bh) >> a.log2_page;
-      int wi = 0, fwin = window_of(cur, 1);
-      for (int st = 0; st < ((n_stages + 1) & ~1) && ok; ++st) {  // (the last one may be without tokens)
-        const int unit0 = cur.ub + st * nbox, tok0 = unit0 << a.log2_bh;
-        // the pages of one stage never straddle a window of 32 (nbox divides 32)
-        const int pwin = ((tok0 >> a.log2_page) - pb) >> 5;
-        while (wi < pwin) {
-          cwin = fwin;
-          ++wi;
-          fwin = window_of(cur, wi + 1);
-        }
-        const int unit = unit0 + lane, btok = unit << a.log2_bh;
-        const int phys = __shfl_sync(FULL, cwin, ((btok >> a.log2_page) - pb) & 31);
-        bool load = false, isbad = false;
-        if (lane < nbox && unit < cur.ue) {
-          load = phys >= 0 && phys < a.num_pages;
-          isbad = !load;
-          if (isbad) atomicOr(status, PA_DEV_BAD_PAGE);
-        }
-        const uint32_t bad = __ballot_sync(FULL, isbad);
-        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL, load)) * (uint32_t)(C::ROWB << a.log2_bh);
-#pragma unroll
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          uint32_t u;
-          const int s = place(kv, u);
-          if (u > 0) ok = mbar_wait(&r_empty[s], (u - 1) & 1, status);
-          ok = __all_sync(FULL, ok);
-          if (!ok) break;
-          in_flight = kv + 1;
-          if (lane == 0) {
-            if (kv == 0) {
-              TreeStage m;
-              m.flags = st >= n_stages ? STAGE_ABSENT
-                                       : (tok0 + BN > min(prefix, tok_hi) || tok0 < lo_max || bad != 0 ? STAGE_MASKED : 0);
-              if (st == 0) m.flags |= STAGE_FIRST;
-              m.tok0 = tok0;
-              m.tok_hi = tok_hi;
-              m.badmask = bad;
-              meta[t % C::META] = m;
-            }
-            mbar_arrive_expect_tx(&r_full[s], bytes);
+      if (has) {
+        const int prefix = cur.L - cur.n;
+        // every node sees the tokens [lo_max, prefix): depths are below n
+        const int lo_max = a.window > 0 ? max(cur.L - a.window, 0) : 0;
+        const int tok_hi = min(cur.L, cur.ue << a.log2_bh);
+        const int n_stages = (cur.ue - cur.ub + nbox - 1) / nbox;
+        const int pb = (cur.ub << a.log2_bh) >> a.log2_page;
+        int wi = 0, fwin = window_of(cur, 1);
+        for (int st = 0; st < ((n_stages + 1) & ~1) && ok; ++st) {  // (the last one may be without tokens)
+          const int unit0 = cur.ub + st * nbox, tok0 = unit0 << a.log2_bh;
+          // the pages of one stage never straddle a window of 32 (nbox divides 32)
+          const int pwin = ((tok0 >> a.log2_page) - pb) >> 5;
+          while (wi < pwin) {
+            cwin = fwin;
+            ++wi;
+            fwin = window_of(cur, wi + 1);
           }
-          __syncwarp();
-          if (load) {
-            if constexpr (C::QUANT) {  // whole rows of codes, one after the other
-              tma_load_4d(smem + S::OFF_RAW + s * C::RAW_SLOT + (lane << a.log2_bh) * C::ROWB, kv ? &tm_v : &tm_k, 0, cur.g,
-                          btok & (P - 1), phys, &r_full[s]);
-            } else {
-              uint8_t *dst = smem + S::OFF_RING + s * C::SLOT + (lane << a.log2_bh) * 128;
+          const int unit = unit0 + lane, btok = unit << a.log2_bh;
+          const int phys = __shfl_sync(FULL, cwin, ((btok >> a.log2_page) - pb) & 31);
+          bool load = false, isbad = false;
+          if (lane < nbox && unit < cur.ue) {
+            load = phys >= 0 && phys < a.num_pages;
+            isbad = !load;
+            if (isbad) atomicOr(status, PA_DEV_BAD_PAGE);
+          }
+          const uint32_t bad = __ballot_sync(FULL, isbad);
+          const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL, load)) * (uint32_t)(C::ROWB << a.log2_bh);
 #pragma unroll
-              for (int p = 0; p < C::NPL; ++p)
-                tma_load_4d(dst + p * C::PLANE, kv ? &tm_v : &tm_k, p * 64, cur.g, btok & (P - 1), phys, &full[s]);
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            uint32_t u;
+            const int s = place(kv, u);
+            if (u > 0) ok = mbar_wait(&r_empty[s], (u - 1) & 1, status);
+            ok = __all_sync(FULL, ok);
+            if (!ok) break;
+            in_flight = kv + 1;
+            if (lane == 0) {
+              if (kv == 0) {
+                TreeStage m;
+                m.flags = st >= n_stages ? STAGE_ABSENT
+                                         : (tok0 + BN > min(prefix, tok_hi) || tok0 < lo_max || bad != 0 ? STAGE_MASKED : 0);
+                if (st == 0) m.flags |= STAGE_FIRST;
+                m.tok0 = tok0;
+                m.tok_hi = tok_hi;
+                m.badmask = bad;
+                meta[t % C::META] = m;
+              }
+              mbar_arrive_expect_tx(&r_full[s], bytes);
+            }
+            __syncwarp();
+            if (load) {
+              if constexpr (C::QUANT) {  // whole rows of codes, one after the other
+                tma_load_4d(smem + S::OFF_RAW + s * C::RAW_SLOT + (lane << a.log2_bh) * C::ROWB, kv ? &tm_v : &tm_k, 0, cur.g,
+                            btok & (P - 1), phys, &r_full[s]);
+              } else {
+                uint8_t *dst = smem + S::OFF_RING + s * C::SLOT + (lane << a.log2_bh) * 128;
+#pragma unroll
+                for (int p = 0; p < C::NPL; ++p)
+                  tma_load_4d(dst + p * C::PLANE, kv ? &tm_v : &tm_k, p * 64, cur.g, btok & (P - 1), phys, &full[s]);
+              }
             }
           }
+          if (ok) {
+            ++t;
+            in_flight = 0;
+          }
         }
-        if (ok) {
-          ++t;
-          in_flight = 0;
-        }
+        if (!ok) break;
+        ++npieces;
       }
-      if (!ok) break;
-      ++npieces;
+      if (!has_next) break;
+      has = true;
       cur = nxt;
       cwin = nwin;
-      has = has_next;
     }
     // the end, for the converting warps: the next stage's tiles, which are none
     for (int kv = 0; C::QUANT && kv < 2 && ok; ++kv) {
@@ -1438,15 +1443,14 @@ __global__ void __launch_bounds__(kCombineThreads, QT == 2 ? 3 : 2) tree_combine
   // the row whose first unit lies in this range, and whose last one does not; k: the ranges that it lies in
   uint32_t ignored = 0;
   const long long W = tree_find<kCombineThreads>(a, &part, &ignored, [&](long long W, long long x, long long v) {
-    const int NG = tree_groups(a, W);
-    if (grp >= NG) return false;
-    const long long xb = tree_cut(W, grp, NG), xe = tree_cut(W, grp + 1, NG), first = x + a.piece_cost;
-    return xb <= first && first < xe && xe < x + v;
+    const TreeShares s(a, W);
+    const long long first = x + a.piece_cost;
+    return grp < s.groups && s.cut(grp) <= first && first < s.cut(grp + 1) && s.cut(grp + 1) < x + v;
   });
   const int b = part.found_b;
   const TreeRow r = b >= 0 ? tree_row(a, b, &ignored) : TreeRow{0, 0, 0};
   const long long end = b >= 0 ? part.found_x + tree_cost(a, r) : 0;
-  const int k = b >= 0 ? (int)tree_div(end * tree_groups(a, W) + W - 1, W) - grp : 0;
+  const int k = b >= 0 ? TreeShares(a, W).behind(grp, end - 1) + 1 : 0;
   pdl_wait();
   pdl_launch_dependents();
   if (cta == 0 && blockIdx.y == 0 && warp == 0) {
