@@ -44,10 +44,10 @@
 // an SM's misses wait for its neighbours'), so what a stage rarely needs is kept out of its path, and with codes the
 // loops over the products' instructions are not unrolled: 32 ragged trees of up to 16 nodes x 8 heads over 128 to
 // 16384 tokens, 8 key heads of 128, FP8 137 -> 111 us, NVFP4 134 -> 104, bf16 107 -> 99.
-// Measured (GB300; bytes: the cache once): a request of 8 nodes x 32 heads over 1000 tokens 15.1 us, start-up and the
-// combine kernel's trips; 16 rows of 64 nodes x 64 heads over 1024 to 8192 tokens 132 us, 874 TFLOP/s, the issue of
-// the products; 16 windowed rows at head_dim 256 56 us, 4.5 TB/s; the ragged trees above 2.05 TB/s of FP8 codes and
-// 1.4 TB/s of NVFP4 ones, the chain from conversion to weights.
+// Measured (GB300; bytes: the cache once): a request of 8 nodes x 32 heads over 1000 tokens 13.6 us, start-up and the
+// combine kernel's trips; 16 rows of 64 nodes x 64 heads over 1024 to 8192 tokens 127 us, 911 TFLOP/s, the score
+// products of N = 64; 16 windowed rows at head_dim 256 57 us, 4.4 TB/s; the ragged trees above 2.1 TB/s of FP8 codes
+// and 1.4 TB/s of NVFP4 ones (109 and 102 us by now), the chain from conversion to weights.
 // Tensor memory: score buffer b (the weights over its first half) at 64 b, outputs at 256.  At head_dim 256 one
 // output fills the rest: one tile, one softmax group and one issuing thread.
 #pragma once
