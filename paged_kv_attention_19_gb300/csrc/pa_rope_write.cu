@@ -12,8 +12,8 @@
 // time (a group): the token's position, slot and angles are loaded once for the segment, and the next three
 // groups' loads are in flight while three are worked on (two, or four, with as many blocks on an SM as the
 // registers allow: 5 to 11% slower).  The warps of one wave stride over the (token,
-// segment) pairs.  8192 tokens of 64 + 8 + 8 heads of 128 into FP8: 63 us, 5.1 TB/s of reads and writes mixed,
-// at 60% of the issue slots; 61 tokens of 32 + 8 + 8: 2.4 us in a graph, a launch.
+// segment) pairs.  8192 tokens of 64 + 8 + 8 heads of 128 into FP8: 68 us, 4.8 TB/s of reads and writes mixed, at
+// over 60% of the issue slots; 61 tokens of 32 + 8 + 8: 2.4 us in a graph, a launch.
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -152,6 +152,10 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
       *reinterpret_cast<uint2 *>(row + at1) = make_uint2(v.z, v.w);
     }
   };
+  // 1 / scale, and what its rounding left out
+  [[maybe_unused]] const float ki = 1.f / a.k_scale.sc, vi = 1.f / a.v_scale.sc;
+  [[maybe_unused]] const float2 k_inv = make_float2(ki, fmaf(-a.k_scale.sc, ki, 1.f) * ki);
+  [[maybe_unused]] const float2 v_inv = make_float2(vi, fmaf(-a.v_scale.sc, vi, 1.f) * vi);
   const bool norm_q = a.q_weight != nullptr, norm_k = a.k_weight != nullptr;
   const uint4 wq = norm_q ? load8(a.q_weight) : make_uint4(0, 0, 0, 0), wk = norm_k ? load8(a.k_weight) : make_uint4(0, 0, 0, 0);
   const int items = a.tokens * a.segs, stride = (int)gridDim.x * (kRopeThreads / 32);
@@ -230,6 +234,48 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
         }
       }
     };
+    // A key as the quotient by its pool's scale, (x w cos - x' w' sin) (1 / (rms scale)): a step of a code is a sixteenth of
+    // the value, so a key beside the middle of two codes goes by its last bits, and fewer roundings put fewer of them on
+    // the wrong side: x w is exact, the factor is a pair of floats, a product's rounding is made good.  (Of 50 million keys 21
+    // codes are not those of 64 bits, 94 with norm, rotation and division one after the other, for 68 us instead of 63.)
+    auto turn_quot = [&](float (&x)[8], bool norm, bool on, float2 inv) {
+      float2 f = inv;  // 1 / scale in two floats
+      if (norm_q || norm_k) {
+        float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) s2 = pair_fma(make_float2(x[e], x[e + 1]), make_float2(x[e], x[e + 1]), s2);
+        float ss = s2.x + s2.y;
+#pragma unroll
+        for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(FULL, ss, o);
+        if (norm) {
+          // one step of Newton's method on 1 / sqrt(m), its change kept apart
+          const float m = ss * (1.f / D) + a.eps, r = rsqrtf(m), r2 = r * r;
+          const float left = fmaf(-m, fmaf(r, r, -r2), fmaf(-m, r2, 1.f)), rl = fabsf(left) < 1.f ? 0.5f * r * left : 0.f;
+          f.x = r * inv.x;
+          f.y = fmaf(rl, inv.x, fmaf(r, inv.y, fmaf(r, inv.x, -f.x)));
+          float w[8];
+          unpack8(wk, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= w[e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = IL ? 2 * e : e, j = IL ? 2 * e + 1 : 4 + e;
+        float u = x[i], v = x[j], ul = 0.f, vl = 0.f;
+        if (on && turned) {
+          const float uc = u * co[e], vc = v * co[e];
+          ul = fmaf(u, co[e], -uc);
+          vl = fmaf(v, co[e], -vc);
+          const float us = fmaf(u, si[e], vc);
+          u = fmaf(-v, si[e], uc);
+          v = us;
+        }
+        const float rest_u = fmaf(ul, f.x, u * f.y), rest_v = fmaf(vl, f.x, v * f.y);
+        x[i] = fmaf(u, f.x, fabsf(rest_u) < INFINITY ? rest_u : 0.f);
+        x[j] = fmaf(v, f.x, fabsf(rest_v) < INFINITY ? rest_v : 0.f);
+      }
+    };
     for (int grp = g0; grp < g1; grp += AHEAD) {
       uint4 cur[AHEAD];
 #pragma unroll
@@ -256,8 +302,17 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
         unpack8(cur[0], x);
 #pragma unroll
         for (int e = 0; e + 1 < AHEAD; ++e) cur[e] = cur[e + 1];
-        if (hw < a.Hq + a.Hkv)   // some row is a query's or a key's
-          turn(x, norm_q || norm_k, is_q ? wq : wk, is_q ? norm_q : norm_k && !is_v, !is_v);
+        const bool keys = FMT != ROPE_BF16 && hw + HPG > a.Hq && hw < a.Hq + a.Hkv;  // some row is a key's
+        if (hw < (FMT != ROPE_BF16 ? a.Hq : a.Hq + a.Hkv)) {  // some row is a query's (or a key's that stays bf16)
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = x[e];
+          turn(y, norm_q || norm_k, is_q ? wq : wk, is_q ? norm_q : norm_k && !is_v, !is_v);
+          if (FMT == ROPE_BF16 || is_q) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = y[e];
+          }
+        }
         if (is_q) store8(a.q_out + ((size_t)t * a.Hq + h) * D, pack8(x));
         if (hw + HPG <= a.Hq) continue;
         // some row of the warp goes into a pool
@@ -267,26 +322,32 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
         if constexpr (FMT == ROPE_BF16) {
           if (store) store8(reinterpret_cast<uint16_t *>(pool) + row * D, pack8(x));
         } else {
+          float q[8];
+          if (keys) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[e] = x[e];
+            turn_quot(q, norm_k && !is_v && !is_q, !is_v, is_v ? v_inv : k_inv);
+          } else {
+            quot8(x, a.v_scale, q);
+          }
           if constexpr (FMT == ROPE_NVFP4 && PIECES) {
             // keys: from two pieces to 8 values in a row, so that a block is two lanes' (values were read so)
             const bool first = l * 8 < half;
             float y[8];
             const int src = lane - l + (turned ? 2 * (first ? l : l - half / 8) : l);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e];
+            for (int e = 0; e < 8; ++e) y[e] = q[e];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int nb = turned ? src + 1 : lane;
               const float a0 = __shfl_sync(FULL, y[e], src), a1 = __shfl_sync(FULL, y[e], nb),
                           b0 = __shfl_sync(FULL, y[4 + e], src), b1 = __shfl_sync(FULL, y[4 + e], nb);
               if (turned && !is_v) {
-                x[e] = first ? a0 : b0;
-                x[4 + e] = first ? a1 : b1;
+                q[e] = first ? a0 : b0;
+                q[4 + e] = first ? a1 : b1;
               }
             }
           }
-          float q[8];
-          quot8(x, is_v ? a.v_scale : a.k_scale, q);
           if constexpr (FMT == ROPE_FP8) {
             const uint2 c = fp8_codes8(q);
             if (store) {
