@@ -463,7 +463,8 @@ int pa_qk_norm_rope_write(const void *q, const void *k, const void *v, const voi
 /*
  * The same into FP8 E4M3 pools: the codes are those nearest to the quotients
  * y / k_scale and v / v_scale in fp32 (the layout and rounding of pa_kv_write_fp8;
- * keys are not rounded to bf16 on the way).
+ * keys are not rounded to bf16 on the way).  Scales in [2^-50, 2^50] (others:
+ * PA_ERR_UNSUPPORTED), here and for NVFP4.
  */
 int pa_qk_norm_rope_write_fp8(const void *q, const void *k, const void *v, const void *q_weight,
                               const void *k_weight, const float *cos_sin, const int32_t *positions,

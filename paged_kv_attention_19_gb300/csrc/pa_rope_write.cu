@@ -459,6 +459,9 @@ int rope_call(const void *q, const void *k, const void *v, const void *q_weight,
   if (D != 64 && D != 128 && D != 256) return PA_ERR_UNSUPPORTED;
   if (rot > D) return PA_ERR_INVALID_ARGUMENT;
   if (rot % 16 != 0 || Hq > 65536 || Hkv > 65536) return PA_ERR_UNSUPPORTED;
+  // (so that 1 / (rms scale) is no infinity, which would make NaN of a key's zeros)
+  if (fmt != ROPE_BF16 && !(k_scale >= 0x1p-50f && k_scale <= 0x1p50f && v_scale >= 0x1p-50f && v_scale <= 0x1p50f))
+    return PA_ERR_UNSUPPORTED;
   if (T == 0) return PA_OK;
   if (!q || !k || !v || !cos_sin || !positions || !slot_mapping || !q_out || !k_pool || !v_pool)
     return PA_ERR_INVALID_ARGUMENT;

@@ -72,6 +72,13 @@ def test_rope_write_refuses_scales(pa, bad):
         assert rope(pa, fmt, ksc=bad) == INVALID and rope(pa, fmt, vsc=bad) == INVALID
 
 
+@pytest.mark.parametrize("bad", [1e-40, 1e-38, 2.0 ** -51, 2.0 ** 51, 3e38])
+def test_rope_write_refuses_scales_out_of_range(pa, bad):
+    for fmt in ("_fp8", "_nvfp4"):
+        assert rope(pa, fmt, ksc=bad) == UNSUPPORTED and rope(pa, fmt, vsc=bad) == UNSUPPORTED
+        assert rope(pa, fmt, T=0, ksc=2.0 ** -50, vsc=2.0 ** 50) == 0
+
+
 def tree(pa, fmt="", **kw):
     a = dict(q=0x100000, k=0x200000, v=0x300000, bt=0x400000, lens=0x410000, qs=0x420000, mask=0x430000, out=0x500000,
              lse=None, batch=2, T=16, mq=8, hq=8, hkv=2, D=128, p=16, pages=10, maxp=5, maxctx=80, scale=0.1, ksc=0.5,
