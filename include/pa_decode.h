@@ -417,6 +417,12 @@ int pa_mla_cache_write(const void *c_lat, const void *k_rope, const int64_t *slo
  * PA_ERR_UNSUPPORTED); page_size >= 1; status: a device word or NULL, whose bits
  * are only ever set.  batch == 0 writes query_start[0],
  * the padding and free_count_out.
+ *   granted      (pa_plan_step_granted) [batch] int32 or NULL, written: 1 for a row whose
+ *                new tokens have their places, also where it has none; 0 for a row that
+ *                was refused or has ended.  query_start counts a refused row's tokens,
+ *                but context_lens_out does not, so pa_tree_gqa_granted and
+ *                pa_kv_compact_granted take this array to leave such a row alone:
+ *                without it they would take its newest tokens for a tree
  */
 int pa_plan_step(const int32_t *context_lens, const int32_t *new_lens, const int32_t *held_pages,
                  int32_t *free_list, const int32_t *free_count, const int32_t *parents,
@@ -424,6 +430,13 @@ int pa_plan_step(const int32_t *context_lens, const int32_t *new_lens, const int
                  int32_t *free_count_out, int32_t *query_start, int64_t *slot_mapping,
                  int32_t *positions, uint64_t *tree_mask, int batch, int page_size, int num_pages,
                  int max_pages_per_seq, int max_tokens, uint32_t *status, cudaStream_t stream);
+int pa_plan_step_granted(const int32_t *context_lens, const int32_t *new_lens, const int32_t *held_pages,
+                         int32_t *free_list, const int32_t *free_count, const int32_t *parents,
+                         int32_t *block_table, int32_t *context_lens_out, int32_t *held_pages_out,
+                         int32_t *free_count_out, int32_t *query_start, int64_t *slot_mapping,
+                         int32_t *positions, uint64_t *tree_mask, int32_t *granted, int batch, int page_size,
+                         int num_pages, int max_pages_per_seq, int max_tokens, uint32_t *status,
+                         cudaStream_t stream);
 
 /*
  * Norms of queries and keys, position rotation and paged write in one pass.
@@ -520,6 +533,9 @@ int pa_qk_norm_rope_write_nvfp4(const void *q, const void *k, const void *v, con
  * pools: codes as exact f16 values, a query row scaled by a power of two to f16,
  * weights rounded to f16.  The calls always use the default wait limit.
  * num_splits == 0: no share is made for less than 128 tokens' work.
+ *   granted      (the _granted calls) [batch] int32 or NULL: a row with 0 is left out, its
+ *                lengths are not looked at and its outputs stay as they were
+ *                (pa_plan_step_granted's: rows whose nodes are not in the cache)
  */
 int pa_tree_gqa(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
                 const int32_t *context_lens, const int32_t *query_start, const uint64_t *tree_mask,
@@ -527,6 +543,12 @@ int pa_tree_gqa(const void *q, const void *k_pool, const void *v_pool, const int
                 int num_kv_heads, int head_dim, int page_size, int num_pages, int max_pages_per_seq,
                 int max_context_len, float scale, int window, int num_splits, void *workspace,
                 size_t workspace_bytes, cudaStream_t stream);
+int pa_tree_gqa_granted(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+                        const int32_t *context_lens, const int32_t *query_start, const uint64_t *tree_mask,
+                        const int32_t *granted, void *out, float *lse, int batch, int num_tokens, int max_query,
+                        int num_q_heads, int num_kv_heads, int head_dim, int page_size, int num_pages,
+                        int max_pages_per_seq, int max_context_len, float scale, int window, int num_splits,
+                        void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* The same over FP8 E4M3 pools (the layout of pa_decode_gqa_fp8); head_dim in {64, 128, 256}. */
 int pa_tree_gqa_fp8(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
@@ -535,6 +557,13 @@ int pa_tree_gqa_fp8(const void *q, const void *k_pool, const void *v_pool, const
                     int num_kv_heads, int head_dim, int page_size, int num_pages, int max_pages_per_seq,
                     int max_context_len, float scale, float k_scale, float v_scale, int window,
                     int num_splits, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+int pa_tree_gqa_fp8_granted(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+                            const int32_t *context_lens, const int32_t *query_start, const uint64_t *tree_mask,
+                            const int32_t *granted, void *out, float *lse, int batch, int num_tokens,
+                            int max_query, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                            int num_pages, int max_pages_per_seq, int max_context_len, float scale, float k_scale,
+                            float v_scale, int window, int num_splits, void *workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
 
 /* The same over NVFP4 pools (the layout of pa_decode_gqa_nvfp4). */
 int pa_tree_gqa_nvfp4(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
@@ -544,6 +573,13 @@ int pa_tree_gqa_nvfp4(const void *q, const void *k_pool, const void *v_pool, con
                       int max_pages_per_seq, int max_context_len, float scale, float k_scale,
                       float v_scale, int window, int num_splits, void *workspace,
                       size_t workspace_bytes, cudaStream_t stream);
+int pa_tree_gqa_nvfp4_granted(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+                              const int32_t *context_lens, const int32_t *query_start, const uint64_t *tree_mask,
+                              const int32_t *granted, void *out, float *lse, int batch, int num_tokens,
+                              int max_query, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                              int num_pages, int max_pages_per_seq, int max_context_len, float scale,
+                              float k_scale, float v_scale, int window, int num_splits, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Bytes of device workspace a pa_tree_gqa call (of any cache format) with these
@@ -564,6 +600,10 @@ size_t pa_tree_workspace_size(int batch, int max_query, int num_q_heads, int num
  *   num_accepted [batch] int32, in [0, max_accepted]
  *   context_lens_out [batch] int32: L - n_b + num_accepted (written); must not overlap
  *                context_lens
+ *   granted      (pa_kv_compact_granted) [batch] int32 or NULL: pa_plan_step_granted's.  A row
+ *                with 0 is left as it is: nothing moves, context_lens_out is L, and
+ *                neither its lengths nor its path are looked at.  So is a row of more than
+ *                64 new tokens (a plan's chain, no tree), with or without this array
  * Token L - n_b + i of every layer gets the rows of node accepted[b][i].  The pages
  * that the rejected nodes filled stay the row's (pa_plan_step takes them up).  A
  * path that is not ascending within [0, n_b) is cut before its first bad entry and
@@ -577,6 +617,11 @@ int pa_kv_compact(void *k_pool, void *v_pool, const int32_t *block_table, const 
                   int32_t *context_lens_out, int num_layers, int batch, int max_accepted,
                   int token_bytes, int page_size, int num_pages, int max_pages_per_seq,
                   uint32_t *status, cudaStream_t stream);
+int pa_kv_compact_granted(void *k_pool, void *v_pool, const int32_t *block_table, const int32_t *context_lens,
+                          const int32_t *query_start, const int32_t *accepted, const int32_t *num_accepted,
+                          const int32_t *granted, int32_t *context_lens_out, int num_layers, int batch,
+                          int max_accepted, int token_bytes, int page_size, int num_pages,
+                          int max_pages_per_seq, uint32_t *status, cudaStream_t stream);
 
 /* Static text for a pa_status value (never NULL). */
 const char *pa_status_string(int status);

@@ -9,7 +9,8 @@ Names follow the C ABI: ``pa_workspace_size``, ``pa_decode_gqa``,
 ``pa_decode_mla_absorbed``, ``pa_verify_gqa``, ``pa_decode_gqa_fp8``, ``pa_decode_gqa_nvfp4``,
 ``pa_decode_gqa_noalloc``, ``pa_kv_write``, ``pa_kv_write_fp8``, ``pa_kv_write_nvfp4``, ``pa_mla_cache_write``, ``pa_plan_step``,
 ``pa_qk_norm_rope_write``, ``pa_qk_norm_rope_write_fp8``, ``pa_qk_norm_rope_write_nvfp4``, ``pa_tree_gqa``, ``pa_tree_gqa_fp8``,
-``pa_tree_gqa_nvfp4``, ``pa_tree_workspace_size``, ``pa_kv_compact``, ``pa_status_string``, ``pa_read_device_status``,
+``pa_tree_gqa_nvfp4``, ``pa_tree_workspace_size``, ``pa_kv_compact`` (the C ABI's ``_granted`` forms are
+reached by the ``granted`` argument), ``pa_status_string``, ``pa_read_device_status``,
 ``pa_set_profile_events``, ``pa_last_launch_count``, ``pa_set_wait_limit_ns``, ``pa_last_cuda_error``,
 ``pa_last_cuda_error_string``.  The operators of tree drafting are called through a compiled module that
 checks their tensors (``csrc/pa_binding.cpp``).  The tensor-taking
@@ -61,6 +62,7 @@ SIGNATURES = {
     "pa_kv_write_fp8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P, _P]),
     "pa_mla_cache_write": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P]),
     "pa_plan_step": (_I, [_P] * 14 + [_I] * 5 + [_P, _P]),
+    "pa_plan_step_granted": (_I, [_P] * 15 + [_I] * 5 + [_P, _P]),
     "pa_qk_norm_rope_write": (_I, [_P] * 11 + [_I] * 4 + [_LL] * 3 + [_I] * 3 + [_F] + [_I, _I, _P, _P]),
     "pa_qk_norm_rope_write_fp8": (_I, [_P] * 11 + [_I] * 4 + [_LL] * 3 + [_I] * 3 + [_F] * 3 + [_I, _I, _P, _P]),
     "pa_qk_norm_rope_write_nvfp4": (_I, [_P] * 11 + [_I] * 4 + [_LL] * 3 + [_I] * 3 + [_F] * 3 + [_I, _I, _P, _P]),
@@ -68,7 +70,11 @@ SIGNATURES = {
     "pa_tree_gqa": (_I, [_P] * 9 + [_I] * 10 + [_F, _I, _I, _P, _Z, _P]),
     "pa_tree_gqa_fp8": (_I, [_P] * 9 + [_I] * 10 + [_F, _F, _F, _I, _I, _P, _Z, _P]),
     "pa_tree_gqa_nvfp4": (_I, [_P] * 9 + [_I] * 10 + [_F, _F, _F, _I, _I, _P, _Z, _P]),
+    "pa_tree_gqa_granted": (_I, [_P] * 10 + [_I] * 10 + [_F, _I, _I, _P, _Z, _P]),
+    "pa_tree_gqa_fp8_granted": (_I, [_P] * 10 + [_I] * 10 + [_F, _F, _F, _I, _I, _P, _Z, _P]),
+    "pa_tree_gqa_nvfp4_granted": (_I, [_P] * 10 + [_I] * 10 + [_F, _F, _F, _I, _I, _P, _Z, _P]),
     "pa_kv_compact": (_I, [_P] * 8 + [_I] * 7 + [_P, _P]),
+    "pa_kv_compact_granted": (_I, [_P] * 9 + [_I] * 7 + [_P, _P]),
     "pa_status_string": (ctypes.c_char_p, [_I]),
     "pa_read_device_status": (_I, [_P, _P, _U32P]),
     "pa_set_profile_events": (_I, [_P, _P]),
@@ -312,20 +318,22 @@ def _done(what: str, answer) -> None:
 
 def pa_plan_step(context_lens, new_lens, held_pages, free_list, free_count, block_table, query_start, slot_mapping,
                  positions, *, page_size: int, context_lens_out=None, held_pages_out=None, free_count_out=None,
-                 parents=None, tree_mask=None, status=None, stream=None) -> None:
+                 parents=None, tree_mask=None, granted=None, status=None, stream=None) -> None:
     """Plan of one step, all on the GPU.  context_lens, new_lens (negative: the row has ended) and
     held_pages [B] int32; free_list [num_pages] int32, a stack of which free_count [1] int32 entries
     are valid; block_table [B, max_pages] int32 gets the new pages' entries; query_start [B + 1] int32,
     slot_mapping [max_tokens] int64 and positions [max_tokens] int32 are written.  parents [max_tokens]
     int32 and tree_mask [max_tokens] int64 (the 64 mask bits) go together: drafted trees.  The _out
-    arrays default to their inputs (updated in place).  status: optional int32 device word that gets
+    arrays default to their inputs (updated in place).  granted: optional [B] int32, 1 for a row whose new
+    tokens have their places and 0 for one that was refused or has ended; what pa_tree_gqa and
+    pa_kv_compact take, so that they leave such a row alone.  status: optional int32 device word that gets
     PA_DEV_* bits (rows that found no pages: PA_DEV_NO_PAGES, their slots are -1)."""
     _done("pa_plan_step", (_native_module or _native()).plan_step(
         context_lens, new_lens, held_pages, free_list, free_count, block_table,
         context_lens if context_lens_out is None else context_lens_out,
         held_pages if held_pages_out is None else held_pages_out,
         free_count if free_count_out is None else free_count_out, query_start, slot_mapping, positions, parents,
-        tree_mask, status, page_size, stream))
+        tree_mask, granted, status, page_size, stream))
 
 
 def pa_qk_norm_rope_write(q, k, v, q_weight, k_weight, cos_sin, positions, slot_mapping, q_out, k_pool, v_pool, *,
@@ -365,45 +373,48 @@ def pa_tree_workspace_size(batch: int, max_query: int, num_q_heads: int, num_kv_
 
 
 def pa_tree_gqa(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse=None, *, max_query: int,
-                scale: float, workspace, window: int = 0, num_splits: int = 0, max_context_len=None,
+                scale: float, workspace, granted=None, window: int = 0, num_splits: int = 0, max_context_len=None,
                 stream=None) -> None:
     """Attention of drafted trees.  q [T, Hq, D] bf16: the rows' nodes one row after the other, row b's
     from query_start[b] to query_start[b + 1] ([B + 1] int32, at most max_query of them); tree_mask [T]
     int64: bit j set if the node attends to its row's node j; context_lens [B] int32 count the nodes;
     out [T, Hq, D] bf16 and lse [T, Hq] fp32 or None (tokens behind the last row stay as they were);
-    pools and block_table as for pa_decode_gqa; workspace: workspace_for_tree(...)."""
+    pools and block_table as for pa_decode_gqa; workspace: workspace_for_tree(...).  granted: optional [B]
+    int32 (pa_plan_step's); a row with 0 has no nodes in the cache, and its outputs stay as they were."""
     _done("pa_tree_gqa", (_native_module or _native()).tree_gqa(
-        0, q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, workspace, max_query,
+        0, q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, granted, workspace, max_query,
         scale, 1.0, 1.0, window, num_splits, max_context_len, stream))
 
 
 def pa_tree_gqa_fp8(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse=None, *,
-                    max_query: int, scale: float, k_scale: float, v_scale: float, workspace, window: int = 0,
-                    num_splits: int = 0, max_context_len=None, stream=None) -> None:
+                    max_query: int, scale: float, k_scale: float, v_scale: float, workspace, granted=None,
+                    window: int = 0, num_splits: int = 0, max_context_len=None, stream=None) -> None:
     """The same over FP8 E4M3 pools [pages, P, Hkv, D] uint8."""
     _done("pa_tree_gqa_fp8", (_native_module or _native()).tree_gqa(
-        1, q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, workspace, max_query,
+        1, q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, granted, workspace, max_query,
         scale, k_scale, v_scale, window, num_splits, max_context_len, stream))
 
 
 def pa_tree_gqa_nvfp4(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse=None, *,
-                      max_query: int, scale: float, k_scale: float, v_scale: float, workspace, window: int = 0,
-                      num_splits: int = 0, max_context_len=None, stream=None) -> None:
+                      max_query: int, scale: float, k_scale: float, v_scale: float, workspace, granted=None,
+                      window: int = 0, num_splits: int = 0, max_context_len=None, stream=None) -> None:
     """The same over NVFP4 pools [pages, P, Hkv, nvfp4_row_bytes(D)] uint8."""
     _done("pa_tree_gqa_nvfp4", (_native_module or _native()).tree_gqa(
-        2, q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, workspace, max_query,
+        2, q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, granted, workspace, max_query,
         scale, k_scale, v_scale, window, num_splits, max_context_len, stream))
 
 
 def pa_kv_compact(k_pool, v_pool, block_table, context_lens, query_start, accepted, num_accepted, *, context_lens_out,
-                  status=None, stream=None) -> None:
+                  granted=None, status=None, stream=None) -> None:
     """Accepted path: node accepted[b][i] (i < num_accepted[b]) of row b's tree becomes the row's token
     L - n_b + i, in every layer.  Pools [pages, P, Hkv, R] or [layers, pages, P, Hkv, R] of any format;
     accepted [B, max_accepted] int32 ascending; num_accepted [B] int32; context_lens_out [B] int32 (not
-    context_lens itself) gets L - n_b + num_accepted."""
+    context_lens itself) gets L - n_b + num_accepted.  granted: optional [B] int32 (pa_plan_step's).  A row
+    with 0 there, and one of more than 64 new tokens, which is no tree, is left as it is: context_lens_out = L,
+    its path is not read."""
     _done("pa_kv_compact", (_native_module or _native()).kv_compact(
-        k_pool, v_pool, block_table, context_lens, query_start, accepted, num_accepted, context_lens_out, status,
-        stream))
+        k_pool, v_pool, block_table, context_lens, query_start, accepted, num_accepted, granted, context_lens_out,
+        status, stream))
 
 
 def pa_read_device_status(workspace, stream=None) -> int:

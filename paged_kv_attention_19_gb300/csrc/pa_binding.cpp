@@ -189,7 +189,7 @@ PyObject *guarded(F f) {
 
 PyObject *plan_step(PyObject *, PyObject *const *v, Py_ssize_t count) {
   return guarded([&] {
-    Args a(v, count, 17);
+    Args a(v, count, 18);
     const int64_t B = peek(v, count, 0, "context_lens", 1).size(0), N = peek(v, count, 3, "free_list", 1).size(0),
                   W = peek(v, count, 5, "block_table", 2).size(1), T = peek(v, count, 11, "positions", 1).size(0);
     auto *lens = (const int32_t *)a.array("context_lens", at::kInt, {B});
@@ -206,11 +206,12 @@ PyObject *plan_step(PyObject *, PyObject *const *v, Py_ssize_t count) {
     auto *pos = (int32_t *)a.array("positions", at::kInt, {T});
     auto *parents = (const int32_t *)a.optional("parents", at::kInt, {T});
     auto *mask = (uint64_t *)a.optional("tree_mask", at::kLong, {T});
+    auto *granted = (int32_t *)a.optional("granted", at::kInt, {B});
     auto *status = (uint32_t *)a.optional("status", at::kInt, {1});
     const int page = a.integer("page_size");
     return a.launch([&](cudaStream_t s) {
-      return pa_plan_step(lens, news, held, list, n_free, parents, table, lens_out, held_out, free_out, start, slots, pos,
-                          mask, (int)B, page, (int)N, (int)W, (int)T, status, s);
+      return pa_plan_step_granted(lens, news, held, list, n_free, parents, table, lens_out, held_out, free_out, start, slots,
+                                  pos, mask, granted, (int)B, page, (int)N, (int)W, (int)T, status, s);
     });
   });
 }
@@ -253,7 +254,7 @@ PyObject *qk_norm_rope_write(PyObject *, PyObject *const *v, Py_ssize_t count) {
 
 PyObject *tree_gqa(PyObject *, PyObject *const *v, Py_ssize_t count) {
   return guarded([&] {
-    Args a(v, count, 19);
+    Args a(v, count, 20);
     const int fmt = a.integer("format");
     const at::Tensor &q0 = peek(v, count, 1, "q", 3), &kp0 = peek(v, count, 2, "k_pool", 4), &bt0 = peek(v, count, 4, "block_table", 2);
     const int64_t T = q0.size(0), Hq = q0.size(1), D = q0.size(2), N = kp0.size(0), P = kp0.size(1), Hkv = kp0.size(2);
@@ -268,6 +269,7 @@ PyObject *tree_gqa(PyObject *, PyObject *const *v, Py_ssize_t count) {
     auto *mask = (const uint64_t *)a.array("tree_mask", at::kLong, {T});
     void *out = a.array("out", at::kBFloat16, {T, Hq, D});
     auto *lse = (float *)a.optional("lse", at::kFloat, {T, Hq});
+    auto *granted = (const int32_t *)a.optional("granted", at::kInt, {B});
     const at::Tensor &ws = a.tensor("workspace");
     if (!ws.is_contiguous() || ws.device() != a.device()) refuse("workspace has to be a dense tensor on ", a.device().str());
     const int mq = a.integer("max_query");
@@ -285,18 +287,18 @@ PyObject *tree_gqa(PyObject *, PyObject *const *v, Py_ssize_t count) {
     const size_t wn = ws.nbytes();
     return a.launch([&](cudaStream_t s) {
       if (fmt == 0)
-        return pa_tree_gqa(q, kp, vp, bt, lens, start, mask, out, lse, (int)B, (int)T, mq, (int)Hq, (int)Hkv, (int)D, (int)P,
-                           (int)N, (int)W, most, scale, window, splits, w, wn, s);
-      auto *f = fmt == 1 ? pa_tree_gqa_fp8 : pa_tree_gqa_nvfp4;
-      return f(q, kp, vp, bt, lens, start, mask, out, lse, (int)B, (int)T, mq, (int)Hq, (int)Hkv, (int)D, (int)P, (int)N,
-               (int)W, most, scale, ks, vs, window, splits, w, wn, s);
+        return pa_tree_gqa_granted(q, kp, vp, bt, lens, start, mask, granted, out, lse, (int)B, (int)T, mq, (int)Hq, (int)Hkv,
+                                   (int)D, (int)P, (int)N, (int)W, most, scale, window, splits, w, wn, s);
+      auto *f = fmt == 1 ? pa_tree_gqa_fp8_granted : pa_tree_gqa_nvfp4_granted;
+      return f(q, kp, vp, bt, lens, start, mask, granted, out, lse, (int)B, (int)T, mq, (int)Hq, (int)Hkv, (int)D, (int)P,
+               (int)N, (int)W, most, scale, ks, vs, window, splits, w, wn, s);
     });
   });
 }
 
 PyObject *kv_compact(PyObject *, PyObject *const *v, Py_ssize_t count) {
   return guarded([&] {
-    Args a(v, count, 10);
+    Args a(v, count, 11);
     if (!THPVariable_Check(v[0])) refuse("k_pool has to be a tensor");
     const at::Tensor &k = THPVariable_Unpack(v[0]);
     if (k.dim() != 4 && k.dim() != 5) refuse("k_pool has to have four or five dimensions; it has ", (long)k.dim());
@@ -317,13 +319,14 @@ PyObject *kv_compact(PyObject *, PyObject *const *v, Py_ssize_t count) {
     auto *start = (const int32_t *)a.array("query_start", at::kInt, {B + 1});
     auto *acc = (const int32_t *)a.array("accepted", at::kInt, {B, M});
     auto *num = (const int32_t *)a.array("num_accepted", at::kInt, {B});
+    auto *granted = (const int32_t *)a.optional("granted", at::kInt, {B});
     auto *out = (int32_t *)a.array("context_lens_out", at::kInt, {B});
     auto *status = (uint32_t *)a.optional("status", at::kInt, {1});
     const int64_t bytes = H * R * (int64_t)k.element_size();
     if (L > INT_MAX || N > INT_MAX || P > INT_MAX || bytes > INT_MAX) refuse("k_pool is too large");
     return a.launch([&](cudaStream_t s) {
-      return pa_kv_compact(kp, vp, bt, lens, start, acc, num, out, (int)L, (int)B, (int)M, (int)bytes, (int)P, (int)N, (int)W,
-                           status, s);
+      return pa_kv_compact_granted(kp, vp, bt, lens, start, acc, num, granted, out, (int)L, (int)B, (int)M, (int)bytes, (int)P,
+                                   (int)N, (int)W, status, s);
     });
   });
 }

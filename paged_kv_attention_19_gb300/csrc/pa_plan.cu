@@ -25,6 +25,7 @@ struct PlanArgs {
   int64_t *slot_mapping;
   int32_t *positions;
   uint64_t *tree_mask;
+  int32_t *granted;  // or null
   uint32_t *status;  // or null
   int batch, page_size, num_pages, max_pages_per_seq, max_tokens;
 };
@@ -212,6 +213,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
   const int first = rank * kPlanThreads + tid, stride = nranks * kPlanThreads;
   for (int b = first; b < a.batch; b += stride) {
     a.query_start[b] = rows[b].start;
+    if (a.granted) a.granted[b] = plan_granted(rows[b], tot.top);
     if (rows[b].need > 0 && !plan_granted(rows[b], tot.top)) bad |= PA_DEV_NO_PAGES;
     if constexpr (MODE != PLAN_AFTER) plan_state(a, rows, tot, b);
   }
@@ -302,6 +304,7 @@ constexpr int kCompactThreads = 256;
 struct CompactArgs {
   uint4 *k_pool, *v_pool;
   const int32_t *block_table, *context_lens, *query_start, *accepted, *num_accepted;
+  const int32_t *granted;  // or null: all rows
   int32_t *context_lens_out;
   uint32_t *status;
   long long columns;      // 2 * layers * vectors per token
@@ -322,9 +325,13 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const Compa
     const int p0 = lane < a.max_accepted ? path[lane] : 0, p1 = lane + 32 < a.max_accepted ? path[lane + 32] : 0;
     uint32_t bad = 0;
     const int L = a.context_lens[b], n = a.query_start[b + 1] - a.query_start[b];
+    const bool granted = !a.granted || a.granted[b] != 0;
     int m = a.num_accepted[b];
     const long long room = (long long)a.max_pages_per_seq * a.page_size;
-    const bool ok = n >= 0 && L >= n && L <= room && m >= 0 && m <= a.max_accepted;
+    // a row whose tokens are not in the cache, or that is no tree (a plan's chain of more than 64), stays as it is
+    const bool whole = !granted || (n > kTreeNodes && L >= n && L <= room);
+    if (whole) m = 0;
+    const bool ok = whole || (n >= 0 && L >= n && L <= room && m >= 0 && m <= a.max_accepted);
     if (!ok) {
       bad |= PA_DEV_BAD_LEN;
       m = 0;
@@ -353,7 +360,7 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const Compa
     if (stop) bad |= PA_DEV_BAD_TREE;
     if (lane == 0) {
       moves = good;
-      if (blockIdx.x == 0) a.context_lens_out[b] = ok ? prefix + good : max(L, 0);
+      if (blockIdx.x == 0) a.context_lens_out[b] = whole ? L : ok ? prefix + good : max(L, 0);
     }
     if (bad && a.status && blockIdx.x == 0) atomicOr(a.status, bad);
   }
@@ -414,6 +421,18 @@ extern "C" int pa_plan_step(const int32_t *context_lens, const int32_t *new_lens
                             int32_t *free_count_out, int32_t *query_start, int64_t *slot_mapping,
                             int32_t *positions, uint64_t *tree_mask, int batch, int page_size, int num_pages,
                             int max_pages_per_seq, int max_tokens, uint32_t *status, cudaStream_t stream) {
+  return pa_plan_step_granted(context_lens, new_lens, held_pages, free_list, free_count, parents, block_table,
+                              context_lens_out, held_pages_out, free_count_out, query_start, slot_mapping, positions,
+                              tree_mask, nullptr, batch, page_size, num_pages, max_pages_per_seq, max_tokens, status, stream);
+}
+
+extern "C" int pa_plan_step_granted(const int32_t *context_lens, const int32_t *new_lens, const int32_t *held_pages,
+                                    int32_t *free_list, const int32_t *free_count, const int32_t *parents,
+                                    int32_t *block_table, int32_t *context_lens_out, int32_t *held_pages_out,
+                                    int32_t *free_count_out, int32_t *query_start, int64_t *slot_mapping,
+                                    int32_t *positions, uint64_t *tree_mask, int32_t *granted, int batch, int page_size,
+                                    int num_pages, int max_pages_per_seq, int max_tokens, uint32_t *status,
+                                    cudaStream_t stream) {
   using namespace pa;
   note_launches(0);
   if (batch < 0 || page_size <= 0 || num_pages <= 0 || max_pages_per_seq <= 0 || max_tokens < 0)
@@ -427,7 +446,7 @@ extern "C" int pa_plan_step(const int32_t *context_lens, const int32_t *new_lens
   if (max_tokens > 0 && (!slot_mapping || !positions)) return PA_ERR_INVALID_ARGUMENT;
   if ((parents != nullptr) != (tree_mask != nullptr)) return PA_ERR_INVALID_ARGUMENT;
   const void *words[] = {context_lens, new_lens, held_pages, free_list, free_count, parents, block_table,
-                         context_lens_out, held_pages_out, free_count_out, query_start, positions, status};
+                         context_lens_out, held_pages_out, free_count_out, query_start, positions, granted, status};
   for (const void *p : words)
     if (!aligned_to(p, 4)) return PA_ERR_MISALIGNED;
   if (!aligned_to(slot_mapping, 8) || !aligned_to(tree_mask, 8)) return PA_ERR_MISALIGNED;
@@ -441,7 +460,7 @@ extern "C" int pa_plan_step(const int32_t *context_lens, const int32_t *new_lens
   const Range out[] = {{context_lens_out, nb}, {held_pages_out, nb}, {free_count_out, 4}, {query_start, nb + 4},
                        {slot_mapping, nt * 8}, {positions, nt * 4}, {tree_mask, tree_mask ? nt * 8 : 0},
                        {block_table, (size_t)max_pages_per_seq * nb}, {free_list, (size_t)num_pages * 4},
-                       {status, status ? 4u : 0u}};
+                       {granted, granted ? nb : 0}, {status, status ? 4u : 0u}};
   constexpr int n_in = sizeof(in) / sizeof(in[0]), n_out = sizeof(out) / sizeof(out[0]);
   for (int i = 0; i < n_out; ++i) {
     for (int j = 0; j < n_in; ++j) {
@@ -452,7 +471,7 @@ extern "C" int pa_plan_step(const int32_t *context_lens, const int32_t *new_lens
       if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return PA_ERR_INVALID_ARGUMENT;
   }
   PlanArgs a = {context_lens, new_lens, held_pages, free_list, free_count, parents, block_table, context_lens_out,
-                held_pages_out, free_count_out, query_start, slot_mapping, positions, tree_mask, status, batch,
+                held_pages_out, free_count_out, query_start, slot_mapping, positions, tree_mask, granted, status, batch,
                 page_size, num_pages, max_pages_per_seq, max_tokens};
   const size_t smem = (size_t)(batch + 1) * sizeof(PlanRow);
   const int chunks = (max_tokens + kPlanThreads - 1) / kPlanThreads;
@@ -487,6 +506,16 @@ extern "C" int pa_kv_compact(void *k_pool, void *v_pool, const int32_t *block_ta
                              int32_t *context_lens_out, int num_layers, int batch, int max_accepted, int token_bytes,
                              int page_size, int num_pages, int max_pages_per_seq, uint32_t *status,
                              cudaStream_t stream) {
+  return pa_kv_compact_granted(k_pool, v_pool, block_table, context_lens, query_start, accepted, num_accepted, nullptr,
+                               context_lens_out, num_layers, batch, max_accepted, token_bytes, page_size, num_pages,
+                               max_pages_per_seq, status, stream);
+}
+
+extern "C" int pa_kv_compact_granted(void *k_pool, void *v_pool, const int32_t *block_table, const int32_t *context_lens,
+                                     const int32_t *query_start, const int32_t *accepted, const int32_t *num_accepted,
+                                     const int32_t *granted, int32_t *context_lens_out, int num_layers, int batch,
+                                     int max_accepted, int token_bytes, int page_size, int num_pages,
+                                     int max_pages_per_seq, uint32_t *status, cudaStream_t stream) {
   using namespace pa;
   note_launches(0);
   if (num_layers <= 0 || batch < 0 || token_bytes <= 0 || page_size <= 0 || num_pages <= 0 || max_pages_per_seq <= 0 ||
@@ -500,14 +529,15 @@ extern "C" int pa_kv_compact(void *k_pool, void *v_pool, const int32_t *block_ta
       !context_lens_out)
     return PA_ERR_INVALID_ARGUMENT;
   if (!aligned_to(k_pool, 16) || !aligned_to(v_pool, 16)) return PA_ERR_MISALIGNED;
-  const void *words[] = {block_table, context_lens, query_start, accepted, num_accepted, context_lens_out, status};
+  const void *words[] = {block_table, context_lens, query_start, accepted, num_accepted, granted, context_lens_out, status};
   for (const void *p : words)
     if (!aligned_to(p, 4)) return PA_ERR_MISALIGNED;
   const size_t nb = (size_t)batch * 4;
   const size_t pool = (size_t)num_layers * num_pages * page_size * token_bytes;
   if (overlap(context_lens_out, nb, context_lens, nb) || overlap(context_lens_out, nb, query_start, nb + 4) ||
       overlap(context_lens_out, nb, num_accepted, nb) || overlap(context_lens_out, nb, accepted, nb * max_accepted) ||
-      overlap(context_lens_out, nb, block_table, nb * max_pages_per_seq) || overlap(k_pool, pool, v_pool, pool))
+      overlap(context_lens_out, nb, block_table, nb * max_pages_per_seq) ||
+      overlap(context_lens_out, nb, granted, granted ? nb : 0) || overlap(k_pool, pool, v_pool, pool))
     return PA_ERR_INVALID_ARGUMENT;
   CompactArgs a;
   a.k_pool = static_cast<uint4 *>(k_pool);
@@ -517,6 +547,7 @@ extern "C" int pa_kv_compact(void *k_pool, void *v_pool, const int32_t *block_ta
   a.query_start = query_start;
   a.accepted = accepted;
   a.num_accepted = num_accepted;
+  a.granted = granted;
   a.context_lens_out = context_lens_out;
   a.status = status;
   a.vecs = token_bytes / 16;

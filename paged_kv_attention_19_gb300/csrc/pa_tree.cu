@@ -105,8 +105,8 @@ int sm_count() {
 }
 
 int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
-              const int32_t *context_lens, const int32_t *query_start, const uint64_t *tree_mask, void *out, float *lse,
-              int batch, int tokens, int max_query, int Hq, int Hkv, int D, int P, int num_pages, int max_pages,
+              const int32_t *context_lens, const int32_t *query_start, const uint64_t *tree_mask, const int32_t *granted,
+              void *out, float *lse, int batch, int tokens, int max_query, int Hq, int Hkv, int D, int P, int num_pages, int max_pages,
               int max_ctx, float scale, int fmt, float k_scale, float v_scale, int window, int num_splits, void *workspace,
               size_t workspace_bytes, cudaStream_t stream) {
   note_launches(0);
@@ -124,7 +124,7 @@ int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32
   const void *vecs[] = {q, k_pool, v_pool, out, workspace};
   for (const void *p : vecs)
     if (!aligned_to(p, 16)) return PA_ERR_MISALIGNED;
-  const void *words[] = {block_table, context_lens, query_start, lse};
+  const void *words[] = {block_table, context_lens, query_start, granted, lse};
   for (const void *p : words)
     if (!aligned_to(p, 4)) return PA_ERR_MISALIGNED;
   if (!aligned_to(tree_mask, 8)) return PA_ERR_MISALIGNED;
@@ -150,6 +150,7 @@ int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32
   a.context_lens = context_lens;
   a.query_start = query_start;
   a.tree_mask = tree_mask;
+  a.granted = granted;
   a.out = static_cast<uint16_t *>(out);
   a.lse = lse;
   a.cta_status = reinterpret_cast<uint32_t *>(ws + pl.off_status);
@@ -208,10 +209,22 @@ extern "C" int pa_tree_gqa(const void *q, const void *k_pool, const void *v_pool
                            int num_kv_heads, int head_dim, int page_size, int num_pages, int max_pages_per_seq,
                            int max_context_len, float scale, int window, int num_splits, void *workspace,
                            size_t workspace_bytes, cudaStream_t stream) {
-  return pa::tree_call(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, batch, num_tokens,
-                       max_query, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, max_pages_per_seq,
-                       max_context_len, scale, pa::TREE_BF16, 1.f, 1.f, window, num_splits, workspace, workspace_bytes,
-                       stream);
+  return pa::tree_call(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, nullptr, out, lse, batch,
+                       num_tokens, max_query, num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
+                       max_pages_per_seq, max_context_len, scale, pa::TREE_BF16, 1.f, 1.f, window, num_splits,
+                       workspace, workspace_bytes, stream);
+}
+
+extern "C" int pa_tree_gqa_granted(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+                                   const int32_t *context_lens, const int32_t *query_start, const uint64_t *tree_mask,
+                                   const int32_t *granted, void *out, float *lse, int batch, int num_tokens,
+                                   int max_query, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                                   int num_pages, int max_pages_per_seq, int max_context_len, float scale, int window,
+                                   int num_splits, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return pa::tree_call(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, granted, out, lse, batch,
+                       num_tokens, max_query, num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
+                       max_pages_per_seq, max_context_len, scale, pa::TREE_BF16, 1.f, 1.f, window, num_splits,
+                       workspace, workspace_bytes, stream);
 }
 
 extern "C" int pa_tree_gqa_fp8(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
@@ -220,10 +233,24 @@ extern "C" int pa_tree_gqa_fp8(const void *q, const void *k_pool, const void *v_
                                int num_kv_heads, int head_dim, int page_size, int num_pages, int max_pages_per_seq,
                                int max_context_len, float scale, float k_scale, float v_scale, int window,
                                int num_splits, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
-  return pa::tree_call(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, batch, num_tokens,
-                       max_query, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, max_pages_per_seq,
-                       max_context_len, scale, pa::TREE_FP8, k_scale, v_scale, window, num_splits, workspace,
-                       workspace_bytes, stream);
+  return pa::tree_call(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, nullptr, out, lse, batch,
+                       num_tokens, max_query, num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
+                       max_pages_per_seq, max_context_len, scale, pa::TREE_FP8, k_scale, v_scale, window, num_splits,
+                       workspace, workspace_bytes, stream);
+}
+
+extern "C" int pa_tree_gqa_fp8_granted(const void *q, const void *k_pool, const void *v_pool,
+                                       const int32_t *block_table, const int32_t *context_lens,
+                                       const int32_t *query_start, const uint64_t *tree_mask, const int32_t *granted,
+                                       void *out, float *lse, int batch, int num_tokens, int max_query, int num_q_heads,
+                                       int num_kv_heads, int head_dim, int page_size, int num_pages,
+                                       int max_pages_per_seq, int max_context_len, float scale, float k_scale,
+                                       float v_scale, int window, int num_splits, void *workspace,
+                                       size_t workspace_bytes, cudaStream_t stream) {
+  return pa::tree_call(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, granted, out, lse, batch,
+                       num_tokens, max_query, num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
+                       max_pages_per_seq, max_context_len, scale, pa::TREE_FP8, k_scale, v_scale, window, num_splits,
+                       workspace, workspace_bytes, stream);
 }
 
 extern "C" int pa_tree_gqa_nvfp4(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
@@ -232,8 +259,22 @@ extern "C" int pa_tree_gqa_nvfp4(const void *q, const void *k_pool, const void *
                                  int num_kv_heads, int head_dim, int page_size, int num_pages, int max_pages_per_seq,
                                  int max_context_len, float scale, float k_scale, float v_scale, int window,
                                  int num_splits, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
-  return pa::tree_call(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, out, lse, batch, num_tokens,
-                       max_query, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, max_pages_per_seq,
-                       max_context_len, scale, pa::TREE_NVFP4, k_scale, v_scale, window, num_splits, workspace,
-                       workspace_bytes, stream);
+  return pa::tree_call(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, nullptr, out, lse, batch,
+                       num_tokens, max_query, num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
+                       max_pages_per_seq, max_context_len, scale, pa::TREE_NVFP4, k_scale, v_scale, window, num_splits,
+                       workspace, workspace_bytes, stream);
+}
+
+extern "C" int pa_tree_gqa_nvfp4_granted(const void *q, const void *k_pool, const void *v_pool,
+                                         const int32_t *block_table, const int32_t *context_lens,
+                                         const int32_t *query_start, const uint64_t *tree_mask, const int32_t *granted,
+                                         void *out, float *lse, int batch, int num_tokens, int max_query,
+                                         int num_q_heads, int num_kv_heads, int head_dim, int page_size, int num_pages,
+                                         int max_pages_per_seq, int max_context_len, float scale, float k_scale,
+                                         float v_scale, int window, int num_splits, void *workspace,
+                                         size_t workspace_bytes, cudaStream_t stream) {
+  return pa::tree_call(q, k_pool, v_pool, block_table, context_lens, query_start, tree_mask, granted, out, lse, batch,
+                       num_tokens, max_query, num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
+                       max_pages_per_seq, max_context_len, scale, pa::TREE_NVFP4, k_scale, v_scale, window, num_splits,
+                       workspace, workspace_bytes, stream);
 }

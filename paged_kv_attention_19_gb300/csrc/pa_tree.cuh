@@ -66,6 +66,7 @@ struct TreeArgs {
   const uint8_t *v_pool;
   const int32_t *block_table, *context_lens, *query_start;
   const uint64_t *tree_mask;
+  const int32_t *granted;  // or null: all rows
   uint16_t *out;
   float *lse;           // or null
   uint32_t *cta_status; // [nparts]: PA_DEV_* bits
@@ -193,7 +194,7 @@ struct TreeRow {
   int start, n, L;  // n = 0: nothing to do
 };
 
-// Row b, its lengths checked: a bad row has no nodes and sets PA_DEV_BAD_LEN.  (From L2: the combine kernel
+// Row b, its lengths checked: a bad row has no nodes and sets PA_DEV_BAD_LEN; one that was not granted has none.  (From L2: the combine kernel
 // reads them before the grids that come before it are known to it as complete.)
 __device__ __forceinline__ TreeRow tree_row(const TreeArgs &a, int b, uint32_t *bad) {
   TreeRow r;
@@ -201,7 +202,9 @@ __device__ __forceinline__ TreeRow tree_row(const TreeArgs &a, int b, uint32_t *
   r.L = __ldcg(a.context_lens + b);
   const int end = __ldcg(a.query_start + b + 1);
   r.n = end - r.start;
-  if (r.start < 0 || end < r.start || end > a.tokens || r.n > a.max_query || r.L < r.n || r.L < 0 ||
+  if (a.granted && __ldcg(a.granted + b) == 0) {  // (whatever its lengths say)
+    r.n = 0;
+  } else if (r.start < 0 || end < r.start || end > a.tokens || r.n > a.max_query || r.L < r.n || r.L < 0 ||
       r.L > a.max_context_len) {
     *bad |= PA_DEV_BAD_LEN;
     r.n = 0;
