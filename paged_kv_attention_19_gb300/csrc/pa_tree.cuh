@@ -588,6 +588,12 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// A bounded wait of a whole warp, with one answer: a lane that gave up by itself would leave the others waiting for it at the
+// warp's next common instruction, without a limit.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t *status) {
+  return __all_sync(FULL, mbar_wait(bar, parity, status));
+}
+
 // ---------------------------------------------------------------------------------------- the kernel
 
 template <class C>
@@ -712,8 +718,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           for (int kv = 0; kv < 2 && ok; ++kv) {
             uint32_t u;
             const int s = place(kv, u);
-            if (u > 0) ok = mbar_wait(&r_empty[s], (u - 1) & 1, status);
-            ok = __all_sync(FULL, ok);
+            if (u > 0) ok = warp_wait(&r_empty[s], (u - 1) & 1, status);
             if (!ok) break;
             in_flight = kv + 1;
             if (lane == 0) {
@@ -759,7 +764,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     for (int kv = 0; C::QUANT && kv < 2 && ok; ++kv) {
       uint32_t u;
       const int s = place(kv, u);
-      if (u > 0) ok = __all_sync(FULL, mbar_wait(&r_empty[s], (u - 1) & 1, status));
+      if (u > 0) ok = warp_wait(&r_empty[s], (u - 1) & 1, status);
       if (ok && lane == 0) {
         if (kv == 0) meta[t % C::META].flags = STAGE_END;
         mbar_arrive(&r_full[s]);
@@ -769,12 +774,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if constexpr (C::QUANT) {
         const uint32_t nf_ = 2 * t + (uint32_t)in_flight;
         for (uint32_t i = nf_ > C::NR ? nf_ - C::NR : 0u; i < nf_; ++i)
-          mbar_wait(&raw_full[i % C::NR], (i / C::NR) & 1, status);
+          warp_wait(&raw_full[i % C::NR], (i / C::NR) & 1, status);
       } else {
         const uint32_t nk = t + (in_flight > 0), nv = t + (in_flight > 1);
-        for (uint32_t i = nk > C::NK ? nk - C::NK : 0u; i < nk; ++i) mbar_wait(&full[i % C::NK], (i / C::NK) & 1, status);
+        for (uint32_t i = nk > C::NK ? nk - C::NK : 0u; i < nk; ++i) warp_wait(&full[i % C::NK], (i / C::NK) & 1, status);
         for (uint32_t i = nv > C::NV ? nv - C::NV : 0u; i < nv; ++i)
-          mbar_wait(&full[C::NK + i % C::NV], (i / C::NV) & 1, status);
+          warp_wait(&full[C::NK + i % C::NV], (i / C::NV) & 1, status);
       }
     }
     if (lane == 0) misc->npieces = npieces;
@@ -906,7 +911,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if constexpr (!C::QUANT) {
         for (int st = 0; st < ((stages + 1) & ~1) && ok; ++st, ++t) {
           const int s = C::NK + t % C::NV;
-          ok = __all_sync(FULL, mbar_wait(&full[s], (t / C::NV) & 1, status));
+          ok = warp_wait(&full[s], (t / C::NV) & 1, status);
           if (!ok) break;
           const int4 m = *reinterpret_cast<const int4 *>(&meta[t % C::META]);  // flags, tok0, tok_hi, badmask
           if (m.x & STAGE_MASKED) {
@@ -961,7 +966,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     // no copy is in flight when the CTA exits, and the issuing threads learn of the end
     if (k > 0) {
-      mbar_wait(q_full, (k - 1) & 1, status);
+      warp_wait(q_full, (k - 1) & 1, status);
       if (ok) ok = scored();
     }
     if (ok && lane == 0) {
@@ -985,12 +990,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       for (uint32_t t = 0;; ++t) {
         const uint32_t f = 2 * t + kv;
         const int rs = f % C::NR;
-        bool ok = __all_sync(FULL, mbar_wait(&raw_full[rs], (f / C::NR) & 1, status));
+        bool ok = warp_wait(&raw_full[rs], (f / C::NR) & 1, status);
         if (!ok) break;
         const int4 m = *reinterpret_cast<const int4 *>(&meta[t % C::META]);  // flags, tok0, tok_hi, badmask
         // a new piece, or the end: the warps of the V tiles, which are needed later, take the query rows
         if (__builtin_expect(kv == 1 && (m.x & (STAGE_FIRST | STAGE_END)), 0)) {
-          ok = __all_sync(FULL, mbar_wait(q_full, kp & 1, status));
+          ok = warp_wait(q_full, kp & 1, status);
           if (!ok) break;
           const TreePieceRec &r = prec[kp & 1];
           if (!(m.x & STAGE_END)) {
@@ -1040,7 +1045,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         {
           const int s = kv ? C::NK + t % C::NV : t % C::NK;
           const uint32_t u = kv ? t / C::NV : t / C::NK;
-          if (u > 0) ok = __all_sync(FULL, mbar_wait(&empty[s], (u - 1) & 1, status));
+          if (u > 0) ok = warp_wait(&empty[s], (u - 1) & 1, status);
           if (!ok) break;
           const uint8_t *raw = smem + S::OFF_RAW + rs * C::RAW_SLOT;
           uint8_t *op = smem + S::OFF_RING + s * C::SLOT;
@@ -1140,14 +1145,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     auto buf = [&](uint32_t i) { return C::buffer(grp, i); };
     auto par = [&](uint32_t i) { return C::buffer_phase(i); };
     int seen = -1;  // the stage of the item before, if its V tile was looked over: what was found is not taken up yet
-    auto take_up = [&]() {  // (its second product is complete)
-      if (seen < 0 || !mbar_wait(&clean[seen % C::META], (seen / C::META) & 1, status)) return;
+    auto take_up = [&]() -> bool {  // (its second product is complete)
+      if (seen < 0) return true;
+      if (!warp_wait(&clean[seen % C::META], (seen / C::META) & 1, status)) return false;
 #pragma unroll
       for (int w = 0; w < C::CLEAN_WARPS; ++w) {
         bad_nodes |= nf[((seen % C::META) * C::CLEAN_WARPS + w) * 2];
         bad_edge |= nf[((seen % C::META) * C::CLEAN_WARPS + w) * 2 + 1];
       }
       seen = -1;
+      return true;
     };
 
     // the group's next item: stage tt, whose record is m (flags, tok0, tok_hi, badmask)
@@ -1157,9 +1164,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const uint32_t tO = tl_base + C::TM_O + o * D;
       if (warp_real && !(m.x & STAGE_ABSENT)) {
         if (__builtin_expect(seen >= 0, 0)) {  // of the item before, whose record is soon another's
-          if (!mbar_wait(&pv_done[buf(c - 1)], par(c - 1), status)) return false;
-          __syncwarp();
-          take_up();
+          if (!warp_wait(&pv_done[buf(c - 1)], par(c - 1), status) || !take_up()) return false;
         }
         const bool masked = m.x & STAGE_MASKED;
         if (__builtin_expect(masked || flip != 1.f, 0)) {
@@ -1197,8 +1202,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           m_run = mx;
         } else if (__builtin_expect(__any_sync(FULL, real && m_run != -INFINITY && mx > m_run + C::TAU), 0)) {
           // raise the maximum: the output so far is scaled, once its products are complete
-          if (!mbar_wait(&pv_done[buf(c - 1)], par(c - 1), status)) return false;
-          __syncwarp();
+          if (!warp_wait(&pv_done[buf(c - 1)], par(c - 1), status)) return false;
           tc_fence_after();
           const float mn = fmaxf(m_run, mx);
           const float al = m_run == -INFINITY ? 1.f : fast_exp2(m_run - mn);
@@ -1247,8 +1251,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
     while (ok) {
       // a new piece: its record comes with its first item
-      if (!mbar_wait(&s_full[buf(c)], par(c), status)) break;
-      __syncwarp();
+      if (!warp_wait(&s_full[buf(c)], par(c), status)) break;
       tc_fence_after();
       const int4 *rp = reinterpret_cast<const int4 *>(&prec[kp & 1]);
       const int4 r0 = rp[0], r1 = rp[1], r2 = rp[2];
@@ -1300,9 +1303,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const uint32_t j0 = C::GROUPS == 2 && !two ? (uint32_t)grp : 0, dj = C::GROUPS == 2 && !two ? 2 : 1;
       for (uint32_t j = j0; j < even && ok; j += dj) {
         if (j != j0) {
-          ok = mbar_wait(&s_full[buf(c)], par(c), status);
+          ok = warp_wait(&s_full[buf(c)], par(c), status);
           if (!ok) break;
-          __syncwarp();
           tc_fence_after();
         }
         ok = item(t0 + j, *reinterpret_cast<const int4 *>(&meta[(t0 + j) % C::META]));
@@ -1311,10 +1313,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       t0 += even;
 
       // ---- end of a piece: the products of the last item, and with them all before, are complete
-      ok = mbar_wait(&pv_done[buf(c - 1)], par(c - 1), status);
+      ok = warp_wait(&pv_done[buf(c - 1)], par(c - 1), status) && take_up();
       if (!ok) break;
-      __syncwarp();
-      take_up();
       TreeHalf other = {-INFINITY, 0.f, 0, 0};
       const bool merge = C::GROUPS == 2 && !two;
       if (merge) {  // both groups have had as many items
@@ -1322,7 +1322,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         *mine = TreeHalf{m_run, l_run, bad_nodes, bad_edge};
         __syncwarp();
         if (lane == 0) mbar_arrive(&half_in[grp]);
-        ok = mbar_wait(&half_in[grp ^ 1], k_half & 1, status) && mbar_wait(&pv_done[C::buffer(grp ^ 1, c - 1)], par(c - 1), status);
+        ok = warp_wait(&half_in[grp ^ 1], k_half & 1, status) && warp_wait(&pv_done[C::buffer(grp ^ 1, c - 1)], par(c - 1), status);
         if (!ok) break;
         ++k_half;
         other = a.halves[((size_t)blockIdx.x * 2 + (grp ^ 1)) * kTreeRows + row];

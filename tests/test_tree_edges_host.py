@@ -1,5 +1,8 @@
 """The tree-drafting operators' arguments at the ends of their ranges, without a GPU (addresses here are never
 touched)."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -43,3 +46,33 @@ def test_binding_refuses_grants(pa):
                            workspace=z(1 << 20, d=torch.uint8), granted=bad)
         with pytest.raises(pa.PaError, match="granted"):
             pa.pa_kv_compact(pool, pool, z(2, 3), z(2), z(3), z(2, 4), z(2), granted=bad, context_lens_out=z(2))
+
+
+# ------------------------------------------------------------------------------------------ waits that give up
+
+def _tree_kernel_source():
+    with open(os.path.join(test_abi_host.ROOT, "paged_kv_attention_19_gb300", "csrc", "pa_tree.cuh")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    return text[text.index("tree_split_kernel("):text.index("tree_combine_kernel(")]
+
+
+def test_waits_of_a_whole_warp_have_one_answer():
+    """In the tree attention's kernel a wait that a thread ends for itself (mbar_wait) stands only in the branch of the elected
+    issuing thread, which has no instruction in common with its warp's other lanes until its end; all others are the whole
+    warp's, with the same answer in every lane.  (Lanes that disagree wait for one another without a limit: nothing to run.)"""
+    text = _tree_kernel_source()
+    a = text.index("if (elect_one()) {")
+    depth, b = 0, text.index("{", a)
+    while True:  # the branch's end
+        depth += {"{": 1, "}": -1}.get(text[b], 0)
+        b += 1
+        if depth == 0:
+            break
+    alone, rest = text[a:b], text[:a] + text[b:]
+    assert re.search(r"\bmbar_wait\(", alone) and not re.search(r"\bmbar_(try_)?wait(_lane)?\(|\bmbar_test\(", rest)
+    assert not re.search(r"__syncwarp|_sync\(|warp_wait\(", alone)
+    assert len(re.findall(r"\bwarp_wait\(", rest)) >= 10
+    # an answer is looked at, but for copies that are only waited out before the end
+    for line in rest.splitlines():
+        if re.match(r"\s*warp_wait\(", line):
+            assert re.search(r"(raw_full|full|q_full)\b", line), line
