@@ -1204,9 +1204,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           // raise the maximum: the output so far is scaled, once its products are complete
           if (!warp_wait(&pv_done[buf(c - 1)], par(c - 1), status)) return false;
           tc_fence_after();
-          const float mn = fmaxf(m_run, mx);
-          const float al = m_run == -INFINITY ? 1.f : fast_exp2(m_run - mn);
-          m_run = mn;
+          // (only of rows past the threshold, so that no row's rounding depends on what its neighbours attend to)
+          const bool raise = m_run == -INFINITY || mx > m_run + C::TAU;
+          const float al = raise && m_run != -INFINITY ? fast_exp2(m_run - mx) : 1.f;
+          if (raise) m_run = mx;
           l_run *= al;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {

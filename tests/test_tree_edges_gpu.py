@@ -180,3 +180,34 @@ def test_steps_in_which_pages_run_out(pa, fmt, captured):
             kept[b] = held_bytes
             longest = max(longest, hl[b])
     assert refused >= 5 and longest >= 40 and long_rows
+
+
+# ------------------------------------------------------------------------------------------ tree attention
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("hq,hkv,D", [(8, 2, 128), (8, 2, 256), (6, 3, 64), (64, 2, 128)])
+def test_tree_large_keys_of_other_nodes(pa, fmt, hq, hkv, D):
+    """A node's key that raises its own running maximum far changes no bit of the nodes that do not attend to it."""
+    rows, G, j = [(700, 13), (1033, 20)], hq // hkv, 5
+    masks = [1 | 1 << i for _, n in rows for i in range(n)]  # all nodes are children of the first
+    t = Tree(300 + D, rows, hq, hkv, D, 16, fmt, masks=masks)
+    want, want_l, _ = t.call(pa, num_splits=1)
+    for b, (L, n) in enumerate(rows):
+        tok = L - n + j
+        row = t.k[int(t.table[b, tok // 16]), tok % 16]
+        for g in range(hkv):
+            up = t.q[int(t.start[b]) + j, g * G].float() > 0  # large scores in the node's own first head
+            if fmt == "bf16":
+                row[g] = torch.where(up, 50.0, -50.0).to(torch.bfloat16)
+            elif fmt == "fp8":
+                row[g] = torch.where(up, 0x7E, 0xFE).to(torch.uint8)
+            else:
+                code = torch.where(up, 7, 15)
+                row[g, :D // 2] = (code[::2] | code[1::2] << 4).to(torch.uint8)
+                row[g, D // 2:D // 2 + D // 16] = 0x70
+    out, lse, ws = t.call(pa, num_splits=1)
+    torch.cuda.synchronize()
+    assert pa.pa_read_device_status(ws) == 0
+    others = [int(t.start[b]) + i for b, (_, n) in enumerate(rows) for i in range(n) if i != j]
+    assert not torch.equal(lse[int(t.start[0]) + j], want_l[int(t.start[0]) + j])
+    assert torch.equal(lse[others], want_l[others]) and torch.equal(out[others], want[others])
