@@ -103,7 +103,7 @@ __device__ __forceinline__ PlanTotals plan_rows(const PlanArgs &a, PlanRow *rows
       ok = ok && pages <= a.max_pages_per_seq;
       if (pass > 0) ok = ok && b < a.batch && rows[b].start + add <= a.max_tokens;
       if (ended ? !held_ok : !ok) bad |= PA_DEV_BAD_LEN;
-      const int need = ok && n > 0 ? max(pages - held, 0) : 0;
+      const int need = ok && !ended ? max(pages - held, 0) : 0;
       PlanSums all;
       const PlanSums v = block_scan({add, ended && held_ok ? held : 0, need}, &all, part);
       if (b < a.batch) {

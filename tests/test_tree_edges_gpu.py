@@ -211,3 +211,38 @@ def test_tree_large_keys_of_other_nodes(pa, fmt, hq, hkv, D):
     others = [int(t.start[b]) + i for b, (_, n) in enumerate(rows) for i in range(n) if i != j]
     assert not torch.equal(lse[int(t.start[0]) + j], want_l[int(t.start[0]) + j])
     assert torch.equal(lse[others], want_l[others]) and torch.equal(out[others], want[others])
+
+
+# ------------------------------------------------------------------------------------------ plan
+
+@pytest.mark.parametrize("free", [6, 2, 1])
+def test_plan_rows_whose_pages_do_not_hold_their_context(pa, free):
+    """The pages that a row needs are those of its context and its new tokens, less the held ones, with or without
+    new tokens."""
+    P, W = 16, 6
+    lens, news, held = [40, 5, 33, 20], [0, 3, 2, 0], [1, 0, 3, 2]
+    need = [max(0, -(-(n + k) // P) - h) for n, k, h in zip(lens, news, held)]
+    assert need == [2, 1, 0, 0]
+    table = np.full((4, W), -1)
+    table[0, 0], table[2, :3], table[3, :2] = 10, [11, 12, 13], [14, 15]
+    want_t, want_l, want_h, stack, wanted, refused = table.copy(), list(lens), list(held), list(range(free)), 0, []
+    for b in range(4):
+        wanted += need[b]
+        if need[b] and wanted > free:
+            refused.append(b)
+            continue
+        for x in range(need[b]):
+            want_t[b, held[b] + x] = stack.pop()
+        want_l[b], want_h[b] = lens[b] + news[b], held[b] + need[b]
+    for in_place in (False, True):
+        tl, tn, th, tt, tf, tc = i32(lens), i32(news), i32(held), i32(table), i32(list(range(free)) + [0] * (16 - free)), i32([free])
+        out = {} if in_place else dict(context_lens_out=torch.empty_like(tl), held_pages_out=torch.empty_like(th),
+                                       free_count_out=torch.empty_like(tc))
+        start, slots, pos, st = i32([0] * 5), dev([0] * 8, torch.int64), i32([0] * 8), i32([0])
+        pa.pa_plan_step(tl, tn, th, tf, tc, tt, start, slots, pos, page_size=P, status=st, **out)
+        got = (tl, th, tc) if in_place else tuple(out.values())
+        assert got[0].tolist() == want_l and got[1].tolist() == want_h and int(got[2]) == len(stack)
+        assert np.array_equal(tt.cpu().numpy(), want_t) and start.tolist() == [0, 0, 3, 5, 5]
+        assert int(st) == (pa.PA_DEV_NO_PAGES if refused else 0)
+        row1 = [-1] * 3 if 1 in refused else [int(want_t[1, 0]) * P + 5 + i for i in range(3)]
+        assert slots.tolist() == row1 + [13 * P + 1, 13 * P + 2] + [-1] * 3
