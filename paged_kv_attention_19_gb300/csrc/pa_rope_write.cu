@@ -42,9 +42,11 @@ struct RopeArgs {
   uint32_t *status;             // or null
   long long q_stride, k_stride, v_stride, n_slots;
   int tokens, Hq, Hkv, rot, max_position;
+  int v0;                     // the values' first row of a token: behind the queries' and keys', at the start of a group
   int groups, segs, per_seg;  // groups of head rows per token, segments of them, groups per segment
   float eps;
-  Fp8Scale k_scale, v_scale;
+  Fp8Scale v_scale;
+  float2 k_inv;  // 1 / the keys' scale, and what its rounding left out
 };
 
 __device__ __forceinline__ float2 pair_mul(float2 a, float2 b) {
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, l = lane % LPH, g = lane / LPH;
-  const int H = a.Hq + 2 * a.Hkv, half = a.rot >> 1;
+  const int v0 = a.v0, HK = a.Hq + a.Hkv, H = v0 + a.Hkv, half = a.rot >> 1;
   constexpr bool PIECES = !IL;
   const bool turned = l * 8 < a.rot;
   // where this lane's two pieces of 4 values start (8 in a row where pairs are adjacent, and from rot on)
@@ -152,10 +154,6 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
       *reinterpret_cast<uint2 *>(row + at1) = make_uint2(v.z, v.w);
     }
   };
-  // 1 / scale, and what its rounding left out
-  [[maybe_unused]] const float ki = 1.f / a.k_scale.sc, vi = 1.f / a.v_scale.sc;
-  [[maybe_unused]] const float2 k_inv = make_float2(ki, fmaf(-a.k_scale.sc, ki, 1.f) * ki);
-  [[maybe_unused]] const float2 v_inv = make_float2(vi, fmaf(-a.v_scale.sc, vi, 1.f) * vi);
   const bool norm_q = a.q_weight != nullptr, norm_k = a.k_weight != nullptr;
   const uint4 wq = norm_q ? load8(a.q_weight) : make_uint4(0, 0, 0, 0), wk = norm_k ? load8(a.k_weight) : make_uint4(0, 0, 0, 0);
   const int items = a.tokens * a.segs, stride = (int)gridDim.x * (kRopeThreads / 32);
@@ -168,12 +166,13 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
     const int pos = next_pos;
     auto fetch = [&](int grp) {  // this lane's values of a group's rows
       const int h = grp * HPG + g;
-      const uint16_t *row = h < a.Hq           ? a.q + t * a.q_stride + h * D
-                            : h < a.Hq + a.Hkv ? a.k + t * a.k_stride + (h - a.Hq) * D
-                                               : a.v + t * a.v_stride + (h - a.Hq - a.Hkv) * D;
-      if (FMT == ROPE_NVFP4 && PIECES && h >= a.Hq + a.Hkv)  // (see the keys' exchange below)
-        return grp < g1 && h < H ? *reinterpret_cast<const uint4 *>(row + l * 8) : make_uint4(0, 0, 0, 0);
-      return grp < g1 && h < H ? load8(row) : make_uint4(0, 0, 0, 0);
+      const uint16_t *row = h < a.Hq ? a.q + t * a.q_stride + h * D
+                            : h < v0 ? a.k + t * a.k_stride + (h - a.Hq) * D
+                                     : a.v + t * a.v_stride + (h - v0) * D;
+      const bool there = grp < g1 && h < H && (h < HK || h >= v0);
+      if (FMT == ROPE_NVFP4 && PIECES && h >= v0)  // (see the keys' exchange below)
+        return there ? *reinterpret_cast<const uint4 *>(row + l * 8) : make_uint4(0, 0, 0, 0);
+      return there ? load8(row) : make_uint4(0, 0, 0, 0);
     };
     uint4 raw[AHEAD];
 #pragma unroll
@@ -195,8 +194,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
       si[0] = s.x, si[1] = s.y, si[2] = s.z, si[3] = s.w;
     }
     // norm and rotation of one lane's values of a row (all lanes of the warp; sums: some row has a norm;
-    // norm, on: this row has one, is turned)
-    auto turn = [&](float (&x)[8], bool sums, uint4 weight, bool norm, bool on) {
+    // norm: this row has one)
+    auto turn = [&](float (&x)[8], bool sums, uint4 weight, bool norm) {
       if (sums) {
         float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
           }
         }
       }
-      if (on && turned) {
+      if (turned) {
         if constexpr (IL) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -238,8 +237,9 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
     // the value, so a key beside the middle of two codes goes by its last bits, and fewer roundings put fewer of them on
     // the wrong side: x w is exact, the factor is a pair of floats, a product's rounding is made good.  (Of 50 million keys 21
     // codes are not those of 64 bits, 94 with norm, rotation and division one after the other, for 68 us instead of 63.)
-    auto turn_quot = [&](float (&x)[8], bool norm, bool on, float2 inv) {
-      float2 f = inv;  // 1 / scale in two floats
+    auto turn_quot = [&](float (&x)[8], bool norm) {
+      const float2 inv = a.k_inv;
+      float2 f = inv;
       if (norm_q || norm_k) {
         float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
       for (int e = 0; e < 4; ++e) {
         const int i = IL ? 2 * e : e, j = IL ? 2 * e + 1 : 4 + e;
         float u = x[i], v = x[j], ul = 0.f, vl = 0.f;
-        if (on && turned) {
+        if (turned) {
           const float uc = u * co[e], vc = v * co[e];
           ul = fmaf(u, co[e], -uc);
           vl = fmaf(v, co[e], -vc);
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
           if (grp + i >= g1) break;
           float x[8];
           unpack8(cur[i], x);
-          turn(x, norm_q, wq, norm_q, true);
+          turn(x, norm_q, wq, norm_q);
           store8(a.q_out + ((size_t)t * a.Hq + (grp + i) * HPG + g) * D, pack8(x));
         }
         continue;
@@ -297,17 +297,16 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
 #pragma unroll 1
       for (int i = 0; i < AHEAD && grp + i < g1; ++i) {
         const int h = (grp + i) * HPG + g, hw = h - g;  // hw: the warp's first row
-        const bool is_v = h >= a.Hq + a.Hkv, is_q = h < a.Hq;
+        const bool is_v = hw >= v0, is_q = h < a.Hq;
         float x[8];
         unpack8(cur[0], x);
 #pragma unroll
         for (int e = 0; e + 1 < AHEAD; ++e) cur[e] = cur[e + 1];
-        const bool keys = FMT != ROPE_BF16 && hw + HPG > a.Hq && hw < a.Hq + a.Hkv;  // some row is a key's
-        if (hw < (FMT != ROPE_BF16 ? a.Hq : a.Hq + a.Hkv)) {  // some row is a query's (or a key's that stays bf16)
+        if (hw < (FMT != ROPE_BF16 ? a.Hq : v0)) {  // some row is a query's (or a key's that stays bf16)
           float y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = x[e];
-          turn(y, norm_q || norm_k, is_q ? wq : wk, is_q ? norm_q : norm_k && !is_v, !is_v);
+          turn(y, norm_q || norm_k, is_q ? wq : wk, is_q ? norm_q : norm_k);
           if (FMT == ROPE_BF16 || is_q) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = y[e];
@@ -316,17 +315,17 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
         if (is_q) store8(a.q_out + ((size_t)t * a.Hq + h) * D, pack8(x));
         if (hw + HPG <= a.Hq) continue;
         // some row of the warp goes into a pool
-        const bool store = !is_q && h < H;
+        const bool store = !is_q && h < H && (h < HK || is_v);
         uint8_t *pool = is_v ? a.v_pool : a.k_pool;
-        const size_t row = (size_t)slot * a.Hkv + (is_v ? h - a.Hq - a.Hkv : h - a.Hq);
+        const size_t row = (size_t)slot * a.Hkv + (is_v ? h - v0 : h - a.Hq);
         if constexpr (FMT == ROPE_BF16) {
           if (store) store8(reinterpret_cast<uint16_t *>(pool) + row * D, pack8(x));
         } else {
           float q[8];
-          if (keys) {
+          if (!is_v) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) q[e] = x[e];
-            turn_quot(q, norm_k && !is_v && !is_q, !is_v, is_v ? v_inv : k_inv);
+            turn_quot(q, norm_k && !is_q);
           } else {
             quot8(x, a.v_scale, q);
           }
@@ -400,7 +399,9 @@ cudaError_t launch_rope(RopeArgs &a, cudaStream_t stream) {
   constexpr auto kernel = qk_norm_rope_write_kernel<D, FMT, IL>;
   const int wave = wave_blocks<kernel>();
   if (wave <= 0) return cudaErrorUnknown;
-  a.groups = (a.Hq + 2 * a.Hkv + HPG - 1) / HPG;
+  // A group's rows are values or are not: the values' codes are the plain write's, their quotients formed as there.
+  a.v0 = (a.Hq + a.Hkv + HPG - 1) / HPG * HPG;
+  a.groups = a.v0 / HPG + (a.Hkv + HPG - 1) / HPG;
   // Segments per token, by the time of the longest warp: rounds of (token, segment) pairs, each the segment's
   // groups and a start (position, slot, angles and first rows from memory) worth about four of them.  (One
   // group a segment everywhere takes 117 us where this takes 65, 8192 tokens of 64 + 8 + 8 heads of 128.)
@@ -515,9 +516,10 @@ int rope_call(const void *q, const void *k, const void *v, const void *q_weight,
   a.Hkv = Hkv;
   a.rot = rot;
   a.max_position = max_position;
-  a.groups = a.segs = a.per_seg = 0;
+  a.v0 = a.groups = a.segs = a.per_seg = 0;
   a.eps = eps;
-  a.k_scale = fp8_scale(k_scale);
+  a.k_inv.x = 1.f / k_scale;
+  a.k_inv.y = std::fma(-k_scale, a.k_inv.x, 1.f) * a.k_inv.x;
   a.v_scale = fp8_scale(v_scale);
   const cudaError_t e = fmt == ROPE_BF16  ? launch_rope_dim<ROPE_BF16>(D, a, interleaved != 0, stream)
                         : fmt == ROPE_FP8 ? launch_rope_dim<ROPE_FP8>(D, a, interleaved != 0, stream)

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import tree_refs as R
-from test_tree_ops_gpu import Tree, compact_case, compacted, dev, f64, i32, pa, raw, stored_ok  # noqa: F401
+from test_tree_ops_gpu import Tree, compact_case, compacted, dev, f64, i32, pa, raw, rope_call, rope_case, stored_ok  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -246,3 +246,25 @@ def test_plan_rows_whose_pages_do_not_hold_their_context(pa, free):
         assert int(st) == (pa.PA_DEV_NO_PAGES if refused else 0)
         row1 = [-1] * 3 if 1 in refused else [int(want_t[1, 0]) * P + 5 + i for i in range(3)]
         assert slots.tolist() == row1 + [13 * P + 1, 13 * P + 2] + [-1] * 3
+
+
+# ------------------------------------------------------------------------------------------ norm, rotation, write
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("hq,hkv,D", [(4, 1, 128), (3, 2, 128), (4, 1, 64), (5, 2, 64), (2, 1, 256), (4, 2, 128)])
+@pytest.mark.parametrize("scale", [0.013, 0.021, 0.3, 0.7, 0.25])
+def test_rope_write_values_are_the_plain_write(pa, fmt, hq, hkv, D, scale):
+    """Whichever rows a value's row shares a warp with, its codes are pa_kv_write's: zeros of either sign, infinities and NaN
+    among them."""
+    c = rope_case(20 + hq + D, 40, hq, hkv, D, D, fmt=fmt, pad=3)
+    c["scales"] = (scale, scale)
+    c["v"][:, :, ::7] = -0.0
+    c["v"][1, 0, 3], c["v"][2, 0, 5], c["v"][3, 0, 9], c["v"][4, 0, 0] = math.inf, -math.inf, math.nan, 0.0
+    c["v"][5] *= 1e30
+    c["v"][6] *= 1e-30
+    kp, vp = c["kp"].clone(), c["vp"].clone()
+    fn = {"fp8": pa.pa_kv_write_fp8, "nvfp4": pa.pa_kv_write_nvfp4}[fmt]
+    fn(c["k"].contiguous(), c["v"].contiguous(), c["slots"], kp, vp, k_scale=scale, v_scale=scale)
+    for interleaved in (False, True):
+        rope_call(pa, c, interleaved=interleaved)
+        assert np.array_equal(raw(c["vp"]), raw(vp))
