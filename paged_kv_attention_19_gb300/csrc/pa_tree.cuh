@@ -1020,7 +1020,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < CH; ++c) amax = fmaxf(amax, absmax8(w[c]));
               }
-              const int sh = min(max(14 - ((int)(__float_as_uint(amax) >> 23) - 127), -100), 100);
+              const int sh = min(14 - ((int)(__float_as_uint(amax) >> 23) - 127), 126);  // at least -114
               const float p2 = __uint_as_float((uint32_t)(sh + 127) << 23);
               shift[r] = (int8_t)sh;
 #pragma unroll 1

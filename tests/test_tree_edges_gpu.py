@@ -213,6 +213,15 @@ def test_tree_large_keys_of_other_nodes(pa, fmt, hq, hkv, D):
     assert torch.equal(lse[others], want_l[others]) and torch.equal(out[others], want[others])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("exponent", [117, -116])
+def test_tree_queries_near_the_ends_of_their_range(pa, fmt, exponent):
+    """Queries of 2^119 or 2^-116 under a scale that brings the scores back to tens."""
+    t = Tree(310, [(300, 9), (64, 20), (1, 1)], 8, 2, 128, 16, fmt, big_q=2.0 ** exponent)
+    t.scale = 2.0 ** (4 - exponent) / math.sqrt(128)
+    t.check(pa)
+
+
 # ------------------------------------------------------------------------------------------ plan
 
 @pytest.mark.parametrize("free", [6, 2, 1])
