@@ -521,7 +521,7 @@ int pa_qk_norm_rope_write_nvfp4(const void *q, const void *k, const void *v, con
  * A node's result does not depend on keys and values that it does not attend to,
  * infinities and NaN among them.  A chain (mask 2^(i + 1) - 1) gives pa_verify_gqa's
  * results within rounding, a single node (mask 1) pa_decode_gqa's.
- *   max_query    in [1, 64]
+ *   max_query    in [1, 64]; max_context_len up to 2^31 - 129 (more: PA_ERR_UNSUPPORTED)
  * Rows whose query_start is not ascending within [0, num_tokens], has more than
  * max_query nodes, or whose L is below n_b or out of range set PA_DEV_BAD_LEN and
  * have unspecified results.  The other arguments and the error codes are those of

@@ -24,6 +24,9 @@ constexpr int kPieceCost = 512;
 // to 3000 tokens 17.8, 17.9, 15.3, 15.6 us; 40 nodes over 1000 tokens 16.0, 16.1, 14.4, 15.3).
 constexpr int kMinShare = 128;
 
+// Longest context: the ends of the stages behind it, two of 64 tokens, are still tokens below 2^31.
+constexpr int kMaxContext = INT_MAX - 128;
+
 bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 int ilog2(int x) {
@@ -43,7 +46,7 @@ int tree_plan(int batch, int max_query, int Hq, int Hkv, int D, int max_ctx, int
   if (batch < 0 || max_query <= 0 || Hq <= 0 || Hkv <= 0 || max_ctx < 0 || num_splits < 0 || Hq % Hkv != 0)
     return PA_ERR_INVALID_ARGUMENT;
   if (max_query > kTreeNodes || num_splits > kMaxSplits || (D != 64 && D != 128 && D != 256) || !is_pow2(P) || P < 8 ||
-      P > 256)
+      P > 256 || max_ctx > kMaxContext)
     return PA_ERR_UNSUPPORTED;
   pl->G = Hq / Hkv;
   pl->gt = pl->G < kTreeRows ? pl->G : kTreeRows;

@@ -76,3 +76,21 @@ def test_waits_of_a_whole_warp_have_one_answer():
     for line in rest.splitlines():
         if re.match(r"\s*warp_wait\(", line):
             assert re.search(r"(raw_full|full|q_full)\b", line), line
+
+
+# ------------------------------------------------------------------------------------------ lengths
+
+@pytest.mark.parametrize("fmt", ["", "_fp8", "_nvfp4"])
+def test_tree_refuses_contexts_whose_last_tile_ends_past_31_bits(pa, fmt):
+    scales = [0.5, 0.5] if fmt else []
+
+    def call(longest, batch):
+        return getattr(pa.lib, "pa_tree_gqa" + fmt)(
+            0x100000, 0x200000, 0x300000, 0x400000, 0x410000, 0x420000, 0x430000, 0x500000, None, batch, 16, 8, 8, 2, 128, 256,
+            10, 1 << 23, longest, 0.1, *scales, 0, 0, 0x700000, 1 << 30, None)
+
+    for longest in (2 ** 31 - 1, 2 ** 31 - 63, 2 ** 31 - 128):
+        assert call(longest, 2) == UNSUPPORTED
+        assert pa.pa_tree_workspace_size(2, 8, 8, 2, 128, longest, 256) == 0
+    assert call(2 ** 31 - 129, 0) == 0
+    assert pa.pa_tree_workspace_size(2, 8, 8, 2, 128, 2 ** 31 - 129, 256) > 0
