@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import tree_refs as R
-from test_tree_ops_gpu import Tree, compact_case, compacted, dev, f64, i32, pa, raw, rope_call, rope_case, stored_ok  # noqa: F401
+from test_tree_ops_gpu import (Tree, check_plan, compact_case, compacted, dev, f64, i32, pa, plan_case, raw,  # noqa: F401
+                               rope_call, rope_case, stored_ok)
 
 pytestmark = pytest.mark.gpu
 
@@ -257,6 +258,18 @@ def test_plan_rows_whose_pages_do_not_hold_their_context(pa, free):
         assert slots.tolist() == row1 + [13 * P + 1, 13 * P + 2] + [-1] * 3
 
 
+
+@pytest.mark.parametrize("tokens", [0, 3, 5000])
+@pytest.mark.parametrize("B", [1708, 8192])
+def test_plan_most_rows(pa, B, tokens):
+    """As many rows as there may be, in one cluster, apart and with the state in a launch of its own; no tokens at all."""
+    c = plan_case(B + tokens, B, 16, 60, 1, ended=B // 9)
+    c["news"] = [n if n < 0 or b % 3 == 0 and b < 3 * tokens else 0 for b, n in enumerate(c["news"])]
+    check_plan(pa, c, max_tokens=tokens)
+    c["news"][5] = 2  # one token too many, or two
+    check_plan(pa, c, max_tokens=sum(max(0, n) for n in c["news"]) - 1)
+
+
 # ------------------------------------------------------------------------------------------ norm, rotation, write
 
 @pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
@@ -277,3 +290,58 @@ def test_rope_write_values_are_the_plain_write(pa, fmt, hq, hkv, D, scale):
     for interleaved in (False, True):
         rope_call(pa, c, interleaved=interleaved)
         assert np.array_equal(raw(c["vp"]), raw(vp))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("hq,hkv,D", [(4, 2, 128), (3, 1, 64), (2, 1, 256), (4, 1, 128)])
+def test_rope_write_nvfp4_keys_without_turn_are_the_plain_write(pa, hq, hkv, D, interleaved):
+    """Block scales and padding byte for byte; codes too, but for the sign of a zero (x cos - y sin loses it)."""
+    c = rope_case(40 + D, 60, hq, hkv, D, D, fmt="nvfp4", pad=4)
+    c["cos_sin"] = torch.cat((torch.ones(c["far"], D // 2), torch.zeros(c["far"], D // 2)), -1).cuda()
+    c["k"][3, 0, :40] = 0.0
+    c["k"][4] *= 1e4  # block scales past 448
+    c["k"][5] *= 1e-5
+    kp, vp = c["kp"].clone(), c["vp"].clone()
+    pa.pa_kv_write_nvfp4(c["k"].contiguous(), c["v"].contiguous(), c["slots"], kp, vp, **dict(zip(("k_scale", "v_scale"), c["scales"])))
+    rope_call(pa, c, None, None, interleaved)
+    mine, theirs = raw(c["kp"]), raw(kp)
+    assert np.array_equal(mine[..., D // 2:], theirs[..., D // 2:])
+    for nibble in (mine[..., :D // 2] & 15, theirs[..., :D // 2] & 15), (mine[..., :D // 2] >> 4, theirs[..., :D // 2] >> 4):
+        assert np.all((nibble[0] == nibble[1]) | ((nibble[0] | nibble[1]) & 7 == 0))
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("hq,hkv,D,rot,interleaved", [(4, 2, 128, 128, False), (4, 1, 64, 32, False), (2, 2, 256, 128, True),
+                                                     (3, 1, 128, 128, True)])
+def test_rope_write_key_codes_are_nearest(pa, fmt, hq, hkv, D, rot, interleaved):
+    """Normed and rotated keys: each code is the one nearest to the quotient in 64 bits, within the arithmetic before it.  The sum
+    of squares has at most 11 roundings of 2^-24 (a lane's four products and one sum, five exchanges, + eps), of which the root
+    takes half; the product with the weight is exact, u cos - v sin rounded once, the last product once: 7.5 x 2^-24 of the
+    quotient, less than 2^-21."""
+    c = rope_case(60 + D, 2000, hq, hkv, D, rot, fmt=fmt)
+    rope_call(pa, c, interleaved=interleaved)
+    cs = f64(c["cos_sin"])[c["positions"].cpu().numpy()]
+    x = R.norm_rope(f64(c["k"]), f64(c["wk"]), cs, rot, interleaved, 1e-6) / float(np.float32(c["scales"][0]))
+    got = raw(c["kp"]).reshape(-1, hkv, c["kp"].shape[-1])[c["slots"].cpu().numpy()]
+    off = 2.0 ** -21
+    near = np.sort(R.e4m3_table()[:127])
+
+    def nearest(values, at, err, codes):
+        """values are among `codes` (ascending, >= 0) the nearest to |at|, if |at| is off by at most err."""
+        mid = (codes[1:] + codes[:-1]) / 2
+        lo, hi = np.searchsorted(mid, np.abs(at) - err, "left"), np.searchsorted(mid, np.abs(at) + err, "right")
+        mine = np.searchsorted(codes, np.abs(values))
+        return (codes[np.minimum(mine, len(codes) - 1)] == np.abs(values)) & (lo <= mine) & (mine <= hi)
+
+    if fmt == "fp8":
+        assert nearest(R.e4m3_table()[got], x, off * np.abs(x), near).all()
+        return
+    blk = R.e4m3_table()[got[..., D // 2:D // 2 + D // 16]]
+    amax = np.abs(x).reshape(*x.shape[:-1], D // 16, 16).max(-1) / 6
+    assert nearest(blk, amax, off * 1.5 * amax, near).all()  # (and the division by 6)
+    by = np.repeat(blk, 16, -1)
+    val = R.pool_values(got, "nvfp4", D, 1.0)
+    assert (val[by == 0] == 0).all()
+    some = by > 0
+    y = x[some] / by[some]
+    assert nearest(val[some] / by[some], y, off * 1.5 * np.abs(y), R.E2M1).all()
