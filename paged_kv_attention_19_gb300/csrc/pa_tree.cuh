@@ -591,7 +591,9 @@ __device__ __forceinline__ bool elect_one() {
 // A bounded wait of a whole warp, with one answer: a lane that gave up by itself would leave the others waiting for it at the
 // warp's next common instruction, without a limit.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t *status) {
-  return __all_sync(FULL, mbar_wait(bar, parity, status));
+  const bool ok = mbar_wait_warp(bar, parity, WAIT_LIMIT_NS);
+  if (!ok && (threadIdx.x & 31) == 0) atomicOr(status, PA_DEV_TIMEOUT);
+  return ok;
 }
 
 // ---------------------------------------------------------------------------------------- the kernel
