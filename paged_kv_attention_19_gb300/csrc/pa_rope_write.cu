@@ -42,7 +42,7 @@ struct RopeArgs {
   uint32_t *status;             // or null
   long long q_stride, k_stride, v_stride, n_slots;
   int tokens, Hq, Hkv, rot, max_position;
-  int v0;                     // the values' first row of a token: behind the queries' and keys', at the start of a group
+  int v0;                     // the values' first row of a token, behind the queries' and keys'
   int groups, segs, per_seg;  // groups of head rows per token, segments of them, groups per segment
   float eps;
   Fp8Scale v_scale;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
       const uint16_t *row = h < a.Hq ? a.q + t * a.q_stride + h * D
                             : h < v0 ? a.k + t * a.k_stride + (h - a.Hq) * D
                                      : a.v + t * a.v_stride + (h - v0) * D;
-      const bool there = grp < g1 && h < H && (h < HK || h >= v0);
+      const bool there = grp < g1 && h < H && (FMT == ROPE_BF16 || h < HK || h >= v0);
       if (FMT == ROPE_NVFP4 && PIECES && h >= v0)  // (see the keys' exchange below)
         return there ? *reinterpret_cast<const uint4 *>(row + l * 8) : make_uint4(0, 0, 0, 0);
       return there ? load8(row) : make_uint4(0, 0, 0, 0);
@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
       si[0] = s.x, si[1] = s.y, si[2] = s.z, si[3] = s.w;
     }
     // norm and rotation of one lane's values of a row (all lanes of the warp; sums: some row has a norm;
-    // norm: this row has one)
-    auto turn = [&](float (&x)[8], bool sums, uint4 weight, bool norm) {
+    // norm, on: this row has one, is turned)
+    auto turn = [&](float (&x)[8], bool sums, uint4 weight, bool norm, bool on) {
       if (sums) {
         float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
           }
         }
       }
-      if (turned) {
+      if (on && turned) {
         if constexpr (IL) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
           if (grp + i >= g1) break;
           float x[8];
           unpack8(cur[i], x);
-          turn(x, norm_q, wq, norm_q);
+          turn(x, norm_q, wq, norm_q, true);
           store8(a.q_out + ((size_t)t * a.Hq + (grp + i) * HPG + g) * D, pack8(x));
         }
         continue;
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
 #pragma unroll 1
       for (int i = 0; i < AHEAD && grp + i < g1; ++i) {
         const int h = (grp + i) * HPG + g, hw = h - g;  // hw: the warp's first row
-        const bool is_v = hw >= v0, is_q = h < a.Hq;
+        const bool is_v = (FMT == ROPE_BF16 ? h : hw) >= v0, is_q = h < a.Hq;
         float x[8];
         unpack8(cur[0], x);
 #pragma unroll
@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
           float y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = x[e];
-          turn(y, norm_q || norm_k, is_q ? wq : wk, is_q ? norm_q : norm_k);
+          const bool still = FMT == ROPE_BF16 && is_v;  // (a value beside a key)
+          turn(y, norm_q || norm_k, is_q ? wq : wk, is_q ? norm_q : norm_k && !still, !still);
           if (FMT == ROPE_BF16 || is_q) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = y[e];
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
         if (is_q) store8(a.q_out + ((size_t)t * a.Hq + h) * D, pack8(x));
         if (hw + HPG <= a.Hq) continue;
         // some row of the warp goes into a pool
-        const bool store = !is_q && h < H && (h < HK || is_v);
+        const bool store = !is_q && h < H && (FMT == ROPE_BF16 || h < HK || is_v);
         uint8_t *pool = is_v ? a.v_pool : a.k_pool;
         const size_t row = (size_t)slot * a.Hkv + (is_v ? h - v0 : h - a.Hq);
         if constexpr (FMT == ROPE_BF16) {
@@ -399,9 +400,9 @@ cudaError_t launch_rope(RopeArgs &a, cudaStream_t stream) {
   constexpr auto kernel = qk_norm_rope_write_kernel<D, FMT, IL>;
   const int wave = wave_blocks<kernel>();
   if (wave <= 0) return cudaErrorUnknown;
-  // A group's rows are values or are not: the values' codes are the plain write's, their quotients formed as there.
-  a.v0 = (a.Hq + a.Hkv + HPG - 1) / HPG * HPG;
-  a.groups = a.v0 / HPG + (a.Hkv + HPG - 1) / HPG;
+  // Into codes a group's rows are all values or none is: the values' quotients are formed as the plain write's.
+  a.v0 = FMT == ROPE_BF16 ? a.Hq + a.Hkv : (a.Hq + a.Hkv + HPG - 1) / HPG * HPG;
+  a.groups = (a.v0 + a.Hkv + HPG - 1) / HPG;
   // Segments per token, by the time of the longest warp: rounds of (token, segment) pairs, each the segment's
   // groups and a start (position, slot, angles and first rows from memory) worth about four of them.  (One
   // group a segment everywhere takes 117 us where this takes 65, 8192 tokens of 64 + 8 + 8 heads of 128.)
