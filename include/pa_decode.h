@@ -394,7 +394,8 @@ int pa_mla_cache_write(const void *c_lat, const void *k_rope, const int64_t *slo
  *   context_lens_out, held_pages_out [batch] int32, free_count_out [1] int32: the
  *                state after the step.  Each may be its input itself (updated in
  *                place); any other overlap is refused
- *   query_start  [batch + 1] int32: row b's tokens are [query_start[b], query_start[b + 1])
+ *   query_start  [batch + 1] int32: row b's tokens are [query_start[b], query_start[b + 1]);
+ *                a sum past 2^31 - 1 stays there (such rows are refused)
  *   slot_mapping [max_tokens] int64: page * page_size + offset of each token, -1 for
  *                tokens of refused rows and behind the last row
  *   positions    [max_tokens] int32: context_lens[b] + i, or context_lens[b] + depth under
@@ -403,7 +404,8 @@ int pa_mla_cache_write(const void *c_lat, const void *k_rope, const int64_t *slo
  *                token's mask is set if token j of its row is itself or one of its
  *                ancestors; 0 behind the last row.  A row of more than 64 new tokens
  *                is a chain: its parents are not read and its masks are 0
- * Row b needs max(0, ceil((context + new) / page_size) - held) pages.  The rows take
+ * Row b needs max(0, ceil((context + new) / page_size) - held) pages, new tokens or not.
+ * The rows take
  * them in row order from the top of the stack; a row that needs any and whose
  * running sum of needs passes the pages there are gets none, and neither do the
  * rows behind it that need some.  Such a row is refused: PA_DEV_NO_PAGES is set in
@@ -607,8 +609,9 @@ size_t pa_tree_workspace_size(int batch, int max_query, int num_q_heads, int num
  * Token L - n_b + i of every layer gets the rows of node accepted[b][i].  The pages
  * that the rejected nodes filled stay the row's (pa_plan_step takes them up).  A
  * path that is not ascending within [0, n_b) is cut before its first bad entry and
- * sets PA_DEV_BAD_TREE; lengths out of range set PA_DEV_BAD_LEN and move nothing; a
- * page outside [0, num_pages) sets PA_DEV_BAD_PAGE and that row is not moved.
+ * sets PA_DEV_BAD_TREE; lengths out of range set PA_DEV_BAD_LEN, move nothing and leave
+ * the row's length; a node whose page, or whose place's, is outside [0, num_pages)
+ * sets PA_DEV_BAD_PAGE and is not moved (the length counts it all the same).
  * max_accepted in [1, 64]; batch up to 65535; max_pages_per_seq * page_size below
  * 2^31; status a device word or NULL.
  */

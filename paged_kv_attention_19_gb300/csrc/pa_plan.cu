@@ -182,8 +182,9 @@ __device__ __forceinline__ void plan_state_all_granted(const PlanArgs &a, const 
 // independent: each has all rows' sums, writes its share of the rows' table entries and of the tokens, and reads of
 // the table and the list what no CTA writes.  Only state that is updated in place makes them meet: with few CTAs
 // (PLAN_CLUSTER) at a barrier of the one cluster that they form, when all have read all of their inputs, with many
-// (PLAN_AFTER) in a launch of its own behind this one.  48 rows of trees: 4.8 us; 512 rows of 1 to 1024 tokens: 5.9 us
-// (one cluster of eight CTAs for those, waiting for one another's sums: 38 us).
+// (PLAN_AFTER) in a launch of its own behind this one.  48 rows of trees: 4.9 us; 512 rows of 1 to 1024 tokens: 6.0 us
+// (one cluster of eight CTAs for those, waiting for one another's sums: 38 us); in place the first 0.4 us more, the second,
+// with its second launch, 2.2.
 enum PlanMode { PLAN_APART = 0, PLAN_CLUSTER = 1, PLAN_AFTER = 2 };
 template <int MODE>
 __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs a) {

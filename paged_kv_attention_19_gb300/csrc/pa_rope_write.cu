@@ -12,8 +12,8 @@
 // time (a group): the token's position, slot and angles are loaded once for the segment, and the next three
 // groups' loads are in flight while three are worked on (two, or four, with as many blocks on an SM as the
 // registers allow: 5 to 11% slower).  The warps of one wave stride over the (token,
-// segment) pairs.  8192 tokens of 64 + 8 + 8 heads of 128 into FP8: 68 us, 4.8 TB/s of reads and writes mixed, at
-// over 60% of the issue slots; 61 tokens of 32 + 8 + 8: 2.4 us in a graph, a launch.
+// segment) pairs.  8192 tokens of 64 + 8 + 8 heads of 128 into FP8: 67 us, 4.8 TB/s of reads and writes mixed, at
+// 65% of the issue slots; 61 tokens of 32 + 8 + 8: 2.4 us in a graph, a launch.
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_write_kernel(con
     // A key as the quotient by its pool's scale, (x w cos - x' w' sin) (1 / (rms scale)): a step of a code is a sixteenth of
     // the value, so a key beside the middle of two codes goes by its last bits, and fewer roundings put fewer of them on
     // the wrong side: x w is exact, the factor is a pair of floats, a product's rounding is made good.  (Of 50 million keys 21
-    // codes are not those of 64 bits, 94 with norm, rotation and division one after the other, for 68 us instead of 63.)
+    // codes are not those of 64 bits, 94 with norm, rotation and division one after the other; that cost 63 -> 68 us.)
     auto turn_quot = [&](float (&x)[8], bool norm) {
       const float2 inv = a.k_inv;
       float2 f = inv;
