@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_state_kernel(const PlanArgs
 // order, eight loads in flight (sixteen: 14.0 us for 12.2, fewer threads fit an SM).  A node's target lies
 // at or before its source and behind every earlier source, so no source is overwritten before it is read.
 // Bound by memory and, before it, by two dependent trips (lengths and path, pages): 48 FP8 layers of 64 rows,
-// 9 nodes of 63 each, 12.2 us (4.0 TB/s read and written); one layer 2.5 us in a graph.
+// 9 nodes of 63 each, 11.8 us (4.2 TB/s read and written); one layer 2.4 us in a graph.
 constexpr int kCompactThreads = 256;
 
 struct CompactArgs {

@@ -45,7 +45,7 @@
 // loops over the products' instructions are not unrolled (32 ragged trees of up to 16 nodes x 8 heads over 128 to
 // 16384 tokens, 8 key heads of 128: with these steps FP8 137 -> 111 us, NVFP4 134 -> 104, bf16 107 -> 99).
 // Measured (GB300; bytes: the cache once): a request of 8 nodes x 32 heads over 1000 tokens 13.6 us, start-up and the
-// combine kernel's trips; 16 rows of 64 nodes x 64 heads over 1024 to 8192 tokens 129 us, 897 TFLOP/s, the score
+// combine kernel's trips; 16 rows of 64 nodes x 64 heads over 1024 to 8192 tokens 126 to 129 us, 900 to 920 TFLOP/s, the score
 // products of N = 64; 16 windowed rows at head_dim 256 57 us, 4.4 TB/s; the ragged trees above 109 us over FP8 (2.1 TB/s
 // of codes) and 105 over NVFP4 (1.4 TB/s), the chain from conversion to weights.
 // Tensor memory: score buffer b (the weights over its first half) at 64 b, outputs at 256.  At head_dim 256 one
