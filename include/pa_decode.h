@@ -24,6 +24,13 @@
  *                           and its own ancestors
  *   pa_kv_compact           moves an accepted path's keys and values together
  *
+ * and long streams in bounded memory:
+ *
+ *   pa_stream_gqa (_fp8, _nvfp4)
+ *                           attention of each row's newest tokens -- one, a chunk or a whole
+ *                           prompt -- to the most recent tokens and the row's first ones
+ *   pa_release_pages        gives back the pages that the window has left behind
+ *
  * The operations are the ones the following pages describe:
  *   - paged cache: K/V pools [pages, block_size, Hkv, D], per-request
  *     seq_lens, and a block table (vllm.cpp kernel-matrix, rows
@@ -625,6 +632,105 @@ int pa_kv_compact_granted(void *k_pool, void *v_pool, const int32_t *block_table
                           const int32_t *granted, int32_t *context_lens_out, int num_layers, int batch,
                           int max_accepted, int token_bytes, int page_size, int num_pages,
                           int max_pages_per_seq, uint32_t *status, cudaStream_t stream);
+
+/*
+ * Attention of each row's newest tokens over its paged cache: single tokens, chunks of prompts and
+ * whole prompts, mixed as a step has them, under an optional window beside which the row's
+ * first tokens stay visible.
+ *   q            [num_tokens, num_q_heads, head_dim] bf16: the rows' new tokens one row after the
+ *                other
+ *   query_start  [batch + 1] int32: row b's are tokens [query_start[b], query_start[b + 1]), n_b of them,
+ *                0 <= n_b <= max_query (0: the row has no query in this step)
+ *   context_lens [batch] int32: L, the row's tokens including its n_b new ones, which are in the
+ *                cache already
+ *   granted      [batch] int32 or NULL (pa_plan_step_granted's): a row with 0 is left out, its lengths
+ *                are not looked at and its outputs stay as they were
+ *   out          [num_tokens, num_q_heads, head_dim] bf16 (written for the rows' tokens; tokens
+ *                behind the last row are left as they were)
+ *   lse          [num_tokens, num_q_heads] fp32 (written likewise), or NULL
+ *   window       <= 0: none.  Else the token at position p attends to positions (p - window, p]
+ *   first        >= 0: and, under a window, to those of [0, first) that are not behind it
+ * New token i of a row is at position p = L - n_b + i and attends to the positions t <= p that the window and
+ * `first` leave.  Its result does not depend on keys and values that it does not attend to, infinities
+ * and NaN among them, nor on table entries of pages that none of the row's new tokens sees
+ * (pa_release_pages's).  One new token a row gives pa_decode_gqa's results within rounding (first 0).
+ * max_query in [1, 2^30]: the bound of n_b that the tiles and the workspace are made for;
+ * max_context_len up to 2^31 - 513, at most 128 query heads a key head (more: PA_ERR_UNSUPPORTED).
+ * Rows whose query_start is not ascending within [0, num_tokens], has more than max_query tokens, or
+ * whose L is below n_b or out of range set PA_DEV_BAD_LEN and have unspecified results.  The other
+ * arguments and the error codes are those of pa_verify_gqa; the workspace is
+ * pa_stream_workspace_size bytes, and its status word is read by pa_read_device_status.  For a fixed
+ * num_splits results are bitwise reproducible and independent of the physical page order.
+ * batch == 0 or num_tokens == 0 is a no-op (the status word stays as it was).
+ * bf16 pools: products of bf16 operands, weights rounded to bf16.  FP8 and NVFP4 pools: codes as
+ * exact f16 values, a query row scaled by a power of two to f16, weights rounded to f16.  The calls
+ * always use the default wait limit.  num_splits == 0: no share is made for less than 128 tokens' work.
+ */
+int pa_stream_gqa(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+                  const int32_t *context_lens, const int32_t *query_start, const int32_t *granted, void *out,
+                  float *lse, int batch, int num_tokens, int max_query, int num_q_heads, int num_kv_heads,
+                  int head_dim, int page_size, int num_pages, int max_pages_per_seq, int max_context_len,
+                  float scale, int window, int first, int num_splits, void *workspace, size_t workspace_bytes,
+                  cudaStream_t stream);
+
+/* The same over FP8 E4M3 pools (the layout of pa_decode_gqa_fp8); head_dim in {64, 128, 256}. */
+int pa_stream_gqa_fp8(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+                      const int32_t *context_lens, const int32_t *query_start, const int32_t *granted, void *out,
+                      float *lse, int batch, int num_tokens, int max_query, int num_q_heads, int num_kv_heads,
+                      int head_dim, int page_size, int num_pages, int max_pages_per_seq, int max_context_len,
+                      float scale, float k_scale, float v_scale, int window, int first, int num_splits,
+                      void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* The same over NVFP4 pools (the layout of pa_decode_gqa_nvfp4). */
+int pa_stream_gqa_nvfp4(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+                        const int32_t *context_lens, const int32_t *query_start, const int32_t *granted, void *out,
+                        float *lse, int batch, int num_tokens, int max_query, int num_q_heads, int num_kv_heads,
+                        int head_dim, int page_size, int num_pages, int max_pages_per_seq, int max_context_len,
+                        float scale, float k_scale, float v_scale, int window, int first, int num_splits,
+                        void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Bytes of device workspace a pa_stream_gqa call (of any cache format) with these arguments needs; 0 for
+ * arguments that the call would reject.
+ */
+size_t pa_stream_workspace_size(int batch, int max_query, int num_q_heads, int num_kv_heads, int head_dim,
+                                int max_context_len, int page_size, int num_splits);
+
+/*
+ * Gives back the pages that a window has left behind, so that a row of any length holds the pages of its
+ * first tokens and of its window only.  A later token of row b is at position context_lens[b] or behind it and
+ * sees no position below context_lens[b] + 1 - window but those of [0, first).
+ *   context_lens [batch] int32: tokens that row b holds in the cache, >= 0
+ *   held_pages   [batch] int32: pages that the row's table names, released ones among them
+ *                (pa_plan_step's count: it goes on as if nothing had been released)
+ *   window_start [batch] int32: the row's pages in [F, window_start[b]) have been given back, where
+ *                F = ceil(first / page_size); 0 for a new row.  The caller keeps it from step to step
+ *   ended        [batch] int32 or NULL: a row with a value other than 0 has ended and gives back all the pages
+ *                that it has left.  (pa_plan_step's new_lens of -1 would give back entries that are no pages
+ *                any more: rows that have released pages end here)
+ *   free_list    [num_pages] int32: a stack of free pages, of which free_count[0] are valid: the
+ *                pages are pushed in row order, a row's in ascending order
+ *   block_table  [batch, max_pages_per_seq] int32
+ *   window_start_out  max(window_start, E) where E, the pages wholly behind the window,
+ *                floor(max(0, context_lens + 1 - window) / page_size) and at most held_pages, is above F; 0
+ *                for an ended row
+ *   context_lens_out, held_pages_out: the inputs, 0 for an ended row
+ *   block_table_out   gets -1 in the entries of the pages that this call gives back; nothing else in it
+ *                is written
+ * Each of the five _out arrays may be its input itself (updated in place); any other overlap is refused.
+ * A row whose context_lens or window_start is negative, whose held_pages is outside [0, max_pages_per_seq] or
+ * whose window_start is above held_pages sets PA_DEV_BAD_LEN in *status (a device word or NULL) and is left as it
+ * is.  A released entry outside [0, num_pages) sets PA_DEV_BAD_PAGE and is pushed as it is; pages past
+ * the list's num_pages entries are lost and set PA_DEV_BAD_LEN, as does a free_count outside
+ * [0, num_pages].  window >= 1, first >= 0; batch in [0, 8192], max_pages_per_seq * page_size and * batch
+ * below 2^31 (more: PA_ERR_UNSUPPORTED).  batch == 0 writes free_count_out.
+ */
+int pa_release_pages(const int32_t *context_lens, const int32_t *held_pages, const int32_t *window_start,
+                     const int32_t *ended, int32_t *free_list, const int32_t *free_count,
+                     const int32_t *block_table, int32_t *context_lens_out, int32_t *held_pages_out,
+                     int32_t *window_start_out, int32_t *free_count_out, int32_t *block_table_out, int batch,
+                     int page_size, int num_pages, int max_pages_per_seq, int window, int first, uint32_t *status,
+                     cudaStream_t stream);
 
 /* Static text for a pa_status value (never NULL). */
 const char *pa_status_string(int status);

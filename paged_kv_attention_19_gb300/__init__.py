@@ -9,10 +9,11 @@ Names follow the C ABI: ``pa_workspace_size``, ``pa_decode_gqa``,
 ``pa_decode_mla_absorbed``, ``pa_verify_gqa``, ``pa_decode_gqa_fp8``, ``pa_decode_gqa_nvfp4``,
 ``pa_decode_gqa_noalloc``, ``pa_kv_write``, ``pa_kv_write_fp8``, ``pa_kv_write_nvfp4``, ``pa_mla_cache_write``, ``pa_plan_step``,
 ``pa_qk_norm_rope_write``, ``pa_qk_norm_rope_write_fp8``, ``pa_qk_norm_rope_write_nvfp4``, ``pa_tree_gqa``, ``pa_tree_gqa_fp8``,
-``pa_tree_gqa_nvfp4``, ``pa_tree_workspace_size``, ``pa_kv_compact`` (the C ABI's ``_granted`` forms are
+``pa_tree_gqa_nvfp4``, ``pa_tree_workspace_size``, ``pa_kv_compact``, ``pa_stream_gqa``, ``pa_stream_gqa_fp8``,
+``pa_stream_gqa_nvfp4``, ``pa_stream_workspace_size``, ``pa_release_pages`` (the C ABI's ``_granted`` forms are
 reached by the ``granted`` argument), ``pa_status_string``, ``pa_read_device_status``,
 ``pa_set_profile_events``, ``pa_last_launch_count``, ``pa_set_wait_limit_ns``, ``pa_last_cuda_error``,
-``pa_last_cuda_error_string``.  The operators of tree drafting are called through a compiled module that
+``pa_last_cuda_error_string``.  The operators of tree drafting and of streams are called through a compiled module that
 checks their tensors (``csrc/pa_binding.cpp``).  The tensor-taking
 functions accept torch tensors (device memory, the layouts of the header) and
 infer every size from their shapes.
@@ -75,6 +76,11 @@ SIGNATURES = {
     "pa_tree_gqa_nvfp4_granted": (_I, [_P] * 10 + [_I] * 10 + [_F, _F, _F, _I, _I, _P, _Z, _P]),
     "pa_kv_compact": (_I, [_P] * 8 + [_I] * 7 + [_P, _P]),
     "pa_kv_compact_granted": (_I, [_P] * 9 + [_I] * 7 + [_P, _P]),
+    "pa_stream_workspace_size": (_Z, [_I] * 8),
+    "pa_stream_gqa": (_I, [_P] * 9 + [_I] * 10 + [_F, _I, _I, _I, _P, _Z, _P]),
+    "pa_stream_gqa_fp8": (_I, [_P] * 9 + [_I] * 10 + [_F, _F, _F, _I, _I, _I, _P, _Z, _P]),
+    "pa_stream_gqa_nvfp4": (_I, [_P] * 9 + [_I] * 10 + [_F, _F, _F, _I, _I, _I, _P, _Z, _P]),
+    "pa_release_pages": (_I, [_P] * 12 + [_I] * 6 + [_P, _P]),
     "pa_status_string": (ctypes.c_char_p, [_I]),
     "pa_read_device_status": (_I, [_P, _P, _U32P]),
     "pa_set_profile_events": (_I, [_P, _P]),
@@ -417,6 +423,65 @@ def pa_kv_compact(k_pool, v_pool, block_table, context_lens, query_start, accept
         status, stream))
 
 
+def pa_stream_workspace_size(batch: int, max_query: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                             max_context_len: int, page_size: int, num_splits: int = 0) -> int:
+    return int(lib.pa_stream_workspace_size(batch, max_query, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                                            page_size, num_splits))
+
+
+def pa_stream_gqa(q, k_pool, v_pool, block_table, context_lens, query_start, out, lse=None, *, max_query: int,
+                  scale: float, workspace, window: int = 0, first: int = 0, granted=None, num_splits: int = 0,
+                  max_context_len=None, stream=None) -> None:
+    """Attention of each row's newest tokens: single tokens, chunks of prompts, whole prompts.  q [T, Hq, D]
+    bf16: the rows' new tokens one row after the other, row b's from query_start[b] to query_start[b + 1]
+    ([B + 1] int32, at most max_query of them); context_lens [B] int32 count them; out [T, Hq, D] bf16 and lse
+    [T, Hq] fp32 or None (tokens behind the last row stay as they were); pools and block_table as for
+    pa_decode_gqa.  The token at position p attends to those of [0, p]; under a window (> 0) to the `window` most
+    recent ones and the row's `first` ones.  workspace: workspace_for_stream(...).  granted: optional [B] int32
+    (pa_plan_step's); a row with 0 is left out and its outputs stay as they were."""
+    _done("pa_stream_gqa", (_native_module or _native()).stream_gqa(
+        0, q, k_pool, v_pool, block_table, context_lens, query_start, out, lse, granted, workspace, max_query, scale,
+        1.0, 1.0, window, first, num_splits, max_context_len, stream))
+
+
+def pa_stream_gqa_fp8(q, k_pool, v_pool, block_table, context_lens, query_start, out, lse=None, *, max_query: int,
+                      scale: float, k_scale: float, v_scale: float, workspace, window: int = 0, first: int = 0,
+                      granted=None, num_splits: int = 0, max_context_len=None, stream=None) -> None:
+    """The same over FP8 E4M3 pools [pages, P, Hkv, D] uint8."""
+    _done("pa_stream_gqa_fp8", (_native_module or _native()).stream_gqa(
+        1, q, k_pool, v_pool, block_table, context_lens, query_start, out, lse, granted, workspace, max_query, scale,
+        k_scale, v_scale, window, first, num_splits, max_context_len, stream))
+
+
+def pa_stream_gqa_nvfp4(q, k_pool, v_pool, block_table, context_lens, query_start, out, lse=None, *, max_query: int,
+                        scale: float, k_scale: float, v_scale: float, workspace, window: int = 0, first: int = 0,
+                        granted=None, num_splits: int = 0, max_context_len=None, stream=None) -> None:
+    """The same over NVFP4 pools [pages, P, Hkv, nvfp4_row_bytes(D)] uint8."""
+    _done("pa_stream_gqa_nvfp4", (_native_module or _native()).stream_gqa(
+        2, q, k_pool, v_pool, block_table, context_lens, query_start, out, lse, granted, workspace, max_query, scale,
+        k_scale, v_scale, window, first, num_splits, max_context_len, stream))
+
+
+def pa_release_pages(context_lens, held_pages, window_start, free_list, free_count, block_table, *, page_size: int,
+                     window: int, first: int = 0, ended=None, context_lens_out=None, held_pages_out=None,
+                     window_start_out=None, free_count_out=None, block_table_out=None, status=None,
+                     stream=None) -> None:
+    """Gives back the pages that no later token sees: those wholly behind the window, but for the pages of the
+    row's `first` tokens.  context_lens, held_pages (pa_plan_step's) and window_start [B] int32: a row's pages in
+    [ceil(first / page_size), window_start) are gone already (0 for a new row; kept by the caller from step to
+    step); free_list [num_pages] int32, a stack of which free_count [1] int32 entries are valid, gets the pages;
+    block_table [B, max_pages] int32 gets -1 in their entries.  ended: optional [B] int32, not 0 for a row
+    that gives back all it has left (a row that has released pages ends here, not by pa_plan_step).  The _out
+    arrays default to their inputs (updated in place).  status: optional int32 device word for PA_DEV_* bits."""
+    _done("pa_release_pages", (_native_module or _native()).release_pages(
+        context_lens, held_pages, window_start, free_list, free_count, block_table,
+        context_lens if context_lens_out is None else context_lens_out,
+        held_pages if held_pages_out is None else held_pages_out,
+        window_start if window_start_out is None else window_start_out,
+        free_count if free_count_out is None else free_count_out,
+        block_table if block_table_out is None else block_table_out, ended, status, page_size, window, first, stream))
+
+
 def pa_read_device_status(workspace, stream=None) -> int:
     bits = ctypes.c_uint32(0)
     _check(lib.pa_read_device_status(_ptr(workspace), _stream(stream), ctypes.byref(bits)),
@@ -484,4 +549,16 @@ def workspace_for_tree(q, k_pool, block_table, max_query: int, num_splits: int =
     n = pa_tree_workspace_size(block_table.shape[0], max_query, Hq, Hkv, D, mcl, P, num_splits)
     if n == 0:
         raise PaError(PA_ERR_INVALID_ARGUMENT, "pa_tree_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device or q.device)
+
+
+def workspace_for_stream(q, k_pool, block_table, max_query: int, num_splits: int = 0, max_context_len=None, device=None):
+    """Allocate a uint8 device workspace sized for a pa_stream_gqa call (of any cache format) with these tensors."""
+    import torch
+    Hq, D = q.shape[-2], q.shape[-1]
+    P, Hkv = k_pool.shape[-3], k_pool.shape[-2]
+    mcl = block_table.shape[1] * P if max_context_len is None else max_context_len
+    n = pa_stream_workspace_size(block_table.shape[0], max_query, Hq, Hkv, D, mcl, P, num_splits)
+    if n == 0:
+        raise PaError(PA_ERR_INVALID_ARGUMENT, "pa_stream_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=device or q.device)

@@ -1,4 +1,4 @@
-// pa_binding.cpp -- the Python calls of the tree-drafting operators: checks of the tensors (type, shape,
+// pa_binding.cpp -- the Python calls of the tree-drafting and streaming operators: checks of the tensors (type, shape,
 // strides, device), then the C ABI on the tensors' device and stream.  In C++ because a step makes these
 // calls often and small: the checks take about a microsecond here and ten or more in Python.
 //
@@ -175,6 +175,14 @@ const at::Tensor &peek(PyObject *const *v, Py_ssize_t count, Py_ssize_t i, const
 
 int64_t row_width(int fmt, int64_t D) { return fmt == 2 ? (D / 2 + D / 16 + 15) / 16 * 16 : D; }
 
+// max_context_len: given, or what a row of the block table can hold.
+int longest(Args &a, int64_t W, int64_t P) {
+  if (!a.none()) return a.integer("max_context_len");
+  a.skip();
+  if (W * P > INT_MAX) refuse("block_table names more than 2^31 - 1 tokens a row: give max_context_len");
+  return (int)(W * P);
+}
+
 template <typename F>
 PyObject *guarded(F f) {
   try {
@@ -275,14 +283,7 @@ PyObject *tree_gqa(PyObject *, PyObject *const *v, Py_ssize_t count) {
     const int mq = a.integer("max_query");
     const float scale = a.real("scale"), ks = a.real("k_scale"), vs = a.real("v_scale");
     const int window = a.integer("window"), splits = a.integer("num_splits");
-    int most = 0;
-    if (a.none()) {
-      a.skip();
-      if (W * P > INT_MAX) refuse("block_table names more than 2^31 - 1 tokens a row: give max_context_len");
-      most = (int)(W * P);
-    } else {
-      most = a.integer("max_context_len");
-    }
+    const int most = longest(a, W, P);
     void *w = ws.data_ptr();
     const size_t wn = ws.nbytes();
     return a.launch([&](cudaStream_t s) {
@@ -331,9 +332,71 @@ PyObject *kv_compact(PyObject *, PyObject *const *v, Py_ssize_t count) {
   });
 }
 
+PyObject *stream_gqa(PyObject *, PyObject *const *v, Py_ssize_t count) {
+  return guarded([&] {
+    Args a(v, count, 20);
+    const int fmt = a.integer("format");
+    const at::Tensor &q0 = peek(v, count, 1, "q", 3), &kp0 = peek(v, count, 2, "k_pool", 4), &bt0 = peek(v, count, 4, "block_table", 2);
+    const int64_t T = q0.size(0), Hq = q0.size(1), D = q0.size(2), N = kp0.size(0), P = kp0.size(1), Hkv = kp0.size(2);
+    const int64_t B = bt0.size(0), W = bt0.size(1), R = row_width(fmt, D);
+    const at::ScalarType kind = fmt == 0 ? at::kBFloat16 : at::kByte;
+    const void *q = a.array("q", at::kBFloat16, {T, Hq, D});
+    const void *kp = a.array("k_pool", kind, {N, P, Hkv, R});
+    const void *vp = a.array("v_pool", kind, {N, P, Hkv, R});
+    auto *bt = (const int32_t *)a.array("block_table", at::kInt, {B, W});
+    auto *lens = (const int32_t *)a.array("context_lens", at::kInt, {B});
+    auto *start = (const int32_t *)a.array("query_start", at::kInt, {B + 1});
+    void *out = a.array("out", at::kBFloat16, {T, Hq, D});
+    auto *lse = (float *)a.optional("lse", at::kFloat, {T, Hq});
+    auto *granted = (const int32_t *)a.optional("granted", at::kInt, {B});
+    const at::Tensor &ws = a.tensor("workspace");
+    if (!ws.is_contiguous() || ws.device() != a.device()) refuse("workspace has to be a dense tensor on ", a.device().str());
+    const int mq = a.integer("max_query");
+    const float scale = a.real("scale"), ks = a.real("k_scale"), vs = a.real("v_scale");
+    const int window = a.integer("window"), first = a.integer("first"), splits = a.integer("num_splits");
+    const int most = longest(a, W, P);
+    void *w = ws.data_ptr();
+    const size_t wn = ws.nbytes();
+    return a.launch([&](cudaStream_t s) {
+      if (fmt == 0)
+        return pa_stream_gqa(q, kp, vp, bt, lens, start, granted, out, lse, (int)B, (int)T, mq, (int)Hq, (int)Hkv, (int)D,
+                             (int)P, (int)N, (int)W, most, scale, window, first, splits, w, wn, s);
+      auto *f = fmt == 1 ? pa_stream_gqa_fp8 : pa_stream_gqa_nvfp4;
+      return f(q, kp, vp, bt, lens, start, granted, out, lse, (int)B, (int)T, mq, (int)Hq, (int)Hkv, (int)D, (int)P, (int)N,
+               (int)W, most, scale, ks, vs, window, first, splits, w, wn, s);
+    });
+  });
+}
+
+PyObject *release_pages(PyObject *, PyObject *const *v, Py_ssize_t count) {
+  return guarded([&] {
+    Args a(v, count, 17);
+    const int64_t B = peek(v, count, 0, "context_lens", 1).size(0), N = peek(v, count, 3, "free_list", 1).size(0),
+                  W = peek(v, count, 5, "block_table", 2).size(1);
+    auto *lens = (const int32_t *)a.array("context_lens", at::kInt, {B});
+    auto *held = (const int32_t *)a.array("held_pages", at::kInt, {B});
+    auto *from = (const int32_t *)a.array("window_start", at::kInt, {B});
+    auto *list = (int32_t *)a.array("free_list", at::kInt, {N});
+    auto *n_free = (const int32_t *)a.array("free_count", at::kInt, {1});
+    auto *table = (const int32_t *)a.array("block_table", at::kInt, {B, W});
+    auto *lens_out = (int32_t *)a.array("context_lens_out", at::kInt, {B});
+    auto *held_out = (int32_t *)a.array("held_pages_out", at::kInt, {B});
+    auto *from_out = (int32_t *)a.array("window_start_out", at::kInt, {B});
+    auto *free_out = (int32_t *)a.array("free_count_out", at::kInt, {1});
+    auto *table_out = (int32_t *)a.array("block_table_out", at::kInt, {B, W});
+    auto *ended = (const int32_t *)a.optional("ended", at::kInt, {B});
+    auto *status = (uint32_t *)a.optional("status", at::kInt, {1});
+    const int page = a.integer("page_size"), window = a.integer("window"), first = a.integer("first");
+    return a.launch([&](cudaStream_t s) {
+      return pa_release_pages(lens, held, from, ended, list, n_free, table, lens_out, held_out, from_out, free_out, table_out,
+                              (int)B, page, (int)N, (int)W, window, first, status, s);
+    });
+  });
+}
+
 #define PA_FUNCTION(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef functions[] = {PA_FUNCTION(plan_step), PA_FUNCTION(qk_norm_rope_write), PA_FUNCTION(tree_gqa),
-                           PA_FUNCTION(kv_compact), {nullptr, nullptr, 0, nullptr}};
+                           PA_FUNCTION(kv_compact), PA_FUNCTION(stream_gqa), PA_FUNCTION(release_pages), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "pa_binding", "Tensor checks and calls of the C ABI.", -1, functions,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -5,6 +5,7 @@
 
 #include "pa_common.cuh"
 #include "pa_decode.h"
+#include "pa_host.h"
 #include "pa_launch.h"
 
 namespace pa {
@@ -382,34 +383,6 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const Compa
     for (int u = 0; u < U; ++u)
       if (i0 + u < m && src[i0 + u] >= 0) pool[dst[i0 + u] * a.vecs] = x[u];
   }
-}
-
-bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-
-// Do [p, p + np) and [q, q + nq) share a byte?
-bool overlap(const void *p, size_t np, const void *q, size_t nq) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + nq && b < a + np;
-}
-
-template <typename Args>
-cudaError_t launch(void (*kernel)(Args), dim3 grid, int threads, size_t smem, int cluster, const Args &a,
-                   cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace

@@ -3,11 +3,9 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
-#include <mutex>
-
-#include <cudaTypedefs.h>
 
 #include "pa_decode.h"
+#include "pa_host.h"
 #include "pa_launch.h"
 #include "pa_tree_launch.cuh"
 
@@ -26,15 +24,6 @@ constexpr int kMinShare = 128;
 
 // Longest context: the ends of the stages behind it, two of 64 tokens, are still tokens below 2^31.
 constexpr int kMaxContext = INT_MAX - 128;
-
-bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
-int ilog2(int x) {
-  int l = 0;
-  while ((1 << l) < x) ++l;
-  return l;
-}
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // How a call's query rows are tiled, and where its workspace's parts lie.
 struct TreePlan {
@@ -68,43 +57,6 @@ int tree_plan(int batch, int max_query, int Hq, int Hkv, int D, int max_ctx, int
   off = round_up(off + np * 2 * kTreeRows * sizeof(TreeHalf), 256);
   pl->total = off;
   return PA_OK;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
-// A dense map of RANK dimensions (the first one contiguous): bf16 values with the 128-byte swizzle, or bytes.
-template <int RANK>
-bool encode_map(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[RANK], const cuuint32_t (&box)[RANK], bool bytes) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t strides[RANK - 1], s = bytes ? 1 : 2;
-  cuuint32_t ones[RANK];
-  for (int i = 0; i < RANK; ++i) {
-    ones[i] = 1u;
-    if (i < RANK - 1) strides[i] = s = s * dims[i];
-  }
-  return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, RANK, const_cast<void *>(base),
-            dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return -1;
-  return n;
 }
 
 int tree_call(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
