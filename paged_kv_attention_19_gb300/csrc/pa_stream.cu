@@ -7,19 +7,26 @@
 #include "pa_decode.h"
 #include "pa_host.h"
 #include "pa_launch.h"
-#include "pa_stream.cuh"
-#include "pa_tree_launch.cuh"
+#include "pa_stream_launch.cuh"
 
 namespace pa {
 
 namespace {
 
-constexpr int kMaxSplits = 4096;
+constexpr int kMaxSplits = 4096, kAutoParts = 256;
 constexpr int kMaxQuery = 1 << 30;
+// Longest context: the ends of the stages behind it, two of 128 tokens, are still tokens below 2^31.
 constexpr int kMaxContext = INT_MAX - 512;
+// Fixed cost of a piece of work in the partition, as the tokens that a CTA passes meanwhile.
+constexpr int kPieceCost = 512;
+// Least share of a CTA, in tokens, where the number of shares is left to the call: below two stages, one for each
+// softmax group, a share takes as long and only adds to what is merged.
+constexpr int kMinShare = 128;
 
+// How a call's query rows are tiled, and where its workspace's parts lie.
 struct StreamPlan {
-  size_t total;
+  int G, qt, QT, nparts_max;
+  size_t off_status, off_lse, off_o, off_half, total;
 };
 
 int stream_plan(int batch, int max_query, int Hq, int Hkv, int D, int max_ctx, int P, int num_splits, StreamPlan *pl) {
@@ -28,15 +35,22 @@ int stream_plan(int batch, int max_query, int Hq, int Hkv, int D, int max_ctx, i
   if (max_query > kMaxQuery || num_splits > kMaxSplits || (D != 64 && D != 128 && D != 256) || !is_pow2(P) || P < 8 ||
       P > 256 || max_ctx > kMaxContext || Hq / Hkv > kTreeRows)
     return PA_ERR_UNSUPPORTED;
-  pl->total = sizeof(WsHeader);
+  pl->G = Hq / Hkv;
+  pl->qt = kTreeRows / pl->G;
+  pl->QT = D <= 128 && max_query > pl->qt ? 2 : 1;
+  pl->nparts_max = num_splits > 0 ? num_splits : kAutoParts;
+  const size_t np = (size_t)pl->nparts_max, rows = np * 2 * pl->QT * kTreeRows;
+  size_t off = sizeof(WsHeader);
+  pl->off_status = off;
+  off = round_up(off + np * sizeof(uint32_t), 256);
+  pl->off_lse = off;
+  off = round_up(off + rows * sizeof(float), 256);
+  pl->off_o = off;
+  off = round_up(off + rows * D * sizeof(float), 256);
+  pl->off_half = off;
+  off = round_up(off + np * 2 * kTreeRows * sizeof(StreamHalf), 256);
+  pl->total = off;
   return PA_OK;
-}
-
-template <int D>
-cudaError_t launch_rows(int fmt, const StreamArgs &a, cudaStream_t stream) {
-  const dim3 grid((unsigned)a.tokens, (unsigned)a.Hq);
-  auto kernel = fmt == TREE_BF16 ? stream_rows_kernel<D, TREE_BF16> : fmt == TREE_FP8 ? stream_rows_kernel<D, TREE_FP8> : stream_rows_kernel<D, TREE_NVFP4>;
-  return launch_pdl(kernel, grid, 128, 0, stream, a);
 }
 
 int stream_call(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table, const int32_t *context_lens,
@@ -62,9 +76,21 @@ int stream_call(const void *q, const void *k_pool, const void *v_pool, const int
   for (const void *p : words)
     if (!aligned_to(p, 4)) return PA_ERR_MISALIGNED;
   if (workspace_bytes < pl.total) return PA_ERR_WORKSPACE_TOO_SMALL;
+  const int BN = stream_stage(fmt, pl.QT), BH = P < BN ? P : BN;  // tokens of a stage, and of a TMA box: a unit
+  const int sms = sm_count();
+  if (sms <= 0) return cuda_fail(cudaSuccess);
+  CUtensorMap tm_k, tm_v, tm_q;
+  const bool codes = fmt != TREE_BF16;
+  const int rowb = tree_row_bytes(fmt, D);
+  const cuuint64_t pool[4] = {(cuuint64_t)(codes ? rowb : D), (cuuint64_t)Hkv, (cuuint64_t)P, (cuuint64_t)num_pages};
+  const cuuint32_t pbox[4] = {codes ? (cuuint32_t)rowb : 64u, 1u, (cuuint32_t)BH, 1u};
+  const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)tokens};
+  const cuuint32_t qbox[3] = {64u, (cuuint32_t)pl.G, (cuuint32_t)(pl.qt < max_query ? pl.qt : max_query)};
+  if (!encode_map(&tm_k, k_pool, pool, pbox, codes) || !encode_map(&tm_v, v_pool, pool, pbox, codes) ||
+      !encode_map(&tm_q, q, qd, qbox, false))
+    return PA_ERR_UNSUPPORTED;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
   StreamArgs a;
-  a.q = static_cast<const uint8_t *>(q);
-  a.k_pool = static_cast<const uint8_t *>(k_pool);
   a.v_pool = static_cast<const uint8_t *>(v_pool);
   a.block_table = block_table;
   a.context_lens = context_lens;
@@ -72,27 +98,37 @@ int stream_call(const void *q, const void *k_pool, const void *v_pool, const int
   a.granted = granted;
   a.out = static_cast<uint16_t *>(out);
   a.lse = lse;
-  a.status = &static_cast<WsHeader *>(workspace)->status;
+  a.cta_status = reinterpret_cast<uint32_t *>(ws + pl.off_status);
+  a.part_lse = reinterpret_cast<float *>(ws + pl.off_lse);
+  a.part_o = reinterpret_cast<float *>(ws + pl.off_o);
+  a.halves = reinterpret_cast<StreamHalf *>(ws + pl.off_half);
   a.batch = batch;
   a.tokens = tokens;
   a.max_query = max_query;
   a.Hq = Hq;
   a.Hkv = Hkv;
-  a.G = Hq / Hkv;
+  a.G = pl.G;
+  a.qt = pl.qt;
+  a.q2 = pl.QT * pl.qt;
   a.log2_page = ilog2(P);
+  a.log2_bh = ilog2(BH);
   a.num_pages = num_pages;
   a.max_pages_per_seq = max_pages;
   a.max_context_len = max_ctx;
   a.window = window > 0 ? window : 0;
-  a.first = window > 0 ? first : 0;
-  a.scale = scale;
-  a.kscale = fmt == TREE_BF16 ? 1.f : k_scale;
-  a.vscale = fmt == TREE_BF16 ? 1.f : v_scale;
-  cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(uint32_t), stream);
+  a.first = window <= 0 ? 0 : first < max_ctx ? first : max_ctx;
+  a.piece_cost = kPieceCost;
+  a.log2_share = num_splits > 0 ? 0 : ilog2(kMinShare);
+  a.nparts = num_splits > 0 ? num_splits : sms < kAutoParts ? sms : kAutoParts;
+  a.qscale = scale * LOG2E * (codes ? k_scale : 1.f);
+  a.vscale = codes ? v_scale : 1.f;
+  uint32_t *status = &reinterpret_cast<WsHeader *>(ws)->status;
+  const StreamLaunch l = {tm_k, tm_v, tm_q, a, status, D, pl.QT};
+  const cudaError_t e = fmt == TREE_BF16  ? launch_stream_bf16(l, stream)
+                        : fmt == TREE_FP8 ? launch_stream_fp8(l, stream)
+                                          : launch_stream_nvfp4(l, stream);
   if (e != cudaSuccess) return cuda_fail(e);
-  e = D == 64 ? launch_rows<64>(fmt, a, stream) : D == 128 ? launch_rows<128>(fmt, a, stream) : launch_rows<256>(fmt, a, stream);
-  if (e != cudaSuccess) return cuda_fail(e);
-  note_launches(1);
+  note_launches(2);
   return PA_OK;
 }
 

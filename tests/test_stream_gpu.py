@@ -372,13 +372,13 @@ def test_stream_two_streams(pa):
 
 def test_stream_without_lse_and_granted(pa):
     t = Rows(96, [(300, 20), (90, 9), (500, 140)], 8, 2, 128, 16, "bf16", 100, 4)
-    want, want_l = t.check(pa)
+    want, want_l = t.check(pa, num_splits=1)  # (one share: where rows are cut depends on all of them)
     out = torch.full(t.q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
-    t.call(pa, out=out)
+    t.call(pa, out=out, num_splits=1)
     assert torch.equal(out, want)
     args = list(t.args())
     args[4] = i32([300, -5, 500])  # what a refused row's lengths say is not looked at
-    out, lse, ws = t.call(pa, args=args, granted=i32([1, 0, 7]))
+    out, lse, ws = t.call(pa, args=args, granted=i32([1, 0, 7]), num_splits=1)
     torch.cuda.synchronize()
     assert pa.pa_read_device_status(ws) == 0
     assert torch.equal(out[:20], want[:20]) and torch.equal(out[29:], want[29:]) and bool((out[20:29] == 7.0).all())
