@@ -30,7 +30,7 @@
 //     (exact; two warps K tiles, two V tiles), and the query rows, scaled by a power of two each, in place; those of
 //     the V tiles then look them over;
 //   * two groups of four warps: one thread per score row.
-// Tensor memory: scores at 0 (the weights over the first half of their buffer), outputs at 256.  At head_dim 256 one output fills
+// Tensor memory: scores at 0 (the weights over a half of their buffer), outputs at 256.  At head_dim 256 one output fills
 // the rest: one tile, one softmax group and one issuing thread.
 #pragma once
 
@@ -101,17 +101,26 @@ struct StreamCfg {
   static constexpr uint32_t IDESC_PV = tc_idesc_bf16(kTreeRows, D, true) & ~IDESC_F16;
   // the maximum is raised when it grows by more than 2^TAU; f16 weights are 2^LIFT times as large: below 2^15, and one of
   // 2^-21 of the largest still has all its bits (its step is 2^-24, so none is off by more than 2^-32 of the largest)
-  static constexpr float TAU = 8.f, LIFT = QUANT ? 7.f : 0.f;
+  static constexpr float TAU = 8.f, LIFT = QUANT ? 7.f : 0.f, WEIGHTS = QUANT ? 32768.f : 256.f;  // 2^(LIFT + TAU)
   // score buffer of item i of group (issuing thread) x, and the parity of its use
   __host__ __device__ static constexpr uint32_t buffer(int x, uint32_t i) {
     return GROUPS == 2 ? (uint32_t)x + 2 * (i % BACK) : i % BACK;
   }
   __host__ __device__ static constexpr uint32_t buffer_phase(uint32_t i) { return (i / BACK) & 1; }
+  // the weights in a score buffer: of 128 scores over the second half, which is in registers when they are written
+  static constexpr uint32_t P_AT = BN == 128 ? 64 : 0;
+  // Products of one thread with accumulators of one shape execute in the order of their issue, so scores may overwrite the weights
+  // of the second product that was issued just before them.
+  static constexpr bool IN_ORDER = BACK == 1 && D == BN;
+  // with one buffer a half of an item's weights is handed over by itself, so that its product runs beside the rest
+  static constexpr bool HALVES = BACK == 1;
+  // and the groups take turns at the exponentials: in step they would share the units for them and then both wait for the products
+  static constexpr bool TURNS = BACK == 1;
   // registers a thread: what the softmax warps hold of a row and its output does not fit the launch's share
   // (384 x 168 or 512 x 128), so the other warps hand some over
   static constexpr bool REG_SPLIT = GROUPS == 2;
   static constexpr int REGS = QUANT ? 128 : 168;
-  static constexpr int REGS_CONTROL = QUANT ? 80 : 88, REGS_SOFTMAX = QUANT ? 160 : 208, REGS_CONVERT = 104;
+  static constexpr int REGS_CONTROL = QUANT ? 80 : 104, REGS_SOFTMAX = QUANT ? 160 : 200, REGS_CONVERT = 104;
   static_assert(!REG_SPLIT || 128 * REGS_CONTROL + 256 * REGS_SOFTMAX + (QUANT ? 128 * REGS_CONVERT : 0) <= THREADS * REGS,
                 "the register split stays within the launch's registers");
   static constexpr int META = 16;  // stage records kept: a record is rewritten sixteen stages later, once the K tile of a
@@ -144,9 +153,9 @@ struct StreamSmem {
   // sets of tokens with infinities or NaN, of the last four pieces: behind the first query, and at the window's edge
   static constexpr int OFF_SET = OFF_PIECE + 2 * (int)sizeof(StreamPieceRec);         // [4][2][kStreamBits]
   // full[NS], empty[NS], clean[META], q_full, q_empty, s_full[NB], p_ready[NB], pv_done[NB], o_free, half[2], drain[2],
-  // q_conv, raw_full[NR], raw_empty[NR]
+  // q_conv, p_half[2], pv_half[2], raw_full[NR], raw_empty[NR]
   static constexpr int OFF_BAR = OFF_SET + 4 * 2 * kStreamBits * 4;
-  static constexpr int NBAR = 2 * C::NS + C::META + 8 + 3 * C::NB + 2 * C::NR;
+  static constexpr int NBAR = 2 * C::NS + C::META + 12 + 3 * C::NB + 2 * C::NR;
   static constexpr int OFF_SHIFT = OFF_BAR + NBAR * 8;  // int8 [2][QT * 128]: exponents of the query rows' scales
   static constexpr int OFF_MISC = (OFF_SHIFT + (C::QUANT ? 2 * C::QT * kTreeRows : 0) + 7) & ~7;
   static constexpr int BYTES = OFF_MISC + (int)sizeof(StreamMisc) + 1024;
@@ -418,6 +427,32 @@ struct StreamTile {
   }
 };
 
+// ---------------------------------------------------------------------------------------- tensor memory
+
+// Warp-wide: lane l reads 64 consecutive columns of tensor-memory lane (taddr.lane + l).  The wait is part of the statement: no
+// use of the values can be moved before it.
+__device__ __forceinline__ void stream_ld(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr), "r"(taddr + 32)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // ---------------------------------------------------------------------------------------- the kernel
 
 template <class C>
@@ -431,7 +466,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR), *empty = full + NS, *clean = empty + NS;
   uint64_t *q_full = clean + C::META, *q_empty = q_full + 1, *s_full = q_full + 2, *p_ready = s_full + C::NB,
            *pv_done = p_ready + C::NB, *o_free = pv_done + C::NB, *half_in = o_free + 1, *drain = half_in + 2, *q_conv = drain + 2,
-           *raw_full = q_conv + 1, *raw_empty = raw_full + C::NR;
+           *p_half = q_conv + 1, *pv_half = p_half + 2, *raw_full = pv_half + 2, *raw_empty = raw_full + C::NR;
   TreeStage *meta = reinterpret_cast<TreeStage *>(smem + S::OFF_META);
   StreamPieceRec *prec = reinterpret_cast<StreamPieceRec *>(smem + S::OFF_PIECE);
   uint32_t *sets = reinterpret_cast<uint32_t *>(smem + S::OFF_SET);
@@ -458,6 +493,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(&p_ready[b], 4);
       mbar_init(&pv_done[b], 1);
     }
+    mbar_init(&pv_half[0], 1);
+    mbar_init(&pv_half[1], 1);
+    mbar_init(&p_half[0], 4);
+    mbar_init(&p_half[1], 4);
     mbar_init(&half_in[0], 4);
     mbar_init(&half_in[1], 4);
     mbar_init(o_free, C::SOFTMAX_WARPS);
@@ -649,9 +688,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       auto begin = [&](uint32_t t, int qx, const StreamTile &tile, bool alone, bool &present) -> bool {
         const uint32_t b = buf(c);
         if (!mbar_wait(&full[t % C::NK], (t / C::NK) & 1, status)) return false;
-        if (c >= (uint32_t)C::BACK && !mbar_wait(&pv_done[b], par(c - C::BACK), status)) return false;
+        if (!C::IN_ORDER && c >= (uint32_t)C::BACK && !mbar_wait(&pv_done[b], par(c - C::BACK), status)) return false;
         const int4 m = *reinterpret_cast<const int4 *>(&meta[t % C::META]);  // flags, tok0, tok_hi, badmask
         present = !(m.x & STAGE_ABSENT) && (!(m.x & STAGE_MASKED) || tile.sees(a, m.y, BN));
+        mbar_arrive(&s_full[b]);
         if (present) {
           tc_fence_after();
           const uint64_t qd = tc_sdesc_sw128(qb + qx * (C::NPL * C::QPLANE), 16, 1024);
@@ -666,30 +706,41 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         } else {
           mbar_arrive(&s_full[b]);  // no scores: the record alone
         }
-        mbar_arrive(&s_full[b]);
         release(&empty[t % C::NK], present, alone);
         ++c;
         return true;
       };
-      // the second product of the oldest item; fresh: the piece's output has had none yet
-      auto finish = [&](uint32_t t, uint32_t piece, bool first, bool &fresh, bool present, bool alone) -> bool {
+      // the second product of the oldest item; fresh: the piece's output has had none yet.  (What usually is there already is
+      // waited for first; next: the stage whose scores follow at once, or none)
+      auto finish = [&](uint32_t t, uint32_t piece, bool first, bool &fresh, bool present, bool alone, int next) -> bool {
         const uint32_t b = buf(d), vs = C::NK + t % C::NV;
-        if (!mbar_wait(&p_ready[b], par(d), status)) return false;
-        // the previous piece's outputs have been read, and all its V tiles with that
-        if (first && piece > 0 && !mbar_wait(o_free, (piece - 1) & 1, status)) return false;
         // (bf16: whoever looked it over has waited for it)
         if (C::QUANT ? !mbar_wait(&full[vs], (t / C::NV) & 1, status)
                      : !mbar_wait(&clean[t % C::META], (t / C::META) & 1, status))
           return false;
+        // the previous piece's outputs have been read, and all its V tiles with that
+        if (first && piece > 0 && !mbar_wait(o_free, (piece - 1) & 1, status)) return false;
+        if (C::BACK == 1 && next >= 0 && !mbar_wait(&full[next % C::NK], (next / C::NK) & 1, status)) return false;
+        if (!(C::HALVES ? mbar_wait(&p_half[x], d & 1, status) : mbar_wait(&p_ready[b], par(d), status))) return false;
         if (present) {
           tc_fence_after();
           const int o = C::GROUPS == 2 ? x : 0;
           const uint64_t vd = tc_sdesc_sw128(ring + vs * C::SLOT, C::PLANE, 1024);
 #pragma unroll(C::QUANT ? 1 : BN / 16)
-          for (int kk = 0; kk < BN / 16; ++kk)
-            tc_mma_ts(tmem + C::TM_O + o * D, tmem + C::TM_S + b * BN + 8 * kk, vd + (uint64_t)((kk * 16 * 128) >> 4),
-                      C::IDESC_PV, fresh && kk == 0 ? 0u : 1u);
+          for (int i = 0; i < BN / 16; ++i) {
+            if (C::HALVES && i == BN / 32) {
+              tc_commit(&pv_half[x]);
+              if (!mbar_wait(&p_ready[b], par(d), status)) return false;
+              tc_fence_after();
+            }
+            const int kk = C::HALVES ? i ^ (BN / 32) : i;  // (the second half of the weights is there first)
+            tc_mma_ts(tmem + C::TM_O + o * D, tmem + C::TM_S + b * BN + C::P_AT + 8 * kk, vd + (uint64_t)((kk * 16 * 128) >> 4),
+                      C::IDESC_PV, fresh && i == 0 ? 0u : 1u);
+          }
           fresh = false;
+        } else if (C::HALVES) {
+          mbar_arrive(&pv_half[x]);
+          if (!mbar_wait(&p_ready[b], par(d), status)) return false;
         }
         tc_commit(&pv_done[b]);
         release(&empty[vs], present, alone);
@@ -713,10 +764,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         bool fresh = true, now = false, before = false;
         for (uint32_t j = j0; j < even + dj && ok; j += dj) {
           // with more than one buffer the next scores come before the second product of the item before them
-          if (C::BACK == 1 && j > j0) ok = finish(t0 + j - dj, piece, j == j0 + dj, fresh, before, alone);
+          if (C::BACK == 1 && j > j0) ok = finish(t0 + j - dj, piece, j == j0 + dj, fresh, before, alone, j < even ? (int)(t0 + j) : -1);
           if (ok && j < even) ok = begin(t0 + j, two ? x : 0, tile, alone, now);
           if (j < even && j + dj >= even) tc_commit(q_empty);
-          if (C::BACK > 1 && ok && j > j0) ok = finish(t0 + j - dj, piece, j == j0 + dj, fresh, before, alone);
+          if (C::BACK > 1 && ok && j > j0) ok = finish(t0 + j - dj, piece, j == j0 + dj, fresh, before, alone, -1);
           before = now;
         }
         t0 += even;
@@ -981,15 +1032,40 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     auto par = [&](uint32_t i) { return C::buffer_phase(i); };
 
     // the group's next item, of a stage with the record m (flags, tok0, tok_hi, badmask)
-    auto item = [&](const StreamTile &tile, int4 m) -> bool {
+    // With pairs of tiles the groups take turns: group 0's item first.
+    auto my_turn = [&]() -> bool {
+      return grp == 0 ? c == 0 || warp_wait(&p_ready[1], (c - 1) & 1, status) : warp_wait(&p_ready[0], c & 1, status);
+    };
+    auto item = [&](const StreamTile &tile, int4 m, bool two) -> bool {
       const uint32_t tS = tl_base + C::TM_S + buf(c) * BN;
       const int o = C::GROUPS == 2 ? grp : 0;
       const uint32_t tO = tl_base + C::TM_O + o * D;
       const bool partly = m.x & STAGE_MASKED;
       if (warp_real && !(m.x & STAGE_ABSENT) && (!partly || tile.sees(a, m.y, BN))) {
-        if (__builtin_expect(partly || flip != 1.f, 0)) {
-          // (few stages, or a scale that is not positive: what the code below would carry along in every stage, and
-          // the instruction cache with it)
+        // The maximum is raised, and the output and the sum so far with it, to that of the scores whose largest is mx.  (Only of rows
+        // that want it, so that no row's rounding depends on what its neighbours attend to.)
+        auto raise = [&](float mx, bool wanted) {
+          const float m_new = mx * qs - C::LIFT;
+          wanted = wanted && m_new > m_run;
+          const float al = wanted && m_run != -INFINITY ? fast_exp2(m_run - m_new) : 1.f;
+          if (wanted) m_run = m_new;
+          l_run *= al;
+          if (had && __any_sync(FULL, al != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float v[32];
+              tc_ld32(tO + c, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] *= al;
+              tc_st32(tO + c, v);
+            }
+            tc_wait_st();
+          }
+        };
+        if (__builtin_expect(partly || !had || flip != 1.f, 0)) {
+          // the first of a piece, few others, or a scale that is not positive: what the code below would carry along in
+          // every stage, and the instruction cache with it
+          float mx = -INFINITY;
 #pragma unroll 1
           for (int k = 0; k < BN / 32; ++k) {
             const int base = m.y + 32 * k;
@@ -999,68 +1075,80 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             float v[32];
             tc_ld32(tS + 32 * k, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = (vis >> i) & 1u ? v[i] * flip : -INFINITY;
+            for (int i = 0; i < 32; ++i) {
+              v[i] = (vis >> i) & 1u ? v[i] * flip : -INFINITY;
+              mx = fmaxf(mx, v[i]);
+            }
             tc_st32(tS + 32 * k, v);
           }
           tc_wait_st();
-        }
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int k = 0; k < BN / 32; ++k) {
-          float v[32];
-          tc_ld32(tS + 32 * k, v);
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 32; i += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(v[i + e], v[i + 4 + e]));
-          mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-        }
-        mx = mx * qs - C::LIFT;
-        if (!had) {
-          m_run = mx;
-        } else if (__builtin_expect(__any_sync(FULL, real && m_run != -INFINITY && mx > m_run + C::TAU), 0)) {
-          // raise the maximum: the output so far is scaled, once its products are complete
-          if (!warp_wait(&pv_done[buf(c - 1)], par(c - 1), status)) return false;
-          tc_fence_after();
-          // (only of rows past the threshold, so that no row's rounding depends on what its neighbours attend to)
-          const bool raise = m_run == -INFINITY || mx > m_run + C::TAU;
-          const float al = raise && m_run != -INFINITY ? fast_exp2(m_run - mx) : 1.f;
-          if (raise) m_run = mx;
-          l_run *= al;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float v[32];
-            tc_ld32(tO + c, v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= al;
-            tc_st32(tO + c, v);
+          const bool higher = mx * qs - C::LIFT > m_run + (m_run == -INFINITY ? 0.f : C::TAU);
+          if (__any_sync(FULL, real && higher)) {
+            // (the output's products so far are complete)
+            if (had && !warp_wait(&pv_done[buf(c - 1)], par(c - 1), status)) return false;
+            tc_fence_after();
+            raise(mx, real && higher);
           }
-          tc_wait_st();
-        } else if (m_run == -INFINITY) {
-          m_run = mx;  // nothing attended to so far: the output is zero
         }
-        const float sub = m_run == -INFINITY ? 0.f : m_run;
-        const float2 q2 = make_float2(qs, qs), sub2 = make_float2(-sub, -sub);
-        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        if (C::TURNS && two && !my_turn()) return false;
+        // 64 weights at a time, of 128 the last 64 first.  Their sum tells whether the maximum is still good: while it is at most
+        // 2^(LIFT + TAU), no weight is larger.
+        const float2 q2 = make_float2(qs, qs);
 #pragma unroll 1
-        for (int k = 0; k < BN / 32; ++k) {
-          uint32_t w[16];
-          float x[32];
-          tc_ld32(tS + 32 * k, x);
+        for (int k = BN / 64 - 1; k >= 0; --k) {
+          uint32_t w[32];
+          float sum;
+          for (int again = 0;; ++again) {
+            float x[64];
+            stream_ld(tS + 64 * k, x);
+            const float sub = m_run == -INFINITY ? 0.f : m_run;
+            const float2 sub2 = make_float2(-sub, -sub);
+            float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 y = fma_pair(make_float2(x[i], x[i + 1]), q2, sub2);
-            const float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-            l2[(i >> 1) & 1] = add_pair(l2[(i >> 1) & 1], pr);
-            w[i >> 1] = C::QUANT ? pack_f16x2(pr.x, pr.y) : pack_bf16x2(pr.x, pr.y);
+            for (int i = 0; i < 64; i += 2) {
+              const float2 y = fma_pair(make_float2(x[i], x[i + 1]), q2, sub2);
+              const float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+              l2[(i >> 1) & 1] = add_pair(l2[(i >> 1) & 1], pr);
+              w[i >> 1] = C::QUANT ? pack_f16x2(pr.x, pr.y) : pack_bf16x2(pr.x, pr.y);
+            }
+            l2[0] = add_pair(l2[0], l2[1]);
+            sum = l2[0].x + l2[0].y;
+            const bool high = real && (!(sum <= C::WEIGHTS) || (m_run == -INFINITY && !partly));
+            if (__builtin_expect(again || !__any_sync(FULL, high), 1)) break;
+            // (the output's products so far are complete: the items' before, and that of this one's other half)
+            if (had && !warp_wait(&pv_done[buf(c - 1)], par(c - 1), status)) return false;
+            if (C::HALVES && k == 0 && !warp_wait(&pv_half[grp], c & 1, status)) return false;
+            tc_fence_after();
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              float v[32];
+              tc_ld32(tS + 64 * k + 32 * h, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
+            }
+            raise(mx, high);
           }
-          tc_st16(tS + 16 * k, w);
+          l_run += sum;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = w[16 * h + i];
+            tc_st16(tS + C::P_AT + 32 * k + 16 * h, u);
+          }
+          had = true;
+          if (C::HALVES && k == 1) {
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_half[grp]);
+          }
         }
-        l2[0] = add_pair(l2[0], l2[1]);
-        l_run += l2[0].x + l2[0].y;
         tc_wait_st();
-        had = true;
+      } else if (C::HALVES) {
+        if (C::TURNS && two && !my_turn()) return false;
+        if (lane == 0) mbar_arrive(&p_half[grp]);
       }
       tc_fence_before();
       __syncwarp();
@@ -1111,7 +1199,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (!ok) break;
           tc_fence_after();
         }
-        ok = item(tile, *reinterpret_cast<const int4 *>(&meta[(t0 + j) % C::META]));
+        ok = item(tile, *reinterpret_cast<const int4 *>(&meta[(t0 + j) % C::META]), two);
       }
       if (!ok) break;
       t0 += even;
