@@ -60,16 +60,18 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// A dense map of RANK dimensions (the first one contiguous): bf16 values with the 128-byte swizzle, or bytes.
+// A map of RANK dimensions (the first one contiguous, the others dense or so many bytes apart): bf16 values with the 128-byte
+// swizzle, or bytes.
 template <int RANK>
-bool encode_map(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[RANK], const cuuint32_t (&box)[RANK], bool bytes) {
+bool encode_map(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[RANK], const cuuint32_t (&box)[RANK], bool bytes,
+                const cuuint64_t *apart = nullptr) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t strides[RANK - 1], s = bytes ? 1 : 2;
   cuuint32_t ones[RANK];
   for (int i = 0; i < RANK; ++i) {
     ones[i] = 1u;
-    if (i < RANK - 1) strides[i] = s = s * dims[i];
+    if (i < RANK - 1) strides[i] = s = apart ? apart[i] : s * dims[i];
   }
   return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, RANK, const_cast<void *>(base),
             dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -82,11 +82,19 @@ int stream_call(const void *q, const void *k_pool, const void *v_pool, const int
   CUtensorMap tm_k, tm_v, tm_q;
   const bool codes = fmt != TREE_BF16;
   const int rowb = tree_row_bytes(fmt, D);
-  const cuuint64_t pool[4] = {(cuuint64_t)(codes ? rowb : D), (cuuint64_t)Hkv, (cuuint64_t)P, (cuuint64_t)num_pages};
-  const cuuint32_t pbox[4] = {codes ? (cuuint32_t)rowb : 64u, 1u, (cuuint32_t)BH, 1u};
+  // bf16 pools: groups of 8 tokens, whose rows of 64 values (planes) of one head lie 128 bytes apart; codes: whole rows
+  const cuuint64_t pool[4] = {(cuuint64_t)rowb, (cuuint64_t)Hkv, (cuuint64_t)P, (cuuint64_t)num_pages};
+  const cuuint32_t pbox[4] = {(cuuint32_t)rowb, 1u, (cuuint32_t)BH, 1u};
+  const cuuint64_t token = (cuuint64_t)Hkv * D * 2;  // bytes
+  const cuuint64_t group[4] = {64u, 8u, (cuuint64_t)Hkv * (D / 64), (cuuint64_t)num_pages * (P / 8)};
+  const cuuint64_t apart[3] = {token, 128u, 8 * token};
+  const cuuint32_t gbox[4] = {64u, 8u, (cuuint32_t)(D / 64), (cuuint32_t)(BH / 8)};
   const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)tokens};
   const cuuint32_t qbox[3] = {64u, (cuuint32_t)pl.G, (cuuint32_t)(pl.qt < max_query ? pl.qt : max_query)};
-  if (!encode_map(&tm_k, k_pool, pool, pbox, codes) || !encode_map(&tm_v, v_pool, pool, pbox, codes) ||
+  auto pool_map = [&](CUtensorMap *m, const void *base) {
+    return codes ? encode_map(m, base, pool, pbox, true) : encode_map(m, base, group, gbox, false, apart);
+  };
+  if ((long long)num_pages * (P / 8) > INT_MAX || !pool_map(&tm_k, k_pool) || !pool_map(&tm_v, v_pool) ||
       !encode_map(&tm_q, q, qd, qbox, false))
     return PA_ERR_UNSUPPORTED;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -120,6 +128,9 @@ int stream_call(const void *q, const void *k_pool, const void *v_pool, const int
   a.piece_cost = kPieceCost;
   a.log2_share = num_splits > 0 ? 0 : ilog2(kMinShare);
   a.nparts = num_splits > 0 ? num_splits : sms < kAutoParts ? sms : kAutoParts;
+  // groups of a CTA for each key head, unless more than a tenth of the CTAs would be left over
+  a.hg = 10 * (a.nparts / Hkv * Hkv) >= 9 * a.nparts ? Hkv : 1;
+  a.hl = Hkv / a.hg;
   a.qscale = scale * LOG2E * (codes ? k_scale : 1.f);
   a.vscale = codes ? v_scale : 1.f;
   uint32_t *status = &reinterpret_cast<WsHeader *>(ws)->status;

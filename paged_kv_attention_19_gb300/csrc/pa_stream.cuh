@@ -13,8 +13,9 @@
 //
 // Work.  An item is (row, key head, pair of tiles); a pair's keys are those that some query of it sees: a run of the row's
 // first tokens and a run that ends at its last query.  The items of all rows are laid end to end, each with its number of
-// tokens and a fixed cost, and the line is cut into equal shares, one for each CTA: long rows are split, short ones share a CTA,
-// whatever the mix.  Where an item lies on the line is known in closed form, so a CTA finds its own without walking the others.
+// tokens and a fixed cost, and the line is cut into equal shares, one for each group of hg CTAs: long rows are split, short ones
+// share a CTA, whatever the mix.  CTA r of a group serves key head r of its share, so that the key heads' parts of a page are
+// read at the same time; where the number of key heads would leave CTAs idle a group is one CTA and the line holds all heads.  Where an item lies on the line is known in closed form, so a CTA finds its own without walking the others.
 // Only a CTA's first and last pieces can be part of an item that another CTA also touches: at most two partial results each.
 //
 // Roles of a CTA (one per SM):
@@ -26,9 +27,9 @@
 //   * warp 3: the query tiles of each piece; and looks over V tiles that hold tokens which not every query sees before they
 //     are used: a token that nobody sees becomes zero, and infinities and NaN of the others are taken out of the product
 //     and handed to the queries that do see them (0 x inf must not reach the ones that do not);
-//   * FP8 and NVFP4 pools: the tiles of codes land in a ring of their own, and four more warps convert them to f16 operands
-//     (exact; two warps K tiles, two V tiles), and the query rows, scaled by a power of two each, in place; those of
-//     the V tiles then look them over;
+//   * FP8 and NVFP4 pools: the tiles of codes land in a ring of their own, and eight more warps convert them to f16 operands
+//     (exact; two teams of four take alternate stages, two warps K tiles and two V tiles), and the query rows, scaled by a
+//     power of two each, in place; those of the V tiles then look them over;
 //   * two groups of four warps: one thread per score row.
 // Tensor memory: scores at 0 (the weights over a half of their buffer), outputs at 256.  At head_dim 256 one output fills
 // the rest: one tile, one softmax group and one issuing thread.
@@ -53,6 +54,7 @@ struct StreamArgs {
   int log2_page, log2_bh, num_pages, max_pages_per_seq, max_context_len;
   int window, first;       // window 0: none
   int piece_cost, log2_share, nparts;  // (in tokens)
+  int hg, hl;              // CTAs of a group, one for each of hg key heads; key heads of a group's line (hg hl = Hkv)
   float qscale;            // scale * log2(e) (* the keys' scale)
   float vscale;
 };
@@ -75,14 +77,17 @@ struct StreamCfg {
   static constexpr int NB = 256 / BN;              // score buffers
   static constexpr int BACK = NB / GROUPS;         // of each issuing thread
   static constexpr int NPL = D / 64;               // 128-byte swizzle planes of a row
-  static constexpr int PLANE = BN * 128, SLOT = NPL * PLANE, QPLANE = kTreeRows * 128;
+  // a tile: groups of 8 tokens, of each the planes' 8 rows one plane after the other, so that one copy brings all planes of a unit
+  static constexpr int PLANE = 1024, GROUP = NPL * PLANE, SLOT = BN / 8 * GROUP, QPLANE = kTreeRows * 128;
   static constexpr int Q_BYTES = QT * NPL * QPLANE;
   static constexpr int ROOM = (QUANT ? 228352 : 229376) - Q_BYTES;
   // codes: up to eight slots of a tile each, copied in order K, V, K, V...; operands converted from them
   static constexpr int RAW_SLOT = QUANT ? (BN * ROWB + 1023) / 1024 * 1024 : 0;
-  static constexpr int NS_QUANT = D == 64 ? 10 : D == 128 ? (QT == 1 ? 8 : 6) : 3;
+  static constexpr int NS_QUANT = D == 64 ? 10 : D == 128 ? 6 : 3;
   static constexpr int NR_FIT = QUANT ? (ROOM - NS_QUANT * SLOT) / (RAW_SLOT > 0 ? RAW_SLOT : 1) : 0;
-  static constexpr int NR = (NR_FIT < 8 ? NR_FIT : 8) & ~1;  // (even: a slot holds tiles of one kind)
+  // (a slot holds tiles of one kind, and of one parity where two teams of warps convert alternate stages)
+  static constexpr int TEAMS = GROUPS;
+  static constexpr int NR = (NR_FIT < 8 ? NR_FIT : 8) & ~(2 * TEAMS - 1);
   static constexpr int NS_FIT = QUANT ? NS_QUANT : ROOM / SLOT < 12 ? ROOM / SLOT : 12;
   // Two rings of slots: a K tile is free after the scores of its stage, a V tile later.  Copies complete out of order,
   // and a wait for a phase of a slot must not come before the phase before it is known to be complete, so whoever
@@ -90,8 +95,8 @@ struct StreamCfg {
   static constexpr int NK = GROUPS == 1 ? NS_FIT / 2 : NS_FIT / 4 * 2;
   static constexpr int NV = GROUPS == 1 ? NS_FIT - NK : (NS_FIT - NK) / 2 * 2, NS = NK + NV;
   static constexpr int SOFTMAX_WARPS = 4 * GROUPS;
-  static constexpr int CONVERT_WARPS = QUANT ? 4 : 0;
-  static constexpr int TILE_WARPS = CONVERT_WARPS / 2;           // half of them for K tiles, half for V tiles
+  static constexpr int CONVERT_WARPS = QUANT ? 8 : 0;
+  static constexpr int TILE_WARPS = CONVERT_WARPS / 2 / TEAMS;   // of a team half of them for K tiles, half for V tiles
   static constexpr int CLEAN_WARPS = QUANT ? TILE_WARPS : 1;     // warps that look over the V tiles
   static constexpr int THREADS = (4 + SOFTMAX_WARPS + CONVERT_WARPS) * 32;
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
@@ -117,11 +122,11 @@ struct StreamCfg {
   // and the groups take turns at the exponentials: in step they would share the units for them and then both wait for the products
   static constexpr bool TURNS = BACK == 1;
   // registers a thread: what the softmax warps hold of a row and its output does not fit the launch's share
-  // (384 x 168 or 512 x 128), so the other warps hand some over
+  // (384 x 168 or 640 x 96), so the other warps hand some over
   static constexpr bool REG_SPLIT = GROUPS == 2;
-  static constexpr int REGS = QUANT ? 128 : 168;
-  static constexpr int REGS_CONTROL = QUANT ? 80 : 104, REGS_SOFTMAX = QUANT ? 160 : 200, REGS_CONVERT = 104;
-  static_assert(!REG_SPLIT || 128 * REGS_CONTROL + 256 * REGS_SOFTMAX + (QUANT ? 128 * REGS_CONVERT : 0) <= THREADS * REGS,
+  static constexpr int REGS = QUANT ? 96 : 168;
+  static constexpr int REGS_CONTROL = QUANT ? 72 : 104, REGS_SOFTMAX = QUANT ? 128 : 200, REGS_CONVERT = 72;
+  static_assert(!REG_SPLIT || 128 * REGS_CONTROL + 256 * REGS_SOFTMAX + 32 * CONVERT_WARPS * REGS_CONVERT <= THREADS * REGS,
                 "the register split stays within the launch's registers");
   static constexpr int META = 16;  // stage records kept: a record is rewritten sixteen stages later, once the K tile of a
                                    // stage at least six later is free, and with that its own softmax long done
@@ -233,7 +238,7 @@ __device__ __forceinline__ int stream_unit(const StreamArgs &a, const StreamSpan
 
 // ---------------------------------------------------------------------------------------- partition
 
-// The total cost W of all rows and key heads; and the row for which is(W, x, v) holds (at most one; x: the costs before it, v:
+// The total cost W of a line, all rows and its key heads; and the row for which is(W, x, v) holds (at most one; x: the costs before it, v:
 // its own) as found_b (-1: none) and found_x = x.
 template <int THREADS, class Is>
 __device__ __forceinline__ long long stream_find(const StreamArgs &a, TreePart *ps, uint32_t *bad, const Is &is) {
@@ -241,7 +246,7 @@ __device__ __forceinline__ long long stream_find(const StreamArgs &a, TreePart *
   if (tid == 0) ps->found_b = -1;
   auto cost = [&](int b, uint32_t *bits) {
     const StreamRow r = stream_row(a, b, bits);
-    return r.n > 0 ? a.Hkv * stream_cost(a, r, stream_pairs(a, r)) : 0ll;
+    return r.n > 0 ? a.hl * stream_cost(a, r, stream_pairs(a, r)) : 0ll;
   };
   // up to THREADS rows: one scan gives the total and the place; more: a pass for the total, one for the place
   const bool once = a.batch <= THREADS;
@@ -267,19 +272,19 @@ __device__ __forceinline__ long long stream_find(const StreamArgs &a, TreePart *
   return W;
 }
 
-// The CTAs that work on a total cost W, none on less than 2^log2_share, and their shares: CTA g has [cut(g), cut(g + 1)).
+// The groups that work on a total cost W, none on less than 2^log2_share, and their shares: group g has [cut(g), cut(g + 1)).
 struct StreamShares {
-  int groups, more;  // the first `more` CTAs have one unit of cost more than `each`
+  int groups, more;  // the first `more` groups have one unit of cost more than `each`
   long long each;
   __device__ __forceinline__ StreamShares(const StreamArgs &a, long long W) {
-    groups = (int)max(1ll, min((long long)a.nparts, W >> a.log2_share));
+    groups = (int)max(1ll, min((long long)(a.nparts / a.hg), W >> a.log2_share));
     each = W >> 32 ? W / groups : (long long)((uint32_t)W / (uint32_t)groups);
     more = (int)(W - each * groups);
   }
   __device__ __forceinline__ long long cut(int g) const { return g * each + min(g, more); }
 };
 
-// Where cost x of a row lies: key head, pair, and the cost within it.
+// Where cost x of a row lies on its line: key head, pair, and the cost within it.
 struct StreamPlace {
   int h, p;
   long long off;
@@ -305,11 +310,11 @@ __device__ __forceinline__ StreamPlace stream_place(const StreamArgs &a, const S
 // This CTA's range [x_begin, x_end) of the costs, and the row that it begins in.
 template <int THREADS>
 __device__ __forceinline__ void stream_partition(const StreamArgs &a, TreePart *ps, uint32_t *status) {
-  const int cta = (int)blockIdx.x;
+  const int grp = (int)blockIdx.x / a.hg;
   uint32_t bad = 0;
   stream_find<THREADS>(a, ps, &bad, [&](long long W, long long x, long long v) {
     const StreamShares s(a, W);
-    const long long xb = cta < s.groups ? s.cut(cta) : 0, xe = cta < s.groups ? s.cut(cta + 1) : 0;
+    const long long xb = grp < s.groups ? s.cut(grp) : 0, xe = grp < s.groups ? s.cut(grp + 1) : 0;
     const bool mine = xb < xe && xb >= x && xb < x + v;
     if (mine) {
       ps->x_begin = xb;
@@ -336,7 +341,7 @@ struct StreamWalker {
   const StreamArgs &a;
   int lane;
   long long R;      // cost that is left of the range
-  int b, h, p;      // the item
+  int b, h, p;      // the item (h: key head of the line)
   long long off;    // cost of it that is behind the walker
   int rb, w_start, w_n, w_L;  // lane l holds row rb + l
 
@@ -377,7 +382,7 @@ struct StreamWalker {
       pc.span = stream_span(a, r, p);
       const long long cost = (long long)pc.span.cost + a.piece_cost, part = min(cost - off, R);
       pc.b = b;
-      pc.g = h;
+      pc.g = h * a.hg + (int)blockIdx.x % a.hg;
       pc.tok0 = r.start + pc.span.i0;
       pc.ub = stream_unit(a, pc.span, off);
       pc.ue = stream_unit(a, pc.span, off + part);
@@ -389,7 +394,7 @@ struct StreamWalker {
         off = 0;
         if (++p >= stream_pairs(a, r)) {
           p = 0;
-          if (++h >= a.Hkv) {
+          if (++h >= a.hl) {
             h = 0;
             ++b;
           }
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], C::TILE_WARPS);
     }
-    mbar_init(q_conv, C::QUANT ? C::TILE_WARPS : 1);
+    mbar_init(q_conv, C::QUANT ? C::TEAMS * C::TILE_WARPS : 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, C::GROUPS);
     for (int b = 0; b < C::NB; ++b) {
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int np = ((((r.ue << a.log2_bh) - 1) >> a.log2_page) + 1) - pb;
       return 32 * w + lane < np ? a.block_table[(size_t)r.b * a.max_pages_per_seq + pb + 32 * w + lane] : 0;
     };
-    // Stage t of units [unit0, ue) of run r, whose pages are in `phys` of the first lanes; absent: without tokens.
+    // Stage t of units [unit0, ue) of run r, whose pages are in `page` of the first lanes; absent: without tokens.
     auto stage = [&](const StreamRun &r, int unit0, int page, bool absent, bool begins) {
       const int tok0 = unit0 << a.log2_bh, tok_hi = min(r.hi, r.ue << a.log2_bh);
       bool load = false, isbad = false;
@@ -605,10 +610,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             tma_load_4d(smem + S::OFF_RAW + s * C::RAW_SLOT + (lane << a.log2_bh) * C::ROWB, kv ? &tm_v : &tm_k, 0, r.g,
                         btok & (P - 1), page, &r_full[s]);
           } else {
-            uint8_t *dst = smem + S::OFF_RING + s * C::SLOT + (lane << a.log2_bh) * 128;
-#pragma unroll
-            for (int p = 0; p < C::NPL; ++p)
-              tma_load_4d(dst + p * C::PLANE, kv ? &tm_v : &tm_k, p * 64, r.g, btok & (P - 1), page, &full[s]);
+            tma_load_4d(smem + S::OFF_RING + s * C::SLOT + (lane << a.log2_bh) * C::ROWB, kv ? &tm_v : &tm_k, 0, 0, r.g * C::NPL,
+                        (page << (a.log2_page - 3)) + ((btok & (P - 1)) >> 3), &full[s]);
           }
         }
       }
@@ -645,15 +648,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       cur = nxt;
       cwin = nwin;
     }
-    // the end, for the converting warps: the next stage's tiles, which are none
-    for (int kv = 0; C::QUANT && kv < 2 && ok; ++kv) {
-      uint32_t u;
-      const int s = place(kv, u);
-      if (u > 0) ok = warp_wait(&r_empty[s], (u - 1) & 1, status);
-      if (ok && lane == 0) {
-        if (kv == 0) meta[t % C::META].flags = STAGE_END;
-        mbar_arrive(&r_full[s]);
+    // the end, for each team of the converting warps: the next stages' tiles, which are none
+    if constexpr (C::QUANT) {
+      const uint32_t end = t;
+      for (int e = 0; e < C::TEAMS && ok; ++e, ++t) {
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          uint32_t u;
+          const int s = place(kv, u);
+          if (u > 0) ok = warp_wait(&r_empty[s], (u - 1) & 1, status);
+          if (ok && lane == 0) {
+            if (kv == 0) meta[t % C::META].flags = STAGE_END;
+            mbar_arrive(&r_full[s]);
+          }
+        }
       }
+      if (!ok) t = end;  // (no copies but those before)
     }
     if (!ok) {  // copies in flight land before the CTA exits
       if constexpr (C::QUANT) {
@@ -695,10 +704,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (present) {
           tc_fence_after();
           const uint64_t qd = tc_sdesc_sw128(qb + qx * (C::NPL * C::QPLANE), 16, 1024);
-          const uint64_t kd = tc_sdesc_sw128(ring + (t % C::NK) * C::SLOT, 16, 1024);
-#pragma unroll(C::QUANT ? 1 : C::NPL)
+          const uint64_t kd = tc_sdesc_sw128(ring + (t % C::NK) * C::SLOT, 16, C::GROUP);
+#pragma unroll
           for (int p = 0; p < C::NPL; ++p)
-#pragma unroll(C::QUANT ? 1 : 4)
+#pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               tc_mma_ss(tmem + C::TM_S + b * BN, qd + (uint64_t)((p * C::QPLANE + 32 * kk) >> 4),
                         kd + (uint64_t)((p * C::PLANE + 32 * kk) >> 4), C::IDESC_S, (p | kk) != 0 ? 1u : 0u);
@@ -714,19 +723,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // waited for first; next: the stage whose scores follow at once, or none)
       auto finish = [&](uint32_t t, uint32_t piece, bool first, bool &fresh, bool present, bool alone, int next) -> bool {
         const uint32_t b = buf(d), vs = C::NK + t % C::NV;
+        // the previous piece's outputs have been read, and all its V tiles with that (before any wait for this one's: the other
+        // thread's tiles of that piece may have been in its slot)
+        if (first && piece > 0 && !mbar_wait(o_free, (piece - 1) & 1, status)) return false;
         // (bf16: whoever looked it over has waited for it)
         if (C::QUANT ? !mbar_wait(&full[vs], (t / C::NV) & 1, status)
                      : !mbar_wait(&clean[t % C::META], (t / C::META) & 1, status))
           return false;
-        // the previous piece's outputs have been read, and all its V tiles with that
-        if (first && piece > 0 && !mbar_wait(o_free, (piece - 1) & 1, status)) return false;
         if (C::BACK == 1 && next >= 0 && !mbar_wait(&full[next % C::NK], (next / C::NK) & 1, status)) return false;
         if (!(C::HALVES ? mbar_wait(&p_half[x], d & 1, status) : mbar_wait(&p_ready[b], par(d), status))) return false;
         if (present) {
           tc_fence_after();
           const int o = C::GROUPS == 2 ? x : 0;
-          const uint64_t vd = tc_sdesc_sw128(ring + vs * C::SLOT, C::PLANE, 1024);
-#pragma unroll(C::QUANT ? 1 : BN / 16)
+          const uint64_t vd = tc_sdesc_sw128(ring + vs * C::SLOT, C::PLANE, C::GROUP);
+#pragma unroll
           for (int i = 0; i < BN / 16; ++i) {
             if (C::HALVES && i == BN / 32) {
               tc_commit(&pv_half[x]);
@@ -734,7 +744,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               tc_fence_after();
             }
             const int kk = C::HALVES ? i ^ (BN / 32) : i;  // (the second half of the weights is there first)
-            tc_mma_ts(tmem + C::TM_O + o * D, tmem + C::TM_S + b * BN + C::P_AT + 8 * kk, vd + (uint64_t)((kk * 16 * 128) >> 4),
+            tc_mma_ts(tmem + C::TM_O + o * D, tmem + C::TM_S + b * BN + C::P_AT + 8 * kk, vd + (uint64_t)((kk * 2 * C::GROUP) >> 4),
                       C::IDESC_PV, fresh && i == 0 ? 0u : 1u);
           }
           fresh = false;
@@ -831,7 +841,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               bool found = false;
 #pragma unroll 4
               for (int c = 0; c < C::NPL * 8; ++c) {
-                uint4 *p = reinterpret_cast<uint4 *>(v + (c >> 3) * C::PLANE + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                uint4 *p = reinterpret_cast<uint4 *>(v + (r >> 3) * C::GROUP + (c >> 3) * C::PLANE + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
                 if (!any) {
                   *p = make_uint4(0, 0, 0, 0);
                   continue;
@@ -881,28 +891,33 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int ct = tid - (4 + C::SOFTMAX_WARPS) * 32, cw = ct >> 5;
       constexpr int TPR = D / 16, NTASK = BN * TPR, STEP = C::TILE_WARPS * 32, ROUND = NTASK / STEP < 4 ? NTASK / STEP : 4;
       static_assert(NTASK % (ROUND * STEP) == 0 && STEP % TPR == 0, "whole rounds of tasks");
-      const int kv = cw / C::TILE_WARPS, tt = ct % STEP;  // this warp's kind of tile; the thread among its warps'
+      // this warp's kind of tile and team; the thread among its warps'
+      const int kv = cw / C::TILE_WARPS & 1, team = cw / (2 * C::TILE_WARPS), tt = ct % STEP;
       uint32_t kp = 0;  // pieces begun
       int pos0 = 0, lo_min = 0, lo_max = 0;
-      for (uint32_t t = 0;; ++t) {
+      for (uint32_t t = team;; t += C::TEAMS) {
         const uint32_t f = 2 * t + kv;
         const int rs = f % C::NR;
         bool ok = warp_wait(&raw_full[rs], (f / C::NR) & 1, status);
         if (!ok) break;
         const int4 m = *reinterpret_cast<const int4 *>(&meta[t % C::META]);  // flags, tok0, tok_hi, badmask
-        // a new piece, or the end: the warps of the V tiles, which are needed later, take the query rows
-        if (__builtin_expect(kv == 1 && (m.x & (STAGE_FIRST | STAGE_END)), 0)) {
+        // A new piece, or the end: the warps of the V tiles, which are needed later, take the query rows.  (A piece's first stage is
+        // an even one, the first team's; the second's is the one behind it.  No scores begin before both teams have been here, so
+        // the next piece's query tiles, whose phase would be this one's parity again after them, are not there yet.)
+        const int begins = team == 0 ? m.x : meta[(t - 1) % C::META].flags;
+        if (__builtin_expect(kv == 1 && (begins & (STAGE_FIRST | STAGE_END)), 0)) {
           ok = warp_wait(q_full, kp & 1, status);
           if (!ok) break;
           const StreamPieceRec &r = prec[kp & 1];
+          pos0 = r.pos0;
+          lo_min = r.lo_min;
+          lo_max = r.lo_max;
           if (!(m.x & STAGE_END)) {
-            pos0 = r.pos0;
-            lo_min = r.lo_min;
-            lo_max = r.lo_max;
-            const bool two = r.two != 0;
+            const int nq = r.nq;
             // times 2^s (largest magnitude in [2^14, 2^15)) to f16, in place
             int8_t *shift = reinterpret_cast<int8_t *>(smem + S::OFF_SHIFT) + (kp & 1) * (C::QT * kTreeRows);
-            for (int r = tt; r < (two ? 2 : 1) * kTreeRows; r += STEP) {
+            for (int i = team * STEP + tt; i < nq * a.G; i += C::TEAMS * STEP) {  // (the rows that hold a query)
+              const int r = i < a.qt * a.G ? i : kTreeRows + i - a.qt * a.G;
               uint8_t *row = smem + (r >> 7) * (C::NPL * C::QPLANE) + (r & 127) * 128;
               auto chunk = [&](int c) {
                 return reinterpret_cast<uint4 *>(row + (c >> 3) * C::QPLANE + (((c & 7) ^ (r & 7)) << 4));
@@ -948,7 +963,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           uint8_t *op = smem + S::OFF_RING + s * C::SLOT;
           const bool look = kv == 1 && (m.x & STAGE_MASKED);
           auto put = [&](int r, int pc, const uint32_t (&h)[8]) {
-            uint8_t *row = op + (pc >> 2) * C::PLANE + r * 128;
+            uint8_t *row = op + (r >> 3) * C::GROUP + (pc >> 2) * C::PLANE + (r & 7) * 128;
             const int c0 = 2 * (pc & 3);
             *reinterpret_cast<uint4 *>(row + ((c0 ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
             *reinterpret_cast<uint4 *>(row + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
@@ -1206,7 +1221,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
       // ---- end of a piece: the products of the last item, and with them all before, are complete; and all V tiles looked over
       ok = warp_wait(&pv_done[buf(c - 1)], par(c - 1), status) &&
-           warp_wait(&clean[(t0 - 1) % C::META], ((t0 - 1) / C::META) & 1, status);
+           warp_wait(&clean[(t0 - 1) % C::META], ((t0 - 1) / C::META) & 1, status) &&
+           (!C::QUANT || warp_wait(&clean[(t0 - 2) % C::META], ((t0 - 2) / C::META) & 1, status));  // (each team's last)
       if (!ok) break;
       StreamHalf other = {-INFINITY, 0.f};
       const bool merge = C::GROUPS == 2 && !two;
@@ -1315,7 +1331,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
 // ---------------------------------------------------------------------------------------- combine
 // Grid (CTAs of the split kernel, rows / rows per block): a block for some rows of the item that CTA x begins
-// and does not end (at most one).  Its pieces lie in CTAs x, x + 1, ..., in ascending order of the keys.  Which one
+// and does not end (at most one).  Its pieces lie in CTAs x, x + hg, ..., in ascending order of the keys.  Which one
 // that is and where it ends follow from the partition, which a block works out while the split kernel's last CTAs run;
 // behind it only the partial results are loaded.  A warp takes 8 rows x 32 columns: the partials of 8 rows lie beside
 // each other, 16 bytes of each.  Several pieces' log-sum-exps and values are loaded together and merged in order.
@@ -1323,12 +1339,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 template <int D, int QT>
 __global__ void __launch_bounds__(kCombineThreads, QT == 2 ? 3 : 2) stream_combine_kernel(const StreamArgs a, uint32_t *status) {
   __shared__ TreePart part;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = (int)blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = (int)blockIdx.x, grp = cta / a.hg;
   // the row in which this CTA's range ends, neither with it nor at its start
   uint32_t ignored = 0;
   const long long W = stream_find<kCombineThreads>(a, &part, &ignored, [&](long long W, long long x, long long v) {
     const StreamShares s(a, W);
-    return cta < s.groups && s.cut(cta + 1) > x && s.cut(cta + 1) < x + v;
+    return grp < s.groups && s.cut(grp + 1) > x && s.cut(grp + 1) < x + v;
   });
   int k = 0, h = 0;  // pieces of the item; its key head
   StreamRow r = {0, 0, 0};
@@ -1336,14 +1352,14 @@ __global__ void __launch_bounds__(kCombineThreads, QT == 2 ? 3 : 2) stream_combi
   if (part.found_b >= 0) {
     const StreamShares s(a, W);
     r = stream_row(a, part.found_b, &ignored);
-    const long long end = s.cut(cta + 1);
+    const long long end = s.cut(grp + 1);
     const StreamPlace at = stream_place(a, r, end - part.found_x);
     span = stream_span(a, r, at.p);
     const long long begin = end - at.off, last = begin + a.piece_cost + span.cost;
-    h = at.h;
+    h = at.h * a.hg + cta % a.hg;
     const int u = stream_unit(a, span, at.off);
-    if (u > 0 && u < span.units && stream_unit(a, span, s.cut(cta) - begin) == 0)
-      for (k = 2; s.cut(cta + k) < last;) ++k;
+    if (u > 0 && u < span.units && stream_unit(a, span, s.cut(grp) - begin) == 0)
+      for (k = 2; s.cut(grp + k) < last;) ++k;
   }
   pdl_wait();
   pdl_launch_dependents();
@@ -1371,7 +1387,7 @@ __global__ void __launch_bounds__(kCombineThreads, QT == 2 ? 3 : 2) stream_combi
         lc[u] = -INFINITY;
         x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i0 + u < k) {
-          const size_t slot = (size_t)(cta + i0 + u) * 2 + (i0 + u == 0 ? 1 : 0);
+          const size_t slot = (size_t)(cta + (i0 + u) * a.hg) * 2 + (i0 + u == 0 ? 1 : 0);
           lc[u] = a.part_lse[slot * RS + pr];
           const float *src = a.part_o + slot * RS * D + (size_t)c0 * RS + pr * 4;
           x[u][0] = *reinterpret_cast<const float4 *>(src);
