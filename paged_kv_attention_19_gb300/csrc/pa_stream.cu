@@ -76,7 +76,7 @@ int stream_call(const void *q, const void *k_pool, const void *v_pool, const int
   for (const void *p : words)
     if (!aligned_to(p, 4)) return PA_ERR_MISALIGNED;
   if (workspace_bytes < pl.total) return PA_ERR_WORKSPACE_TOO_SMALL;
-  const int BN = stream_stage(fmt, pl.QT), BH = P < BN ? P : BN;  // tokens of a stage, and of a TMA box: a unit
+  const int BN = stream_stage(D, fmt, pl.QT), BH = P < BN ? P : BN;  // tokens of a stage, and of a TMA box: a unit
   const int sms = sm_count();
   if (sms <= 0) return cuda_fail(cudaSuccess);
   CUtensorMap tm_k, tm_v, tm_q;

@@ -28,8 +28,8 @@
 //     are used: a token that nobody sees becomes zero, and infinities and NaN of the others are taken out of the product
 //     and handed to the queries that do see them (0 x inf must not reach the ones that do not);
 //   * FP8 and NVFP4 pools: the tiles of codes land in a ring of their own, and eight more warps convert them to f16 operands
-//     (exact; two teams of four take alternate stages, two warps K tiles and two V tiles), and the query rows, scaled by a
-//     power of two each, in place; those of the V tiles then look them over;
+//     (exact; four warps K tiles, four V tiles), and the query rows, scaled by a power of two each, in place; those of
+//     the V tiles then look them over;
 //   * two groups of four warps: one thread per score row.
 // Tensor memory: scores at 0 (the weights over a half of their buffer), outputs at 256.  At head_dim 256 one output fills
 // the rest: one tile, one softmax group and one issuing thread.
@@ -63,9 +63,10 @@ struct StreamHalf {  // one row's state in one softmax group, for the merge of a
   float m, l;
 };
 
-// Tokens of a stage.  With pairs of bf16 tiles 128: half as many waits for each score, and score products of N = 128, which read
-// the query tile from shared memory half as often as those of N = 64.
-constexpr int stream_stage(int fmt, int QT) { return fmt == TREE_BF16 && QT == 2 ? 128 : 64; }
+// Tokens of a stage: what two groups' scores, or four buffers of one group's, have room for in the tensor memory beside the
+// outputs; with pairs of tiles over codes half of that, or the shared memory would hold one tile of codes of each kind only
+// (head_dim 128: FP8 chunks 673 us for 635, NVFP4 286 for 255).
+constexpr int stream_stage(int D, int fmt, int QT) { return D == 256 || (D == 128 && fmt != TREE_BF16 && QT == 2) ? 64 : 128; }
 
 template <int D_, int FMT_, int QT_>
 struct StreamCfg {
@@ -73,21 +74,19 @@ struct StreamCfg {
   static constexpr bool QUANT = FMT != TREE_BF16;  // codes in the cache, f16 operands
   static constexpr int ROWB = tree_row_bytes(FMT, D);
   static constexpr int GROUPS = D <= 128 ? 2 : 1;  // softmax groups, and output regions
-  static constexpr int BN = stream_stage(FMT, QT);
+  static constexpr int BN = stream_stage(D, FMT, QT);
   static constexpr int NB = 256 / BN;              // score buffers
   static constexpr int BACK = NB / GROUPS;         // of each issuing thread
   static constexpr int NPL = D / 64;               // 128-byte swizzle planes of a row
   // a tile: groups of 8 tokens, of each the planes' 8 rows one plane after the other, so that one copy brings all planes of a unit
   static constexpr int PLANE = 1024, GROUP = NPL * PLANE, SLOT = BN / 8 * GROUP, QPLANE = kTreeRows * 128;
   static constexpr int Q_BYTES = QT * NPL * QPLANE;
-  static constexpr int ROOM = (QUANT ? 228352 : 229376) - Q_BYTES;
+  static constexpr int ROOM = 229376 - Q_BYTES;
   // codes: up to eight slots of a tile each, copied in order K, V, K, V...; operands converted from them
   static constexpr int RAW_SLOT = QUANT ? (BN * ROWB + 1023) / 1024 * 1024 : 0;
-  static constexpr int NS_QUANT = D == 64 ? 10 : D == 128 ? 6 : 3;
+  static constexpr int NS_QUANT = D == 64 ? 8 : D == 128 ? (QT == 1 ? 4 : 6) : 3;
   static constexpr int NR_FIT = QUANT ? (ROOM - NS_QUANT * SLOT) / (RAW_SLOT > 0 ? RAW_SLOT : 1) : 0;
-  // (a slot holds tiles of one kind, and of one parity where two teams of warps convert alternate stages)
-  static constexpr int TEAMS = GROUPS;
-  static constexpr int NR = (NR_FIT < 8 ? NR_FIT : 8) & ~(2 * TEAMS - 1);
+  static constexpr int NR = (NR_FIT < 8 ? NR_FIT : 8) & ~1;  // (even: a slot holds tiles of one kind)
   static constexpr int NS_FIT = QUANT ? NS_QUANT : ROOM / SLOT < 12 ? ROOM / SLOT : 12;
   // Two rings of slots: a K tile is free after the scores of its stage, a V tile later.  Copies complete out of order,
   // and a wait for a phase of a slot must not come before the phase before it is known to be complete, so whoever
@@ -96,7 +95,7 @@ struct StreamCfg {
   static constexpr int NV = GROUPS == 1 ? NS_FIT - NK : (NS_FIT - NK) / 2 * 2, NS = NK + NV;
   static constexpr int SOFTMAX_WARPS = 4 * GROUPS;
   static constexpr int CONVERT_WARPS = QUANT ? 8 : 0;
-  static constexpr int TILE_WARPS = CONVERT_WARPS / 2 / TEAMS;   // of a team half of them for K tiles, half for V tiles
+  static constexpr int TILE_WARPS = CONVERT_WARPS / 2;           // half of them for K tiles, half for V tiles
   static constexpr int CLEAN_WARPS = QUANT ? TILE_WARPS : 1;     // warps that look over the V tiles
   static constexpr int THREADS = (4 + SOFTMAX_WARPS + CONVERT_WARPS) * 32;
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
@@ -490,7 +489,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], C::TILE_WARPS);
     }
-    mbar_init(q_conv, C::QUANT ? C::TEAMS * C::TILE_WARPS : 1);
+    mbar_init(q_conv, C::QUANT ? C::TILE_WARPS : 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, C::GROUPS);
     for (int b = 0; b < C::NB; ++b) {
@@ -648,21 +647,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       cur = nxt;
       cwin = nwin;
     }
-    // the end, for each team of the converting warps: the next stages' tiles, which are none
-    if constexpr (C::QUANT) {
-      const uint32_t end = t;
-      for (int e = 0; e < C::TEAMS && ok; ++e, ++t) {
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          uint32_t u;
-          const int s = place(kv, u);
-          if (u > 0) ok = warp_wait(&r_empty[s], (u - 1) & 1, status);
-          if (ok && lane == 0) {
-            if (kv == 0) meta[t % C::META].flags = STAGE_END;
-            mbar_arrive(&r_full[s]);
-          }
-        }
+    // the end, for the converting warps: the next stage's tiles, which are none
+    for (int kv = 0; C::QUANT && kv < 2 && ok; ++kv) {
+      uint32_t u;
+      const int s = place(kv, u);
+      if (u > 0) ok = warp_wait(&r_empty[s], (u - 1) & 1, status);
+      if (ok && lane == 0) {
+        if (kv == 0) meta[t % C::META].flags = STAGE_END;
+        mbar_arrive(&r_full[s]);
       }
-      if (!ok) t = end;  // (no copies but those before)
     }
     if (!ok) {  // copies in flight land before the CTA exits
       if constexpr (C::QUANT) {
@@ -891,21 +884,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int ct = tid - (4 + C::SOFTMAX_WARPS) * 32, cw = ct >> 5;
       constexpr int TPR = D / 16, NTASK = BN * TPR, STEP = C::TILE_WARPS * 32, ROUND = NTASK / STEP < 4 ? NTASK / STEP : 4;
       static_assert(NTASK % (ROUND * STEP) == 0 && STEP % TPR == 0, "whole rounds of tasks");
-      // this warp's kind of tile and team; the thread among its warps'
-      const int kv = cw / C::TILE_WARPS & 1, team = cw / (2 * C::TILE_WARPS), tt = ct % STEP;
+      const int kv = cw / C::TILE_WARPS, tt = ct % STEP;  // this warp's kind of tile; the thread among its warps'
       uint32_t kp = 0;  // pieces begun
       int pos0 = 0, lo_min = 0, lo_max = 0;
-      for (uint32_t t = team;; t += C::TEAMS) {
+      for (uint32_t t = 0;; ++t) {
         const uint32_t f = 2 * t + kv;
         const int rs = f % C::NR;
         bool ok = warp_wait(&raw_full[rs], (f / C::NR) & 1, status);
         if (!ok) break;
         const int4 m = *reinterpret_cast<const int4 *>(&meta[t % C::META]);  // flags, tok0, tok_hi, badmask
-        // A new piece, or the end: the warps of the V tiles, which are needed later, take the query rows.  (A piece's first stage is
-        // an even one, the first team's; the second's is the one behind it.  No scores begin before both teams have been here, so
-        // the next piece's query tiles, whose phase would be this one's parity again after them, are not there yet.)
-        const int begins = team == 0 ? m.x : meta[(t - 1) % C::META].flags;
-        if (__builtin_expect(kv == 1 && (begins & (STAGE_FIRST | STAGE_END)), 0)) {
+        // a new piece, or the end: the warps of the V tiles, which are needed later, take the query rows
+        if (__builtin_expect(kv == 1 && (m.x & (STAGE_FIRST | STAGE_END)), 0)) {
           ok = warp_wait(q_full, kp & 1, status);
           if (!ok) break;
           const StreamPieceRec &r = prec[kp & 1];
@@ -916,7 +905,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int nq = r.nq;
             // times 2^s (largest magnitude in [2^14, 2^15)) to f16, in place
             int8_t *shift = reinterpret_cast<int8_t *>(smem + S::OFF_SHIFT) + (kp & 1) * (C::QT * kTreeRows);
-            for (int i = team * STEP + tt; i < nq * a.G; i += C::TEAMS * STEP) {  // (the rows that hold a query)
+            for (int i = tt; i < nq * a.G; i += STEP) {  // (the rows that hold a query)
               const int r = i < a.qt * a.G ? i : kTreeRows + i - a.qt * a.G;
               uint8_t *row = smem + (r >> 7) * (C::NPL * C::QPLANE) + (r & 127) * 128;
               auto chunk = [&](int c) {
@@ -1221,8 +1210,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
       // ---- end of a piece: the products of the last item, and with them all before, are complete; and all V tiles looked over
       ok = warp_wait(&pv_done[buf(c - 1)], par(c - 1), status) &&
-           warp_wait(&clean[(t0 - 1) % C::META], ((t0 - 1) / C::META) & 1, status) &&
-           (!C::QUANT || warp_wait(&clean[(t0 - 2) % C::META], ((t0 - 2) / C::META) & 1, status));  // (each team's last)
+           warp_wait(&clean[(t0 - 1) % C::META], ((t0 - 1) / C::META) & 1, status);
       if (!ok) break;
       StreamHalf other = {-INFINITY, 0.f};
       const bool merge = C::GROUPS == 2 && !two;
