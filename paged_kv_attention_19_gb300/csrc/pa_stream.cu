@@ -118,6 +118,7 @@ int stream_call(const void *q, const void *k_pool, const void *v_pool, const int
   a.G = pl.G;
   a.qt = pl.qt;
   a.q2 = pl.QT * pl.qt;
+  a.single = max_query <= a.q2;
   a.log2_page = ilog2(P);
   a.log2_bh = ilog2(BH);
   a.num_pages = num_pages;

@@ -54,6 +54,7 @@ struct StreamArgs {
   int log2_page, log2_bh, num_pages, max_pages_per_seq, max_context_len;
   int window, first;       // window 0: none
   int piece_cost, log2_share, nparts;  // (in tokens)
+  int single;              // no row has more than one pair
   int hg, hl;              // CTAs of a group, one for each of hg key heads; key heads of a group's line (hg hl = Hkv)
   float qscale;            // scale * log2(e) (* the keys' scale)
   float vscale;
@@ -190,13 +191,15 @@ __device__ __forceinline__ StreamRow stream_row(const StreamArgs &a, int b, uint
 }
 
 __device__ __forceinline__ int stream_pairs(const StreamArgs &a, const StreamRow &r) {
-  return (int)(((unsigned)r.n + (unsigned)a.q2 - 1u) / (unsigned)a.q2);
+  return a.single ? r.n > 0 : (int)(((unsigned)r.n + (unsigned)a.q2 - 1u) / (unsigned)a.q2);
 }
 
 // Cost of the first p pairs of a row.  Pair i has the tokens up to its last query, less those behind its window and the first
 // ones: hi - max(0, A + i q2) with hi = prefix + min((i + 1) q2, n), A = prefix + 1 - window - first.
 __device__ __forceinline__ long long stream_cost(const StreamArgs &a, const StreamRow &r, int p) {
   if (p <= 0) return 0;
+  if (a.single)
+    return (long long)a.piece_cost + r.L - (a.window > 0 ? max(0ll, (long long)(r.L - r.n + 1 - a.window) - a.first) : 0ll);
   const long long prefix = r.L - r.n, q2 = a.q2, P = p;
   long long c = P * (a.piece_cost + prefix) + q2 * (P * (P + 1) / 2);
   c -= max(0ll, P * q2 - r.n);  // (the last pair's queries)
@@ -229,10 +232,11 @@ __device__ __forceinline__ StreamSpan stream_span(const StreamArgs &a, const Str
   return s;
 }
 
-// Units that lie before cost c of a pair.
+// Units that lie before cost c of a pair.  (A pair has at least as many units as its tokens would fill; what the edges of its runs
+// add comes with the last ones.)
 __device__ __forceinline__ int stream_unit(const StreamArgs &a, const StreamSpan &s, long long c) {
   const long long x = c - a.piece_cost;
-  return x <= 0 ? 0 : x >= s.cost ? s.units : (int)(x * s.units / s.cost);
+  return x <= 0 ? 0 : x >= s.cost ? s.units : (int)x >> a.log2_bh;
 }
 
 // ---------------------------------------------------------------------------------------- partition
@@ -290,11 +294,14 @@ struct StreamPlace {
 };
 __device__ __forceinline__ StreamPlace stream_place(const StreamArgs &a, const StreamRow &r, long long x) {
   const int pairs = stream_pairs(a, r);
-  StreamPlace s = {0, 0, 0};
+  StreamPlace s = {0, 0, x};
   if (pairs == 0) return s;
-  const long long head = stream_cost(a, r, pairs);
-  s.h = (x | head) >> 32 ? (int)(x / head) : (int)((uint32_t)x / (uint32_t)head);
-  x -= s.h * head;
+  if (a.hl > 1) {
+    const long long head = stream_cost(a, r, pairs);
+    s.h = (x | head) >> 32 ? (int)(x / head) : (int)((uint32_t)x / (uint32_t)head);
+    s.off = x -= s.h * head;
+  }
+  if (a.single) return s;
   int lo = 0, hi = pairs - 1;  // the last pair that begins at or before x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -479,36 +486,37 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nbox = BN >> a.log2_bh;
 
-  if (tid == 0) {
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], C::QUANT ? C::TILE_WARPS : 1);
-      mbar_init(&empty[s], C::GROUPS);  // an arrival of each issuing thread (both of one where the stage is its own)
+  if (lane == 0 && warp < 4) {  // (four threads' worth of barriers)
+    if (warp == 0) {
+      for (int s = 0; s < NS; ++s) mbar_init(&full[s], C::QUANT ? C::TILE_WARPS : 1);
+      for (int s = 0; s < NS; ++s) mbar_init(&empty[s], C::GROUPS);  // an arrival of each issuing thread (both of one where the stage is its own)
+      misc->status = 0;
+      misc->npieces = 0;
+    } else if (warp == 1) {
+      for (int s = 0; s < C::META; ++s) mbar_init(&clean[s], C::CLEAN_WARPS);
+    } else if (warp == 2) {
+      for (int s = 0; s < C::NR; ++s) {
+        mbar_init(&raw_full[s], 1);
+        mbar_init(&raw_empty[s], C::TILE_WARPS);
+      }
+      mbar_init(q_conv, C::QUANT ? C::TILE_WARPS : 1);
+      mbar_init(q_full, 1);
+      mbar_init(q_empty, C::GROUPS);
+      mbar_init(o_free, C::SOFTMAX_WARPS);
+    } else {
+      for (int b = 0; b < C::NB; ++b) {
+        mbar_init(&s_full[b], 2);  // the scores' commit and the issuing thread's arrive
+        mbar_init(&p_ready[b], 4);
+        mbar_init(&pv_done[b], 1);
+      }
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&pv_half[x], 1);
+        mbar_init(&p_half[x], 4);
+        mbar_init(&half_in[x], 4);
+        mbar_init(&drain[x], 1);
+      }
     }
-    for (int s = 0; s < C::META; ++s) mbar_init(&clean[s], C::CLEAN_WARPS);
-    for (int s = 0; s < C::NR; ++s) {
-      mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], C::TILE_WARPS);
-    }
-    mbar_init(q_conv, C::QUANT ? C::TILE_WARPS : 1);
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, C::GROUPS);
-    for (int b = 0; b < C::NB; ++b) {
-      mbar_init(&s_full[b], 2);  // the scores' commit and the issuing thread's arrive
-      mbar_init(&p_ready[b], 4);
-      mbar_init(&pv_done[b], 1);
-    }
-    mbar_init(&pv_half[0], 1);
-    mbar_init(&pv_half[1], 1);
-    mbar_init(&p_half[0], 4);
-    mbar_init(&p_half[1], 4);
-    mbar_init(&half_in[0], 4);
-    mbar_init(&half_in[1], 4);
-    mbar_init(o_free, C::SOFTMAX_WARPS);
-    mbar_init(&drain[0], 1);
-    mbar_init(&drain[1], 1);
     fence_mbar_init();
-    misc->status = 0;
-    misc->npieces = 0;
   }
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tm_k);
@@ -1213,7 +1221,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
            warp_wait(&clean[(t0 - 1) % C::META], ((t0 - 1) / C::META) & 1, status);
       if (!ok) break;
       StreamHalf other = {-INFINITY, 0.f};
-      const bool merge = C::GROUPS == 2 && !two;
+      const bool merge = C::GROUPS == 2 && !two && r0.y > 1;  // (one stage: the other group has had nothing)
       if (merge) {  // both groups have had as many items
         a.halves[((size_t)blockIdx.x * 2 + grp) * kTreeRows + row] = StreamHalf{m_run, l_run};
         __syncwarp();
@@ -1239,7 +1247,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       uint16_t *orow = a.out + ((size_t)node_tok * a.Hq + head) * D;
       constexpr int RS = C::QT * kTreeRows;
       float *po = a.part_o + (pi - prow) * D + prow * 4;  // value d of the row: po[d / 4 * 4 RS + d % 4]
-      if (warp_real) {
+      if (warp_real && (two || merge || C::GROUPS == 1 || grp == 0)) {
 #pragma unroll 1
         for (int c = c0; c < c1; c += 32) {
           float v[32], u[32];
