@@ -19,12 +19,13 @@
 // Only a CTA's first and last pieces can be part of an item that another CTA also touches: at most two partial results each.
 //
 // Roles of a CTA (one per SM):
-//   * warp 0: the K and V tiles of a stage (64 or 128 tokens) into two rings of slots (TMA, 128-byte swizzle);
+//   * warp 3: the K and V tiles of a stage (64 or 128 tokens) into two rings of slots (TMA, 128-byte swizzle); its quarter of the SM
+//     has no softmax warp that works where a tile has up to 96 rows, as single tokens' do;
 //   * warps 1 and 2, one thread each: the products of softmax group x = 0, 1.  With two tiles thread x takes tile x of every
 //     stage; with one tile the threads take alternate stages of the same rows, and the two outputs are merged at the
 //     end of the piece.  A piece has an even number of stages, so that a stage's parity says whose it is; the last may be
 //     without tokens;
-//   * warp 3: the query tiles of each piece; and looks over V tiles that hold tokens which not every query sees before they
+//   * warp 0: the query tiles of each piece; and looks over V tiles that hold tokens which not every query sees before they
 //     are used: a token that nobody sees becomes zero, and infinities and NaN of the others are taken out of the product
 //     and handed to the queries that do see them (0 x inf must not reach the ones that do not);
 //   * FP8 and NVFP4 pools: the tiles of codes land in a ring of their own, and eight more warps convert them to f16 operands
@@ -534,21 +535,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (warp < 4) {
   if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_CONTROL>();
-  if (warp == 0) {
+  if (warp == 3) {
     // ------------------------------------------------------------ K and V tiles
     const int P = 1 << a.log2_page;
     uint32_t t = 0;
     int in_flight = 0;  // tiles of stage t whose copies were issued
-    // where tile kv of stage t goes: slot, its phase, and the barriers of the ring
-    auto place = [&](int kv, uint32_t &u) -> int {
-      if constexpr (C::QUANT) {
-        u = (2 * t + kv) / C::NR;
-        return (2 * t + kv) % C::NR;
-      } else {
-        u = kv ? t / C::NV : t / C::NK;
-        return kv ? C::NK + t % C::NV : t % C::NK;
-      }
-    };
+    // where the next K and V tile go: slots, the rings' sizes, and the parity of the phase that frees a slot (a slot's first use
+    // waits for the phase before the first, which counts as complete)
+    constexpr int K0 = 0, V0 = C::QUANT ? 1 : C::NK, STEP = C::QUANT ? 2 : 1, KEND = C::QUANT ? C::NR : C::NK, VEND = C::QUANT ? C::NR + 1 : C::NS;
+    int slot[2] = {K0, V0};
+    uint32_t freed[2] = {1u, 1u};
     uint64_t *const r_full = C::QUANT ? raw_full : full, *const r_empty = C::QUANT ? raw_empty : empty;
     bool ok = true;
     StreamWalker walker(a, &misc->part, lane);
@@ -580,36 +576,35 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int np = ((((r.ue << a.log2_bh) - 1) >> a.log2_page) + 1) - pb;
       return 32 * w + lane < np ? a.block_table[(size_t)r.b * a.max_pages_per_seq + pb + 32 * w + lane] : 0;
     };
+    // The tile kv of a stage goes to the next slot of its ring.
+    auto next_slot = [&](int kv) {
+      slot[kv] += STEP;
+      if (slot[kv] >= (kv ? VEND : KEND)) {
+        slot[kv] = kv ? V0 : K0;
+        freed[kv] ^= 1u;
+      }
+    };
     // Stage t of units [unit0, ue) of run r, whose pages are in `page` of the first lanes; absent: without tokens.
     auto stage = [&](const StreamRun &r, int unit0, int page, bool absent, bool begins) {
-      const int tok0 = unit0 << a.log2_bh, tok_hi = min(r.hi, r.ue << a.log2_bh);
-      bool load = false, isbad = false;
-      if (!absent && lane < nbox && unit0 + lane < r.ue) {
-        load = page >= 0 && page < a.num_pages;
-        isbad = !load;
-        if (isbad) atomicOr(status, PA_DEV_BAD_PAGE);
-      }
-      const uint32_t bad = __ballot_sync(FULL, isbad);
-      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL, load)) * (uint32_t)(C::ROWB << a.log2_bh);
+      const bool mine = !absent && lane < nbox && unit0 + lane < r.ue, load = mine && page >= 0 && page < a.num_pages;
+      if (mine && !load) atomicOr(status, PA_DEV_BAD_PAGE);
+      const uint32_t bad = __ballot_sync(FULL, mine && !load);
+      const int boxes = absent ? 0 : min(nbox, r.ue - unit0) - __popc(bad);
       const int btok = (unit0 + lane) << a.log2_bh;
 #pragma unroll
       for (int kv = 0; kv < 2 && ok; ++kv) {
-        uint32_t u;
-        const int s = place(kv, u);
-        if (u > 0) ok = warp_wait(&r_empty[s], (u - 1) & 1, status);
+        const int s = slot[kv];
+        ok = warp_wait(&r_empty[s], freed[kv], status);
         if (!ok) break;
         in_flight = kv + 1;
         if (lane == 0) {
           if (kv == 0) {
+            const int tok0 = unit0 << a.log2_bh, tok_hi = min(r.hi, r.ue << a.log2_bh);
             const bool whole = tok0 + BN <= min(r.pos0 + 1, tok_hi) && (tok0 >= r.lo_max || tok0 + BN <= a.first) && bad == 0;
-            TreeStage m;
-            m.flags = (absent ? STAGE_ABSENT : whole ? 0 : STAGE_MASKED) | (begins ? STAGE_FIRST : 0);
-            m.tok0 = tok0;
-            m.tok_hi = tok_hi;
-            m.badmask = bad;
-            meta[t % C::META] = m;
+            *reinterpret_cast<int4 *>(&meta[t % C::META]) =
+                make_int4((absent ? STAGE_ABSENT : whole ? 0 : STAGE_MASKED) | (begins ? STAGE_FIRST : 0), tok0, tok_hi, (int)bad);
           }
-          mbar_arrive_expect_tx(&r_full[s], bytes);
+          mbar_arrive_expect_tx(&r_full[s], (uint32_t)boxes * (uint32_t)(C::ROWB << a.log2_bh));
         }
         __syncwarp();
         if (load) {
@@ -621,6 +616,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         (page << (a.log2_page - 3)) + ((btok & (P - 1)) >> 3), &full[s]);
           }
         }
+        next_slot(kv);
       }
       if (ok) {
         ++t;
@@ -657,12 +653,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     // the end, for the converting warps: the next stage's tiles, which are none
     for (int kv = 0; C::QUANT && kv < 2 && ok; ++kv) {
-      uint32_t u;
-      const int s = place(kv, u);
-      if (u > 0) ok = warp_wait(&r_empty[s], (u - 1) & 1, status);
+      ok = warp_wait(&r_empty[slot[kv]], freed[kv], status);
       if (ok && lane == 0) {
         if (kv == 0) meta[t % C::META].flags = STAGE_END;
-        mbar_arrive(&r_full[s]);
+        mbar_arrive(&r_full[slot[kv]]);
       }
     }
     if (!ok) {  // copies in flight land before the CTA exits
@@ -788,7 +782,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_wait(&drain[x], 0, status);
     }
     __syncwarp();
-  } else if (warp == 3) {
+  } else if (warp == 0) {
     // ------------------------------------------------------------ query tiles; V tiles looked over (bf16)
     StreamWalker walker(a, &misc->part, lane);
     StreamPiece pc;
