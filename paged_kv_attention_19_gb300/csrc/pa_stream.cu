@@ -22,6 +22,8 @@ constexpr int kPieceCost = 512;
 // Least share of a CTA, in tokens, where the number of shares is left to the call: below two stages, one for each
 // softmax group, a share takes as long and only adds to what is merged.
 constexpr int kMinShare = 128;
+// Pairs of at most so many tokens are not cut.
+constexpr int kWhole = 768;
 
 // How a call's query rows are tiled, and where its workspace's parts lie.
 struct StreamPlan {
@@ -127,6 +129,7 @@ int stream_call(const void *q, const void *k_pool, const void *v_pool, const int
   a.window = window > 0 ? window : 0;
   a.first = window <= 0 ? 0 : first < max_ctx ? first : max_ctx;
   a.piece_cost = kPieceCost;
+  a.whole = kWhole;
   a.log2_share = num_splits > 0 ? 0 : ilog2(kMinShare);
   a.nparts = num_splits > 0 ? num_splits : sms < kAutoParts ? sms : kAutoParts;
   // groups of a CTA for each key head, unless more than a tenth of the CTAs would be left over

@@ -54,7 +54,7 @@ struct StreamArgs {
   int qt, q2;              // queries of a tile (each with its G heads), and of a pair
   int log2_page, log2_bh, num_pages, max_pages_per_seq, max_context_len;
   int window, first;       // window 0: none
-  int piece_cost, log2_share, nparts;  // (in tokens)
+  int piece_cost, whole, log2_share, nparts;  // (in tokens)
   int single;              // no row has more than one pair
   int hg, hl;              // CTAs of a group, one for each of hg key heads; key heads of a group's line (hg hl = Hkv)
   float qscale;            // scale * log2(e) (* the keys' scale)
@@ -236,6 +236,8 @@ __device__ __forceinline__ StreamSpan stream_span(const StreamArgs &a, const Str
 // Units that lie before cost c of a pair.  (A pair has at least as many units as its tokens would fill; what the edges of its runs
 // add comes with the last ones.)
 __device__ __forceinline__ int stream_unit(const StreamArgs &a, const StreamSpan &s, long long c) {
+  // a short pair is not cut: its middle says whose it is
+  if (s.cost <= a.whole) return 2 * c >= (long long)a.piece_cost + s.cost ? s.units : 0;
   const long long x = c - a.piece_cost;
   return x <= 0 ? 0 : x >= s.cost ? s.units : (int)x >> a.log2_bh;
 }
