@@ -22,9 +22,8 @@
 //   * warp 3: the K and V tiles of a stage (64 or 128 tokens) into two rings of slots (TMA, 128-byte swizzle); its quarter of the SM
 //     has no softmax warp that works where a tile has up to 96 rows, as single tokens' do;
 //   * warps 1 and 2, one thread each: the products of softmax group x = 0, 1.  With two tiles thread x takes tile x of every
-//     stage; with one tile the threads take alternate stages of the same rows, and the two outputs are merged at the
-//     end of the piece.  A piece has an even number of stages, so that a stage's parity says whose it is; the last may be
-//     without tokens;
+//     stage; with one tile the threads take alternate stages of the same rows, by their parity, and the two outputs are
+//     merged at the end of the piece, which then has an even number of stages: the last may be without tokens;
 //   * warp 0: the query tiles of each piece; and looks over V tiles that hold tokens which not every query sees before they
 //     are used: a token that nobody sees becomes zero, and infinities and NaN of the others are taken out of the product
 //     and handed to the queries that do see them (0 x inf must not reach the ones that do not);
@@ -425,7 +424,7 @@ __device__ __forceinline__ int stream_stages(int ub, int ue, int su, int nbox) {
 struct StreamRun {
   int b, g, ub, ue;           // units of the row
   int hi, pos0, lo_max;       // tokens that some query of the pair sees end at hi
-  bool first, last, odd;      // of the piece's runs; its stages are odd in number
+  bool first, last, odd;      // of the piece's runs; a stage without tokens makes its stages even in number
 };
 
 // A tile's queries, and whether any of them sees a token of [tok, tok + count).
@@ -465,6 +464,26 @@ __device__ __forceinline__ void stream_ld(uint32_t taddr, float (&v)[64]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The same for 16 columns: where code is run once in a while a short loop costs less than the fetch of a long one.
+__device__ __forceinline__ void stream_ld(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void stream_st(uint32_t taddr, const float (&v)[16]) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i]);
+  tc_st16(taddr, w);
 }
 
 // ---------------------------------------------------------------------------------------- the kernel
@@ -567,7 +586,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       r.lo_max = s.lo_max;
       r.first = begins;
       r.last = next_part == 1 || pc.ue <= s.su;
-      r.odd = stream_stages(pc.ub, pc.ue, s.su, nbox) & 1;
+      r.odd = C::GROUPS == 2 && s.nq <= a.qt && (stream_stages(pc.ub, pc.ue, s.su, nbox) & 1);
       r.ub = next_part == 0 ? pc.ub : max(pc.ub, s.su) - s.su + s.wlo;
       r.ue = next_part == 0 ? min(pc.ue, s.su) : pc.ue - s.su + s.wlo;
       next_part = r.last ? 2 : 1;
@@ -763,21 +782,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           for (int k = 0; k < 2; ++k) mbar_arrive(&s_full[buf(c)]);  // the softmax groups stop here
           break;
         }
-        const uint32_t even = ((uint32_t)r.y + 1) & ~1u;
         const bool two = r.z != 0, alone = !two;
+        const uint32_t stages = (uint32_t)r.y, count = C::GROUPS == 2 && alone ? (stages + 1) & ~1u : stages;
         const StreamTile tile(a, r1.y, r1.z, two ? x : 0);
-        // this thread's stages: all of them, or every other one
-        const uint32_t j0 = C::GROUPS == 2 && !two ? (uint32_t)x : 0, dj = C::GROUPS == 2 && !two ? 2 : 1;
-        bool fresh = true, now = false, before = false;
-        for (uint32_t j = j0; j < even + dj && ok; j += dj) {
+        // this thread's stages: all of them, or those of its parity
+        const uint32_t j0 = C::GROUPS == 2 && alone ? (x + t0) & 1 : 0, dj = C::GROUPS == 2 && alone ? 2 : 1;
+        bool fresh = true, now = false, before = false, told = false;
+        for (uint32_t j = j0; j < count + dj && ok; j += dj) {
           // with more than one buffer the next scores come before the second product of the item before them
-          if (C::BACK == 1 && j > j0) ok = finish(t0 + j - dj, piece, j == j0 + dj, fresh, before, alone, j < even ? (int)(t0 + j) : -1);
-          if (ok && j < even) ok = begin(t0 + j, two ? x : 0, tile, alone, now);
-          if (j < even && j + dj >= even) tc_commit(q_empty);
+          if (C::BACK == 1 && j > j0) ok = finish(t0 + j - dj, piece, j == j0 + dj, fresh, before, alone, j < count ? (int)(t0 + j) : -1);
+          if (ok && j < count) ok = begin(t0 + j, two ? x : 0, tile, alone, now);
+          if (!told && j + dj >= stages) {  // the query tiles have been read
+            tc_commit(q_empty);
+            told = true;
+          }
           if (C::BACK > 1 && ok && j > j0) ok = finish(t0 + j - dj, piece, j == j0 + dj, fresh, before, alone, -1);
           before = now;
         }
-        t0 += even;
+        t0 += count;
       }
       // every operation of this thread has completed before the tensor memory is released
       tc_commit(&drain[x]);
@@ -821,7 +843,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       __syncwarp();
       ++k;
       if constexpr (!C::QUANT) {
-        for (int st = 0; st < ((stages + 1) & ~1) && ok; ++st, ++t) {
+        for (int st = 0; st < (C::GROUPS == 2 && !two ? (stages + 1) & ~1 : stages) && ok; ++st, ++t) {
           const int s = C::NK + t % C::NV;
           ok = warp_wait(&full[s], (t / C::NV) & 1, status);
           if (!ok) break;
@@ -835,25 +857,29 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                ((loaded_bits((uint32_t)m.w, r >> 5, a.log2_bh) >> (r & 31)) & 1u);
               const bool some = tok > sp.pos0 || (tok < sp.lo_max && tok >= a.first);  // seen by some and not by others
               if (any && !some) continue;
-              bool found = false;
-#pragma unroll 4
+              auto chunk = [&](int c) {
+                return reinterpret_cast<uint4 *>(v + (r >> 3) * C::GROUP + (c >> 3) * C::PLANE + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
+              };
+              if (!any) {
+#pragma unroll 8
+                for (int c = 0; c < C::NPL * 8; ++c) *chunk(c) = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              // exponents of all ones (infinities and NaN) carry into the sign's place
+              auto odd = [](uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; };
+              uint32_t seen = 0;
+#pragma unroll 8
               for (int c = 0; c < C::NPL * 8; ++c) {
-                uint4 *p = reinterpret_cast<uint4 *>(v + (r >> 3) * C::GROUP + (c >> 3) * C::PLANE + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
-                if (!any) {
-                  *p = make_uint4(0, 0, 0, 0);
-                  continue;
-                }
-                uint4 x = *p;
-                uint32_t w[4] = {x.x, x.y, x.z, x.w}, hit = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {  // exponents of all ones: infinities and NaN
-                  const uint32_t bits = ((w[e] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w[e] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
-                  hit |= bits;
-                  w[e] &= ~bits;
-                }
-                if (hit) {
-                  found = true;
-                  *p = make_uint4(w[0], w[1], w[2], w[3]);
+                const uint4 x = *chunk(c);
+                seen |= odd(x.x) | odd(x.y) | odd(x.z) | odd(x.w);
+              }
+              const bool found = seen & 0x80008000u;
+              if (__builtin_expect(found, 0)) {
+#pragma unroll 1
+                for (int c = 0; c < C::NPL * 8; ++c) {
+                  uint4 x = *chunk(c);
+                  auto without = [&](uint32_t w) { return w & ~((odd(w) >> 15 & 0x00010001u) * 0xffffu); };
+                  *chunk(c) = make_uint4(without(x.x), without(x.y), without(x.z), without(x.w));
                 }
               }
               if (found) {
@@ -1050,93 +1076,84 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const uint32_t tO = tl_base + C::TM_O + o * D;
       const bool partly = m.x & STAGE_MASKED;
       if (warp_real && !(m.x & STAGE_ABSENT) && (!partly || tile.sees(a, m.y, BN))) {
-        // The maximum is raised, and the output and the sum so far with it, to that of the scores whose largest is mx.  (Only of rows
-        // that want it, so that no row's rounding depends on what its neighbours attend to.)
-        auto raise = [&](float mx, bool wanted) {
-          const float m_new = mx * qs - C::LIFT;
-          wanted = wanted && m_new > m_run;
-          const float al = wanted && m_run != -INFINITY ? fast_exp2(m_run - m_new) : 1.f;
-          if (wanted) m_run = m_new;
-          l_run *= al;
-          if (had && __any_sync(FULL, al != 1.f)) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float v[32];
-              tc_ld32(tO + c, v);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] *= al;
-              tc_st32(tO + c, v);
-            }
-            tc_wait_st();
-          }
-        };
-        if (__builtin_expect(partly || !had || flip != 1.f, 0)) {
-          // the first of a piece, few others, or a scale that is not positive: what the code below would carry along in
-          // every stage, and the instruction cache with it
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int k = 0; k < BN / 32; ++k) {
-            const int base = m.y + 32 * k;
-            const uint32_t vis = partly ? (range_bits(base, lo_row, pos + 1) | range_bits(base, 0, min(a.first, pos + 1))) &
-                                              range_bits(base, 0, m.z) & loaded_bits((uint32_t)m.w, k, a.log2_bh)
-                                        : ~0u;
-            float v[32];
-            tc_ld32(tS + 32 * k, v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              v[i] = (vis >> i) & 1u ? v[i] * flip : -INFINITY;
-              mx = fmaxf(mx, v[i]);
-            }
-            tc_st32(tS + 32 * k, v);
-          }
-          tc_wait_st();
-          const bool higher = mx * qs - C::LIFT > m_run + (m_run == -INFINITY ? 0.f : C::TAU);
-          if (__any_sync(FULL, real && higher)) {
-            // (the output's products so far are complete)
-            if (had && !warp_wait(&pv_done[buf(c - 1)], par(c - 1), status)) return false;
-            tc_fence_after();
-            raise(mx, real && higher);
-          }
-        }
-        if (C::TURNS && two && !my_turn()) return false;
         // 64 weights at a time, of 128 the last 64 first.  Their sum tells whether the maximum is still good: while it is at most
         // 2^(LIFT + TAU), no weight is larger.
         const float2 q2 = make_float2(qs, qs);
-#pragma unroll 1
-        for (int k = BN / 64 - 1; k >= 0; --k) {
-          uint32_t w[32];
-          float sum;
-          for (int again = 0;; ++again) {
-            float x[64];
-            stream_ld(tS + 64 * k, x);
-            const float sub = m_run == -INFINITY ? 0.f : m_run;
-            const float2 sub2 = make_float2(-sub, -sub);
-            float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              const float2 y = fma_pair(make_float2(x[i], x[i + 1]), q2, sub2);
-              const float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-              l2[(i >> 1) & 1] = add_pair(l2[(i >> 1) & 1], pr);
-              w[i >> 1] = C::QUANT ? pack_f16x2(pr.x, pr.y) : pack_bf16x2(pr.x, pr.y);
-            }
-            l2[0] = add_pair(l2[0], l2[1]);
-            sum = l2[0].x + l2[0].y;
-            const bool high = real && (!(sum <= C::WEIGHTS) || (m_run == -INFINITY && !partly));
-            if (__builtin_expect(again || !__any_sync(FULL, high), 1)) break;
-            // (the output's products so far are complete: the items' before, and that of this one's other half)
-            if (had && !warp_wait(&pv_done[buf(c - 1)], par(c - 1), status)) return false;
-            if (C::HALVES && k == 0 && !warp_wait(&pv_half[grp], c & 1, status)) return false;
-            tc_fence_after();
+        int k = BN / 64 - 1;
+        // the maximum is looked for: over all scores in the first item of a piece, in stages that are seen in part and with scales that
+        // are not positive (the last two change the scores on the way), over 64 of them where their sum says so
+        bool all = partly || !had || flip != 1.f, find = all, looked = false;
+        bool wanted = true;
+        if (C::TURNS && two && !all && !my_turn()) return false;
+        while (k >= 0) {
+          if (__builtin_expect(find, 0)) {
             float mx = -INFINITY;
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              float v[32];
-              tc_ld32(tS + 64 * k + 32 * h, v);
+            for (int e = all ? 0 : 64 * k; e < (all ? BN : 64 * k + 64); e += 16) {
+              float v[16];
+              stream_ld(tS + e, v);
+              if (all && (partly || flip != 1.f)) {
+                const int base = m.y + (e & ~31);
+                const uint32_t vis = partly ? (range_bits(base, lo_row, pos + 1) | range_bits(base, 0, min(a.first, pos + 1))) &
+                                                  range_bits(base, 0, m.z) & loaded_bits((uint32_t)m.w, e >> 5, a.log2_bh)
+                                            : ~0u;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
+                for (int i = 0; i < 16; ++i) v[i] = (vis >> (e & 16) >> i) & 1u ? v[i] * flip : -INFINITY;
+                stream_st(tS + e, v);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) mx = fmaxf(mx, v[i]);
             }
-            raise(mx, high);
+            tc_wait_st();
+            // The maximum is raised, and the output and the sum so far with it.  (Only of rows that want it, so that no row's rounding
+            // depends on what its neighbours attend to.)
+            const float m_new = mx * qs - C::LIFT;
+            const bool up = real && wanted && m_new > m_run + (all && m_run != -INFINITY ? C::TAU : 0.f);
+            if (__any_sync(FULL, up)) {
+              const float al = up && m_run != -INFINITY ? fast_exp2(m_run - m_new) : 1.f;
+              if (up) m_run = m_new;
+              l_run *= al;
+              if (had) {
+                // the output's products so far are complete: the items' before, and that of this one's other half
+                if (!warp_wait(&pv_done[buf(c - 1)], par(c - 1), status)) return false;
+                if (C::HALVES && k == 0 && !warp_wait(&pv_half[grp], c & 1, status)) return false;
+                tc_fence_after();
+#pragma unroll 1
+                for (int e = 0; e < D; e += 16) {
+                  float v[16];
+                  stream_ld(tO + e, v);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) v[i] *= al;
+                  stream_st(tO + e, v);
+                }
+                tc_wait_st();
+              }
+            }
+            if (C::TURNS && two && all && !my_turn()) return false;
+            looked = !all;
+            find = all = false;
           }
+          uint32_t w[32];
+          float x[64];
+          stream_ld(tS + 64 * k, x);
+          const float sub = m_run == -INFINITY ? 0.f : m_run;
+          const float2 sub2 = make_float2(-sub, -sub);
+          float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            const float2 y = fma_pair(make_float2(x[i], x[i + 1]), q2, sub2);
+            const float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            l2[(i >> 1) & 1] = add_pair(l2[(i >> 1) & 1], pr);
+            w[i >> 1] = C::QUANT ? pack_f16x2(pr.x, pr.y) : pack_bf16x2(pr.x, pr.y);
+          }
+          l2[0] = add_pair(l2[0], l2[1]);
+          const float sum = l2[0].x + l2[0].y;
+          wanted = !(sum <= C::WEIGHTS) || (m_run == -INFINITY && !partly);
+          if (__builtin_expect(!looked && __any_sync(FULL, real && wanted), 0)) {
+            find = true;
+            continue;
+          }
+          looked = false;
           l_run += sum;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -1152,6 +1169,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_half[grp]);
           }
+          --k;
         }
         tc_wait_st();
       } else if (C::HALVES) {
@@ -1172,8 +1190,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int4 *rp = reinterpret_cast<const int4 *>(&prec[kp & 1]);
       const int4 r0 = rp[0], r1 = rp[1], r2 = rp[2];
       if (r0.x) break;
-      const uint32_t even = ((uint32_t)r0.y + 1) & ~1u;
       const bool two = r0.z != 0;
+      const uint32_t count = C::GROUPS == 2 && !two ? ((uint32_t)r0.y + 1) & ~1u : (uint32_t)r0.y;
       const int tx = two ? grp : 0;
       slot = r0.w;
       b = r1.x;
@@ -1200,8 +1218,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       m_run = -INFINITY;
       l_run = 0.f;
       had = false;
-      const uint32_t j0 = C::GROUPS == 2 && !two ? (uint32_t)grp : 0, dj = C::GROUPS == 2 && !two ? 2 : 1;
-      for (uint32_t j = j0; j < even && ok; j += dj) {
+      const uint32_t j0 = C::GROUPS == 2 && !two ? (grp + t0) & 1 : 0, dj = C::GROUPS == 2 && !two ? 2 : 1;
+      for (uint32_t j = j0; j < count && ok; j += dj) {
         if (j != j0) {
           ok = warp_wait(&s_full[buf(c)], par(c), status);
           if (!ok) break;
@@ -1210,14 +1228,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         ok = item(tile, *reinterpret_cast<const int4 *>(&meta[(t0 + j) % C::META]), two);
       }
       if (!ok) break;
-      t0 += even;
+      t0 += count;
 
       // ---- end of a piece: the products of the last item, and with them all before, are complete; and all V tiles looked over
       ok = warp_wait(&pv_done[buf(c - 1)], par(c - 1), status) &&
            warp_wait(&clean[(t0 - 1) % C::META], ((t0 - 1) / C::META) & 1, status);
       if (!ok) break;
       StreamHalf other = {-INFINITY, 0.f};
-      const bool merge = C::GROUPS == 2 && !two && r0.y > 1;  // (one stage: the other group has had nothing)
+      const bool merge = C::GROUPS == 2 && !two && r0.y > 1;  // (one stage: one group, that of its parity, has had it)
       if (merge) {  // both groups have had as many items
         a.halves[((size_t)blockIdx.x * 2 + grp) * kTreeRows + row] = StreamHalf{m_run, l_run};
         __syncwarp();
@@ -1243,31 +1261,27 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       uint16_t *orow = a.out + ((size_t)node_tok * a.Hq + head) * D;
       constexpr int RS = C::QT * kTreeRows;
       float *po = a.part_o + (pi - prow) * D + prow * 4;  // value d of the row: po[d / 4 * 4 RS + d % 4]
-      if (warp_real && (two || merge || C::GROUPS == 1 || grp == 0)) {
+      if (warp_real && (two || merge || C::GROUPS == 1 || grp == (int)(t0 & 1))) {
 #pragma unroll 1
-        for (int c = c0; c < c1; c += 32) {
-          float v[32], u[32];
-          if (merge) {
-            tree_ld_pair(tl_base + C::TM_O + o * D + c, tl_base + C::TM_O + (o ^ 1) * D + c, v, u);
-          } else {
-            tc_ld32(tl_base + C::TM_O + o * D + c, v);
-          }
+        for (int c = c0; c < c1; c += 16) {
+          float v[16], u[16];
+          stream_ld(tl_base + C::TM_O + o * D + c, v);
+          if (merge) stream_ld(tl_base + C::TM_O + (o ^ 1) * D + c, u);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = use_own ? v[i] * s_own : 0.f;
-          if (merge) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = use_oth ? fmaf(u[i], s_oth, v[i]) : v[i];
+          for (int i = 0; i < 16; ++i) {
+            v[i] = use_own ? v[i] * s_own : 0.f;
+            if (merge) v[i] = use_oth ? fmaf(u[i], s_oth, v[i]) : v[i];
           }
           if (real) {
             if (slot < 0) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 8)
+              for (int i = 0; i < 16; i += 8)
                 *reinterpret_cast<uint4 *>(orow + c + i) =
                     make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]), pack_bf16x2(v[i + 4], v[i + 5]),
                                pack_bf16x2(v[i + 6], v[i + 7]));
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
+              for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<float4 *>(po + (size_t)(c + i) * RS) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
           }
