@@ -1089,20 +1089,22 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (__builtin_expect(find, 0)) {
             float mx = -INFINITY;
 #pragma unroll 1
-            for (int e = all ? 0 : 64 * k; e < (all ? BN : 64 * k + 64); e += 16) {
-              float v[16];
-              stream_ld(tS + e, v);
+            for (int e = all ? 0 : 64 * k; e < (all ? BN : 64 * k + 64); e += 32) {
+              float v[32];
+              tc_ld32(tS + e, v);
               if (all && (partly || flip != 1.f)) {
-                const int base = m.y + (e & ~31);
+                const int base = m.y + e;
                 const uint32_t vis = partly ? (range_bits(base, lo_row, pos + 1) | range_bits(base, 0, min(a.first, pos + 1))) &
                                                   range_bits(base, 0, m.z) & loaded_bits((uint32_t)m.w, e >> 5, a.log2_bh)
                                             : ~0u;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = (vis >> (e & 16) >> i) & 1u ? v[i] * flip : -INFINITY;
-                stream_st(tS + e, v);
+                for (int i = 0; i < 32; ++i) v[i] = (vis >> i) & 1u ? v[i] * flip : -INFINITY;
+                tc_st32(tS + e, v);
               }
+              float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int i = 0; i < 16; ++i) mx = fmaxf(mx, v[i]);
+              for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], v[i]);
+              mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             }
             tc_wait_st();
             // The maximum is raised, and the output and the sum so far with it.  (Only of rows that want it, so that no row's rounding
