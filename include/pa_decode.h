@@ -658,8 +658,8 @@ int pa_kv_compact_granted(void *k_pool, void *v_pool, const int32_t *block_table
  * max_context_len up to 2^31 - 513, at most 128 query heads a key head (more: PA_ERR_UNSUPPORTED).
  * Rows whose query_start is not ascending within [0, num_tokens], has more than max_query tokens, or
  * whose L is below n_b or out of range set PA_DEV_BAD_LEN and have unspecified results.  The other
- * arguments and the error codes are those of pa_verify_gqa; the workspace is
- * pa_stream_workspace_size bytes, and its status word is read by pa_read_device_status.  For a fixed
+ * arguments and the error codes are those of pa_verify_gqa (a scale that with log2(e), and with k_scale,
+ * passes fp32's range is refused too); the workspace is pa_stream_workspace_size bytes, and its status word is read by pa_read_device_status.  For a fixed
  * num_splits results are bitwise reproducible and independent of the physical page order.
  * batch == 0 or num_tokens == 0 is a no-op (the status word stays as it was).
  * bf16 pools: products of bf16 operands, weights rounded to bf16.  FP8 and NVFP4 pools: codes as

@@ -67,6 +67,8 @@ int stream_call(const void *q, const void *k_pool, const void *v_pool, const int
   if (tokens < 0 || num_pages <= 0 || max_pages <= 0 || first < 0 || !std::isfinite(scale)) return PA_ERR_INVALID_ARGUMENT;
   if (fmt != TREE_BF16 && !(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
     return PA_ERR_INVALID_ARGUMENT;
+  const float qscale = scale * LOG2E * (fmt == TREE_BF16 ? 1.f : k_scale);
+  if (!std::isfinite(qscale)) return PA_ERR_INVALID_ARGUMENT;
   if ((long long)max_pages * P < (long long)max_ctx) return PA_ERR_INVALID_ARGUMENT;
   if (batch == 0 || tokens == 0) return PA_OK;
   if (!q || !k_pool || !v_pool || !block_table || !context_lens || !query_start || !out || !workspace)
@@ -135,7 +137,7 @@ int stream_call(const void *q, const void *k_pool, const void *v_pool, const int
   // groups of a CTA for each key head, unless more than a tenth of the CTAs would be left over
   a.hg = 10 * (a.nparts / Hkv * Hkv) >= 9 * a.nparts ? Hkv : 1;
   a.hl = Hkv / a.hg;
-  a.qscale = scale * LOG2E * (codes ? k_scale : 1.f);
+  a.qscale = qscale;
   a.vscale = codes ? v_scale : 1.f;
   uint32_t *status = &reinterpret_cast<WsHeader *>(ws)->status;
   const StreamLaunch l = {tm_k, tm_v, tm_q, a, status, D, pl.QT};

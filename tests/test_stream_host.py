@@ -45,6 +45,8 @@ def test_stream_refuses_scales_and_sizes(pa):
     for fmt in ("_fp8", "_nvfp4"):
         for bad in (0.0, -1.0, float("inf"), float("nan")):
             assert stream(pa, fmt, ksc=bad) == INVALID and stream(pa, fmt, vsc=bad) == INVALID
+        assert stream(pa, fmt, scale=1e30, ksc=1e20) == INVALID and stream(pa, fmt, scale=1e30, ksc=1.0, T=0) == 0
+    assert stream(pa, scale=3e38) == INVALID and stream(pa, scale=-3e38) == INVALID
     ws = pa.pa_stream_workspace_size
     assert ws(4, 8, 8, 2, 128, 1000, 16) >= 256 and ws(4, 100000, 8, 2, 128, 1000, 16) >= 256
     for bad in (dict(max_query=0), dict(max_query=(1 << 30) + 1), dict(num_kv_heads=3), dict(num_q_heads=258), dict(head_dim=96),
