@@ -120,7 +120,7 @@ struct StreamCfg {
   // with one buffer a half of an item's weights is handed over by itself, so that its product runs beside the rest
   static constexpr bool HALVES = BACK == 1;
   // and the groups take turns at the exponentials: in step they would share the units for them and then both wait for the products
-  static constexpr bool TURNS = BACK == 1;
+  static constexpr bool TURNS = BACK == 1 && QT == 2;
   // registers a thread: what the softmax warps hold of a row and its output does not fit the launch's share
   // (384 x 168 or 640 x 96), so the other warps hand some over
   static constexpr bool REG_SPLIT = GROUPS == 2;
@@ -158,9 +158,9 @@ struct StreamSmem {
   // sets of tokens with infinities or NaN, of the last four pieces: behind the first query, and at the window's edge
   static constexpr int OFF_SET = OFF_PIECE + 2 * (int)sizeof(StreamPieceRec);         // [4][2][kStreamBits]
   // full[NS], empty[NS], clean[META], q_full, q_empty, s_full[NB], p_ready[NB], pv_done[NB], o_free, half[2], drain[2],
-  // q_conv, p_half[2], pv_half[2], raw_full[NR], raw_empty[NR]
+  // q_conv, p_half[2], pv_half[2], turn[2][4], raw_full[NR], raw_empty[NR]
   static constexpr int OFF_BAR = OFF_SET + 4 * 2 * kStreamBits * 4;
-  static constexpr int NBAR = 2 * C::NS + C::META + 12 + 3 * C::NB + 2 * C::NR;
+  static constexpr int NBAR = 2 * C::NS + C::META + 20 + 3 * C::NB + 2 * C::NR;
   static constexpr int OFF_SHIFT = OFF_BAR + NBAR * 8;  // int8 [2][QT * 128]: exponents of the query rows' scales
   static constexpr int OFF_MISC = (OFF_SHIFT + (C::QUANT ? 2 * C::QT * kTreeRows : 0) + 7) & ~7;
   static constexpr int BYTES = OFF_MISC + (int)sizeof(StreamMisc) + 1024;
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR), *empty = full + NS, *clean = empty + NS;
   uint64_t *q_full = clean + C::META, *q_empty = q_full + 1, *s_full = q_full + 2, *p_ready = s_full + C::NB,
            *pv_done = p_ready + C::NB, *o_free = pv_done + C::NB, *half_in = o_free + 1, *drain = half_in + 2, *q_conv = drain + 2,
-           *p_half = q_conv + 1, *pv_half = p_half + 2, *raw_full = pv_half + 2, *raw_empty = raw_full + C::NR;
+           *p_half = q_conv + 1, *pv_half = p_half + 2, *turn = pv_half + 2, *raw_full = turn + 8, *raw_empty = raw_full + C::NR;
   TreeStage *meta = reinterpret_cast<TreeStage *>(smem + S::OFF_META);
   StreamPieceRec *prec = reinterpret_cast<StreamPieceRec *>(smem + S::OFF_PIECE);
   uint32_t *sets = reinterpret_cast<uint32_t *>(smem + S::OFF_SET);
@@ -531,6 +531,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         mbar_init(&p_ready[b], 4);
         mbar_init(&pv_done[b], 1);
       }
+      for (int w = 0; w < 8; ++w) mbar_init(&turn[w], 1);
       for (int x = 0; x < 2; ++x) {
         mbar_init(&pv_half[x], 1);
         mbar_init(&p_half[x], 4);
@@ -1066,9 +1067,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     auto par = [&](uint32_t i) { return C::buffer_phase(i); };
 
     // the group's next item, of a stage with the record m (flags, tok0, tok_hi, badmask)
-    // With pairs of tiles the groups take turns: group 0's item first.
+    // With pairs of tiles the two warps that share a quarter of the SM take turns at the exponentials, group 0's item first.  (Barriers
+    // of their own, each of whose phases is waited for once: a barrier that goes on without its waiter, as those of the
+    // weights do where one tile's stages alternate, can be a whole turn of its parity ahead.)
+    uint32_t turns = 0;
     auto my_turn = [&]() -> bool {
-      return grp == 0 ? c == 0 || warp_wait(&p_ready[1], (c - 1) & 1, status) : warp_wait(&p_ready[0], c & 1, status);
+      return grp == 0 ? turns == 0 || warp_wait(&turn[warp & 3], (turns - 1) & 1, status)
+                      : warp_wait(&turn[4 + (warp & 3)], turns & 1, status);
+    };
+    auto your_turn = [&]() {
+      if (lane == 0) mbar_arrive(&turn[(grp ? 0 : 4) + (warp & 3)]);
+      ++turns;
     };
     auto item = [&](const StreamTile &tile, int4 m, bool two) -> bool {
       const uint32_t tS = tl_base + C::TM_S + buf(c) * BN;
@@ -1084,7 +1093,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // are not positive (the last two change the scores on the way), over 64 of them where their sum says so
         bool all = partly || !had || flip != 1.f, find = all, looked = false;
         bool wanted = true;
-        if (C::TURNS && two && !all && !my_turn()) return false;
+        bool turned = false;
         while (k >= 0) {
           if (__builtin_expect(find, 0)) {
             float mx = -INFINITY;
@@ -1131,13 +1140,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tc_wait_st();
               }
             }
-            if (C::TURNS && two && all && !my_turn()) return false;
             looked = !all;
             find = all = false;
           }
           uint32_t w[32];
           float x[64];
           stream_ld(tS + 64 * k, x);
+          if (C::TURNS && two && !turned) {
+            if (!my_turn()) return false;
+            turned = true;
+          }
           const float sub = m_run == -INFINITY ? 0.f : m_run;
           const float2 sub2 = make_float2(-sub, -sub);
           float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -1156,6 +1168,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             continue;
           }
           looked = false;
+          if (C::TURNS && two && k == 0) your_turn();
           l_run += sum;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -1175,7 +1188,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         tc_wait_st();
       } else if (C::HALVES) {
-        if (C::TURNS && two && !my_turn()) return false;
+        if (C::TURNS && two) {
+          if (!my_turn()) return false;
+          your_turn();
+        }
         if (lane == 0) mbar_arrive(&p_half[grp]);
       }
       tc_fence_before();

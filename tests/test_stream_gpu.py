@@ -196,6 +196,55 @@ def test_stream_long(pa, fmt):
     Rows(74, [(20011, 600), (9000, 1)], 4, 1, 64, 16, fmt, 2000, 100).check(pa)
 
 
+@pytest.mark.parametrize("fmt,hq,hkv,D", [("bf16", 40, 40, 64), ("bf16", 66, 33, 128), ("fp8", 41, 41, 128), ("nvfp4", 90, 45, 64),
+                                          ("bf16", 37, 37, 256), ("bf16", 160, 160, 64)])
+def test_stream_many_key_heads(pa, fmt, hq, hkv, D):
+    """More key heads than a group of CTAs has members: a CTA's share of the work holds several, and more than there are CTAs."""
+    rows = [(200, 200), (3, 2), (700, 1), (150, 131), (64, 0)]
+    Rows(100 + hkv, rows, hq, hkv, D, 16, fmt).check(pa)
+    Rows(101 + hkv, rows, hq, hkv, D, 16, fmt, 60, 20).check(pa)
+    Rows(102 + hkv, rows[:3], hq, hkv, D, 16, fmt, 60, 20).check(pa, num_splits=7)
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_stream_drawn(pa, seed):
+    """Sizes, windows, formats and splits drawn over their whole ranges."""
+    rng = np.random.default_rng(1000 + seed)
+    log = lambda lo, hi: int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))  # noqa: E731
+    D, fmt = int(rng.choice([64, 128, 256])), str(rng.choice(["bf16", "fp8", "nvfp4"]))
+    hkv, G = int(rng.choice([1, 2, 3, 5, 8, 19])), log(1, 128 if seed % 5 == 0 else 16)
+    rows = []
+    for _ in range(log(1, 40)):
+        L = log(1, 3000 // hkv)
+        rows.append((L, min(L, int(rng.choice([0, 1, 1, log(1, 40), log(1, max(1, 3000 // (G * hkv)))])))))
+    window = int(rng.choice([0, log(1, 2000)]))
+    Rows(200 + seed, rows, hkv * G, hkv, D, int(rng.choice([8, 16, 32, 64, 128, 256])), fmt, window,
+         int(rng.choice([0, log(1, 300)])) if window else 0).check(pa, num_splits=int(rng.choice([0, 0, log(1, 300)])))
+
+
+MIXED = [([16, 29, 4, 168, 126, 52, 3153, 70, 7, 12, 94, 2352, 6, 729, 226, 406, 303, 5, 977, 544, 9, 1309, 39, 3, 1755, 2, 22, 5],
+          [0, 1, 12, 16, 35, 36, 49, 50, 51, 58, 66, 82, 124, 130, 131, 132, 133, 155, 156, 186, 212, 213, 248, 249, 250, 251, 252, 262, 267],
+          56, 8, 128, 8, 2447, 4),
+         ([80, 42, 53, 84, 72, 45, 40, 614, 88, 60, 78, 47, 61, 1424, 74, 76, 54, 114, 86, 50, 51, 3301, 46, 65, 70, 55, 43, 57, 265, 91, 63, 44, 66],
+          [0, 1, 2, 3, 4, 5, 6, 7, 621, 622, 623, 624, 625, 626, 2050, 2051, 2052, 2053, 2167, 2168, 2169, 2170, 5471, 5472, 5473, 5474, 5475, 5476,
+           5477, 5742, 5743, 5744, 5745, 5746], 64, 8, 64, 16, 18, 4)]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("lens,start,hq,hkv,D,page,window,first", MIXED)
+def test_stream_mixed_tiles(pa, fmt, lens, start, hq, hkv, D, page, window, first):
+    """Pieces of one tile, whose stages the two groups share, and of two, which take turns, in one CTA one after the other: the
+    same bits ten times, and no wait that gives up."""
+    rows = [(L, b - a) for L, a, b in zip(lens, start, start[1:])]
+    t = Rows(150, rows, hq, hkv, D, page, fmt, window, first)
+    out, lse, ws = t.call(pa)
+    t.compare(out, lse)
+    for _ in range(10):
+        o, l, _ = t.call(pa, ws=ws)
+        torch.cuda.synchronize()
+        assert pa.pa_read_device_status(ws) == 0 and torch.equal(o, out) and torch.equal(l, lse)
+
+
 def test_stream_many_rows(pa):
     """More rows than threads of a block, and than a wave of them."""
     Rows(75, [(1 + (i * 7) % 50, 1 if i % 9 else (i * 7) % 50 % 5) for i in range(2000)], 4, 2, 64, 8).check(pa)
