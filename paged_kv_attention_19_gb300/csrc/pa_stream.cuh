@@ -15,7 +15,8 @@
 // first tokens and a run that ends at its last query.  The items of all rows are laid end to end, each with its number of
 // tokens and a fixed cost, and the line is cut into equal shares, one for each group of hg CTAs: long rows are split, short ones
 // share a CTA, whatever the mix.  CTA r of a group serves key head r of its share, so that the key heads' parts of a page are
-// read at the same time; where the number of key heads would leave CTAs idle a group is one CTA and the line holds all heads.  Where an item lies on the line is known in closed form, so a CTA finds its own without walking the others.
+// read at the same time; where the number of key heads would leave CTAs idle a group is one CTA and the line holds all heads.
+// Where an item lies on the line is known in closed form, so a CTA finds its own without walking the others.
 // Only a CTA's first and last pieces can be part of an item that another CTA also touches: at most two partial results each.
 //
 // Roles of a CTA (one per SM):
@@ -33,6 +34,12 @@
 //   * two groups of four warps: one thread per score row.
 // Tensor memory: scores at 0 (the weights over a half of their buffer), outputs at 256.  At head_dim 256 one output fills
 // the rest: one tile, one softmax group and one issuing thread.
+//
+// Measured (head_dim 128; per call, calls back to back, inputs in turn).  bf16: a prompt of 8192 tokens x 32 heads 448 us (1.23 PFLOP/s,
+// 65 % of the measured 1886 TFLOP/s; a stage of two tiles takes 3540 cycles for 2048 of products, tensor pipe 47 % at 4096 tokens);
+// 32 single tokens x 64 heads, 128 to 16384 tokens in a window of 4096 + 128, 59 us (266 MB, 4.5 TB/s; 28000 of 100000 cycles
+// before the first weights).  The same shape over FP8, without a window, 89 us, issue slots 38 %.  NVFP4: 64 x 32 heads to 32768 tokens 182 us,
+// issue slots 46 %.
 #pragma once
 
 #include "pa_tree.cuh"
@@ -120,6 +127,7 @@ struct StreamCfg {
   // with one buffer a half of an item's weights is handed over by itself, so that its product runs beside the rest
   static constexpr bool HALVES = BACK == 1;
   // and the groups take turns at the exponentials: in step they would share the units for them and then both wait for the products
+  // (prompt 456 us for 488 without, chunks 739 for 784)
   static constexpr bool TURNS = BACK == 1 && QT == 2;
   // registers a thread: what the softmax warps hold of a row and its output does not fit the launch's share
   // (384 x 168 or 640 x 96), so the other warps hand some over
