@@ -710,7 +710,7 @@ size_t pa_stream_workspace_size(int batch, int max_query, int num_q_heads, int n
  *                any more: rows that have released pages end here)
  *   free_list    [num_pages] int32: a stack of free pages, of which free_count[0] are valid: the
  *                pages are pushed in row order, a row's in ascending order
- *   block_table  [batch, max_pages_per_seq] int32
+ *   block_table  [batch, max_pages_per_seq] int32; a page that rows share would be given back by each of them
  *   window_start_out  max(window_start, E) where E, the pages wholly behind the window,
  *                floor(max(0, context_lens + 1 - window) / page_size) and at most held_pages, is above F; 0
  *                for an ended row

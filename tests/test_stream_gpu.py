@@ -245,6 +245,14 @@ def test_stream_mixed_tiles(pa, fmt, lens, start, hq, hkv, D, page, window, firs
         assert pa.pa_read_device_status(ws) == 0 and torch.equal(o, out) and torch.equal(l, lse)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("window,first", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1), (300, 2 ** 31 - 1),
+                                          (1, 2 ** 30), (0, 2 ** 31 - 1)])
+@pytest.mark.parametrize("rows", [[(300, 1), (40, 1)], [(700, 300), (513, 2)]])
+def test_stream_largest_windows_and_firsts(pa, fmt, window, first, rows):
+    Rows(97, rows, 8, 2, 128, 16, fmt, window, first).check(pa)
+
+
 def test_stream_many_rows(pa):
     """More rows than threads of a block, and than a wave of them."""
     Rows(75, [(1 + (i * 7) % 50, 1 if i % 9 else (i * 7) % 50 % 5) for i in range(2000)], 4, 2, 64, 8).check(pa)
