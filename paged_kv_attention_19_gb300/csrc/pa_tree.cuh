@@ -160,9 +160,10 @@ struct alignas(16) TreePieceRec {  // written by the query warp before the piece
 };
 static_assert(sizeof(TreeStage) == 16 && sizeof(TreePieceRec) == 48, "records of 16-byte words");
 
+constexpr int kPartWarps = 20;  // most warps of a block that works out its part (the streams' over codes)
 struct TreePart {
   int32_t found_b, pad;
-  long long found_x, x_begin, x_end, warp_part[16];
+  long long found_x, x_begin, x_end, warp_part[kPartWarps];
 };
 
 struct TreeMisc {
@@ -256,8 +257,9 @@ __device__ __forceinline__ TreeTile tree_tile(const TreeArgs &a, int t, int n) {
 // ---------------------------------------------------------------------------------------- partition
 // The rows' costs laid end to end are cut into one equal range per group of HG CTAs (see the top).
 
-template <int THREADS>
-__device__ __forceinline__ long long tree_scan(long long v, long long *excl, long long *part) {
+template <int THREADS, int WARPS>
+__device__ __forceinline__ long long tree_scan(long long v, long long *excl, long long (&part)[WARPS]) {
+  static_assert(THREADS % 32 == 0 && THREADS / 32 <= WARPS, "a place for each warp's sum");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long x = v;
 #pragma unroll

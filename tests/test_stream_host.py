@@ -1,5 +1,7 @@
 """Refusals of the streams' operators: every check that the host can make, made before any CUDA call (addresses here are never
 touched)."""
+import subprocess
+
 import pytest
 import torch
 
@@ -128,3 +130,16 @@ def test_reference_of_the_release():
     assert got["free_list"][:2].tolist() == [8, 3] and got["start"] == [2, 2] and got["bits"] == 0
     got = S.release([13, 15], [4, 5], [2, 2], [8] + [0] * 9, 1, got["table"], 4, 10, 6, 1, [0, 1])
     assert got["free_list"][:5].tolist() == [8, 1, 2, 4, 0] and got["lens"] == [13, 0] and got["held"] == [4, 0]
+
+
+@pytest.mark.parametrize("threads,places,compiles", [(640, 20, True), (640, 16, False), (512, 16, True), (256, 7, False)])
+def test_scan_has_a_place_for_each_warp(pa, tmp_path, threads, places, compiles):
+    """A block of more warps than its array of partial sums has places is no program: the streams' kernels over codes have 20."""
+    from paged_kv_attention_19_gb300 import build
+    src = tmp_path / "scan.cu"
+    src.write_text("#include \"pa_tree.cuh\"\n__global__ void f(long long *x) {\n  __shared__ long long part[%d];\n  long long before;\n"
+                   "  *x = pa::tree_scan<%d>(1, &before, part);\n}\n" % (places, threads))
+    r = subprocess.run([build.nvcc(), *build.ARCH, *build.NVCC_FLAGS, "-c", str(src), "-o", str(tmp_path / "scan.o")],
+                       capture_output=True, text=True)
+    assert (r.returncode == 0) == compiles, r.stderr
+    assert compiles or "a place for each warp" in r.stderr
