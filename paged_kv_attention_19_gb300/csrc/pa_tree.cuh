@@ -1279,7 +1279,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         prow = tx * kTreeRows + row;
         if constexpr (C::QUANT) {  // the scores are 2^s times too large
           const int sh = reinterpret_cast<const int8_t *>(smem + S::OFF_SHIFT)[(kp & 1) * (C::QT * kTreeRows) + prow];
-          qs = scale * __uint_as_float((uint32_t)(127 - sh) << 23);
+          // (never 0, which masked scores of -inf would make NaN of: these scores are below 2^35, so 2^-126 of them is nothing)
+          qs = fmaxf(scale * __uint_as_float((uint32_t)(127 - sh) << 23), 0x1p-126f);
         }
         head = g * a.G + tile.h0 + h;
         node_tok = start + tile.i0 + pos;

@@ -347,6 +347,23 @@ def test_stream_scales(pa, scale):
     u.check(pa)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("hq,hkv,D,window,first", [(8, 2, 128, 90, 5), (2, 2, 64, 0, 0), (4, 1, 256, 30, 0)])
+@pytest.mark.parametrize("k_scale,sign", [(0.02, 1), (1e-7, 1), (1e-7, -1), (1e-20, 1)])
+def test_stream_zero_and_tiny_queries(pa, fmt, hq, hkv, D, window, first, k_scale, sign):
+    """Padding's zero queries, and ones at the end of bf16's range, attend to all that they see alike, however small the keys' scale."""
+    t = Rows(85, [(200, 9), (65, 17), (700, 300), (40, 1)], hq, hkv, D, 16, fmt, window, first)
+    t.q[::2, 0] = 0.0
+    t.q[1::3, 1] *= 2.0 ** -126
+    t.q[5] = 0.0
+    t.scale *= sign
+    if fmt == "bf16":
+        t.scale *= k_scale
+    else:
+        t.scales = (k_scale, 0.02)
+    t.check(pa)
+
+
 def test_stream_is_decode_verify_and_tree(pa):
     """Within both sides' rounding: half a bf16 step of each output and of each weight."""
     rows = [(100, 5), (685, 5), (33, 5)]

@@ -223,6 +223,22 @@ def test_tree_queries_near_the_ends_of_their_range(pa, fmt, exponent):
     t.check(pa)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("k_scale", [0.02, 1e-7, 1e-20])
+def test_tree_zero_and_tiny_queries(pa, fmt, k_scale):
+    """Padding's zero queries, and ones at the end of bf16's range, attend to all that they see alike, however small the keys' scale."""
+    for hq, hkv, D, window in ((8, 2, 128, 90), (2, 2, 64, 0), (4, 1, 256, 30)):
+        t = Tree(86, [(200, 9), (65, 17), (700, 64), (40, 1)], hq, hkv, D, 16, fmt)
+        t.q[::2, 0] = 0.0
+        t.q[1::3, 1] *= 2.0 ** -126
+        t.q[5] = 0.0
+        if fmt == "bf16":
+            t.scale *= k_scale
+        else:
+            t.scales = (k_scale, 0.02)
+        t.check(pa, window=window)
+
+
 # ------------------------------------------------------------------------------------------ plan
 
 @pytest.mark.parametrize("free", [6, 2, 1])
