@@ -121,9 +121,6 @@ struct StreamCfg {
   __host__ __device__ static constexpr uint32_t buffer_phase(uint32_t i) { return (i / BACK) & 1; }
   // the weights in a score buffer: of 128 scores over the second half, which is in registers when they are written
   static constexpr uint32_t P_AT = BN == 128 ? 64 : 0;
-  // Products of one thread with accumulators of one shape execute in the order of their issue, so scores may overwrite the weights
-  // of the second product that was issued just before them.
-  static constexpr bool IN_ORDER = BACK == 1 && D == BN;
   // with one buffer a half of an item's weights is handed over by itself, so that its product runs beside the rest
   static constexpr bool HALVES = BACK == 1;
   // and the groups take turns at the exponentials: in step they would share the units for them and then both wait for the products
@@ -722,7 +719,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       auto begin = [&](uint32_t t, int qx, const StreamTile &tile, bool alone, bool &present) -> bool {
         const uint32_t b = buf(c);
         if (!mbar_wait(&full[t % C::NK], (t / C::NK) & 1, status)) return false;
-        if (!C::IN_ORDER && c >= (uint32_t)C::BACK && !mbar_wait(&pv_done[b], par(c - C::BACK), status)) return false;
+        if (c >= (uint32_t)C::BACK && !mbar_wait(&pv_done[b], par(c - C::BACK), status)) return false;
         const int4 m = *reinterpret_cast<const int4 *>(&meta[t % C::META]);  // flags, tok0, tok_hi, badmask
         present = !(m.x & STAGE_ABSENT) && (!(m.x & STAGE_MASKED) || tile.sees(a, m.y, BN));
         mbar_arrive(&s_full[b]);

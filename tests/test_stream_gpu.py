@@ -190,6 +190,23 @@ def test_stream_splits(pa, splits):
     Rows(72, rows, 4, 2, 256, 16, "bf16", 300, 20).check(pa, num_splits=splits)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("hq,hkv,D,n", [(8, 2, 128, 1), (8, 2, 128, 64), (2, 2, 64, 250), (8, 4, 256, 60)])
+def test_stream_long_pieces_repeat(pa, fmt, hq, hkv, D, n):
+    """Pieces of a hundred stages, of one tile and of two: the same bits twenty times, with a second call beside them."""
+    t = Rows(110 + n, [(12900, n), (13001, n)], hq, hkv, D, 64, fmt)
+    out, lse = t.check(pa, num_splits=4)
+    other, side = Rows(111, [(3000, 40)], hq, hkv, D, 64, fmt), torch.cuda.Stream()
+    args, pre = t.args(), (torch.zeros_like(out), torch.zeros_like(lse))
+    ws, ws_other, args_other = pa.workspace_for_stream(t.q, t.k, args[3], n, 4), None, other.args()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        _, _, ws_other = other.call(pa, args=args_other, ws=ws_other, stream=side)
+        t.call(pa, num_splits=4, args=args, out=pre[0], lse=pre[1], ws=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(pre[0][:t.T], out[:t.T]) and torch.equal(pre[1][:t.T], lse[:t.T])
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
 def test_stream_long(pa, fmt):
     Rows(73, [(20011, 6), (9000, 700), (3000, 3000)], 4, 1, 128, 64, fmt).check(pa)

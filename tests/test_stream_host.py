@@ -1,5 +1,7 @@
 """Refusals of the streams' operators: every check that the host can make, made before any CUDA call (addresses here are never
 touched)."""
+import os
+import re
 import subprocess
 
 import pytest
@@ -143,3 +145,20 @@ def test_scan_has_a_place_for_each_warp(pa, tmp_path, threads, places, compiles)
                        capture_output=True, text=True)
     assert (r.returncode == 0) == compiles, r.stderr
     assert compiles or "a place for each warp" in r.stderr
+
+
+def kernel_source(name):
+    return open(os.path.join(test_abi_host.ROOT, "paged_kv_attention_19_gb300", "csrc", name)).read()
+
+
+@pytest.mark.parametrize("name", ["pa_stream.cuh", "pa_tree.cuh"])
+def test_scores_wait_for_the_products_of_their_buffer(name):
+    """The scores of an item are written over the weights of an earlier one, which its product reads from tensor memory.  Products
+    with different accumulators are in no order of their own, so in every form of the kernel the wait stands before the scores."""
+    text = kernel_source(name)
+    begin = text[text.index("auto begin ="):]
+    begin = begin[:begin.index("tc_mma_ss(")]
+    waits = re.findall(r"if \(([^;]*?mbar_wait\(&pv_done\[b\], par\(c - (?:C::)?BACK\), status\))\) return false;", begin)
+    assert len(waits) == 1
+    condition = waits[0].split("!mbar_wait")[0]
+    assert re.fullmatch(r"c >= (\(uint32_t\))?(C::)?BACK && ", condition), condition
