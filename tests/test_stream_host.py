@@ -162,3 +162,14 @@ def test_scores_wait_for_the_products_of_their_buffer(name):
     assert len(waits) == 1
     condition = waits[0].split("!mbar_wait")[0]
     assert re.fullmatch(r"c >= (\(uint32_t\))?(C::)?BACK && ", condition), condition
+
+
+def test_tensor_memory_loads_carry_their_wait():
+    """A load's registers hold nothing before its wait, and to the compiler they are ready behind the statement: so the wait is in it."""
+    loads = 0
+    for path in sorted(os.listdir(os.path.join(test_abi_host.ROOT, "paged_kv_attention_19_gb300", "csrc"))):
+        for statement in re.findall(r"\basm\b[^;(]*\((?:[^;\"]|\"[^\"]*\")*;", kernel_source(path)):
+            if "tcgen05.ld." in statement:
+                loads += 1
+                assert statement.rfind("tcgen05.wait::ld.sync.aligned;") > statement.rfind("tcgen05.ld."), (path, statement[:90])
+    assert loads >= 4
