@@ -421,7 +421,9 @@ int pa_mla_cache_write(const void *c_lat, const void *k_rope, const int64_t *slo
  * pass max_pages_per_seq pages, or its tokens would pass max_tokens; an ended row
  * with held_pages out of range gives nothing back and sets PA_DEV_BAD_LEN.  A
  * parent out of order sets PA_DEV_BAD_TREE and counts as -1; a page outside
- * [0, num_pages) sets PA_DEV_BAD_PAGE and gives slot -1.
+ * [0, num_pages) sets PA_DEV_BAD_PAGE and gives slot -1.  So does such an entry of an
+ * ended row, which goes onto the list as it is: a row that pa_release_pages has taken pages
+ * from ends there and not here.
  * batch in [0, 8192], max_pages_per_seq * page_size and * batch below 2^31 (more:
  * PA_ERR_UNSUPPORTED); page_size >= 1; status: a device word or NULL, whose bits
  * are only ever set.  batch == 0 writes query_start[0],
@@ -707,7 +709,7 @@ size_t pa_stream_workspace_size(int batch, int max_query, int num_q_heads, int n
  *                F = ceil(first / page_size); 0 for a new row.  The caller keeps it from step to step
  *   ended        [batch] int32 or NULL: a row with a value other than 0 has ended and gives back all the pages
  *                that it has left.  (pa_plan_step's new_lens of -1 would give back entries that are no pages
- *                any more: rows that have released pages end here)
+ *                any more, and sets PA_DEV_BAD_PAGE: rows that have released pages end here)
  *   free_list    [num_pages] int32: a stack of free pages, of which free_count[0] are valid: the
  *                pages are pushed in row order, a row's in ascending order
  *   block_table  [batch, max_pages_per_seq] int32; a page that rows share would be given back by each of them

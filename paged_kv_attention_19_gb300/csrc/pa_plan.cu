@@ -223,7 +223,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
     a.query_start[a.batch] = total;
     if constexpr (MODE != PLAN_AFTER) plan_state_all_granted(a, tot);
   }
-  for (int r = first; r < tot.top - tot.count; r += stride) a.free_list[tot.count + r] = plan_given(a, rows, r);
+  for (int r = first; r < tot.top - tot.count; r += stride) {
+    const int page = plan_given(a, rows, r);
+    if (page < 0 || page >= a.num_pages) bad |= PA_DEV_BAD_PAGE;
+    a.free_list[tot.count + r] = page;
+  }
   for (int j = first; j < min(tot.need, tot.top); j += stride) {
     const int b = plan_find<&PlanRow::first>(rows, a.batch, j);
     const PlanRow r = rows[b];

@@ -625,6 +625,27 @@ def test_release_without_status_or_rows(pa):
         assert out is None or out.tolist() == [3]
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan_says_that_an_ended_row_gives_no_pages(pa, in_place):
+    """A row whose window has passed pages and that ends in the plan instead of the release: what goes onto the list is what the table
+    holds, and the status says that some of it are no pages, in that call already."""
+    P, pages, W = 16, 40, 12
+    for first, bits in ((20, pa.PA_DEV_BAD_PAGE), (200, 0)):
+        lens, held, start = i32([150, 40]), i32([10, 3]), i32([0, 0])
+        table = i32(np.arange(2 * W).reshape(2, W))
+        free, count, st = i32([30, 31, 32] + [-9] * (pages - 3)), i32([3]), i32([0])
+        pa.pa_release_pages(lens, held, start, free, count, table, page_size=P, window=64, first=first, status=st)
+        gone = 3 if first == 20 else 0  # pages 2 to 4 lie between the first tokens' two and the window
+        assert int(count) == 3 + gone and int(st) == 0
+        row, before = table[0, :10].tolist(), int(count)
+        out = {} if in_place else {"context_lens_out": i32([0] * 2), "held_pages_out": i32([0] * 2), "free_count_out": i32([0])}
+        pa.pa_plan_step(lens, i32([-1, 0]), held, free, count, table, i32([0] * 3), dev([0] * 4, torch.int64), i32([0] * 4),
+                        page_size=P, status=st, **out)
+        after = int(out.get("free_count_out", count))
+        assert int(st) == bits and after == before + 10 and free[before:after].tolist() == row
+        assert row.count(-1) == gone
+
+
 # ------------------------------------------------------------------------------------------ steps together
 
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
