@@ -490,6 +490,23 @@ def test_stream_refuses_lengths_on_the_device(pa):
         assert np.abs(f64(out[:20]) - f64(want[:20])).max() <= 0.05
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("splits", [0, 1, 40])
+def test_stream_rows_beside_refused_lengths(pa, fmt, splits):
+    """Rows before and behind a row with bad lengths are those of the 64-bit reference, and tokens behind the last row stay."""
+    good = Rows(97, [(3000, 20), (200, 3), (900, 150)], 8, 2, 128, 16, fmt, 700, 9)
+    o, l, spread, size = good.reference()
+    q, k, v, table, _, _ = good.args()
+    for lens, start in (([3000, -1, 900], [0, 20, 23, 173]), ([3000, 2, 900], [0, 20, 23, 173]), ([3000, 1 << 30, 900], [0, 20, 23, 173]),
+                        ([3000, 200, 900], [0, 20, 200, 173]), ([3000, 200, 900], [0, 20, -5, 173])):
+        out, lse, ws = good.call(pa, max_query=150, num_splits=splits, args=(q, k, v, table, i32(lens), i32(start)))
+        torch.cuda.synchronize()
+        assert pa.pa_read_device_status(ws) == pa.PA_DEV_BAD_LEN, (lens, start)
+        assert bool((out[173:] == 7.0).all()) and bool((lse[173:] == 7.0).all())
+        for s in (slice(0, 20), slice(23, 173))[:2 if start[2] == 23 else 1]:  # (a bad start makes the row behind it another one)
+            R.check_tree(f64(out[s]), f64(lse[s]), o[s], l[s], spread[s], size[s], good.D, good.lost())
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "fp8"])
 def test_stream_bad_pages(pa, fmt):
     """A visited entry outside the pool sets the status bit and is not loaded; rows that do not visit it keep their bits."""
