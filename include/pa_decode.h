@@ -666,7 +666,9 @@ int pa_kv_compact_granted(void *k_pool, void *v_pool, const int32_t *block_table
  * batch == 0 or num_tokens == 0 is a no-op (the status word stays as it was).
  * bf16 pools: products of bf16 operands, weights rounded to bf16.  FP8 and NVFP4 pools: codes as
  * exact f16 values, a query row scaled by a power of two to f16, weights rounded to f16.  The calls
- * always use the default wait limit.  num_splits == 0: no share is made for less than 128 tokens' work.
+ * always use the default wait limit.  num_splits == 0: no share is made for less than 128 tokens' work, and
+ * a row's queries that see at most 768 tokens stay in one share; a lone short row may be faster in more
+ * (num_splits > 0).
  */
 int pa_stream_gqa(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
                   const int32_t *context_lens, const int32_t *query_start, const int32_t *granted, void *out,

@@ -23,8 +23,10 @@ constexpr int kPieceCost = 512;
 // Least share of a CTA, in tokens, where the number of shares is left to the call: below two stages, one for each
 // softmax group, a share takes as long and only adds to what is merged (128, 256: one token 15.2, 15.8 us).
 constexpr int kMinShare = 128;
-// Pairs of at most so many tokens are not cut (400, 768: single tokens and chunks in a window of 512 30.5, 28.4 us; 1100 gains
-// nothing there).
+// Pairs of at most so many tokens are not cut, where the number of shares is left to the call (400, 768: single tokens and chunks
+// in a window of 512 30.5, 28.4 us; 1100 gains nothing there).  The rule does not look at how much work there is beside them: a
+// lone token over 768 tokens and 8 key heads takes 14.3 us whole and 13.0 in six shares a head, over FP8 19.8 and 16.6; over 512
+// it is 12.5 and 12.1, over 256 whole is as fast.
 constexpr int kWhole = 768;
 
 // How a call's query rows are tiled, and where its workspace's parts lie.
@@ -133,7 +135,7 @@ int stream_call(const void *q, const void *k_pool, const void *v_pool, const int
   a.window = window > 0 ? window : 0;
   a.first = window <= 0 ? 0 : first < max_ctx ? first : max_ctx;
   a.piece_cost = kPieceCost;
-  a.whole = kWhole;
+  a.whole = num_splits > 0 ? 0 : kWhole;  // (a caller's number of shares is what it gets)
   a.log2_share = num_splits > 0 ? 0 : ilog2(kMinShare);
   a.nparts = num_splits > 0 ? num_splits : sms < kAutoParts ? sms : kAutoParts;
   // groups of a CTA for each key head, unless more than a tenth of the CTAs would be left over (8 heads on 152: single tokens

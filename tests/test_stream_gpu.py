@@ -207,6 +207,18 @@ def test_stream_long_pieces_repeat(pa, fmt, hq, hkv, D, n):
         assert torch.equal(pre[0][:t.T], out[:t.T]) and torch.equal(pre[1][:t.T], lse[:t.T])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("rows,hkv", [([(700, 1)], 1), ([(300, 2), (650, 90)], 2), ([(513, 1)] * 3, 4)])
+def test_stream_splits_cut_short_rows(pa, fmt, rows, hkv):
+    """A number of shares that the caller gives holds for short rows too: their sums are then formed in parts, whose rounding shows
+    in the log-sum-exps of hundreds of values."""
+    t = Rows(112, rows, 64 * hkv, hkv, 64, 16, fmt)
+    whole, parts = t.check(pa, num_splits=hkv), t.check(pa, num_splits=9 * hkv)
+    assert not torch.equal(whole[1], parts[1])
+    again = t.call(pa, num_splits=9 * hkv)
+    assert torch.equal(again[0], parts[0]) and torch.equal(again[1], parts[1])
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
 def test_stream_long(pa, fmt):
     Rows(73, [(20011, 6), (9000, 700), (3000, 3000)], 4, 1, 128, 64, fmt).check(pa)
