@@ -438,7 +438,8 @@ def pa_stream_gqa(q, k_pool, v_pool, block_table, context_lens, query_start, out
     [T, Hq] fp32 or None (tokens behind the last row stay as they were); pools and block_table as for
     pa_decode_gqa.  The token at position p attends to those of [0, p]; under a window (> 0) to the `window` most
     recent ones and the row's `first` ones.  workspace: workspace_for_stream(...).  granted: optional [B] int32
-    (pa_plan_step's); a row with 0 is left out and its outputs stay as they were."""
+    (pa_plan_step's); a row with 0 is left out and its outputs stay as they were.  Single tokens without first
+    tokens are faster by pa_decode_gqa."""
     _done("pa_stream_gqa", (_native_module or _native()).stream_gqa(
         0, q, k_pool, v_pool, block_table, context_lens, query_start, out, lse, granted, workspace, max_query, scale,
         1.0, 1.0, window, first, num_splits, max_context_len, stream))

@@ -18,15 +18,15 @@ constexpr int kMaxQuery = 1 << 30;
 // Longest context: the ends of the stages behind it, two of 128 tokens, are still tokens below 2^31.
 constexpr int kMaxContext = INT_MAX - 512;
 // Fixed cost of a piece of work in the partition, as the tokens that a CTA passes meanwhile (256, 512, 1024: a prompt of
-// 8192 tokens 512, 448, 448 us; FP8 single tokens 98.3, 92.9, 97.6).
+// 8192 tokens 476, 471, 495 us; FP8 single tokens 92.9, 88.8, 95.4).
 constexpr int kPieceCost = 512;
 // Least share of a CTA, in tokens, where the number of shares is left to the call: below two stages, one for each
-// softmax group, a share takes as long and only adds to what is merged (128, 256: one token 15.2, 15.8 us).
+// softmax group, a share takes as long and only adds to what is merged (128, 256: one token 14.1, 15.3 us).
 constexpr int kMinShare = 128;
 // Pairs of at most so many tokens are not cut, where the number of shares is left to the call (400, 768: single tokens and chunks
-// in a window of 512 30.5, 28.4 us; 1100 gains nothing there).  The rule does not look at how much work there is beside them: a
-// lone token over 768 tokens and 8 key heads takes 14.3 us whole and 13.0 in six shares a head, over FP8 19.8 and 16.6; over 512
-// it is 12.5 and 12.1, over 256 whole is as fast.
+// in a window of 512 30.1, 28.1 us; 1100 gains nothing there, and one token over 1028 takes 18.1 us for 14.1).  The rule does not
+// look at how much work there is beside them: a lone token over 768 tokens and 8 key heads takes 14.3 us whole and 13.0 in six
+// shares a head, over FP8 19.8 and 16.6; over 512 it is 12.5 and 12.1, over 256 whole is as fast.
 constexpr int kWhole = 768;
 
 // How a call's query rows are tiled, and where its workspace's parts lie.
@@ -139,7 +139,7 @@ int stream_call(const void *q, const void *k_pool, const void *v_pool, const int
   a.log2_share = num_splits > 0 ? 0 : ilog2(kMinShare);
   a.nparts = num_splits > 0 ? num_splits : sms < kAutoParts ? sms : kAutoParts;
   // groups of a CTA for each key head, unless more than a tenth of the CTAs would be left over (8 heads on 152: single tokens
-  // over FP8 103 us for 113 with one line of all heads, NVFP4 228 for 255; bf16 64 for 62)
+  // over FP8 89.1 us for 92.0 with one line of all heads, NVFP4 189.5 for 191.3; bf16 59.9 for 59.3)
   a.hg = 10 * (a.nparts / Hkv * Hkv) >= 9 * a.nparts ? Hkv : 1;
   a.hl = Hkv / a.hg;
   a.qscale = qscale;

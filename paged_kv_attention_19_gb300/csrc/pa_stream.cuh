@@ -35,11 +35,12 @@
 // Tensor memory: scores at 0 (the weights over a half of their buffer), outputs at 256.  At head_dim 256 one output fills
 // the rest: one tile, one softmax group and one issuing thread.
 //
-// Measured (head_dim 128; per call, calls back to back, inputs in turn).  bf16: a prompt of 8192 tokens x 32 heads 448 us (1.23 PFLOP/s,
-// 65 % of the measured 1886 TFLOP/s; a stage of two tiles takes 3540 cycles for 2048 of products, tensor pipe 47 % at 4096 tokens);
-// 32 single tokens x 64 heads, 128 to 16384 tokens in a window of 4096 + 128, 59 us (266 MB, 4.5 TB/s; 28000 of 100000 cycles
-// before the first weights).  The same shape over FP8, without a window, 89 us, issue slots 38 %.  NVFP4: 64 x 32 heads to 32768 tokens 182 us,
-// issue slots 46 %.
+// Measured (head_dim 128; per call, calls back to back, inputs in turn).  bf16: a prompt of 8192 tokens x 32 heads 470 us (1.17 PFLOP/s,
+// 62 % of the measured 1886 TFLOP/s; a stage of two tiles takes 3640 cycles for 2048 of products, tensor pipe 45 % at 4096 tokens);
+// 32 single tokens x 64 heads, 128 to 16384 tokens in a window of 4096 + 128, 60 us (266 MB, 4.4 TB/s; 30500 of 103000 cycles
+// before the first weights).  The same shape over FP8, without a window, 89 us, issue slots 38 %.  NVFP4: 64 x 32 heads to 32768 tokens 189 us,
+// issue slots 44 %.  Over codes at head_dim 64 (where 96 registers a thread spill 132 to 164 bytes) 32 x 64 heads to 16384 tokens 72 us, FP8
+// and NVFP4 alike; at head_dim 256 32 x 32 heads 90 and 88.
 #pragma once
 
 #include "pa_tree.cuh"
@@ -124,7 +125,7 @@ struct StreamCfg {
   // with one buffer a half of an item's weights is handed over by itself, so that its product runs beside the rest
   static constexpr bool HALVES = BACK == 1;
   // and the groups take turns at the exponentials: in step they would share the units for them and then both wait for the products
-  // (prompt 456 us for 488 without, chunks 739 for 784)
+  // (prompt 470 us for 476 without, chunks 782 for 790)
   static constexpr bool TURNS = BACK == 1 && QT == 2;
   // registers a thread: what the softmax warps hold of a row and its output does not fit the launch's share
   // (384 x 168 or 640 x 96), so the other warps hand some over
